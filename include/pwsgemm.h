@@ -368,6 +368,122 @@ int gemm_set_scratch_pool(int enable);
 int gemm_f16_nt_plan(int64_t M, int64_t N, int64_t K, const gemm_f16_t* lhs, const gemm_f16_t* rhs,
                      const gemm_f16_t* out, int stages, int64_t* plan);
 
+/*
+ * The operators around the products.
+ *
+ * Entry points that fuse a product with what a language model does next to
+ * it, forward and backward, on the same tensor-core pipeline:
+ *
+ *   gemm_gated_nt / _bwd  -- the gated feed-forward block: both projections,
+ *                            the activation and the elementwise product.
+ *   gemm_xent_nt / _bwd   -- softmax cross entropy over a linear head; the
+ *                            logits are never kept.
+ *   gemm_nt_bwd           -- the backward pass of out = lhs . rhs^T.
+ *
+ * Conventions beyond the ones above:
+ *   - Matrices are dense, row-major, of 16-bit elements of one type
+ *     (gemm_type), 2-byte aligned; any size from 0 below 2^31.  Sums,
+ *     activations, softmax statistics and losses are fp32; an output is
+ *     rounded once from its fp32 value (nearest, ties to even).
+ *   - `workspace` is device memory of the caller, 256-byte aligned, of at
+ *     least the bytes that the _workspace call of the same arguments reports
+ *     (host logic only, on the device that will run the call; null where it
+ *     reports 0).  Its contents need not be set, it is free again once the
+ *     call's work on `stream` is done, and nothing is kept in it from one call
+ *     to the next.  Nothing is allocated, so every call can be captured into a
+ *     CUDA graph.
+ *   - An optional output is a null pointer; outputs overlap neither inputs nor
+ *     each other.
+ *   - Results depend on the arguments alone: no atomics, partial sums are
+ *     joined in a fixed order.
+ *   - Return codes: GEMM_OK, GEMM_ERR_INVALID_ARG (a size out of range, a
+ *     missing pointer, an unknown type or activation, an overlap, a missing,
+ *     misaligned or too small workspace), GEMM_ERR_ALIGNMENT (a pointer not
+ *     aligned to its element), GEMM_ERR_UNSUPPORTED_ARCH, GEMM_ERR_LAUNCH.
+ */
+typedef enum {
+    GEMM_TYPE_HALF = 0,   /* IEEE binary16 */
+    GEMM_TYPE_BFLOAT = 1  /* bfloat16      */
+} gemm_type;
+
+typedef enum {
+    GEMM_ACT_SILU = 0,    /* g / (1 + exp(-g))                                              */
+    GEMM_ACT_GELU = 1     /* (g / 2) (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))            */
+} gemm_act;
+
+/*
+ * gemm_gated_nt -- h = act(x . w_gate^T) * (x . w_up^T).
+ *
+ *   x            : [M, K]          w_gate, w_up : [F, K]
+ *   h            : [M, F], written
+ *   g, u         : [M, F], x . w_gate^T and x . w_up^T, written for the
+ *                  backward pass where not null (both or neither)
+ *
+ * M = 1 (one token) to any number of rows.  K == 0 gives zeros.
+ */
+int gemm_gated_nt(int64_t M, int64_t F, int64_t K, const void* x, const void* w_gate, const void* w_up, void* h,
+                  void* g, void* u, int type, int act, void* workspace, int64_t workspace_bytes,
+                  cudaStream_t stream);
+int gemm_gated_nt_workspace(int64_t M, int64_t F, int64_t K, const void* x, const void* w_gate, const void* w_up,
+                            int type, int64_t* bytes);
+
+/*
+ * gemm_gated_nt_bwd -- the gradients of gemm_gated_nt from dh and the kept g, u:
+ *
+ *   dg = dh * u * act'(g),  du = dh * act(g)          (rounded to 16 bits)
+ *   dx      : [M, K] = dg . w_gate + du . w_up        (null: not wanted)
+ *   dw_gate : [F, K] = dg^T . x,  dw_up : [F, K] = du^T . x   (both or neither)
+ */
+int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh, const void* g, const void* u, const void* x,
+                      const void* w_gate, const void* w_up, void* dx, void* dw_gate, void* dw_up, int type, int act,
+                      void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+int gemm_gated_nt_bwd_workspace(int64_t M, int64_t F, int64_t K, const void* dh, const void* g, const void* u,
+                                const void* x, const void* w_gate, const void* w_up, int type, int64_t* bytes);
+
+/*
+ * gemm_xent_nt -- softmax cross entropy of the logits z = x . w^T [M, V].
+ *
+ *   x      : [M, K]      w : [V, K], V >= 1
+ *   target : int64 [M], a class in [0, V) or ignore_index
+ *   lse    : float [M], log sum_v exp(z[i][v]), written for every row
+ *   loss   : float [M], lse[i] - z[i][target[i]]; 0 where target[i] is
+ *            ignore_index; NaN for any other target outside [0, V)
+ */
+int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, const void* w, const int64_t* target,
+                 int64_t ignore_index, float* loss, float* lse, int type, void* workspace, int64_t workspace_bytes,
+                 cudaStream_t stream);
+int gemm_xent_nt_workspace(int64_t M, int64_t V, int64_t K, const void* x, const void* w, int type, int64_t* bytes);
+
+/*
+ * gemm_xent_nt_bwd -- the gradients of sum_i dloss[i] loss[i].
+ *
+ *   D[i][v] = dloss[i] (exp(z[i][v] - lse[i]) - [v == target[i]]), 0 in rows
+ *             whose target is ignore_index, NaN in rows of any other target
+ *             outside [0, V); rounded to 16 bits at a scale that keeps it in range
+ *   dx : [M, K] = D . w   (null: not wanted)
+ *   dw : [V, K] = D^T . x (null: not wanted)
+ *
+ * lse is gemm_xent_nt's.  The vocabulary is taken in pieces and the logits of
+ * a piece are computed again; the workspace holds one piece of D.
+ */
+int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, const void* w, const int64_t* target,
+                     int64_t ignore_index, const float* lse, const float* dloss, void* dx, void* dw, int type,
+                     void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+int gemm_xent_nt_bwd_workspace(int64_t M, int64_t V, int64_t K, const void* x, const void* w, int type,
+                               int64_t* bytes);
+
+/*
+ * gemm_nt_bwd -- the gradients of out [M, N] = x [M, K] . w [N, K]^T.
+ *
+ *   dy : [M, N]
+ *   dx : [M, K] = dy . w    (null: not wanted)
+ *   dw : [N, K] = dy^T . x  (null: not wanted)
+ */
+int gemm_nt_bwd(int64_t M, int64_t N, int64_t K, const void* dy, const void* x, const void* w, void* dx, void* dw,
+                int type, void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+int gemm_nt_bwd_workspace(int64_t M, int64_t N, int64_t K, const void* dy, const void* x, const void* w, int type,
+                          int64_t* bytes);
+
 #if defined(__GNUC__)
 #pragma GCC visibility pop
 #endif

@@ -45,6 +45,12 @@ GEMM_DEBUG_FORCE_DOUBLE_SLOT = 4096
 GEMM_DEBUG_NO_DOUBLE_SLOT = 8192
 GEMM_DEBUG_IN_PLACE = 16384
 
+GEMM_TYPE_HALF = 0
+GEMM_TYPE_BFLOAT = 1
+GEMM_ACT_SILU = 0
+GEMM_ACT_GELU = 1
+_ACTS = {"silu": GEMM_ACT_SILU, "gelu": GEMM_ACT_GELU}
+
 _lib = None
 
 
@@ -85,6 +91,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.gemm_set_scratch_pool.restype = i32
     lib.gemm_f16_nt_plan.argtypes = [i64, i64, i64, vp, vp, vp, i32, ctypes.POINTER(i64)]
     lib.gemm_f16_nt_plan.restype = i32
+    pi64 = ctypes.POINTER(i64)
+    for name, args in (
+            ("gemm_gated_nt", [i64] * 3 + [vp] * 6 + [i32, i32, vp, i64, vp]),
+            ("gemm_gated_nt_workspace", [i64] * 3 + [vp] * 3 + [i32, pi64]),
+            ("gemm_gated_nt_bwd", [i64] * 3 + [vp] * 9 + [i32, i32, vp, i64, vp]),
+            ("gemm_gated_nt_bwd_workspace", [i64] * 3 + [vp] * 6 + [i32, pi64]),
+            ("gemm_xent_nt", [i64] * 3 + [vp] * 3 + [i64, vp, vp, i32, vp, i64, vp]),
+            ("gemm_xent_nt_workspace", [i64] * 3 + [vp] * 2 + [i32, pi64]),
+            ("gemm_xent_nt_bwd", [i64] * 3 + [vp] * 3 + [i64] + [vp] * 4 + [i32, vp, i64, vp]),
+            ("gemm_xent_nt_bwd_workspace", [i64] * 3 + [vp] * 2 + [i32, pi64]),
+            ("gemm_nt_bwd", [i64] * 3 + [vp] * 5 + [i32, vp, i64, vp]),
+            ("gemm_nt_bwd_workspace", [i64] * 3 + [vp] * 3 + [i32, pi64])):
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = i32
     if path is None:
         _lib = lib
     return lib
@@ -221,6 +242,209 @@ def gemm_f16_nt_noalloc(lhs, rhs, out=None, stages: int = 4, stream=None):
     return out
 
 
+# ---------------------------------------------------------------- the operators around the products
+
+def _type_of(name, tensors):
+    """The GEMM_TYPE_* of tensors that must share one 16-bit type, be dense
+    matrices and lie on one CUDA device."""
+    import torch
+    first = tensors[0]
+    if first.dtype == torch.bfloat16:
+        code = GEMM_TYPE_BFLOAT
+    elif first.dtype == torch.float16:
+        code = GEMM_TYPE_HALF
+    else:
+        raise TypeError(f"{name} takes float16 or bfloat16 tensors")
+    for t in tensors:
+        if t.dtype != first.dtype:
+            raise TypeError(f"{name}: all matrices must have one type, got {first.dtype} and {t.dtype}")
+        if t.dim() != 2:
+            raise ValueError(f"{name} takes matrices, got a tensor of shape {tuple(t.shape)}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} takes contiguous CUDA tensors")
+        if t.device != first.device:
+            raise ValueError(f"{name}: all tensors must be on one device, got {first.device} and {t.device}")
+    return code
+
+
+def _act_code(name, act):
+    if act not in _ACTS:
+        raise ValueError(f"{name}: act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _vector(name, what, t, rows, dtype, device):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != rows or not t.is_contiguous():
+        raise ValueError(f"{name}: {what} must be a contiguous vector of {rows} elements, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: all tensors must be on one device, got {device} and {t.device}")
+
+
+class _Launch:
+    """Makes the operand's device and the call's stream current, so that
+    outputs and workspaces are taken from that stream's memory and are not
+    handed to other work while the call still uses them."""
+
+    def __init__(self, stream, device):
+        import torch
+        self._contexts = []
+        if torch.cuda.current_device() != device.index:
+            self._contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self._contexts.append(torch.cuda.stream(stream))
+        self._stream, self._device = stream, device
+
+    def __enter__(self):
+        for c in self._contexts:
+            c.__enter__()
+        return _stream_ptr(self._stream, self._device)
+
+    def __exit__(self, *exc):
+        for c in reversed(self._contexts):
+            c.__exit__(*exc)
+        return False
+
+
+def _workspace(name, device, *args):
+    """(tensor or None, address, bytes) of the workspace the call reports."""
+    import torch
+    need = ctypes.c_int64()
+    _check(getattr(load_library(), name + "_workspace")(*args, ctypes.byref(need)), name)
+    if need.value == 0:
+        return None, None, 0
+    ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), need.value
+
+
+def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream=None):
+    """h[M,F] = act(x[M,K] @ w_gate[F,K].T) * (x @ w_up[F,K].T), one kernel.
+
+    float16 or bfloat16; sums, activation and product in fp32, h rounded once.
+    act is "silu" or "gelu" (tanh form).  With save=True returns (h, g, u),
+    where g and u are the two products, for gemm_gated_nt_bwd.
+    """
+    import torch
+    name = "gemm_gated_nt"
+    code, act_code = _type_of(name, (x, w_gate, w_up)), _act_code(name, act)
+    M, K = x.shape
+    F = w_gate.shape[0]
+    if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
+        raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w_gate.shape)}, {tuple(w_up.shape)} do not form "
+                         "[M,K], [F,K], [F,K]")
+    with _Launch(stream, x.device) as s:
+        h = torch.empty((M, F), dtype=x.dtype, device=x.device)
+        g, u = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
+        px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, F, K, px, pg, pu, code)
+        _check(load_library().gemm_gated_nt(M, F, K, px, pg, pu, h.data_ptr(), g.data_ptr() if save else None,
+                                            u.data_ptr() if save else None, code, act_code, ws_ptr, ws_bytes, s), name)
+    return (h, g, u) if save else h
+
+
+def gemm_gated_nt_bwd(dh, g, u, x, w_gate, w_up, act: str = "silu", need_dx: bool = True, need_dw: bool = True,
+                      stream=None):
+    """The gradients of gemm_gated_nt: (dx[M,K], dw_gate[F,K], dw_up[F,K]).
+
+    g and u are what gemm_gated_nt(..., save=True) returned.  Gradients not
+    needed are None.
+    """
+    import torch
+    name = "gemm_gated_nt_bwd"
+    code, act_code = _type_of(name, (dh, g, u, x, w_gate, w_up)), _act_code(name, act)
+    M, K = x.shape
+    F = w_gate.shape[0]
+    if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
+        raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w_gate.shape)}, {tuple(w_up.shape)} do not form "
+                         "[M,K], [F,K], [F,K]")
+    if any(tuple(t.shape) != (M, F) for t in (dh, g, u)):
+        raise ValueError(f"{name}: dh, g and u must have shape {(M, F)}")
+    with _Launch(stream, x.device) as s:
+        dx = torch.empty_like(x) if need_dx else None
+        dwg, dwu = (torch.empty_like(w_gate), torch.empty_like(w_up)) if need_dw else (None, None)
+        ptrs = [t.data_ptr() for t in (dh, g, u, x, w_gate, w_up)]
+        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, F, K, *ptrs, code)
+        outs = [t.data_ptr() if t is not None else None for t in (dx, dwg, dwu)]
+        _check(load_library().gemm_gated_nt_bwd(M, F, K, *ptrs, *outs, code, act_code, ws_ptr, ws_bytes, s), name)
+    return dx, dwg, dwu
+
+
+def _xent_shapes(name, x, w, target):
+    import torch
+    code = _type_of(name, (x, w))
+    if w.shape[1] != x.shape[1]:
+        raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w.shape)} do not form [M,K], [V,K]")
+    _vector(name, "target", target, x.shape[0], torch.int64, x.device)
+    return code, x.shape[0], w.shape[0], x.shape[1]
+
+
+def gemm_xent_nt(x, w, target, ignore_index: int = -100, stream=None):
+    """Softmax cross entropy of the logits x[M,K] @ w[V,K].T, never kept.
+
+    target is int64 [M].  Returns (loss, lse), float32 [M]: loss is 0 in rows
+    whose target is ignore_index and NaN for any other target outside [0, V).
+    """
+    import torch
+    name = "gemm_xent_nt"
+    code, M, V, K = _xent_shapes(name, x, w, target)
+    with _Launch(stream, x.device) as s:
+        loss = torch.empty(M, dtype=torch.float32, device=x.device)
+        lse = torch.empty_like(loss)
+        px, pw = x.data_ptr(), w.data_ptr()
+        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, V, K, px, pw, code)
+        _check(load_library().gemm_xent_nt(M, V, K, px, pw, target.data_ptr(), int(ignore_index), loss.data_ptr(),
+                                           lse.data_ptr(), code, ws_ptr, ws_bytes, s), name)
+    return loss, lse
+
+
+def gemm_xent_nt_bwd(x, w, target, lse, dloss, ignore_index: int = -100, need_dx: bool = True, need_dw: bool = True,
+                     stream=None):
+    """The gradients of sum(dloss * loss) of gemm_xent_nt: (dx[M,K], dw[V,K]).
+
+    lse is gemm_xent_nt's, dloss float32 [M].  Gradients not needed are None.
+    """
+    import torch
+    name = "gemm_xent_nt_bwd"
+    code, M, V, K = _xent_shapes(name, x, w, target)
+    _vector(name, "lse", lse, M, torch.float32, x.device)
+    _vector(name, "dloss", dloss, M, torch.float32, x.device)
+    with _Launch(stream, x.device) as s:
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(w) if need_dw else None
+        px, pw = x.data_ptr(), w.data_ptr()
+        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, V, K, px, pw, code)
+        _check(load_library().gemm_xent_nt_bwd(M, V, K, px, pw, target.data_ptr(), int(ignore_index), lse.data_ptr(),
+                                               dloss.data_ptr(), dx.data_ptr() if need_dx else None,
+                                               dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
+    return dx, dw
+
+
+def gemm_nt_bwd(dy, x, w, need_dx: bool = True, need_dw: bool = True, stream=None):
+    """The gradients of y[M,N] = x[M,K] @ w[N,K].T: (dx = dy @ w, dw = dy.T @ x).
+
+    float16 or bfloat16, fp32 sums.  Gradients not needed are None.
+    """
+    import torch
+    name = "gemm_nt_bwd"
+    code = _type_of(name, (dy, x, w))
+    M, N = dy.shape
+    K = x.shape[1]
+    if x.shape[0] != M or tuple(w.shape) != (N, K):
+        raise ValueError(f"{name}: shapes {tuple(dy.shape)}, {tuple(x.shape)}, {tuple(w.shape)} do not form "
+                         "[M,N], [M,K], [N,K]")
+    with _Launch(stream, x.device) as s:
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(w) if need_dw else None
+        ptrs = [t.data_ptr() for t in (dy, x, w)]
+        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, N, K, *ptrs, code)
+        _check(load_library().gemm_nt_bwd(M, N, K, *ptrs, dx.data_ptr() if need_dx else None,
+                                          dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
+    return dx, dw
+
+
 def gemm_device_status(stream=None) -> int:
     """Synchronizes the stream; returns and clears the device status word."""
     return load_library().gemm_device_status(_stream_ptr(stream, None))
@@ -259,4 +483,5 @@ __all__ = [
     "GemmError", "load_library", "header_functions", "gemm_s32_nn", "gemm_f16_nt", "gemm_device_status",
     "gemm_status_string", "gemm_set_wait_timeout_ns", "gemm_set_debug_flags", "gemm_set_scratch_pool",
     "gemm_f16_nt_plan", "gemm_f16_nt_noalloc", "gemm_s32_nn_ring",
+    "gemm_gated_nt", "gemm_gated_nt_bwd", "gemm_xent_nt", "gemm_xent_nt_bwd", "gemm_nt_bwd",
 ]

@@ -23,9 +23,10 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libpwsgemm.so")
 PEAKS_PATH = os.path.join(OUT_DIR, "libpwspeaks.so")
 
-SOURCES = ["runtime.cu", "gemm_s32_nn.cu", "gemm_f16_nt.cu"]
+SOURCES = ["runtime.cu", "gemm_s32_nn.cu", "gemm_f16_nt.cu", "gemm_gated.cu", "gemm_xent.cu", "gemm_bwd.cu"]
 PEAKS_SOURCES = ["peaks.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("ptx.cuh", "internal.h")] + [os.path.join(INCLUDE, "pwsgemm.h")]
+HEADERS = [os.path.join(CSRC, h) for h in ("ptx.cuh", "internal.h", "waiter.cuh", "product.cuh",
+                                                 "product_host.cuh")] + [os.path.join(INCLUDE, "pwsgemm.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

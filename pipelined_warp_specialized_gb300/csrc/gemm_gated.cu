@@ -1,0 +1,292 @@
+// gemm_gated.cu -- the gated feed-forward block h = act(x Wg^T) * (x Wu^T) and
+// its backward pass.
+//
+// Forward: one product with the gate's and the up projection's rows side by
+// side in every tile (the first and second half of the accumulator's
+// columns), so x is read once and the activation and the product happen in
+// the epilogue on fp32 sums: h is rounded once, and g, u are rounded only to
+// be kept for the backward pass.
+//
+// Backward: dg = dh u act'(g) and du = dh act(g) elementwise, rounded to the
+// inputs' type because the tensor cores multiply 16-bit operands (the rounding
+// an unfused backward pass makes as well); then dx = dg Wg + du Wu as one
+// accumulation over both weights, and dWg = dg^T x, dWu = du^T x as one launch.
+#include "product_host.cuh"
+
+namespace pws {
+namespace fused {
+namespace {
+
+// dg, du [M, F] with rows ldo apart from dh, g, u [M, F] (dense).  Memory
+// bound: reads three and writes two 16-bit matrices.  VEC: eight elements a
+// thread where every row starts on a 16-byte boundary, else one.
+template <bool VEC>
+__global__ void __launch_bounds__(256)
+gated_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g, const uint16_t* __restrict__ u,
+                  uint16_t* __restrict__ dg, uint16_t* __restrict__ du, int64_t M, int F, int64_t ldo, int act,
+                  int bf16) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    constexpr int E = VEC ? 8 : 1;
+    const int per_row = F / E;
+    const int64_t total = M * per_row;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t row = i / per_row;
+        const int c = static_cast<int>(i - row * per_row) * E;
+        const int64_t at = row * F + c, to = row * ldo + c;
+        if constexpr (VEC) {
+            const uint4 a = *reinterpret_cast<const uint4*>(dh + at);
+            const uint4 b = *reinterpret_cast<const uint4*>(g + at);
+            const uint4 d = *reinterpret_cast<const uint4*>(u + at);
+            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w}, dv[4] = {d.x, d.y, d.z, d.w};
+            uint32_t og[4], ou[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 h2 = unpack16(av[j], bf16), g2 = unpack16(bv[j], bf16), u2 = unpack16(dv[j], bf16);
+                float v0, s0, v1, s1;
+                act_value_slope(g2.x, act, v0, s0);
+                act_value_slope(g2.y, act, v1, s1);
+                og[j] = pack16(h2.x * u2.x * s0, h2.y * u2.y * s1, bf16);
+                ou[j] = pack16(h2.x * v0, h2.y * v1, bf16);
+            }
+            *reinterpret_cast<uint4*>(dg + to) = make_uint4(og[0], og[1], og[2], og[3]);
+            *reinterpret_cast<uint4*>(du + to) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        } else {
+            const float h1 = unpack16(dh[at], bf16).x, g1 = unpack16(g[at], bf16).x, u1 = unpack16(u[at], bf16).x;
+            float v, s;
+            act_value_slope(g1, act, v, s);
+            const uint32_t o = pack16(h1 * u1 * s, h1 * v, bf16);
+            dg[to] = static_cast<uint16_t>(o & 0xFFFFu);
+            du[to] = static_cast<uint16_t>(o >> 16);
+        }
+    }
+}
+
+bool bad_codes(int type, int act) {
+    return (type != GEMM_TYPE_HALF && type != GEMM_TYPE_BFLOAT) || (act != GEMM_ACT_SILU && act != GEMM_ACT_GELU);
+}
+
+int check_gated(int64_t M, int64_t F, int64_t K, const void* x, const void* wg, const void* wu, const void* h,
+                const void* g, const void* u, int type, int act) {
+    if (bad_size(M) || bad_size(F) || bad_size(K) || bad_codes(type, act)) return GEMM_ERR_INVALID_ARG;
+    if (too_many_tiles(M, F)) return GEMM_ERR_INVALID_ARG;
+    if ((g == nullptr) != (u == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (odd_address(x) || odd_address(wg) || odd_address(wu) || odd_address(h) || odd_address(g) || odd_address(u))
+        return GEMM_ERR_ALIGNMENT;
+    if (M > 0 && F > 0 && K > 0 && (!x || !wg || !wu)) return GEMM_ERR_INVALID_ARG;
+    const Range in[3] = {{x, bytes16(M, K)}, {wg, bytes16(F, K)}, {wu, bytes16(F, K)}};
+    const Range out[3] = {{h, bytes16(M, F)}, {g, bytes16(M, F)}, {u, bytes16(M, F)}};
+    return overlaps(in, out) ? GEMM_ERR_INVALID_ARG : GEMM_OK;
+}
+
+struct GatedPlan {
+    Product pr;
+    Layout l;
+    Source x, wg, wu;
+    size_t bytes = 0;
+};
+
+GatedPlan plan_gated(int64_t M, int64_t F, int64_t K, const void* x, const void* wg, const void* wu, int num_sms,
+                     void* ws) {
+    GatedPlan pl;
+    Carver c;
+    c.base = static_cast<char*>(ws);
+    pl.pr.M = M; pl.pr.N = F; pl.pr.K = K;
+    pl.pr.gated = true;
+    pl.l = choose_layout(pl.pr, num_sms);
+    pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
+    // both weights share one row stride
+    const bool rw = !tma_ok(wg, K) || !tma_ok(wu, K);
+    pl.wg = source_of(wg, F, K, rw, &c);
+    pl.wu = source_of(wu, F, K, rw, &c);
+    pl.bytes = c.used;
+    return pl;
+}
+
+int check_gated_bwd(int64_t M, int64_t F, int64_t K, const void* dh, const void* g, const void* u, const void* x,
+                    const void* wg, const void* wu, const void* dx, const void* dwg, const void* dwu, int type,
+                    int act) {
+    if (bad_size(M) || bad_size(F) || bad_size(K) || bad_codes(type, act)) return GEMM_ERR_INVALID_ARG;
+    if (too_many_tiles(M, K) || too_many_tiles(2 * F, K)) return GEMM_ERR_INVALID_ARG;
+    if ((dwg == nullptr) != (dwu == nullptr)) return GEMM_ERR_INVALID_ARG;
+    const void* all[9] = {dh, g, u, x, wg, wu, dx, dwg, dwu};
+    for (const void* q : all)
+        if (odd_address(q)) return GEMM_ERR_ALIGNMENT;
+    if (M > 0 && F > 0 && K > 0 && (!dh || !g || !u || (dwg && !x) || (dx && (!wg || !wu))))
+        return GEMM_ERR_INVALID_ARG;
+    const Range in[6] = {{dh, bytes16(M, F)}, {g, bytes16(M, F)},  {u, bytes16(M, F)},
+                         {x, bytes16(M, K)},  {wg, bytes16(F, K)}, {wu, bytes16(F, K)}};
+    const Range out[3] = {{dx, bytes16(M, K)}, {dwg, bytes16(F, K)}, {dwu, bytes16(F, K)}};
+    return overlaps(in, out) ? GEMM_ERR_INVALID_ARG : GEMM_OK;
+}
+
+struct GatedBwdPlan {
+    Product dx, dw;
+    Layout ldx, ldw;
+    Source x, wg, wu;
+    uint16_t* dg = nullptr;
+    uint16_t* du = nullptr;
+    int64_t ldf = 0;
+    float* partial = nullptr;
+    size_t bytes = 0;
+};
+
+GatedBwdPlan plan_gated_bwd(int64_t M, int64_t F, int64_t K, const void* x, const void* wg, const void* wu,
+                            bool want_dx, bool want_dw, int num_sms, void* ws) {
+    GatedBwdPlan pl;
+    Carver c;
+    c.base = static_cast<char*>(ws);
+    pl.ldf = round_up(F, 64);
+    pl.dg = c.take<uint16_t>(M * pl.ldf);
+    pl.du = c.take<uint16_t>(M * pl.ldf);
+    pl.dx.M = M; pl.dx.N = K; pl.dx.K = F;
+    pl.dx.segments = 2;
+    pl.dx.bmn = true;
+    pl.dx.may_split = true;
+    pl.dw.M = F; pl.dw.N = K; pl.dw.K = M;
+    pl.dw.problems = 2;
+    pl.dw.amn = pl.dw.bmn = true;
+    pl.dw.may_split = true;
+    pl.x = source_of(x, M, K, want_dw && !tma_ok(x, K), &c);
+    const bool rw = want_dx && (!tma_ok(wg, K) || !tma_ok(wu, K));
+    pl.wg = source_of(wg, F, K, rw, &c);
+    pl.wu = source_of(wu, F, K, rw, &c);
+    pl.ldx = choose_layout(pl.dx, num_sms);
+    pl.ldw = choose_layout(pl.dw, num_sms);
+    const int64_t fx = want_dx ? split_floats(pl.dx, pl.ldx) : 0, fw = want_dw ? split_floats(pl.dw, pl.ldw) : 0;
+    pl.partial = c.take<float>(fx > fw ? fx : fw);
+    pl.bytes = c.used;
+    return pl;
+}
+
+int zero16(void* p, int64_t rows, int64_t cols, cudaStream_t stream) {
+    if (!p || rows == 0 || cols == 0) return GEMM_OK;
+    return cudaMemsetAsync(p, 0, bytes16(rows, cols), stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace fused
+}  // namespace pws
+
+extern "C" int gemm_gated_nt_workspace(int64_t M, int64_t F, int64_t K, const void* x, const void* w_gate,
+                                       const void* w_up, int type, int64_t* bytes) {
+    using namespace pws::fused;
+    const int rc = check_gated(M, F, K, x, w_gate, w_up, nullptr, nullptr, nullptr, type, GEMM_ACT_SILU);
+    if (rc != GEMM_OK) return rc;
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    *bytes = M && F && K ? static_cast<int64_t>(
+                               plan_gated(M, F, K, x, w_gate, w_up, pws::sm_count_or_default(), nullptr).bytes)
+                         : 0;
+    return GEMM_OK;
+}
+
+extern "C" int gemm_gated_nt(int64_t M, int64_t F, int64_t K, const void* x, const void* w_gate, const void* w_up,
+                             void* h, void* g, void* u, int type, int act, void* workspace, int64_t workspace_bytes,
+                             cudaStream_t stream) {
+    using namespace pws;
+    using namespace pws::fused;
+    int rc = check_gated(M, F, K, x, w_gate, w_up, h, g, u, type, act);
+    if (rc != GEMM_OK) return rc;
+    if (M == 0 || F == 0) return GEMM_OK;
+    if (!h) return GEMM_ERR_INVALID_ARG;
+    DeviceInfo info;
+    rc = current_device(&info);
+    if (rc != GEMM_OK) return rc;
+    if (K == 0) {
+        // g = u = 0, so h = act(0) * 0 = 0
+        if ((rc = zero16(h, M, F, stream)) != GEMM_OK) return rc;
+        if ((rc = zero16(g, M, F, stream)) != GEMM_OK) return rc;
+        return zero16(u, M, F, stream);
+    }
+    GatedPlan pl = plan_gated(M, F, K, x, w_gate, w_up, info.num_sms, workspace);
+    if (pl.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
+                     workspace_bytes < static_cast<int64_t>(pl.bytes)))
+        return GEMM_ERR_INVALID_ARG;
+    if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_source(&pl.wg, F, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_source(&pl.wu, F, K, stream)) != GEMM_OK) return rc;
+    Maps maps;
+    const void* a[2] = {pl.x.ptr, nullptr};
+    const void* b[2] = {pl.wg.ptr, pl.wu.ptr};
+    if (!encode_operands(&maps, pl.pr, pl.l, a, pl.x.ld, b, pl.wg.ld)) return GEMM_ERR_LAUNCH;
+    Params p = base_params(pl.pr, pl.l, type, info, stream);
+    p.act = act;
+    p.ld16 = F;
+    p.out16[0] = static_cast<uint16_t*>(h);
+    p.g_out = static_cast<uint16_t*>(g);
+    p.u_out = static_cast<uint16_t*>(u);
+    p.tma_store = output_map(&maps.c[0], pl.l, h, M, F, F) &&
+                  (!g || (output_map(&maps.c[1], pl.l, g, M, F, F) && output_map(&maps.c[2], pl.l, u, M, F, F)));
+    return launch_product<kEpiGated, false, false>(pl.l, maps, p, info, stream);
+}
+
+extern "C" int gemm_gated_nt_bwd_workspace(int64_t M, int64_t F, int64_t K, const void* dh, const void* g,
+                                           const void* u, const void* x, const void* w_gate, const void* w_up,
+                                           int type, int64_t* bytes) {
+    using namespace pws::fused;
+    const int rc = check_gated_bwd(M, F, K, dh, g, u, x, w_gate, w_up, nullptr, nullptr, nullptr, type, GEMM_ACT_SILU);
+    if (rc != GEMM_OK) return rc;
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    *bytes = M && F && K ? static_cast<int64_t>(plan_gated_bwd(M, F, K, x, w_gate, w_up, true, true,
+                                                               pws::sm_count_or_default(), nullptr)
+                                                    .bytes)
+                         : 0;
+    return GEMM_OK;
+}
+
+extern "C" int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh, const void* g, const void* u,
+                                 const void* x, const void* w_gate, const void* w_up, void* dx, void* dw_gate,
+                                 void* dw_up, int type, int act, void* workspace, int64_t workspace_bytes,
+                                 cudaStream_t stream) {
+    using namespace pws;
+    using namespace pws::fused;
+    int rc = check_gated_bwd(M, F, K, dh, g, u, x, w_gate, w_up, dx, dw_gate, dw_up, type, act);
+    if (rc != GEMM_OK) return rc;
+    if (K == 0 || (M == 0 && F == 0) || (!dx && !dw_gate)) return GEMM_OK;
+    DeviceInfo info;
+    rc = current_device(&info);
+    if (rc != GEMM_OK) return rc;
+    if (M == 0 || F == 0) {
+        if ((rc = zero16(dx, M, K, stream)) != GEMM_OK) return rc;
+        if ((rc = zero16(dw_gate, F, K, stream)) != GEMM_OK) return rc;
+        return zero16(dw_up, F, K, stream);
+    }
+    GatedBwdPlan pl = plan_gated_bwd(M, F, K, x, w_gate, w_up, dx != nullptr, dw_gate != nullptr, info.num_sms,
+                                     workspace);
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
+        workspace_bytes < static_cast<int64_t>(pl.bytes))
+        return GEMM_ERR_INVALID_ARG;
+    if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_source(&pl.wg, F, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_source(&pl.wu, F, K, stream)) != GEMM_OK) return rc;
+    {
+        const bool vec = tma_ok(dh, F) && tma_ok(g, F) && tma_ok(u, F);
+        int64_t blocks = cdiv(M * (vec ? F / 8 : F), 256);
+        if (blocks > 16ll * info.num_sms) blocks = 16ll * info.num_sms;
+        auto kern = vec ? gated_grad_kernel<true> : gated_grad_kernel<false>;
+        if (launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                       static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(g),
+                       static_cast<const uint16_t*>(u), pl.dg, pl.du, M, static_cast<int>(F), pl.ldf, act,
+                       type == GEMM_TYPE_BFLOAT ? 1 : 0) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+    }
+    const void* d[2] = {pl.dg, pl.du};
+    if (dx) {
+        const void* b[2] = {pl.wg.ptr, pl.wu.ptr};
+        StoreTarget to;
+        to.out16[0] = dx;
+        rc = run_store_product(pl.dx, pl.ldx, d, pl.ldf, b, pl.wg.ld, to, pl.partial, type, info, stream);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (dw_gate) {
+        const void* b[2] = {pl.x.ptr, nullptr};
+        StoreTarget to;
+        to.out16[0] = dw_gate;
+        to.out16[1] = dw_up;
+        rc = run_store_product(pl.dw, pl.ldw, d, pl.ldf, b, pl.x.ld, to, pl.partial, type, info, stream);
+    }
+    return rc;
+}

@@ -1,0 +1,348 @@
+// gemm_xent.cu -- softmax cross entropy over a linear head, without keeping
+// the logits z = x W^T.
+//
+// Forward: the product's epilogue reduces each tile's columns of a row to
+// their maximum and sum of exponentials (fp32, from the fp32 accumulator), and
+// keeps the target's logit; a second kernel joins the tiles' pairs in a fixed
+// order:  lse = m + log sum_t s_t exp(m_t - m),  loss = lse - z_target.
+//
+// Backward: the vocabulary is taken in pieces.  For each piece the logits are
+// computed again, the epilogue turns them into D = dloss (exp(z - lse) -
+// onehot) in 16 bits, and the piece's two products follow: dx += D W (fp32
+// between pieces) and the piece's rows of dW = D^T x.  The largest buffer is
+// one piece of D.
+//
+// D is rounded to the inputs' type because the tensor cores multiply 16-bit
+// operands of one type.  It is scaled by a power of two that brings the
+// largest |dloss| to [2^13, 2^14), undone in fp32 when dx and dW are rounded:
+// without it binary16 would lose the probabilities below 6e-8 / dloss.
+#include "product_host.cuh"
+
+namespace pws {
+namespace fused {
+namespace {
+
+// One block: the power-of-two scale, its inverse, and per row the scaled loss
+// gradient: 0 for an ignored row, NaN for a target outside the vocabulary.
+__global__ void __launch_bounds__(1024)
+xent_rows_kernel(const int64_t* __restrict__ target, const float* __restrict__ dloss, int M, int64_t V,
+                 int64_t ignore_index, float* __restrict__ coef, float* __restrict__ inv_scale) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    __shared__ float part[32];
+    float top = 0.0f;
+    for (int i = threadIdx.x; i < M; i += blockDim.x) {
+        const float d = fabsf(dloss[i]);
+        if (target[i] != ignore_index && d <= 3.0e38f) top = fmaxf(top, d);     // (finite ones)
+    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+    __syncthreads();
+    top = part[threadIdx.x % 32];
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    int e = top > 0.0f ? 13 - ilogbf(top) : 0;
+    e = e > 100 ? 100 : (e < -100 ? -100 : e);
+    const float scale = ldexpf(1.0f, e);
+    if (threadIdx.x == 0) *inv_scale = ldexpf(1.0f, -e);
+    for (int i = threadIdx.x; i < M; i += blockDim.x) {
+        const int64_t t = target[i];
+        float c = 0.0f;
+        if (t != ignore_index) c = t >= 0 && t < V ? dloss[i] * scale : __int_as_float(0x7fffffff);
+        coef[i] = c;
+    }
+}
+
+// One warp per row joins its tiles' (maximum, sum) pairs.  tiles == 0: K == 0,
+// every logit is 0.
+__global__ void __launch_bounds__(256)
+xent_join_kernel(const float2* __restrict__ stats, const float* __restrict__ z_target,
+                 const int64_t* __restrict__ target, int M, int tiles, int64_t V, int64_t ignore_index,
+                 float* __restrict__ loss, float* __restrict__ lse) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int row = static_cast<int>((blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / 32);
+    const int lane = threadIdx.x % 32;
+    if (row >= M) return;
+    const float inf = __int_as_float(0x7f800000);
+    float m = -inf, s = 0.0f;
+    for (int t = lane; t < tiles; t += 32) {
+        const float2 v = stats[static_cast<int64_t>(t) * M + row];
+        const float top = fmaxf(m, v.x);
+        const float ref = top == -inf ? 0.0f : top;
+        s = s * expf(m - ref) + v.y * expf(v.x - ref);
+        m = top;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        const float top = fmaxf(m, m2);
+        const float ref = top == -inf ? 0.0f : top;
+        s = s * expf(m - ref) + s2 * expf(m2 - ref);
+        m = top;
+    }
+    if (lane == 0) {
+        const float total = tiles ? m + logf(s) : logf(static_cast<float>(V));
+        const int64_t t = target[row];
+        float l = 0.0f;
+        if (t != ignore_index) l = t >= 0 && t < V ? total - (tiles ? z_target[row] : 0.0f) : __int_as_float(0x7fffffff);
+        lse[row] = total;
+        loss[row] = l;
+    }
+}
+
+int check_xent(int64_t M, int64_t V, int64_t K, const void* x, const void* w, const int64_t* target, int type) {
+    if (bad_size(M) || bad_size(V) || bad_size(K) || V == 0) return GEMM_ERR_INVALID_ARG;
+    if (type != GEMM_TYPE_HALF && type != GEMM_TYPE_BFLOAT) return GEMM_ERR_INVALID_ARG;
+    if (too_many_tiles(M, V)) return GEMM_ERR_INVALID_ARG;
+    if (odd_address(x) || odd_address(w) || reinterpret_cast<uintptr_t>(target) % 8 != 0) return GEMM_ERR_ALIGNMENT;
+    if (M > 0 && (!target || (K > 0 && (!x || !w)))) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+bool odd_float(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 != 0; }
+
+struct XentPlan {
+    Product pr;
+    Layout l;
+    Source x, w;
+    float2* stats = nullptr;
+    float* z_target = nullptr;
+    size_t bytes = 0;
+};
+
+XentPlan plan_xent(int64_t M, int64_t V, int64_t K, const void* x, const void* w, int num_sms, void* ws) {
+    XentPlan pl;
+    Carver c;
+    c.base = static_cast<char*>(ws);
+    pl.pr.M = M; pl.pr.N = V; pl.pr.K = K;
+    pl.l = choose_layout(pl.pr, num_sms);
+    pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
+    pl.w = source_of(w, V, K, !tma_ok(w, K), &c);
+    pl.stats = c.take<float2>(static_cast<int64_t>(pl.l.tiles_n) * M);
+    pl.z_target = c.take<float>(M);
+    pl.bytes = c.used;
+    return pl;
+}
+
+// Bytes of D a piece may take; at least kMinPiece columns.
+constexpr int64_t kPieceBytes = 256ll << 20;
+constexpr int64_t kMinPiece = 8192;
+
+struct XentBwdPlan {
+    int64_t piece = 0, ldd = 0;
+    int pieces = 0;
+    Source x, w;
+    float* coef = nullptr;
+    float* inv_scale = nullptr;
+    uint16_t* d = nullptr;
+    float* acc = nullptr;
+    float* partial = nullptr;
+    size_t bytes = 0;
+};
+
+// The three products of a piece of `v` columns.
+Product logits_of(int64_t M, int64_t v, int64_t K) {
+    Product p;
+    p.M = M; p.N = v; p.K = K;
+    return p;
+}
+Product dx_of(int64_t M, int64_t v, int64_t K) {
+    Product p;
+    p.M = M; p.N = K; p.K = v;
+    p.bmn = true;
+    p.may_split = true;
+    return p;
+}
+Product dw_of(int64_t M, int64_t v, int64_t K) {
+    Product p;
+    p.M = v; p.N = K; p.K = M;
+    p.amn = p.bmn = true;
+    p.may_split = true;
+    return p;
+}
+
+XentBwdPlan plan_xent_bwd(int64_t M, int64_t V, int64_t K, const void* x, const void* w, bool want_dx, bool want_dw,
+                          int num_sms, void* ws) {
+    XentBwdPlan pl;
+    Carver c;
+    c.base = static_cast<char*>(ws);
+    int64_t cols = kPieceBytes / (2 * M);
+    if (cols < kMinPiece) cols = kMinPiece;
+    pl.pieces = static_cast<int>(cdiv(V, cols));
+    pl.piece = round_up(cdiv(V, pl.pieces), 256);
+    pl.pieces = static_cast<int>(cdiv(V, pl.piece));
+    pl.ldd = pl.pieces > 1 ? pl.piece : round_up(V, 64);
+    pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
+    pl.w = source_of(w, V, K, !tma_ok(w, K), &c);
+    pl.coef = c.take<float>(M);
+    pl.inv_scale = c.take<float>(1);
+    pl.d = c.take<uint16_t>(M * pl.ldd);
+    if (want_dx && pl.pieces > 1) pl.acc = c.take<float>(M * ld32_of(K));
+    int64_t most = 0;
+    for (int i = 0; i < 2; ++i) {          // the pieces' width, and the last one's
+        const int64_t v = i ? V - (pl.pieces - 1) * pl.piece : (pl.pieces > 1 ? pl.piece : V);
+        const Product a = dx_of(M, v, K), b = dw_of(M, v, K);
+        const int64_t fa = want_dx ? split_floats(a, choose_layout(a, num_sms)) : 0;
+        const int64_t fb = want_dw ? split_floats(b, choose_layout(b, num_sms)) : 0;
+        if (fa > most) most = fa;
+        if (fb > most) most = fb;
+    }
+    pl.partial = c.take<float>(most);
+    pl.bytes = c.used;
+    return pl;
+}
+
+}  // namespace
+}  // namespace fused
+}  // namespace pws
+
+extern "C" int gemm_xent_nt_workspace(int64_t M, int64_t V, int64_t K, const void* x, const void* w, int type,
+                                      int64_t* bytes) {
+    using namespace pws::fused;
+    const int64_t* any = reinterpret_cast<const int64_t*>(static_cast<uintptr_t>(8));       // (not read)
+    const int rc = check_xent(M, V, K, x, w, any, type);
+    if (rc != GEMM_OK) return rc;
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    *bytes = M && K ? static_cast<int64_t>(plan_xent(M, V, K, x, w, pws::sm_count_or_default(), nullptr).bytes) : 0;
+    return GEMM_OK;
+}
+
+extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, const void* w, const int64_t* target,
+                            int64_t ignore_index, float* loss, float* lse, int type, void* workspace,
+                            int64_t workspace_bytes, cudaStream_t stream) {
+    using namespace pws;
+    using namespace pws::fused;
+    int rc = check_xent(M, V, K, x, w, target, type);
+    if (rc != GEMM_OK) return rc;
+    if (M == 0) return GEMM_OK;
+    if (!loss || !lse) return GEMM_ERR_INVALID_ARG;
+    if (odd_float(loss) || odd_float(lse)) return GEMM_ERR_ALIGNMENT;
+    const uint64_t row_bytes = static_cast<uint64_t>(M) * 4;
+    const Range in[3] = {{x, bytes16(M, K)}, {w, bytes16(V, K)}, {target, 2 * row_bytes}};
+    const Range out[2] = {{loss, row_bytes}, {lse, row_bytes}};
+    if (overlaps(in, out)) return GEMM_ERR_INVALID_ARG;
+    DeviceInfo info;
+    rc = current_device(&info);
+    if (rc != GEMM_OK) return rc;
+    XentPlan pl;
+    if (K > 0) {
+        pl = plan_xent(M, V, K, x, w, info.num_sms, workspace);
+        if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
+            workspace_bytes < static_cast<int64_t>(pl.bytes))
+            return GEMM_ERR_INVALID_ARG;
+        if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
+        if ((rc = fill_source(&pl.w, V, K, stream)) != GEMM_OK) return rc;
+        Maps maps;
+        const void* a[2] = {pl.x.ptr, nullptr};
+        const void* b[2] = {pl.w.ptr, nullptr};
+        if (!encode_operands(&maps, pl.pr, pl.l, a, pl.x.ld, b, pl.w.ld)) return GEMM_ERR_LAUNCH;
+        Params p = base_params(pl.pr, pl.l, type, info, stream);
+        p.target = target;
+        p.stats = pl.stats;
+        p.z_target = pl.z_target;
+        rc = launch_product<kEpiXentStats, false, false>(pl.l, maps, p, info, stream);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>(cdiv(M, 8))), dim3(256), 0, stream,
+                   static_cast<const float2*>(pl.stats), static_cast<const float*>(pl.z_target), target,
+                   static_cast<int>(M), K > 0 ? pl.l.tiles_n : 0, V, ignore_index, loss, lse) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+extern "C" int gemm_xent_nt_bwd_workspace(int64_t M, int64_t V, int64_t K, const void* x, const void* w, int type,
+                                          int64_t* bytes) {
+    using namespace pws::fused;
+    const int64_t* any = reinterpret_cast<const int64_t*>(static_cast<uintptr_t>(8));       // (not read)
+    const int rc = check_xent(M, V, K, x, w, any, type);
+    if (rc != GEMM_OK) return rc;
+    if (too_many_tiles(M, K) || too_many_tiles(V, K)) return GEMM_ERR_INVALID_ARG;
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    *bytes = M && K ? static_cast<int64_t>(
+                          plan_xent_bwd(M, V, K, x, w, true, true, pws::sm_count_or_default(), nullptr).bytes)
+                    : 0;
+    return GEMM_OK;
+}
+
+extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, const void* w, const int64_t* target,
+                                int64_t ignore_index, const float* lse, const float* dloss, void* dx, void* dw,
+                                int type, void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+    using namespace pws;
+    using namespace pws::fused;
+    int rc = check_xent(M, V, K, x, w, target, type);
+    if (rc != GEMM_OK) return rc;
+    if (too_many_tiles(M, K) || too_many_tiles(V, K)) return GEMM_ERR_INVALID_ARG;
+    if (odd_address(dx) || odd_address(dw) || odd_float(lse) || odd_float(dloss)) return GEMM_ERR_ALIGNMENT;
+    if (M > 0 && (!lse || !dloss)) return GEMM_ERR_INVALID_ARG;
+    const uint64_t row_bytes = static_cast<uint64_t>(M) * 4;
+    const Range in[5] = {{x, bytes16(M, K)}, {w, bytes16(V, K)}, {target, 2 * row_bytes}, {lse, row_bytes},
+                         {dloss, row_bytes}};
+    const Range out[2] = {{dx, bytes16(M, K)}, {dw, bytes16(V, K)}};
+    if (overlaps(in, out)) return GEMM_ERR_INVALID_ARG;
+    if (K == 0 || (!dx && !dw)) return GEMM_OK;
+    DeviceInfo info;
+    rc = current_device(&info);
+    if (rc != GEMM_OK) return rc;
+    if (M == 0)
+        return !dw || cudaMemsetAsync(dw, 0, bytes16(V, K), stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    XentBwdPlan pl = plan_xent_bwd(M, V, K, x, w, dx != nullptr, dw != nullptr, info.num_sms, workspace);
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
+        workspace_bytes < static_cast<int64_t>(pl.bytes))
+        return GEMM_ERR_INVALID_ARG;
+    if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_source(&pl.w, V, K, stream)) != GEMM_OK) return rc;
+    if (launch_pdl(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, target, dloss, static_cast<int>(M), V,
+                   ignore_index, pl.coef, pl.inv_scale) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    for (int i = 0; i < pl.pieces; ++i) {
+        const int64_t v0 = i * pl.piece, v = V - v0 < pl.piece ? V - v0 : pl.piece;
+        const uint16_t* w_piece = static_cast<const uint16_t*>(pl.w.ptr) + v0 * pl.w.ld;
+        {
+            const Product pr = logits_of(M, v, K);
+            const Layout l = choose_layout(pr, info.num_sms);
+            Maps maps;
+            const void* a[2] = {pl.x.ptr, nullptr};
+            const void* b[2] = {w_piece, nullptr};
+            if (!encode_operands(&maps, pr, l, a, pl.x.ld, b, pl.w.ld)) return GEMM_ERR_LAUNCH;
+            Params p = base_params(pr, l, type, info, stream);
+            p.target = target;
+            p.lse = lse;
+            p.coef = pl.coef;
+            p.col0 = v0;
+            p.out16[0] = pl.d;
+            p.ld16 = pl.ldd;
+            p.tma_store = output_map(&maps.c[0], l, pl.d, M, v, pl.ldd);
+            if ((rc = launch_product<kEpiXentGrad, false, false>(l, maps, p, info, stream)) != GEMM_OK) return rc;
+        }
+        const void* a[2] = {pl.d, nullptr};
+        if (dx) {
+            const Product pr = dx_of(M, v, K);
+            const void* b[2] = {w_piece, nullptr};
+            StoreTarget to;
+            to.acc_in = i ? pl.acc : nullptr;
+            if (i + 1 < pl.pieces) {
+                to.acc_out = pl.acc;
+            } else {
+                to.out16[0] = dx;
+                to.scale = pl.inv_scale;
+            }
+            rc = run_store_product(pr, choose_layout(pr, info.num_sms), a, pl.ldd, b, pl.w.ld, to, pl.partial, type,
+                                   info, stream);
+            if (rc != GEMM_OK) return rc;
+        }
+        if (dw) {
+            const Product pr = dw_of(M, v, K);
+            const void* b[2] = {pl.x.ptr, nullptr};
+            StoreTarget to;
+            to.out16[0] = static_cast<uint16_t*>(dw) + v0 * K;
+            to.scale = pl.inv_scale;
+            rc = run_store_product(pr, choose_layout(pr, info.num_sms), a, pl.ldd, b, pl.x.ld, to, pl.partial, type,
+                                   info, stream);
+            if (rc != GEMM_OK) return rc;
+        }
+    }
+    return GEMM_OK;
+}

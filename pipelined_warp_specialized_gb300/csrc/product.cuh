@@ -1,0 +1,623 @@
+// product.cuh -- the tensor-core product under the fused operators: a
+// persistent, warp-specialized tcgen05 kernel whose operands may be stored
+// with K or with rows/columns innermost, and whose epilogue is the model's
+// next operation instead of a plain store.
+//
+//   D[m, n] = sum_k A[m, k] B[n, k]           fp32 in tensor memory
+//
+//   operands  "K-major" (rows of K elements, as lhs and rhs of gemm_f16_nt) or
+//             "MN-major" (K rows of M or N elements): the backward products
+//             dx = dy W and dW = dy^T x read the forward pass's matrices as
+//             they lie, so nothing is ever transposed in memory.
+//   segments  the K axis may run over two operand pairs, one after the other
+//             (dx = dg Wg + du Wu is one accumulation).
+//   problems  two products of one shape may share a launch (dWg and dWu).
+//   splits    few output tiles with a long K are split over K; the fp32
+//             partial sums are joined in a fixed order by a later kernel, so a
+//             result never depends on the order in which CTAs finish.
+//
+// The pipeline is the one of gemm_f16_nt (TMA producer thread, ring of
+// shared-memory slots with full/empty barriers, one MMA-issuing thread,
+// double-buffered accumulator, four epilogue warps, bounded waits), with a
+// tile width, box height and ring depth chosen at run time: one token's
+// product wants slots of 1 KB + a few weight rows and 32 of them in flight, a
+// training product wants 256 x 256 on a CTA pair.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "pwsgemm.h"
+#include "waiter.cuh"
+
+namespace pws {
+namespace fused {
+
+constexpr int BK = 64;                      // K per ring slot: one 128-byte swizzle row of 16-bit elements
+constexpr int UMMA_K = 16;
+constexpr int BM_CTA = 128;                 // accumulator rows per CTA (tensor-memory lanes)
+constexpr int MAX_BN = 256;                 // accumulator columns per buffer
+constexpr int MAX_STAGES = 32;
+constexpr int EPI_COLS = 64;                // output columns per staged chunk: 128 bytes
+constexpr int EPI_BUF = 32 * EPI_COLS * 2;  // one warp's 32 rows of a chunk
+constexpr int EPI_BYTES = 4 * 2 * EPI_BUF;
+constexpr int THREADS = 6 * 32;             // producer, MMA issuer, four epilogue warps
+constexpr int MN_BOX = 64 * BK * 2;         // one MN-major box: 64 K rows of 64 elements
+constexpr int GROUP_M = 8;                  // tile rows walked together, so their A strips stay in L2
+
+// Shared memory: ring, epilogue staging, barriers.
+constexpr int SMEM_LIMIT = 232448;
+constexpr int BAR_BYTES = 1024;
+constexpr int RING_BYTES = (SMEM_LIMIT - 1024 - EPI_BYTES - BAR_BYTES) / 1024 * 1024;
+constexpr int OFF_EPI = RING_BYTES;
+constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
+constexpr int OFF_FULL = OFF_BAR;
+constexpr int OFF_EMPTY = OFF_FULL + 8 * MAX_STAGES;
+constexpr int OFF_TFULL = OFF_EMPTY + 8 * MAX_STAGES;
+constexpr int OFF_TEMPTY = OFF_TFULL + 16;
+constexpr int OFF_DRAIN = OFF_TEMPTY + 16;
+constexpr int OFF_TMEM = OFF_DRAIN + 8;
+constexpr int OFF_ABORT = OFF_TMEM + 4;
+constexpr int OFF_PROGRESS = OFF_ABORT + 4;
+static_assert(OFF_PROGRESS + 4 <= OFF_BAR + BAR_BYTES, "barriers");
+constexpr int SMEM_BYTES = OFF_BAR + BAR_BYTES + 1024;      // + slack to align the base to 1024
+static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
+static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: each owns all of tensor memory");
+
+enum Epilogue { kEpiStore = 0, kEpiGated = 1, kEpiXentStats = 2, kEpiXentGrad = 3 };
+
+struct Params {
+    int M, N;                       // output rows and columns (of the epilogue's output)
+    int nkb0, nkb;                  // K blocks of the first segment, of all segments
+    int tiles_m, tiles_n, num_tiles;    // tiles of one problem; num_tiles counts all problems
+    int splits, kb_per_split;
+    int total_units;                // num_tiles * splits
+    int a_rows;                     // rows of a K-major A box (<= 128): fewer than 128 for few tokens
+    int bn;                         // accumulator columns per tile (a multiple of 16)
+    int tile_n;                     // output columns per tile (bn, or bn / 2 for the gated epilogue)
+    int stages, a_bytes, slot_bytes;
+    int tx_bytes;                   // bytes one CTA's copies bring per slot
+    uint32_t idesc;
+    int bf16;                       // output type
+    int tma_store;
+    int act;
+    unsigned long long timeout_ns;
+    unsigned* status;
+    // kEpiStore: out = scale * acc, to 16 bits (out16), or to fp32 (out32,
+    // partial sums: split s of problem i at out32 + s * split_stride +
+    // i * problem_stride), plus acc_in
+    uint16_t* out16[2];
+    int64_t ld16;
+    float* out32;
+    const float* acc_in;
+    int64_t ld32, split_stride, problem_stride;
+    const float* scale;             // device scalar, or null for 1
+    // kEpiGated: h = act(gate) * up, and gate, up where g_out is not null
+    uint16_t* g_out;
+    uint16_t* u_out;
+    // cross entropy
+    const int64_t* target;
+    float2* stats;                  // [tiles_n][M]: maximum and sum of exponentials of a tile's columns
+    float* z_target;                // [M]
+    const float* lse;
+    const float* coef;              // [M]: scaled loss gradient; 0 for a row that does not count
+    int64_t col0;                   // vocabulary index of column 0
+};
+
+struct Maps {
+    CUtensorMap a[2], b[2], c[3];
+};
+
+// K-major operand in the 128-byte swizzle: rows of 128 bytes, 8-row atoms
+// 1024 bytes apart (stride offset).
+// MN-major operand: a box is 64 K rows of 128 bytes (64 elements of M or N);
+// 8 K rows form an atom, atoms 1024 bytes apart along K (stride offset), boxes
+// 8192 bytes apart along M or N (leading offset).
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((MN ? MN_BOX : 16) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// (address >> 4) step of one UMMA_K: 32 bytes inside the swizzle row, or 16 K rows.
+template <bool MN>
+constexpr uint32_t k_step() { return (MN ? UMMA_K * 128 : UMMA_K * 2) >> 4; }
+
+struct Tile {
+    int problem, tm, tn, kb0, kb1, split;
+};
+
+__device__ __forceinline__ Tile tile_of(int u, const Params& p) {
+    Tile t;
+    t.split = u / p.num_tiles;
+    int r = u - t.split * p.num_tiles;
+    const int per = p.tiles_m * p.tiles_n;
+    t.problem = r / per;
+    r -= t.problem * per;
+    // tile rows are walked GROUP_M at a time and odd groups right to left, so
+    // the CTAs at work share A and B strips in L2
+    const int group = GROUP_M * p.tiles_n;
+    const int g = r / group;
+    const int first = g * GROUP_M;
+    const int rows = min(p.tiles_m - first, GROUP_M);
+    const int v = r - g * group;
+    t.tm = first + v % rows;
+    t.tn = v / rows;
+    if (g & 1) t.tn = p.tiles_n - 1 - t.tn;
+    t.kb0 = t.split * p.kb_per_split;
+    t.kb1 = min(p.nkb, t.kb0 + p.kb_per_split);
+    return t;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Both activations are g * sigma(s(g)): silu with s = g, gelu (tanh form)
+// with s = 2 sqrt(2/pi) (g + 0.044715 g^3), since (1 + tanh y) / 2 = sigma(2 y).
+constexpr float kGeluC = 1.5957691216057308f;       // 2 sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float sigmoid(float s) { return __fdividef(1.0f, 1.0f + ex2(-kLog2e * s)); }
+
+__device__ __forceinline__ float act_arg(float g, int act) {
+    return act == GEMM_ACT_SILU ? g : kGeluC * g * (1.0f + kGeluA * g * g);
+}
+
+__device__ __forceinline__ float act_value(float g, int act) { return g * sigmoid(act_arg(g, act)); }
+
+// act(g) and act'(g) = sigma + g sigma (1 - sigma) s'(g)
+__device__ __forceinline__ void act_value_slope(float g, int act, float& value, float& slope) {
+    const float s = sigmoid(act_arg(g, act));
+    value = g * s;
+    const float t = value * (1.0f - s);
+    const float ds = act == GEMM_ACT_SILU ? 1.0f : kGeluC * (1.0f + 3.0f * kGeluA * g * g);
+    slope = s + (t == 0.0f ? 0.0f : t * ds);        // (a saturated gate's s' may overflow)
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
+    if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+template <int CG, int EPI, bool AMN, bool BMN>
+__global__ void __launch_bounds__(THREADS, 1)
+product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;       // swizzle atoms are 1024-byte aligned
+    uint8_t* const gbase = smem_raw + (base - raw);
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+    const int group_id = blockIdx.x / CG;
+    const int num_groups = gridDim.x / CG;
+    const uint32_t bFULL = base + OFF_FULL, bEMPTY = base + OFF_EMPTY;
+    const uint32_t bTFULL = base + OFF_TFULL, bTEMPTY = base + OFF_TEMPTY, bDRAIN = base + OFF_DRAIN;
+    const uint32_t sPROGRESS = base + OFF_PROGRESS;
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + OFF_ABORT);
+    const uint32_t S = static_cast<uint32_t>(p.stages);
+
+    // ------------------------------------------------------------ set-up
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < S; ++s) {
+            mbar_init(bFULL + 8 * s, 1);
+            mbar_init(bEMPTY + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bTFULL + 8 * b, 1);
+            mbar_init(bTEMPTY + 8 * b, 4 * CG);
+        }
+        mbar_init(bDRAIN, 1);
+        *abort_flag = 0u;
+        *reinterpret_cast<volatile uint32_t*>(gbase + OFF_PROGRESS) = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.a[0]);
+        tma_prefetch_desc(&maps.b[0]);
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(base + OFF_TMEM, 512);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *reinterpret_cast<uint32_t*>(gbase + OFF_TMEM);
+    // everything above overlaps the previous grid's tail; global memory is
+    // touched only once that grid has completed
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const bool leader = CG == 1 || rank == 0;
+
+    if (warp == 0) {
+        // ======================================================== producer
+        if (lane == 0) {
+            const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
+            const uint32_t full_leader = CG == 2 ? mapa_shared(bFULL, 0) : bFULL;
+            uint32_t stage = 0, phase = 0, issued = 0;
+            bool ok = true;
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+                if constexpr (CG == 1) tma_load_2d(dst, map, x, y, bar);
+                else tma_load_2d_pair(dst, map, x, y, bar);
+            };
+            for (int u = group_id; ok && u < p.total_units; u += num_groups) {
+                const Tile t = tile_of(u, p);
+                const int m_cta = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA;
+                const int b_rows = p.bn / CG;                    // B rows (accumulator columns) of this CTA
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!W.wait(bEMPTY + 8 * stage, phase)) { ok = false; break; }
+                    const uint32_t a_dst = base + stage * p.slot_bytes, b_dst = a_dst + p.a_bytes;
+                    const uint32_t bar = full_leader + 8 * stage;
+                    const int seg = kb >= p.nkb0 ? 1 : 0;
+                    const int k = (kb - (seg ? p.nkb0 : 0)) * BK;
+                    const CUtensorMap* ma = &maps.a[seg | t.problem];
+                    if (leader) mbar_arrive_expect_tx(bFULL + 8 * stage, CG * p.tx_bytes);
+                    if constexpr (AMN) {
+                        load(a_dst, ma, m_cta, k, bar);
+                        load(a_dst + MN_BOX, ma, m_cta + 64, k, bar);
+                    } else {
+                        load(a_dst, ma, k, m_cta, bar);
+                    }
+                    if constexpr (EPI == kEpiGated) {
+                        // gate rows are the first half of the tile's columns, up rows the second
+                        const int n = t.tn * p.tile_n;
+                        if constexpr (CG == 2) {
+                            load(b_dst, &maps.b[rank], k, n, bar);
+                        } else {
+                            load(b_dst, &maps.b[0], k, n, bar);
+                            load(b_dst + p.tile_n * 128, &maps.b[1], k, n, bar);
+                        }
+                    } else {
+                        const int n = t.tn * p.tile_n + static_cast<int>(rank) * b_rows;
+                        const CUtensorMap* mb = &maps.b[seg];
+                        if constexpr (BMN) {
+                            for (int j = 0; j < b_rows; j += 64) load(b_dst + j * (MN_BOX / 64), mb, n + j, k, bar);
+                        } else {
+                            load(b_dst, mb, k, n, bar);
+                        }
+                    }
+                    ++issued;
+                    st_volatile_shared_u32(sPROGRESS, issued);
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (!ok && leader) {
+                // drain: wait (bounded) for the copies still in flight into this CTA
+                volatile uint32_t no_abort = 0;
+                const Waiter D{p.timeout_ns, &no_abort, p.status, kStatusRoleProducer};
+                const uint32_t first = issued > S ? issued - S : 0u;
+                for (uint32_t it = first; it < issued; ++it)
+                    if (!D.wait(bFULL + 8 * (it % S), (it / S) & 1u)) break;
+            } else if (!ok && issued > 0) {
+                // a pair's peer cannot wait on the leader's barriers: its copies
+                // land within microseconds, so a bounded millisecond outlasts them
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ======================================================== MMA issuer
+        if (lane == 0)
+            for (uint32_t s = 0; s < S; ++s) mbar_arrive(bEMPTY + 8 * s);      // every slot starts empty
+        if (leader && lane == 0) {
+            const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleMma};
+            // descriptors of slot s: slot 0's plus s slots (addresses lie below
+            // 256 KB, so the 14-bit address field never carries)
+            const uint64_t adesc0 = operand_desc<AMN>(base), bdesc0 = operand_desc<BMN>(base + p.a_bytes);
+            const uint32_t slot16 = static_cast<uint32_t>(p.slot_bytes) >> 4;
+            uint32_t stage = 0, phase = 0, tcount = 0;
+            bool ok = true, issued_any = false;
+            for (int u = group_id; ok && u < p.total_units; u += num_groups, ++tcount) {
+                const Tile t = tile_of(u, p);
+                const uint32_t b = tcount & 1u, aph = (tcount >> 1) & 1u;
+                if (!W.template wait<CG == 2>(bTEMPTY + 8 * b, aph)) { ok = false; break; }
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + b * MAX_BN;
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!W.wait(bFULL + 8 * stage, phase)) { ok = false; break; }
+                    tc_fence_after_sync();
+                    const uint64_t ad = adesc0 + stage * slot16, bd = bdesc0 + stage * slot16;
+#pragma unroll
+                    for (int k = 0; k < BK / UMMA_K; ++k)
+                        tc_mma_f16<CG>(d_tmem, ad + k * k_step<AMN>(), bd + k * k_step<BMN>(), p.idesc,
+                                       kb != t.kb0 || k != 0);
+                    issued_any = true;
+                    if constexpr (CG == 1) tc_commit_1(bEMPTY + 8 * stage);
+                    else tc_commit_2_mc(bEMPTY + 8 * stage, 0x3);
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                if constexpr (CG == 1) tc_commit_1(bTFULL + 8 * b);
+                else tc_commit_2_mc(bTFULL + 8 * b, 0x3);
+            }
+            if (issued_any) {
+                // all multiplies have finished before tensor memory is released
+                if constexpr (CG == 1) tc_commit_1(bDRAIN);
+                else tc_commit_2_mc(bDRAIN, 0x1);
+                volatile uint32_t no_abort = 0;
+                const Waiter D{p.timeout_ns, &no_abort, p.status, kStatusRoleMma};
+                D.wait(bDRAIN, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ======================================================== epilogue
+        const int e = warp - 2;
+        const int q = warp & 3;                  // tensor-memory lane quarter of this warp
+        const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleEpilogue};
+        const uint32_t tempty_leader = CG == 2 ? mapa_shared(bTEMPTY, 0) : bTEMPTY;
+        if (lane == 0)
+            for (int b = 0; b < 2; ++b) {
+                if constexpr (CG == 1) mbar_arrive(bTEMPTY + 8 * b);
+                else mbar_arrive_cluster(tempty_leader + 8 * b);
+            }
+        const uint32_t bufs = base + OFF_EPI + static_cast<uint32_t>(e) * 2 * EPI_BUF;
+        uint32_t nbuf = 0;
+        // One 64-column chunk (this lane's row, 32 packed pairs) of a 16-bit
+        // output: staged in the swizzle its tensor map uses and stored by TMA
+        // (the staging buffers in turn), or stored by the lane itself where
+        // TMA cannot address the output or the chunk is narrower (col_end).
+        auto emit = [&](const uint32_t(&h)[32], const CUtensorMap* map, uint16_t* out, int64_t ld, int row0, int col0,
+                        int col_end) {
+            if (p.tma_store) {
+                const uint32_t buf = bufs + (nbuf & 1u) * EPI_BUF;
+                ++nbuf;
+                if (lane == 0) bulk_wait_group_read<1>();
+                __syncwarp();
+                const uint32_t row_addr = buf + static_cast<uint32_t>(lane) * 128;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t dst = row_addr + ((static_cast<uint32_t>(j) ^ static_cast<uint32_t>(lane & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[4 * j]),
+                                 "r"(h[4 * j + 1]), "r"(h[4 * j + 2]), "r"(h[4 * j + 3])
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (row0 < p.M && col0 < p.N) tma_store_2d(map, buf, col0, row0);
+                    bulk_commit_group();
+                }
+                return;
+            }
+            const int row = row0 + lane;
+            if (row >= p.M) return;
+            uint16_t* dst = out + static_cast<int64_t>(row) * ld;
+            const bool wide = ((reinterpret_cast<uintptr_t>(dst + col0) & 15u) == 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = col0 + 8 * j;
+                if (wide && col + 8 <= col_end) {
+                    *reinterpret_cast<uint4*>(dst + col) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t v = h[4 * j + i];
+                        if (col + 2 * i < col_end) dst[col + 2 * i] = static_cast<uint16_t>(v & 0xFFFFu);
+                        if (col + 2 * i + 1 < col_end) dst[col + 2 * i + 1] = static_cast<uint16_t>(v >> 16);
+                    }
+                }
+            }
+        };
+        uint32_t tcount = 0;
+        for (int u = group_id; u < p.total_units; u += num_groups, ++tcount) {
+            const Tile t = tile_of(u, p);
+            const uint32_t b = tcount & 1u, aph = (tcount >> 1) & 1u;
+            const int row0 = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA + q * 32;
+            const int row = row0 + lane;
+            const int n0 = t.tn * p.tile_n;
+            const int col_end = min(p.N, n0 + p.tile_n);
+            bool got = true;
+            if (lane == 0) got = W.wait_progress(bTFULL + 8 * b, aph, sPROGRESS, false);
+            got = __shfl_sync(0xffffffffu, got, 0);
+            if (!got) break;
+            tc_fence_after_sync();
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_BN;
+            if (row0 < p.M) {
+                if constexpr (EPI == kEpiStore) {
+                    const float scale = p.scale ? *p.scale : 1.0f;
+                    if (p.out32) {
+                        // fp32 partial or running sums
+                        float* out = p.out32 + t.split * p.split_stride + t.problem * p.problem_stride +
+                                     static_cast<int64_t>(row) * p.ld32;
+                        const float* in = p.acc_in ? p.acc_in + static_cast<int64_t>(row) * p.ld32 : nullptr;
+                        for (int c = n0; c < col_end; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0), v);
+                            tmem_ld_wait();
+                            if (row < p.M) {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4) {
+                                    if (c + i < col_end) {          // rows are padded to a multiple of 4
+                                        float4 o = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                                                               __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                                        if (in) {
+                                            const float4 a = *reinterpret_cast<const float4*>(in + c + i);
+                                            o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
+                                        }
+                                        *reinterpret_cast<float4*>(out + c + i) = o;
+                                    }
+                                }
+                            }
+                        }
+                    } else {
+                        const float* in = p.acc_in ? p.acc_in + static_cast<int64_t>(row) * p.ld32 : nullptr;
+                        for (int c = n0; c < col_end; c += EPI_COLS) {
+                            uint32_t h[32];
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t v[32];
+                                tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0 + 32 * half), v);
+                                tmem_ld_wait();
+                                if (in && row < p.M) {
+#pragma unroll
+                                    for (int i = 0; i < 32; i += 4) {
+                                        if (c + 32 * half + i < col_end) {
+                                            const float4 a = *reinterpret_cast<const float4*>(in + c + 32 * half + i);
+                                            v[i] = __float_as_uint(__uint_as_float(v[i]) + a.x);
+                                            v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) + a.y);
+                                            v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) + a.z);
+                                            v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + a.w);
+                                        }
+                                    }
+                                }
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    h[16 * half + i] = pack16(scale * __uint_as_float(v[2 * i]),
+                                                              scale * __uint_as_float(v[2 * i + 1]), p.bf16);
+                            }
+                            emit(h, &maps.c[t.problem], p.out16[t.problem], p.ld16, row0, c, col_end);
+                        }
+                    }
+                } else if constexpr (EPI == kEpiGated) {
+                    for (int c = n0; c < col_end; c += EPI_COLS) {
+                        uint32_t h[32], hg[32], hu[32];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t g[32], up[32];
+                            const uint32_t off = static_cast<uint32_t>(c - n0 + 32 * half);
+                            if (off < static_cast<uint32_t>(p.tile_n)) {
+                                tmem_ld_32x32b_x32(tbase + off, g);
+                                tmem_ld_32x32b_x32(tbase + p.tile_n + off, up);
+                                tmem_ld_wait();
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) g[i] = up[i] = 0u;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
+                                const float u0 = __uint_as_float(up[2 * i]), u1 = __uint_as_float(up[2 * i + 1]);
+                                h[16 * half + i] =
+                                    pack16(act_value(g0, p.act) * u0, act_value(g1, p.act) * u1, p.bf16);
+                                hg[16 * half + i] = pack16(g0, g1, p.bf16);
+                                hu[16 * half + i] = pack16(u0, u1, p.bf16);
+                            }
+                        }
+                        emit(h, &maps.c[0], p.out16[0], p.ld16, row0, c, col_end);
+                        if (p.g_out) {
+                            emit(hg, &maps.c[1], p.g_out, p.ld16, row0, c, col_end);
+                            emit(hu, &maps.c[2], p.u_out, p.ld16, row0, c, col_end);
+                        }
+                    }
+                } else if constexpr (EPI == kEpiXentStats) {
+                    // running maximum m and sum s = sum exp(z - m) of this row over the tile's columns
+                    const int64_t tgt = row < p.M ? p.target[row] - p.col0 : -1;
+                    float m = -__int_as_float(0x7f800000), s = 0.0f;
+                    for (int c = n0; c < col_end; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0), v);
+                        tmem_ld_wait();
+                        if (c + 32 > col_end) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i >= col_end) v[i] = 0xff800000u;
+                        }
+                        const bool mine = tgt >= c && tgt < c + 32;
+                        if (__any_sync(0xffffffffu, mine)) {
+                            float z = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (tgt == c + i) z = __uint_as_float(v[i]);
+                            if (mine && tgt < col_end) p.z_target[row] = z;
+                        }
+                        float top = m;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+                        // a row of -inf so far: any finite reference gives exp(-inf) = 0
+                        const float ref = top == -__int_as_float(0x7f800000) ? 0.0f : top * kLog2e;
+                        s *= ex2(m * kLog2e - ref);
+                        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            s0 += ex2(fmaf(__uint_as_float(v[i]), kLog2e, -ref));
+                            s1 += ex2(fmaf(__uint_as_float(v[i + 1]), kLog2e, -ref));
+                            s2 += ex2(fmaf(__uint_as_float(v[i + 2]), kLog2e, -ref));
+                            s3 += ex2(fmaf(__uint_as_float(v[i + 3]), kLog2e, -ref));
+                        }
+                        s += (s0 + s1) + (s2 + s3);
+                        m = top;
+                    }
+                    if (row < p.M) p.stats[static_cast<int64_t>(t.tn) * p.M + row] = make_float2(m, s);
+                } else {
+                    // D = coef (exp(z - lse) - [column = target])
+                    const int64_t tgt = row < p.M ? p.target[row] - p.col0 : -1;
+                    const float ref = row < p.M ? p.lse[row] * kLog2e : 0.0f;
+                    const float coef = row < p.M ? p.coef[row] : 0.0f;
+                    for (int c = n0; c < col_end; c += EPI_COLS) {
+                        uint32_t h[32];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t v[32];
+                            const int cc = c + 32 * half;
+                            tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(cc - n0), v);
+                            tmem_ld_wait();
+                            float d[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) d[i] = ex2(fmaf(__uint_as_float(v[i]), kLog2e, -ref));
+                            if (__any_sync(0xffffffffu, tgt >= cc && tgt < cc + 32)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (tgt == cc + i) d[i] -= 1.0f;
+                            }
+                            // a row that does not count is zero whatever its logits are
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                h[16 * half + i] = pack16(coef == 0.0f ? 0.0f : coef * d[2 * i],
+                                                          coef == 0.0f ? 0.0f : coef * d[2 * i + 1], p.bf16);
+                        }
+                        emit(h, &maps.c[0], p.out16[0], p.ld16, row0, c, col_end);
+                    }
+                }
+            }
+            // this warp's reads of the accumulator are complete
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1) mbar_arrive(bTEMPTY + 8 * b);
+                else mbar_arrive_cluster(tempty_leader + 8 * b);
+            }
+        }
+        // the staging buffers must stay until the last stores have read them
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+    }
+
+    // ------------------------------------------------------------ tear-down
+    tc_fence_before_sync();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<CG>(tmem_base, 512);
+    }
+}
+
+}  // namespace fused
+}  // namespace pws

@@ -1,0 +1,297 @@
+// product_host.cuh -- host side of product.cuh: how a product is laid out
+// (tile, splits, ring depth), its tensor maps and its launch.
+#pragma once
+
+#include <atomic>
+#include <cstring>
+
+#include "product.cuh"
+
+namespace pws {
+namespace fused {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+// One product as an entry point asks for it.
+struct Product {
+    int64_t M = 0, N = 0, K = 0;        // output rows and columns, length of one K segment
+    int segments = 1, problems = 1;
+    bool gated = false, amn = false, bmn = false;
+    bool may_split = false;
+};
+
+// How it runs.
+struct Layout {
+    int cg = 1, bn = 256, tile_n = 256, a_rows = 128;
+    int tiles_m = 0, tiles_n = 0, splits = 1, kb_per_split = 0;
+    int nkb0 = 0, nkb = 0;
+    int stages = 0, a_bytes = 0, slot_bytes = 0, tx_bytes = 0;
+};
+
+// Chooses the tile (CTA pair or single CTA, accumulator width) and the K
+// split with the least estimated time, in SM clocks:
+//   per K block   the larger of the multiplies (a tile of bn columns takes
+//                 2 bn clocks), the copy into shared memory (about 60 bytes a
+//                 clock and SM from L2) and a ring slot's share of one
+//                 round trip (1500 clocks over the ring's depth);
+//   per wave      the K blocks of one unit, and 300 clocks between units;
+//   per launch    a fill and a last epilogue (1500 + 4 bn);
+//   a split       the join's launch (4000) and its traffic (3000 bytes a clock).
+inline Layout choose_layout(const Product& pr, int num_sms) {
+    Layout best;
+    double best_time = 1e300;
+    const int64_t nkb0 = cdiv(pr.K, BK), nkb = nkb0 * pr.segments;
+    for (int cg = 1; cg <= 2; ++cg) {
+        for (int bn = MAX_BN; bn >= 16; bn -= 16) {
+            if (cg == 2 && bn % 128 != 0) continue;
+            if (pr.bmn && (bn / cg) % 64 != 0) continue;
+            // widths between are used for the narrow tiles of few rows only
+            if (bn > 128 && bn % 32 != 0) continue;
+            Layout l;
+            l.cg = cg;
+            l.bn = bn;
+            l.tile_n = pr.gated ? bn / 2 : bn;
+            l.a_rows = pr.amn || cg == 2 ? BM_CTA : static_cast<int>(pr.M < BM_CTA ? round_up(pr.M, 8) : BM_CTA);
+            l.a_bytes = pr.amn ? 2 * MN_BOX : l.a_rows * 128;
+            const int b_bytes = bn / cg * 128;
+            l.tx_bytes = l.a_bytes + b_bytes;
+            l.slot_bytes = static_cast<int>(round_up(l.tx_bytes, 1024));
+            // the multiply reads 128 A rows from a slot's start: past a short
+            // box it reads what follows, which must still be the ring
+            const int slack = l.a_rows < BM_CTA ? BM_CTA * 128 : 0;
+            l.stages = (RING_BYTES - slack) / l.slot_bytes;
+            if (l.stages > MAX_STAGES) l.stages = MAX_STAGES;
+            l.tiles_m = static_cast<int>(cdiv(pr.M, BM_CTA * cg));
+            l.tiles_n = static_cast<int>(cdiv(pr.N, l.tile_n));
+            l.nkb0 = static_cast<int>(nkb0);
+            l.nkb = static_cast<int>(nkb);
+            const int64_t tiles = static_cast<int64_t>(l.tiles_m) * l.tiles_n * pr.problems;
+            const int64_t groups = num_sms / cg;
+            double per_kb = 2.0 * bn;
+            const double copy = l.tx_bytes / 60.0, trip = 1500.0 / l.stages;
+            if (copy > per_kb) per_kb = copy;
+            if (trip > per_kb) per_kb = trip;
+            const int64_t most = !pr.may_split || tiles >= groups ? 1 : (groups / tiles < nkb / 4 ? groups / tiles : nkb / 4);
+            for (int64_t s = 1; s <= (most > 1 ? most : 1); ++s) {
+                const int64_t kbps = cdiv(nkb, s), splits = cdiv(nkb, kbps);
+                const int64_t waves = cdiv(tiles * splits, groups);
+                double time = waves * (kbps * per_kb + 300.0) + 1500.0 + 4.0 * bn;
+                if (splits > 1) time += 4000.0 + 8.0 * splits * pr.M * pr.N * pr.problems / 3000.0;
+                if (time < best_time) {
+                    best_time = time;
+                    best = l;
+                    best.splits = static_cast<int>(splits);
+                    best.kb_per_split = static_cast<int>(kbps);
+                }
+            }
+        }
+    }
+    return best;
+}
+
+// fp32 partial sums of a split product: rows padded to 16 bytes.
+inline int64_t ld32_of(int64_t N) { return round_up(N, 4); }
+
+// Whether the tensor memory accelerator can address rows of `ld` 16-bit elements at p.
+inline bool tma_ok(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+
+// Tensor map of an operand: K-major, `mn` rows of K elements, a box of
+// box_rows rows; or MN-major, K rows of `mn` elements, a box of 64 x 64.
+inline bool operand_map(CUtensorMap* map, const void* p, bool mn_major, int64_t mn, int64_t K, int64_t ld,
+                        int box_rows) {
+    return mn_major ? encode_tmap_f16_2d(map, p, mn, K, ld * 2, 64, BK)
+                    : encode_tmap_f16_2d(map, p, K, mn, ld * 2, BK, box_rows);
+}
+
+// The parts of Params every epilogue shares.
+inline Params base_params(const Product& pr, const Layout& l, int type, const DeviceInfo& info, cudaStream_t stream) {
+    Params p;
+    memset(&p, 0, sizeof(p));
+    p.M = static_cast<int>(pr.M);
+    p.N = static_cast<int>(pr.N);
+    p.nkb0 = l.nkb0;
+    p.nkb = l.nkb;
+    p.tiles_m = l.tiles_m;
+    p.tiles_n = l.tiles_n;
+    p.num_tiles = l.tiles_m * l.tiles_n * pr.problems;
+    p.splits = l.splits;
+    p.kb_per_split = l.kb_per_split;
+    p.total_units = p.num_tiles * l.splits;
+    p.a_rows = l.a_rows;
+    p.bn = l.bn;
+    p.tile_n = l.tile_n;
+    p.stages = l.stages;
+    p.a_bytes = l.a_bytes;
+    p.slot_bytes = l.slot_bytes;
+    p.tx_bytes = l.tx_bytes;
+    p.bf16 = type == GEMM_TYPE_BFLOAT;
+    // instruction descriptor: fp32 accumulator, operand types, operands'
+    // majors, N >> 3, M >> 4
+    const uint32_t t = p.bf16 ? 1u : 0u;
+    p.idesc = (1u << 4) | (t << 7) | (t << 10) | ((pr.amn ? 1u : 0u) << 15) | ((pr.bmn ? 1u : 0u) << 16) |
+              (static_cast<uint32_t>(l.bn >> 3) << 17) | (static_cast<uint32_t>((BM_CTA * l.cg) >> 4) << 24);
+    p.timeout_ns = wait_timeout_ns();
+    p.status = status_word(info, stream);
+    return p;
+}
+
+// Encodes the operands' maps: a[i], b[i] for segment (or problem) i.
+inline bool encode_operands(Maps* maps, const Product& pr, const Layout& l, const void* const a[2], int64_t lda,
+                            const void* const b[2], int64_t ldb) {
+    memset(maps, 0, sizeof(*maps));
+    for (int i = 0; i < 2; ++i) {
+        const void* pa = a[i] ? a[i] : a[0];
+        const void* pb = b[i] ? b[i] : b[0];
+        if (!operand_map(&maps->a[i], pa, pr.amn, pr.M, pr.K, lda, l.a_rows)) return false;
+        const int b_box = pr.gated ? l.tile_n : l.bn / l.cg;
+        if (!operand_map(&maps->b[i], pb, pr.bmn, pr.N, pr.K, ldb, b_box)) return false;
+    }
+    return true;
+}
+
+// A 16-bit output's store map; false where its epilogue has to store directly.
+inline bool output_map(CUtensorMap* map, const Layout& l, const void* out, int64_t M, int64_t N, int64_t ld) {
+    if (!tma_ok(out, ld) || l.tile_n % EPI_COLS != 0) return false;
+    return encode_tmap_f16_2d(map, out, N, M, ld * 2, EPI_COLS, 32);
+}
+
+template <int CG, int EPI, bool AMN, bool BMN>
+int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStream_t stream) {
+    auto kern = product_kernel<CG, EPI, AMN, BMN>;
+    static std::atomic<int> capacity[64] = {};
+    if (info.device < 0 || info.device >= 64) return GEMM_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1] = pdl_attribute();
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.attrs = attr;
+    int cap = capacity[info.device].load(std::memory_order_relaxed);
+    if (cap == 0) {
+        // concurrent first calls compute and store the same value
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        cap = info.num_sms;
+        if (CG == 2) {
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(2 * info.num_sms, 1, 1);
+            if (cudaOccupancyMaxActiveClusters(&cap, kern, &cfg) != cudaSuccess || cap <= 0) {
+                cudaGetLastError();
+                cap = info.num_sms / 2;
+            }
+        }
+        capacity[info.device].store(cap, std::memory_order_relaxed);
+    }
+    const int groups = p.total_units < cap ? p.total_units : cap;
+    cfg.gridDim = dim3(CG * groups, 1, 1);
+    cfg.stream = stream;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, maps, p) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+template <int EPI, bool AMN, bool BMN>
+int launch_product(const Layout& l, const Maps& maps, const Params& p, const DeviceInfo& info, cudaStream_t stream) {
+    return l.cg == 2 ? launch_cg<2, EPI, AMN, BMN>(maps, p, info, stream)
+                     : launch_cg<1, EPI, AMN, BMN>(maps, p, info, stream);
+}
+
+// Hands out 256-byte aligned parts of a workspace; with no base it only counts.
+struct Carver {
+    char* base = nullptr;
+    size_t used = 0;
+    template <typename T>
+    T* take(int64_t count) {
+        const size_t at = used;
+        used += (static_cast<size_t>(count) * sizeof(T) + 255) / 256 * 256;
+        return base ? reinterpret_cast<T*>(base + at) : nullptr;
+    }
+};
+
+// An operand TMA cannot address is copied once to rows of a multiple of 64
+// elements (128-byte rows) in the workspace; `ld` becomes the copy's.
+struct Source {
+    const void* ptr = nullptr;
+    int64_t ld = 0;
+    uint16_t* copy = nullptr;
+    bool repack = false;
+};
+
+inline Source source_of(const void* p, int64_t rows, int64_t cols, bool repack, Carver* c) {
+    Source s;
+    s.ptr = p;
+    s.ld = cols;
+    s.repack = repack;
+    if (repack) {
+        s.ld = round_up(cols, 64);
+        s.copy = c->take<uint16_t>(rows * s.ld);
+    }
+    return s;
+}
+
+// Copies the source's rows where needed; its pointer is then TMA's to read.
+int fill_source(Source* s, int64_t rows, int64_t cols, cudaStream_t stream);
+
+// ---- the backward products (gemm_bwd.cu)
+
+// fp32 values a split product's partial sums take.
+inline int64_t split_floats(const Product& pr, const Layout& l) {
+    return l.splits > 1 ? static_cast<int64_t>(l.splits) * pr.problems * pr.M * ld32_of(pr.N) : 0;
+}
+
+// out = scale (acc_in + A B^T) to 16 bits at out16[problem] (rows N apart), or
+// acc_out = acc_in + A B^T in fp32 (rows ld32_of(N) apart).  `partial` holds
+// split_floats() floats.
+struct StoreTarget {
+    void* out16[2] = {nullptr, nullptr};
+    float* acc_out = nullptr;
+    const float* acc_in = nullptr;
+    const float* scale = nullptr;
+};
+int run_store_product(const Product& pr, const Layout& l, const void* const a[2], int64_t lda, const void* const b[2],
+                      int64_t ldb, const StoreTarget& to, float* partial, int type, const DeviceInfo& info,
+                      cudaStream_t stream);
+
+// ---- argument checks
+
+inline bool bad_size(int64_t n) { return n < 0 || n >= (1ll << 31); }
+inline bool odd_address(const void* p) { return reinterpret_cast<uintptr_t>(p) & 1u; }
+// accumulator tiles are counted in an int
+inline bool too_many_tiles(int64_t rows, int64_t cols) { return cdiv(rows, 128) * cdiv(cols, 16) >= (1ll << 31); }
+
+struct Range {
+    const void* p;
+    uint64_t bytes;
+};
+// Whether any output overlaps an input or another output.
+template <int NI, int NO>
+bool overlaps(const Range (&in)[NI], const Range (&out)[NO]) {
+    for (int i = 0; i < NO; ++i) {
+        if (!out[i].p) continue;
+        for (int j = 0; j < NI; ++j)
+            if (in[j].p && ranges_overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
+        for (int j = 0; j < i; ++j)
+            if (out[j].p && ranges_overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+    }
+    return false;
+}
+inline uint64_t bytes16(int64_t a, int64_t b) { return static_cast<uint64_t>(a) * static_cast<uint64_t>(b) * 2u; }
+
+}  // namespace fused
+
+namespace f16nt {
+// (gemm_f16_nt.cu) copies rows of K 16-bit elements to rows Kp apart
+cudaError_t launch_repack(const void* lhs, int64_t M, const void* rhs, int64_t N, int64_t K, int64_t Kw, int64_t Kp,
+                          uint16_t* da, uint16_t* db, cudaStream_t stream);
+}  // namespace f16nt
+}  // namespace pws
