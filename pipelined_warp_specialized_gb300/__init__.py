@@ -13,6 +13,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -244,26 +245,29 @@ def gemm_f16_nt_noalloc(lhs, rhs, out=None, stages: int = 4, stream=None):
 
 # ---------------------------------------------------------------- the operators around the products
 
-def _type_of(name, tensors):
+_codes = None
+
+
+def _type_of(name, *tensors):
     """The GEMM_TYPE_* of tensors that must share one 16-bit type, be dense
     matrices and lie on one CUDA device."""
-    import torch
-    first = tensors[0]
-    if first.dtype == torch.bfloat16:
-        code = GEMM_TYPE_BFLOAT
-    elif first.dtype == torch.float16:
-        code = GEMM_TYPE_HALF
-    else:
+    global _codes
+    if _codes is None:
+        import torch
+        _codes = {torch.float16: GEMM_TYPE_HALF, torch.bfloat16: GEMM_TYPE_BFLOAT}
+    dtype, device = tensors[0].dtype, tensors[0].device
+    code = _codes.get(dtype)
+    if code is None:
         raise TypeError(f"{name} takes float16 or bfloat16 tensors")
     for t in tensors:
-        if t.dtype != first.dtype:
-            raise TypeError(f"{name}: all matrices must have one type, got {first.dtype} and {t.dtype}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: all matrices must have one type, got {dtype} and {t.dtype}")
         if t.dim() != 2:
             raise ValueError(f"{name} takes matrices, got a tensor of shape {tuple(t.shape)}")
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} takes contiguous CUDA tensors")
-        if t.device != first.device:
-            raise ValueError(f"{name}: all tensors must be on one device, got {first.device} and {t.device}")
+        if t.device != device:
+            raise ValueError(f"{name}: all tensors must be on one device, got {device} and {t.device}")
     return code
 
 
@@ -282,40 +286,36 @@ def _vector(name, what, t, rows, dtype, device):
         raise ValueError(f"{name}: all tensors must be on one device, got {device} and {t.device}")
 
 
-class _Launch:
-    """Makes the operand's device and the call's stream current, so that
-    outputs and workspaces are taken from that stream's memory and are not
-    handed to other work while the call still uses them."""
-
-    def __init__(self, stream, device):
-        import torch
-        self._contexts = []
-        if torch.cuda.current_device() != device.index:
-            self._contexts.append(torch.cuda.device(device))
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self._contexts.append(torch.cuda.stream(stream))
-        self._stream, self._device = stream, device
-
-    def __enter__(self):
-        for c in self._contexts:
-            c.__enter__()
-        return _stream_ptr(self._stream, self._device)
-
-    def __exit__(self, *exc):
-        for c in reversed(self._contexts):
-            c.__exit__(*exc)
-        return False
+_HERE = contextlib.nullcontext()
 
 
-def _workspace(name, device, *args):
-    """(tensor or None, address, bytes) of the workspace the call reports."""
+def _on(stream, device):
+    """(raw stream, context): inside the context the operands' device and the
+    call's stream are current, so that outputs and workspaces are taken from
+    that stream's memory and are not handed to other work while the call still
+    uses them."""
     import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return torch.cuda.current_stream(device).cuda_stream, _HERE
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    else:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stack.enter_context(torch.cuda.stream(stream))
+        raw = stream.cuda_stream
+    return raw, stack
+
+
+def _workspace(name, lib, device, *args):
+    """(tensor or None, address, bytes) of the workspace the call reports."""
     need = ctypes.c_int64()
-    _check(getattr(load_library(), name + "_workspace")(*args, ctypes.byref(need)), name)
+    _check(getattr(lib, name + "_workspace")(*args, ctypes.byref(need)), name)
     if need.value == 0:
         return None, None, 0
+    import torch
     ws = torch.empty(need.value, dtype=torch.uint8, device=device)
     return ws, ws.data_ptr(), need.value
 
@@ -329,18 +329,20 @@ def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream
     """
     import torch
     name = "gemm_gated_nt"
-    code, act_code = _type_of(name, (x, w_gate, w_up)), _act_code(name, act)
+    code, act_code = _type_of(name, x, w_gate, w_up), _act_code(name, act)
     M, K = x.shape
     F = w_gate.shape[0]
     if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
         raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w_gate.shape)}, {tuple(w_up.shape)} do not form "
                          "[M,K], [F,K], [F,K]")
-    with _Launch(stream, x.device) as s:
-        h = torch.empty((M, F), dtype=x.dtype, device=x.device)
+    lib, device = load_library(), x.device
+    s, here = _on(stream, device)
+    with here:
+        h = torch.empty((M, F), dtype=x.dtype, device=device)
         g, u = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
         px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
-        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, F, K, px, pg, pu, code)
-        _check(load_library().gemm_gated_nt(M, F, K, px, pg, pu, h.data_ptr(), g.data_ptr() if save else None,
+        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, F, K, px, pg, pu, code)
+        _check(lib.gemm_gated_nt(M, F, K, px, pg, pu, h.data_ptr(), g.data_ptr() if save else None,
                                             u.data_ptr() if save else None, code, act_code, ws_ptr, ws_bytes, s), name)
     return (h, g, u) if save else h
 
@@ -354,7 +356,7 @@ def gemm_gated_nt_bwd(dh, g, u, x, w_gate, w_up, act: str = "silu", need_dx: boo
     """
     import torch
     name = "gemm_gated_nt_bwd"
-    code, act_code = _type_of(name, (dh, g, u, x, w_gate, w_up)), _act_code(name, act)
+    code, act_code = _type_of(name, dh, g, u, x, w_gate, w_up), _act_code(name, act)
     M, K = x.shape
     F = w_gate.shape[0]
     if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
@@ -362,19 +364,21 @@ def gemm_gated_nt_bwd(dh, g, u, x, w_gate, w_up, act: str = "silu", need_dx: boo
                          "[M,K], [F,K], [F,K]")
     if any(tuple(t.shape) != (M, F) for t in (dh, g, u)):
         raise ValueError(f"{name}: dh, g and u must have shape {(M, F)}")
-    with _Launch(stream, x.device) as s:
+    lib, device = load_library(), x.device
+    s, here = _on(stream, device)
+    with here:
         dx = torch.empty_like(x) if need_dx else None
         dwg, dwu = (torch.empty_like(w_gate), torch.empty_like(w_up)) if need_dw else (None, None)
         ptrs = [t.data_ptr() for t in (dh, g, u, x, w_gate, w_up)]
-        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, F, K, *ptrs, code)
+        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, F, K, *ptrs, code)
         outs = [t.data_ptr() if t is not None else None for t in (dx, dwg, dwu)]
-        _check(load_library().gemm_gated_nt_bwd(M, F, K, *ptrs, *outs, code, act_code, ws_ptr, ws_bytes, s), name)
+        _check(lib.gemm_gated_nt_bwd(M, F, K, *ptrs, *outs, code, act_code, ws_ptr, ws_bytes, s), name)
     return dx, dwg, dwu
 
 
 def _xent_shapes(name, x, w, target):
     import torch
-    code = _type_of(name, (x, w))
+    code = _type_of(name, x, w)
     if w.shape[1] != x.shape[1]:
         raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w.shape)} do not form [M,K], [V,K]")
     _vector(name, "target", target, x.shape[0], torch.int64, x.device)
@@ -390,12 +394,14 @@ def gemm_xent_nt(x, w, target, ignore_index: int = -100, stream=None):
     import torch
     name = "gemm_xent_nt"
     code, M, V, K = _xent_shapes(name, x, w, target)
-    with _Launch(stream, x.device) as s:
-        loss = torch.empty(M, dtype=torch.float32, device=x.device)
+    lib, device = load_library(), x.device
+    s, here = _on(stream, device)
+    with here:
+        loss = torch.empty(M, dtype=torch.float32, device=device)
         lse = torch.empty_like(loss)
         px, pw = x.data_ptr(), w.data_ptr()
-        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, V, K, px, pw, code)
-        _check(load_library().gemm_xent_nt(M, V, K, px, pw, target.data_ptr(), int(ignore_index), loss.data_ptr(),
+        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, V, K, px, pw, code)
+        _check(lib.gemm_xent_nt(M, V, K, px, pw, target.data_ptr(), int(ignore_index), loss.data_ptr(),
                                            lse.data_ptr(), code, ws_ptr, ws_bytes, s), name)
     return loss, lse
 
@@ -411,12 +417,14 @@ def gemm_xent_nt_bwd(x, w, target, lse, dloss, ignore_index: int = -100, need_dx
     code, M, V, K = _xent_shapes(name, x, w, target)
     _vector(name, "lse", lse, M, torch.float32, x.device)
     _vector(name, "dloss", dloss, M, torch.float32, x.device)
-    with _Launch(stream, x.device) as s:
+    lib, device = load_library(), x.device
+    s, here = _on(stream, device)
+    with here:
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty_like(w) if need_dw else None
         px, pw = x.data_ptr(), w.data_ptr()
-        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, V, K, px, pw, code)
-        _check(load_library().gemm_xent_nt_bwd(M, V, K, px, pw, target.data_ptr(), int(ignore_index), lse.data_ptr(),
+        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, V, K, px, pw, code)
+        _check(lib.gemm_xent_nt_bwd(M, V, K, px, pw, target.data_ptr(), int(ignore_index), lse.data_ptr(),
                                                dloss.data_ptr(), dx.data_ptr() if need_dx else None,
                                                dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
     return dx, dw
@@ -429,18 +437,20 @@ def gemm_nt_bwd(dy, x, w, need_dx: bool = True, need_dw: bool = True, stream=Non
     """
     import torch
     name = "gemm_nt_bwd"
-    code = _type_of(name, (dy, x, w))
+    code = _type_of(name, dy, x, w)
     M, N = dy.shape
     K = x.shape[1]
     if x.shape[0] != M or tuple(w.shape) != (N, K):
         raise ValueError(f"{name}: shapes {tuple(dy.shape)}, {tuple(x.shape)}, {tuple(w.shape)} do not form "
                          "[M,N], [M,K], [N,K]")
-    with _Launch(stream, x.device) as s:
+    lib, device = load_library(), x.device
+    s, here = _on(stream, device)
+    with here:
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty_like(w) if need_dw else None
         ptrs = [t.data_ptr() for t in (dy, x, w)]
-        ws, ws_ptr, ws_bytes = _workspace(name, x.device, M, N, K, *ptrs, code)
-        _check(load_library().gemm_nt_bwd(M, N, K, *ptrs, dx.data_ptr() if need_dx else None,
+        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, N, K, *ptrs, code)
+        _check(lib.gemm_nt_bwd(M, N, K, *ptrs, dx.data_ptr() if need_dx else None,
                                           dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
     return dx, dw
 

@@ -17,38 +17,45 @@ namespace pws {
 namespace fused {
 namespace {
 
-// dg, du [M, F] with rows ldo apart from dh, g, u [M, F] (dense).  Memory
+// dg, du [M, F] with rows ldo apart from dh, g, u [M, F] (dense); with
+// lo_offset also what their rounding left, that many elements further.  Memory
 // bound: reads three and writes two 16-bit matrices.  VEC: eight elements a
-// thread where every row starts on a 16-byte boundary, else one.
+// thread where every row starts on a 16-byte boundary, else one; a block takes
+// one row's next 256 threads' worth, so nothing divides.
 template <bool VEC>
 __global__ void __launch_bounds__(256)
 gated_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g, const uint16_t* __restrict__ u,
-                  uint16_t* __restrict__ dg, uint16_t* __restrict__ du, int64_t M, int F, int64_t ldo, int act,
-                  int bf16) {
+                  uint16_t* __restrict__ dg, uint16_t* __restrict__ du, int F, int64_t ldo,
+                  int64_t lo_offset, int act, int bf16) {
     grid_dependency_wait();
     allow_dependent_launch();
     constexpr int E = VEC ? 8 : 1;
-    const int per_row = F / E;
-    const int64_t total = M * per_row;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = i / per_row;
-        const int c = static_cast<int>(i - row * per_row) * E;
+    const int64_t row = blockIdx.x;
+    for (int64_t c = (blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x) * E; c < F;
+         c += static_cast<int64_t>(gridDim.y) * blockDim.x * E) {
         const int64_t at = row * F + c, to = row * ldo + c;
         if constexpr (VEC) {
             const uint4 a = *reinterpret_cast<const uint4*>(dh + at);
             const uint4 b = *reinterpret_cast<const uint4*>(g + at);
             const uint4 d = *reinterpret_cast<const uint4*>(u + at);
             const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w}, dv[4] = {d.x, d.y, d.z, d.w};
-            uint32_t og[4], ou[4];
+            uint32_t og[4], ou[4], rg[4], ru[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 h2 = unpack16(av[j], bf16), g2 = unpack16(bv[j], bf16), u2 = unpack16(dv[j], bf16);
                 float v0, s0, v1, s1;
                 act_value_slope(g2.x, act, v0, s0);
                 act_value_slope(g2.y, act, v1, s1);
-                og[j] = pack16(h2.x * u2.x * s0, h2.y * u2.y * s1, bf16);
-                ou[j] = pack16(h2.x * v0, h2.y * v1, bf16);
+                const float g0 = h2.x * u2.x * s0, g1 = h2.y * u2.y * s1, u0 = h2.x * v0, u1 = h2.y * v1;
+                og[j] = pack16(g0, g1, bf16);
+                ou[j] = pack16(u0, u1, bf16);
+                const float2 cg = unpack16(og[j], bf16), cu = unpack16(ou[j], bf16);
+                rg[j] = pack16(g0 - cg.x, g1 - cg.y, bf16);
+                ru[j] = pack16(u0 - cu.x, u1 - cu.y, bf16);
+            }
+            if (lo_offset) {
+                *reinterpret_cast<uint4*>(dg + to + lo_offset) = make_uint4(rg[0], rg[1], rg[2], rg[3]);
+                *reinterpret_cast<uint4*>(du + to + lo_offset) = make_uint4(ru[0], ru[1], ru[2], ru[3]);
             }
             *reinterpret_cast<uint4*>(dg + to) = make_uint4(og[0], og[1], og[2], og[3]);
             *reinterpret_cast<uint4*>(du + to) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
@@ -57,6 +64,12 @@ gated_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ 
             float v, s;
             act_value_slope(g1, act, v, s);
             const uint32_t o = pack16(h1 * u1 * s, h1 * v, bf16);
+            if (lo_offset) {
+                const float2 c2 = unpack16(o, bf16);
+                const uint32_t r = pack16(h1 * u1 * s - c2.x, h1 * v - c2.y, bf16);
+                dg[to + lo_offset] = static_cast<uint16_t>(r & 0xFFFFu);
+                du[to + lo_offset] = static_cast<uint16_t>(r >> 16);
+            }
             dg[to] = static_cast<uint16_t>(o & 0xFFFFu);
             du[to] = static_cast<uint16_t>(o >> 16);
         }
@@ -87,6 +100,7 @@ struct GatedPlan {
     size_t bytes = 0;
 };
 
+// num_sms 0: the workspace only.
 GatedPlan plan_gated(int64_t M, int64_t F, int64_t K, const void* x, const void* wg, const void* wu, int num_sms,
                      void* ws) {
     GatedPlan pl;
@@ -94,7 +108,7 @@ GatedPlan plan_gated(int64_t M, int64_t F, int64_t K, const void* x, const void*
     c.base = static_cast<char*>(ws);
     pl.pr.M = M; pl.pr.N = F; pl.pr.K = K;
     pl.pr.gated = true;
-    pl.l = choose_layout(pl.pr, num_sms);
+    if (num_sms) pl.l = choose_layout(pl.pr, num_sms);
     pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
     // both weights share one row stride
     const bool rw = !tma_ok(wg, K) || !tma_ok(wu, K);
@@ -127,7 +141,7 @@ struct GatedBwdPlan {
     Source x, wg, wu;
     uint16_t* dg = nullptr;
     uint16_t* du = nullptr;
-    int64_t ldf = 0;
+    int64_t ldf = 0, lo_offset = 0;
     float* partial = nullptr;
     size_t bytes = 0;
 };
@@ -138,14 +152,20 @@ GatedBwdPlan plan_gated_bwd(int64_t M, int64_t F, int64_t K, const void* x, cons
     Carver c;
     c.base = static_cast<char*>(ws);
     pl.ldf = round_up(F, 64);
-    pl.dg = c.take<uint16_t>(M * pl.ldf);
-    pl.du = c.take<uint16_t>(M * pl.ldf);
-    pl.dx.M = M; pl.dx.N = K; pl.dx.K = F;
+    const int halves = M <= kFewRows ? 2 : 1;
+    pl.lo_offset = halves == 2 ? M * pl.ldf : 0;
+    pl.dg = c.take<uint16_t>(halves * M * pl.ldf);
+    pl.du = c.take<uint16_t>(halves * M * pl.ldf);
+    // dx: the gate's F and the up projection's F are two segments of K; the
+    // remainders are M more rows
+    pl.dx.M = halves * M; pl.dx.N = K; pl.dx.K = F;
+    pl.dx.halves = halves;
     pl.dx.segments = 2;
     pl.dx.bmn = true;
     pl.dx.may_split = true;
     pl.dw.M = F; pl.dw.N = K; pl.dw.K = M;
     pl.dw.problems = 2;
+    pl.dw.segments = halves;        // dW: the remainders are M more tokens
     pl.dw.amn = pl.dw.bmn = true;
     pl.dw.may_split = true;
     pl.x = source_of(x, M, K, want_dw && !tma_ok(x, K), &c);
@@ -175,9 +195,7 @@ extern "C" int gemm_gated_nt_workspace(int64_t M, int64_t F, int64_t K, const vo
     const int rc = check_gated(M, F, K, x, w_gate, w_up, nullptr, nullptr, nullptr, type, GEMM_ACT_SILU);
     if (rc != GEMM_OK) return rc;
     if (!bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = M && F && K ? static_cast<int64_t>(
-                               plan_gated(M, F, K, x, w_gate, w_up, pws::sm_count_or_default(), nullptr).bytes)
-                         : 0;
+    *bytes = M && F && K ? static_cast<int64_t>(plan_gated(M, F, K, x, w_gate, w_up, 0, nullptr).bytes) : 0;
     return GEMM_OK;
 }
 
@@ -203,11 +221,9 @@ extern "C" int gemm_gated_nt(int64_t M, int64_t F, int64_t K, const void* x, con
     if (pl.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
                      workspace_bytes < static_cast<int64_t>(pl.bytes)))
         return GEMM_ERR_INVALID_ARG;
-    if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
-    if ((rc = fill_source(&pl.wg, F, K, stream)) != GEMM_OK) return rc;
-    if ((rc = fill_source(&pl.wu, F, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_sources({{&pl.x, M}, {&pl.wg, F}, {&pl.wu, F}}, K, stream)) != GEMM_OK) return rc;
     Maps maps;
-    const void* a[2] = {pl.x.ptr, nullptr};
+    const void* a[4] = {pl.x.ptr};
     const void* b[2] = {pl.wg.ptr, pl.wu.ptr};
     if (!encode_operands(&maps, pl.pr, pl.l, a, pl.x.ld, b, pl.wg.ld)) return GEMM_ERR_LAUNCH;
     Params p = base_params(pl.pr, pl.l, type, info, stream);
@@ -257,24 +273,22 @@ extern "C" int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
         workspace_bytes < static_cast<int64_t>(pl.bytes))
         return GEMM_ERR_INVALID_ARG;
-    if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
-    if ((rc = fill_source(&pl.wg, F, K, stream)) != GEMM_OK) return rc;
-    if ((rc = fill_source(&pl.wu, F, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_sources({{&pl.x, M}, {&pl.wg, F}, {&pl.wu, F}}, K, stream)) != GEMM_OK) return rc;
     {
         const bool vec = tma_ok(dh, F) && tma_ok(g, F) && tma_ok(u, F);
-        int64_t blocks = cdiv(M * (vec ? F / 8 : F), 256);
-        if (blocks > 16ll * info.num_sms) blocks = 16ll * info.num_sms;
+        int64_t across = cdiv(F, vec ? 8 * 256 : 256);
+        if (across > 65535) across = 65535;
         auto kern = vec ? gated_grad_kernel<true> : gated_grad_kernel<false>;
-        if (launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+        if (launch_pdl(kern, dim3(static_cast<unsigned>(M), static_cast<unsigned>(across)), dim3(256), 0, stream,
                        static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(g),
-                       static_cast<const uint16_t*>(u), pl.dg, pl.du, M, static_cast<int>(F), pl.ldf, act,
-                       type == GEMM_TYPE_BFLOAT ? 1 : 0) != cudaSuccess) {
+                       static_cast<const uint16_t*>(u), pl.dg, pl.du, static_cast<int>(F), pl.ldf,
+                       pl.lo_offset, act, type == GEMM_TYPE_BFLOAT ? 1 : 0) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_LAUNCH;
         }
     }
-    const void* d[2] = {pl.dg, pl.du};
     if (dx) {
+        const void* d[4] = {pl.dg, pl.du};
         const void* b[2] = {pl.wg.ptr, pl.wu.ptr};
         StoreTarget to;
         to.out16[0] = dx;
@@ -282,6 +296,7 @@ extern "C" int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh
         if (rc != GEMM_OK) return rc;
     }
     if (dw_gate) {
+        const void* d[4] = {pl.dg, pl.dg + pl.lo_offset, pl.du, pl.du + pl.lo_offset};
         const void* b[2] = {pl.x.ptr, nullptr};
         StoreTarget to;
         to.out16[0] = dw_gate;

@@ -13,17 +13,20 @@
 // one piece of D.
 //
 // D is rounded to the inputs' type because the tensor cores multiply 16-bit
-// operands of one type.  It is scaled by a power of two that brings the
-// largest |dloss| to [2^13, 2^14), undone in fp32 when dx and dW are rounded:
-// without it binary16 would lose the probabilities below 6e-8 / dloss.
+// operands of one type.  It is scaled so that the largest |dloss| becomes 2^13,
+// undone in fp32 when dx and dW are rounded: without it binary16 would lose
+// the probabilities below 6e-8 / dloss, and with it the usual uniform dloss
+// adds no rounding of its own (2^13 (p - 1) rounds as p - 1 does).  With few
+// rows D keeps its rounding remainder too (kFewRows).
 #include "product_host.cuh"
 
 namespace pws {
 namespace fused {
 namespace {
 
-// One block: the power-of-two scale, its inverse, and per row the scaled loss
-// gradient: 0 for an ignored row, NaN for a target outside the vocabulary.
+// One block: the largest finite |dloss| of a row that counts, brought to 2^13;
+// per row the scaled loss gradient, 0 for an ignored row, NaN for a target
+// outside the vocabulary.
 __global__ void __launch_bounds__(1024)
 xent_rows_kernel(const int64_t* __restrict__ target, const float* __restrict__ dloss, int M, int64_t V,
                  int64_t ignore_index, float* __restrict__ coef, float* __restrict__ inv_scale) {
@@ -31,6 +34,7 @@ xent_rows_kernel(const int64_t* __restrict__ target, const float* __restrict__ d
     allow_dependent_launch();
     __shared__ float part[32];
     float top = 0.0f;
+#pragma unroll 8
     for (int i = threadIdx.x; i < M; i += blockDim.x) {
         const float d = fabsf(dloss[i]);
         if (target[i] != ignore_index && d <= 3.0e38f) top = fmaxf(top, d);     // (finite ones)
@@ -40,19 +44,18 @@ xent_rows_kernel(const int64_t* __restrict__ target, const float* __restrict__ d
     __syncthreads();
     top = part[threadIdx.x % 32];
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    int e = top > 0.0f ? 13 - ilogbf(top) : 0;
-    e = e > 100 ? 100 : (e < -100 ? -100 : e);
-    const float scale = ldexpf(1.0f, e);
-    if (threadIdx.x == 0) *inv_scale = ldexpf(1.0f, -e);
+    top = fmaxf(top, 1e-30f);
+    if (threadIdx.x == 0) *inv_scale = top * (1.0f / 8192.0f);
+#pragma unroll 8
     for (int i = threadIdx.x; i < M; i += blockDim.x) {
         const int64_t t = target[i];
         float c = 0.0f;
-        if (t != ignore_index) c = t >= 0 && t < V ? dloss[i] * scale : __int_as_float(0x7fffffff);
+        if (t != ignore_index) c = t >= 0 && t < V ? dloss[i] / top * 8192.0f : __int_as_float(0x7fffffff);
         coef[i] = c;
     }
 }
 
-// One warp per row joins its tiles' (maximum, sum) pairs.  tiles == 0: K == 0,
+// One warp per row joins its half tiles' (maximum, sum) pairs.  tiles == 0: K == 0,
 // every logit is 0.
 __global__ void __launch_bounds__(256)
 xent_join_kernel(const float2* __restrict__ stats, const float* __restrict__ z_target,
@@ -66,7 +69,7 @@ xent_join_kernel(const float2* __restrict__ stats, const float* __restrict__ z_t
     const float inf = __int_as_float(0x7f800000);
     float m = -inf, s = 0.0f;
     for (int t = lane; t < tiles; t += 32) {
-        const float2 v = stats[static_cast<int64_t>(t) * M + row];
+        const float2 v = stats[static_cast<int64_t>(row) * tiles + t];
         const float top = fmaxf(m, v.x);
         const float ref = top == -inf ? 0.0f : top;
         s = s * expf(m - ref) + v.y * expf(v.x - ref);
@@ -114,10 +117,11 @@ XentPlan plan_xent(int64_t M, int64_t V, int64_t K, const void* x, const void* w
     Carver c;
     c.base = static_cast<char*>(ws);
     pl.pr.M = M; pl.pr.N = V; pl.pr.K = K;
+    pl.pr.chunk = kStatsChunk;
     pl.l = choose_layout(pl.pr, num_sms);
     pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
     pl.w = source_of(w, V, K, !tma_ok(w, K), &c);
-    pl.stats = c.take<float2>(static_cast<int64_t>(pl.l.tiles_n) * M);
+    pl.stats = c.take<float2>(2ll * pl.l.tiles_n * M);
     pl.z_target = c.take<float>(M);
     pl.bytes = c.used;
     return pl;
@@ -128,7 +132,8 @@ constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int64_t kMinPiece = 8192;
 
 struct XentBwdPlan {
-    int64_t piece = 0, ldd = 0;
+    int64_t piece = 0, ldd = 0, lo_offset = 0;
+    int halves = 1;
     int pieces = 0;
     Source x, w;
     float* coef = nullptr;
@@ -145,16 +150,18 @@ Product logits_of(int64_t M, int64_t v, int64_t K) {
     p.M = M; p.N = v; p.K = K;
     return p;
 }
-Product dx_of(int64_t M, int64_t v, int64_t K) {
+Product dx_of(int64_t M, int64_t v, int64_t K, int halves) {
     Product p;
-    p.M = M; p.N = K; p.K = v;
+    p.M = halves * M; p.N = K; p.K = v;
+    p.halves = halves;          // the remainders are M more rows
     p.bmn = true;
     p.may_split = true;
     return p;
 }
-Product dw_of(int64_t M, int64_t v, int64_t K) {
+Product dw_of(int64_t M, int64_t v, int64_t K, int halves) {
     Product p;
     p.M = v; p.N = K; p.K = M;
+    p.segments = halves;        // the remainders are M more tokens
     p.amn = p.bmn = true;
     p.may_split = true;
     return p;
@@ -175,12 +182,14 @@ XentBwdPlan plan_xent_bwd(int64_t M, int64_t V, int64_t K, const void* x, const 
     pl.w = source_of(w, V, K, !tma_ok(w, K), &c);
     pl.coef = c.take<float>(M);
     pl.inv_scale = c.take<float>(1);
-    pl.d = c.take<uint16_t>(M * pl.ldd);
+    pl.halves = M <= kFewRows ? 2 : 1;
+    pl.lo_offset = pl.halves == 2 ? M * pl.ldd : 0;
+    pl.d = c.take<uint16_t>(pl.halves * M * pl.ldd);
     if (want_dx && pl.pieces > 1) pl.acc = c.take<float>(M * ld32_of(K));
     int64_t most = 0;
     for (int i = 0; i < 2; ++i) {          // the pieces' width, and the last one's
         const int64_t v = i ? V - (pl.pieces - 1) * pl.piece : (pl.pieces > 1 ? pl.piece : V);
-        const Product a = dx_of(M, v, K), b = dw_of(M, v, K);
+        const Product a = dx_of(M, v, K, pl.halves), b = dw_of(M, v, K, pl.halves);
         const int64_t fa = want_dx ? split_floats(a, choose_layout(a, num_sms)) : 0;
         const int64_t fb = want_dw ? split_floats(b, choose_layout(b, num_sms)) : 0;
         if (fa > most) most = fa;
@@ -229,10 +238,9 @@ extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, cons
         if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
             workspace_bytes < static_cast<int64_t>(pl.bytes))
             return GEMM_ERR_INVALID_ARG;
-        if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
-        if ((rc = fill_source(&pl.w, V, K, stream)) != GEMM_OK) return rc;
+        if ((rc = fill_sources({{&pl.x, M}, {&pl.w, V}, {}}, K, stream)) != GEMM_OK) return rc;
         Maps maps;
-        const void* a[2] = {pl.x.ptr, nullptr};
+        const void* a[4] = {pl.x.ptr};
         const void* b[2] = {pl.w.ptr, nullptr};
         if (!encode_operands(&maps, pl.pr, pl.l, a, pl.x.ld, b, pl.w.ld)) return GEMM_ERR_LAUNCH;
         Params p = base_params(pl.pr, pl.l, type, info, stream);
@@ -244,7 +252,7 @@ extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, cons
     }
     if (launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>(cdiv(M, 8))), dim3(256), 0, stream,
                    static_cast<const float2*>(pl.stats), static_cast<const float*>(pl.z_target), target,
-                   static_cast<int>(M), K > 0 ? pl.l.tiles_n : 0, V, ignore_index, loss, lse) != cudaSuccess) {
+                   static_cast<int>(M), K > 0 ? 2 * pl.l.tiles_n : 0, V, ignore_index, loss, lse) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
@@ -290,8 +298,7 @@ extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, 
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
         workspace_bytes < static_cast<int64_t>(pl.bytes))
         return GEMM_ERR_INVALID_ARG;
-    if ((rc = fill_source(&pl.x, M, K, stream)) != GEMM_OK) return rc;
-    if ((rc = fill_source(&pl.w, V, K, stream)) != GEMM_OK) return rc;
+    if ((rc = fill_sources({{&pl.x, M}, {&pl.w, V}, {}}, K, stream)) != GEMM_OK) return rc;
     if (launch_pdl(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, target, dloss, static_cast<int>(M), V,
                    ignore_index, pl.coef, pl.inv_scale) != cudaSuccess) {
         cudaGetLastError();
@@ -304,7 +311,7 @@ extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, 
             const Product pr = logits_of(M, v, K);
             const Layout l = choose_layout(pr, info.num_sms);
             Maps maps;
-            const void* a[2] = {pl.x.ptr, nullptr};
+            const void* a[4] = {pl.x.ptr};
             const void* b[2] = {w_piece, nullptr};
             if (!encode_operands(&maps, pr, l, a, pl.x.ld, b, pl.w.ld)) return GEMM_ERR_LAUNCH;
             Params p = base_params(pr, l, type, info, stream);
@@ -314,12 +321,14 @@ extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, 
             p.col0 = v0;
             p.out16[0] = pl.d;
             p.ld16 = pl.ldd;
-            p.tma_store = output_map(&maps.c[0], l, pl.d, M, v, pl.ldd);
+            p.lo_offset = pl.lo_offset;
+            p.tma_store = output_map(&maps.c[0], l, pl.d, M, v, pl.ldd) &&
+                          (!pl.lo_offset || output_map(&maps.c[1], l, pl.d + pl.lo_offset, M, v, pl.ldd));
             if ((rc = launch_product<kEpiXentGrad, false, false>(l, maps, p, info, stream)) != GEMM_OK) return rc;
         }
-        const void* a[2] = {pl.d, nullptr};
         if (dx) {
-            const Product pr = dx_of(M, v, K);
+            const void* a[4] = {pl.d};
+            const Product pr = dx_of(M, v, K, pl.halves);
             const void* b[2] = {w_piece, nullptr};
             StoreTarget to;
             to.acc_in = i ? pl.acc : nullptr;
@@ -334,7 +343,8 @@ extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, 
             if (rc != GEMM_OK) return rc;
         }
         if (dw) {
-            const Product pr = dw_of(M, v, K);
+            const void* a[4] = {pl.d, pl.d + pl.lo_offset};
+            const Product pr = dw_of(M, v, K, pl.halves);
             const void* b[2] = {pl.x.ptr, nullptr};
             StoreTarget to;
             to.out16[0] = static_cast<uint16_t*>(dw) + v0 * K;

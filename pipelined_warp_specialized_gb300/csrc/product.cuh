@@ -12,6 +12,10 @@
 //   segments  the K axis may run over two operand pairs, one after the other
 //             (dx = dg Wg + du Wu is one accumulation).
 //   problems  two products of one shape may share a launch (dWg and dWu).
+//   chunks    the softmax statistics sum each logit over K in chunks of
+//             kStatsChunk blocks, each chunk's tensor-memory sum added in
+//             registers (round to nearest): the tensor core's own accumulation
+//             truncates, which over a long K shifts every logit the same way.
 //   splits    few output tiles with a long K are split over K; the fp32
 //             partial sums are joined in a fixed order by a later kernel, so a
 //             result never depends on the order in which CTAs finish.
@@ -46,7 +50,6 @@ constexpr int MAX_STAGES = 32;
 constexpr int EPI_COLS = 64;                // output columns per staged chunk: 128 bytes
 constexpr int EPI_BUF = 32 * EPI_COLS * 2;  // one warp's 32 rows of a chunk
 constexpr int EPI_BYTES = 4 * 2 * EPI_BUF;
-constexpr int THREADS = 6 * 32;             // producer, MMA issuer, four epilogue warps
 constexpr int MN_BOX = 64 * BK * 2;         // one MN-major box: 64 K rows of 64 elements
 constexpr int GROUP_M = 8;                  // tile rows walked together, so their A strips stay in L2
 
@@ -71,11 +74,20 @@ static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: each owns all of tensor 
 
 enum Epilogue { kEpiStore = 0, kEpiGated = 1, kEpiXentStats = 2, kEpiXentGrad = 3 };
 
+// Epilogue warps: one per tensor-memory lane quarter, or two for the softmax
+// statistics, whose running sums take 128 registers a thread.
+constexpr int epi_warps(int epi) { return epi == kEpiXentStats ? 8 : 4; }
+constexpr int threads_of(int epi) { return (2 + epi_warps(epi)) * 32; }
+
+// K blocks per chunk of the softmax statistics' sums.
+constexpr int kStatsChunk = 8;
+
 struct Params {
     int M, N;                       // output rows and columns (of the epilogue's output)
     int nkb0, nkb;                  // K blocks of the first segment, of all segments
     int tiles_m, tiles_n, num_tiles;    // tiles of one problem; num_tiles counts all problems
     int splits, kb_per_split;
+    int chunk;                      // K blocks per accumulator hand-over (all of a unit's, but for the statistics)
     int total_units;                // num_tiles * splits
     int a_rows;                     // rows of a K-major A box (<= 128): fewer than 128 for few tokens
     int bn;                         // accumulator columns per tile (a multiple of 16)
@@ -102,15 +114,16 @@ struct Params {
     uint16_t* u_out;
     // cross entropy
     const int64_t* target;
-    float2* stats;                  // [tiles_n][M]: maximum and sum of exponentials of a tile's columns
+    float2* stats;                  // [M][2 tiles_n]: maximum and sum of exponentials of half a tile's columns
     float* z_target;                // [M]
     const float* lse;
     const float* coef;              // [M]: scaled loss gradient; 0 for a row that does not count
     int64_t col0;                   // vocabulary index of column 0
+    int64_t lo_offset;              // elements from D to its rounding remainder, 0 for none
 };
 
 struct Maps {
-    CUtensorMap a[2], b[2], c[3];
+    CUtensorMap a[4], b[2], c[3];   // a[2 * problem + segment], b[segment]
 };
 
 // K-major operand in the 128-byte swizzle: rows of 128 bytes, 8-row atoms
@@ -203,7 +216,7 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
 }
 
 template <int CG, int EPI, bool AMN, bool BMN>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(threads_of(EPI), 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -228,7 +241,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bTFULL + 8 * b, 1);
-            mbar_init(bTEMPTY + 8 * b, 4 * CG);
+            mbar_init(bTEMPTY + 8 * b, epi_warps(EPI) * CG);
         }
         mbar_init(bDRAIN, 1);
         *abort_flag = 0u;
@@ -275,7 +288,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     const uint32_t bar = full_leader + 8 * stage;
                     const int seg = kb >= p.nkb0 ? 1 : 0;
                     const int k = (kb - (seg ? p.nkb0 : 0)) * BK;
-                    const CUtensorMap* ma = &maps.a[seg | t.problem];
+                    const CUtensorMap* ma = &maps.a[2 * t.problem + seg];
                     if (leader) mbar_arrive_expect_tx(bFULL + 8 * stage, CG * p.tx_bytes);
                     if constexpr (AMN) {
                         load(a_dst, ma, m_cta, k, bar);
@@ -333,28 +346,31 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             const uint32_t slot16 = static_cast<uint32_t>(p.slot_bytes) >> 4;
             uint32_t stage = 0, phase = 0, tcount = 0;
             bool ok = true, issued_any = false;
-            for (int u = group_id; ok && u < p.total_units; u += num_groups, ++tcount) {
+            for (int u = group_id; ok && u < p.total_units; u += num_groups) {
                 const Tile t = tile_of(u, p);
-                const uint32_t b = tcount & 1u, aph = (tcount >> 1) & 1u;
-                if (!W.template wait<CG == 2>(bTEMPTY + 8 * b, aph)) { ok = false; break; }
-                tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + b * MAX_BN;
-                for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!W.wait(bFULL + 8 * stage, phase)) { ok = false; break; }
+                for (int c0 = t.kb0; ok && c0 < t.kb1; c0 += p.chunk, ++tcount) {
+                    const int c1 = min(t.kb1, c0 + p.chunk);
+                    const uint32_t b = tcount & 1u, aph = (tcount >> 1) & 1u;
+                    if (!W.template wait<CG == 2>(bTEMPTY + 8 * b, aph)) { ok = false; break; }
                     tc_fence_after_sync();
-                    const uint64_t ad = adesc0 + stage * slot16, bd = bdesc0 + stage * slot16;
+                    const uint32_t d_tmem = tmem_base + b * MAX_BN;
+                    for (int kb = c0; kb < c1; ++kb) {
+                        if (!W.wait(bFULL + 8 * stage, phase)) { ok = false; break; }
+                        tc_fence_after_sync();
+                        const uint64_t ad = adesc0 + stage * slot16, bd = bdesc0 + stage * slot16;
 #pragma unroll
-                    for (int k = 0; k < BK / UMMA_K; ++k)
-                        tc_mma_f16<CG>(d_tmem, ad + k * k_step<AMN>(), bd + k * k_step<BMN>(), p.idesc,
-                                       kb != t.kb0 || k != 0);
-                    issued_any = true;
-                    if constexpr (CG == 1) tc_commit_1(bEMPTY + 8 * stage);
-                    else tc_commit_2_mc(bEMPTY + 8 * stage, 0x3);
-                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                        for (int k = 0; k < BK / UMMA_K; ++k)
+                            tc_mma_f16<CG>(d_tmem, ad + k * k_step<AMN>(), bd + k * k_step<BMN>(), p.idesc,
+                                           kb != c0 || k != 0);
+                        issued_any = true;
+                        if constexpr (CG == 1) tc_commit_1(bEMPTY + 8 * stage);
+                        else tc_commit_2_mc(bEMPTY + 8 * stage, 0x3);
+                        if (++stage == S) { stage = 0; phase ^= 1u; }
+                    }
+                    if (!ok) break;
+                    if constexpr (CG == 1) tc_commit_1(bTFULL + 8 * b);
+                    else tc_commit_2_mc(bTFULL + 8 * b, 0x3);
                 }
-                if (!ok) break;
-                if constexpr (CG == 1) tc_commit_1(bTFULL + 8 * b);
-                else tc_commit_2_mc(bTFULL + 8 * b, 0x3);
             }
             if (issued_any) {
                 // all multiplies have finished before tensor memory is released
@@ -379,13 +395,14 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             }
         const uint32_t bufs = base + OFF_EPI + static_cast<uint32_t>(e) * 2 * EPI_BUF;
         uint32_t nbuf = 0;
+        int tile_end = 0;                        // the tile's last column + 1, past N or not
         // One 64-column chunk (this lane's row, 32 packed pairs) of a 16-bit
         // output: staged in the swizzle its tensor map uses and stored by TMA
-        // (the staging buffers in turn), or stored by the lane itself where
-        // TMA cannot address the output or the chunk is narrower (col_end).
+        // (the staging buffers in turn), or, where TMA cannot address the
+        // output or the tile ends inside the chunk, staged and stored by the warp.
         auto emit = [&](const uint32_t(&h)[32], const CUtensorMap* map, uint16_t* out, int64_t ld, int row0, int col0,
                         int col_end) {
-            if (p.tma_store) {
+            if (p.tma_store && col0 + EPI_COLS <= tile_end) {
                 const uint32_t buf = bufs + (nbuf & 1u) * EPI_BUF;
                 ++nbuf;
                 if (lane == 0) bulk_wait_group_read<1>();
@@ -406,39 +423,144 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 }
                 return;
             }
-            const int row = row0 + lane;
-            if (row >= p.M) return;
-            uint16_t* dst = out + static_cast<int64_t>(row) * ld;
-            const bool wide = ((reinterpret_cast<uintptr_t>(dst + col0) & 15u) == 0);
+            // The lane's row goes through the staging buffer, so that the warp
+            // then writes one row at a time, consecutive lanes at consecutive
+            // addresses (rows of any alignment; a lane storing its own row's
+            // elements touches 32 lines an instruction: measured slower).
+            const uint32_t row_addr = bufs + static_cast<uint32_t>(lane) * 128;
+            if (p.tma_store && lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int col = col0 + 8 * j;
-                if (wide && col + 8 <= col_end) {
-                    *reinterpret_cast<uint4*>(dst + col) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+                const uint32_t dst = row_addr + ((static_cast<uint32_t>(j) ^ static_cast<uint32_t>(lane & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[4 * j]),
+                             "r"(h[4 * j + 1]), "r"(h[4 * j + 2]), "r"(h[4 * j + 3])
+                             : "memory");
+            }
+            __syncwarp();
+            const int rows = min(32, p.M - row0);
+            const int col = col0 + 2 * lane;
+            const bool both = (reinterpret_cast<uintptr_t>(out) & 3u) == 0 && (ld & 1) == 0 && (col0 & 1) == 0;
+            for (int r = 0; r < rows; ++r) {
+                const uint32_t v = ld_shared_u32(bufs + static_cast<uint32_t>(r) * 128 +
+                                                 ((static_cast<uint32_t>(lane >> 2) ^ static_cast<uint32_t>(r & 7)) << 4) +
+                                                 static_cast<uint32_t>(lane & 3) * 4);
+                uint16_t* dst = out + static_cast<int64_t>(row0 + r) * ld + col;
+                if (both && col + 1 < col_end) {
+                    *reinterpret_cast<uint32_t*>(dst) = v;
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t v = h[4 * j + i];
-                        if (col + 2 * i < col_end) dst[col + 2 * i] = static_cast<uint16_t>(v & 0xFFFFu);
-                        if (col + 2 * i + 1 < col_end) dst[col + 2 * i + 1] = static_cast<uint16_t>(v >> 16);
-                    }
+                    if (col < col_end) dst[0] = static_cast<uint16_t>(v & 0xFFFFu);
+                    if (col + 1 < col_end) dst[1] = static_cast<uint16_t>(v >> 16);
                 }
             }
         };
         uint32_t tcount = 0;
-        for (int u = group_id; u < p.total_units; u += num_groups, ++tcount) {
+        // waits for the next accumulator hand-over; its tensor-memory address
+        auto acquire = [&](uint32_t& tbase) {
+            const uint32_t b = tcount & 1u;
+            bool got = true;
+            if (lane == 0) got = W.wait_progress(bTFULL + 8 * b, (tcount >> 1) & 1u, sPROGRESS, false);
+            got = __shfl_sync(0xffffffffu, got, 0);
+            tc_fence_after_sync();
+            tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_BN;
+            return got;
+        };
+        // this warp's reads of the accumulator are complete
+        auto release = [&]() {
+            const uint32_t b = tcount & 1u;
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1) mbar_arrive(bTEMPTY + 8 * b);
+                else mbar_arrive_cluster(tempty_leader + 8 * b);
+            }
+            ++tcount;
+        };
+        for (int u = group_id; u < p.total_units; u += num_groups) {
             const Tile t = tile_of(u, p);
-            const uint32_t b = tcount & 1u, aph = (tcount >> 1) & 1u;
             const int row0 = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA + q * 32;
             const int row = row0 + lane;
             const int n0 = t.tn * p.tile_n;
-            const int col_end = min(p.N, n0 + p.tile_n);
-            bool got = true;
-            if (lane == 0) got = W.wait_progress(bTFULL + 8 * b, aph, sPROGRESS, false);
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got) break;
-            tc_fence_after_sync();
-            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_BN;
+            tile_end = n0 + p.tile_n;
+            const int col_end = min(p.N, tile_end);
+            uint32_t tbase;
+            if constexpr (EPI == kEpiXentStats) {
+                // This warp's 32-column groups are 2 j + half of the tile's.
+                // The logits are summed over K chunk by chunk, then reduced to
+                // the running maximum m and sum s = sum exp(z - m) of the row.
+                const int half = e >> 2;
+                const bool rows_live = row0 < p.M;
+                float z[4][32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[j][i] = 0.0f;
+                bool got = true;
+                for (int c0 = t.kb0; c0 < t.kb1; c0 += p.chunk) {
+                    if (!acquire(tbase)) { got = false; break; }
+                    if (rows_live) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int c = 32 * (2 * j + half);
+                            if (c < p.tile_n) {
+                                // (16 columns at a time: 128 running sums leave
+                                // 40 registers of the 168 a thread can have)
+#pragma unroll
+                                for (int h = 0; h < 32; h += 16) {
+                                    uint32_t v[16];
+                                    tmem_ld_32x32b_x16(tbase + static_cast<uint32_t>(c + h), v);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) z[j][h + i] += __uint_as_float(v[i]);
+                                }
+                            }
+                        }
+                    }
+                    release();
+                }
+                if (!got) break;
+                if (!rows_live) continue;
+                const float inf = __int_as_float(0x7f800000);
+                const int64_t tgt = row < p.M ? p.target[row] - p.col0 : -1;
+                float m = -inf, s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = n0 + 32 * (2 * j + half);
+                    if (c >= col_end) continue;
+                    if (c + 32 > col_end) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i >= col_end) z[j][i] = -inf;
+                    }
+                    const bool mine = tgt >= c && tgt < c + 32;
+                    if (__any_sync(0xffffffffu, mine)) {
+                        float zt = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (tgt == c + i) zt = z[j][i];
+                        if (mine && tgt < col_end) p.z_target[row] = zt;
+                    }
+                    float top = m;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, z[j][i]);
+                    // a row of -inf so far: any finite reference gives exp(-inf) = 0
+                    const float ref = top == -inf ? 0.0f : top * kLog2e;
+                    s *= ex2(m * kLog2e - ref);
+                    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        s0 += ex2(fmaf(z[j][i], kLog2e, -ref));
+                        s1 += ex2(fmaf(z[j][i + 1], kLog2e, -ref));
+                        s2 += ex2(fmaf(z[j][i + 2], kLog2e, -ref));
+                        s3 += ex2(fmaf(z[j][i + 3], kLog2e, -ref));
+                    }
+                    s += (s0 + s1) + (s2 + s3);
+                    m = top;
+                }
+                if (row < p.M) p.stats[static_cast<int64_t>(row) * (2 * p.tiles_n) + 2 * t.tn + half] = make_float2(m, s);
+                continue;
+            }
+            if (!acquire(tbase)) break;
             if (row0 < p.M) {
                 if constexpr (EPI == kEpiStore) {
                     const float scale = p.scale ? *p.scale : 1.0f;
@@ -526,52 +648,13 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                             emit(hu, &maps.c[2], p.u_out, p.ld16, row0, c, col_end);
                         }
                     }
-                } else if constexpr (EPI == kEpiXentStats) {
-                    // running maximum m and sum s = sum exp(z - m) of this row over the tile's columns
-                    const int64_t tgt = row < p.M ? p.target[row] - p.col0 : -1;
-                    float m = -__int_as_float(0x7f800000), s = 0.0f;
-                    for (int c = n0; c < col_end; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0), v);
-                        tmem_ld_wait();
-                        if (c + 32 > col_end) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c + i >= col_end) v[i] = 0xff800000u;
-                        }
-                        const bool mine = tgt >= c && tgt < c + 32;
-                        if (__any_sync(0xffffffffu, mine)) {
-                            float z = 0.0f;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (tgt == c + i) z = __uint_as_float(v[i]);
-                            if (mine && tgt < col_end) p.z_target[row] = z;
-                        }
-                        float top = m;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-                        // a row of -inf so far: any finite reference gives exp(-inf) = 0
-                        const float ref = top == -__int_as_float(0x7f800000) ? 0.0f : top * kLog2e;
-                        s *= ex2(m * kLog2e - ref);
-                        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            s0 += ex2(fmaf(__uint_as_float(v[i]), kLog2e, -ref));
-                            s1 += ex2(fmaf(__uint_as_float(v[i + 1]), kLog2e, -ref));
-                            s2 += ex2(fmaf(__uint_as_float(v[i + 2]), kLog2e, -ref));
-                            s3 += ex2(fmaf(__uint_as_float(v[i + 3]), kLog2e, -ref));
-                        }
-                        s += (s0 + s1) + (s2 + s3);
-                        m = top;
-                    }
-                    if (row < p.M) p.stats[static_cast<int64_t>(t.tn) * p.M + row] = make_float2(m, s);
-                } else {
+                } else if constexpr (EPI == kEpiXentGrad) {
                     // D = coef (exp(z - lse) - [column = target])
                     const int64_t tgt = row < p.M ? p.target[row] - p.col0 : -1;
                     const float ref = row < p.M ? p.lse[row] * kLog2e : 0.0f;
                     const float coef = row < p.M ? p.coef[row] : 0.0f;
                     for (int c = n0; c < col_end; c += EPI_COLS) {
-                        uint32_t h[32];
+                        uint32_t h[32], lo[32];
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             uint32_t v[32];
@@ -588,21 +671,21 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                             }
                             // a row that does not count is zero whatever its logits are
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                h[16 * half + i] = pack16(coef == 0.0f ? 0.0f : coef * d[2 * i],
-                                                          coef == 0.0f ? 0.0f : coef * d[2 * i + 1], p.bf16);
+                            for (int i = 0; i < 16; ++i) {
+                                const float d0 = coef == 0.0f ? 0.0f : coef * d[2 * i];
+                                const float d1 = coef == 0.0f ? 0.0f : coef * d[2 * i + 1];
+                                const uint32_t hi = pack16(d0, d1, p.bf16);
+                                h[16 * half + i] = hi;
+                                const float2 r = unpack16(hi, p.bf16);
+                                lo[16 * half + i] = pack16(d0 - r.x, d1 - r.y, p.bf16);
+                            }
                         }
                         emit(h, &maps.c[0], p.out16[0], p.ld16, row0, c, col_end);
+                        if (p.lo_offset) emit(lo, &maps.c[1], p.out16[0] + p.lo_offset, p.ld16, row0, c, col_end);
                     }
                 }
             }
-            // this warp's reads of the accumulator are complete
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 1) mbar_arrive(bTEMPTY + 8 * b);
-                else mbar_arrive_cluster(tempty_leader + 8 * b);
-            }
+            release();
         }
         // the staging buffers must stay until the last stores have read them
         if (lane == 0) bulk_wait_group_read<0>();

@@ -19,6 +19,10 @@ struct Product {
     int segments = 1, problems = 1;
     bool gated = false, amn = false, bmn = false;
     bool may_split = false;
+    int chunk = 0;                      // K blocks per accumulator hand-over, 0: all of a unit's
+    // 2: A is a 16-bit value and its rounding remainder, M rows each (M counts
+    // both); the two halves' outputs are added
+    int halves = 1;
 };
 
 // How it runs.
@@ -42,12 +46,10 @@ inline Layout choose_layout(const Product& pr, int num_sms) {
     Layout best;
     double best_time = 1e300;
     const int64_t nkb0 = cdiv(pr.K, BK), nkb = nkb0 * pr.segments;
-    for (int cg = 1; cg <= 2; ++cg) {
+    for (int cg = 1; cg <= (pr.M > BM_CTA ? 2 : 1); ++cg) {
         for (int bn = MAX_BN; bn >= 16; bn -= 16) {
-            if (cg == 2 && bn % 128 != 0) continue;
+            if (cg == 2 && (bn % 32 != 0 || bn < 64)) continue;
             if (pr.bmn && (bn / cg) % 64 != 0) continue;
-            // widths between are used for the narrow tiles of few rows only
-            if (bn > 128 && bn % 32 != 0) continue;
             Layout l;
             l.cg = cg;
             l.bn = bn;
@@ -72,8 +74,10 @@ inline Layout choose_layout(const Product& pr, int num_sms) {
             const double copy = l.tx_bytes / 60.0, trip = 1500.0 / l.stages;
             if (copy > per_kb) per_kb = copy;
             if (trip > per_kb) per_kb = trip;
-            const int64_t most = !pr.may_split || tiles >= groups ? 1 : (groups / tiles < nkb / 4 ? groups / tiles : nkb / 4);
-            for (int64_t s = 1; s <= (most > 1 ? most : 1); ++s) {
+            // splits up to a full wave of the GPU, four K blocks each at least
+            int64_t most = !pr.may_split || tiles >= groups ? 1 : (groups / tiles < nkb / 4 ? groups / tiles : nkb / 4);
+            if (most < 1) most = 1;
+            for (int64_t s = 1; s <= most; s = s == most ? s + 1 : (2 * s < most ? 2 * s : most)) {
                 const int64_t kbps = cdiv(nkb, s), splits = cdiv(nkb, kbps);
                 const int64_t waves = cdiv(tiles * splits, groups);
                 double time = waves * (kbps * per_kb + 300.0) + 1500.0 + 4.0 * bn;
@@ -118,6 +122,7 @@ inline Params base_params(const Product& pr, const Layout& l, int type, const De
     p.splits = l.splits;
     p.kb_per_split = l.kb_per_split;
     p.total_units = p.num_tiles * l.splits;
+    p.chunk = pr.chunk ? pr.chunk : l.kb_per_split;
     p.a_rows = l.a_rows;
     p.bn = l.bn;
     p.tile_n = l.tile_n;
@@ -136,23 +141,26 @@ inline Params base_params(const Product& pr, const Layout& l, int type, const De
     return p;
 }
 
-// Encodes the operands' maps: a[i], b[i] for segment (or problem) i.
-inline bool encode_operands(Maps* maps, const Product& pr, const Layout& l, const void* const a[2], int64_t lda,
+// Encodes the operands' maps: a[2 * problem + segment], b[segment]; a null
+// entry repeats the first.
+inline bool encode_operands(Maps* maps, const Product& pr, const Layout& l, const void* const a[4], int64_t lda,
                             const void* const b[2], int64_t ldb) {
     memset(maps, 0, sizeof(*maps));
+    for (int i = 0; i < 4; ++i) {
+        if (i > 0 && !a[i]) maps->a[i] = maps->a[0];
+        else if (!operand_map(&maps->a[i], a[i], pr.amn, pr.M, pr.K, lda, l.a_rows)) return false;
+    }
+    const int b_box = pr.gated ? l.tile_n : l.bn / l.cg;
     for (int i = 0; i < 2; ++i) {
-        const void* pa = a[i] ? a[i] : a[0];
-        const void* pb = b[i] ? b[i] : b[0];
-        if (!operand_map(&maps->a[i], pa, pr.amn, pr.M, pr.K, lda, l.a_rows)) return false;
-        const int b_box = pr.gated ? l.tile_n : l.bn / l.cg;
-        if (!operand_map(&maps->b[i], pb, pr.bmn, pr.N, pr.K, ldb, b_box)) return false;
+        if (i > 0 && !b[i]) maps->b[i] = maps->b[0];
+        else if (!operand_map(&maps->b[i], b[i], pr.bmn, pr.N, pr.K, ldb, b_box)) return false;
     }
     return true;
 }
 
 // A 16-bit output's store map; false where its epilogue has to store directly.
 inline bool output_map(CUtensorMap* map, const Layout& l, const void* out, int64_t M, int64_t N, int64_t ld) {
-    if (!tma_ok(out, ld) || l.tile_n % EPI_COLS != 0) return false;
+    if (!tma_ok(out, ld) || l.tile_n < EPI_COLS) return false;
     return encode_tmap_f16_2d(map, out, N, M, ld * 2, EPI_COLS, 32);
 }
 
@@ -168,7 +176,7 @@ int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStr
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1] = pdl_attribute();
-    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.blockDim = dim3(threads_of(EPI), 1, 1);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.attrs = attr;
     int cap = capacity[info.device].load(std::memory_order_relaxed);
@@ -239,14 +247,25 @@ inline Source source_of(const void* p, int64_t rows, int64_t cols, bool repack, 
     return s;
 }
 
-// Copies the source's rows where needed; its pointer is then TMA's to read.
-int fill_source(Source* s, int64_t rows, int64_t cols, cudaStream_t stream);
+// Copies the rows of the sources that need it, in one launch (sources of
+// `cols` columns each); their pointers are then TMA's to read.
+struct Fill {
+    Source* s;
+    int64_t rows;
+};
+int fill_sources(const Fill (&f)[3], int64_t cols, cudaStream_t stream);
 
 // ---- the backward products (gemm_bwd.cu)
 
+// Few rows: up to here a 16-bit gradient that the tensor cores multiply comes
+// with its rounding remainder as a second 16-bit value, since few rows average
+// no rounding out: twice the rows (dx) or tokens (dW) of a product whose time
+// is the weights' bytes.  Both halves' rows fit one CTA's 128.
+constexpr int64_t kFewRows = 64;
+
 // fp32 values a split product's partial sums take.
 inline int64_t split_floats(const Product& pr, const Layout& l) {
-    return l.splits > 1 ? static_cast<int64_t>(l.splits) * pr.problems * pr.M * ld32_of(pr.N) : 0;
+    return l.splits > 1 || pr.halves > 1 ? static_cast<int64_t>(l.splits) * pr.problems * pr.M * ld32_of(pr.N) : 0;
 }
 
 // out = scale (acc_in + A B^T) to 16 bits at out16[problem] (rows N apart), or
@@ -258,7 +277,7 @@ struct StoreTarget {
     const float* acc_in = nullptr;
     const float* scale = nullptr;
 };
-int run_store_product(const Product& pr, const Layout& l, const void* const a[2], int64_t lda, const void* const b[2],
+int run_store_product(const Product& pr, const Layout& l, const void* const a[4], int64_t lda, const void* const b[2],
                       int64_t ldb, const StoreTarget& to, float* partial, int type, const DeviceInfo& info,
                       cudaStream_t stream);
 
@@ -288,10 +307,4 @@ bool overlaps(const Range (&in)[NI], const Range (&out)[NO]) {
 inline uint64_t bytes16(int64_t a, int64_t b) { return static_cast<uint64_t>(a) * static_cast<uint64_t>(b) * 2u; }
 
 }  // namespace fused
-
-namespace f16nt {
-// (gemm_f16_nt.cu) copies rows of K 16-bit elements to rows Kp apart
-cudaError_t launch_repack(const void* lhs, int64_t M, const void* rhs, int64_t N, int64_t K, int64_t Kw, int64_t Kp,
-                          uint16_t* da, uint16_t* db, cudaStream_t stream);
-}  // namespace f16nt
 }  // namespace pws
