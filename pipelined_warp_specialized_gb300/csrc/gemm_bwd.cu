@@ -102,82 +102,113 @@ int fill_sources(const Fill (&f)[3], int64_t cols, cudaStream_t stream) {
 
 namespace {
 
-// Joins the partial sums of a split product, in split order:
+// The partial sums of one split product.
+struct Join {
+    const float* partial;
+    int64_t stride;                 // from one split's to the next
+    int splits;
+    int N;
+    int64_t rows;                   // of all problems
+    int64_t rows_per_problem;
+    int64_t ld;
+    const float* acc_in;            // (may be acc_out)
+    float* acc_out;
+    uint16_t* out16[2];
+    const float* scale;
+};
+
+// Joins the partial sums of one or two split products, in split order:
 // sum = acc_in + p[0] + p[1] + ..., to fp32 (acc_out) or scaled to 16 bits.
-// Reads splits * 4 bytes per output; one thread sums four columns, a block
-// takes one row's next 512.  acc_in and acc_out may be the same buffer.
+// Memory bound: reads splits * 4 bytes per output.  One thread sums four
+// columns; a block takes one row's next 512.
 __global__ void __launch_bounds__(128)
-join_splits_kernel(const float* __restrict__ partial, int splits, int64_t split_stride, int64_t rows_per_problem,
-                   int N, int64_t ld, const float* acc_in, float* acc_out,
-                   uint16_t* __restrict__ out0, uint16_t* __restrict__ out1, const float* __restrict__ scale, int bf16) {
+join_splits_kernel(const __grid_constant__ Join first, const __grid_constant__ Join second, int bf16) {
     grid_dependency_wait();
     allow_dependent_launch();
-    const float f = scale ? *scale : 1.0f;
-    const int64_t row = blockIdx.x;
-    for (int64_t c = 4ll * (blockIdx.y * blockDim.x + threadIdx.x); c < ld; c += 4ll * gridDim.y * blockDim.x) {
-        const int64_t at = row * ld + c;
-        float4 v = acc_in ? *reinterpret_cast<const float4*>(acc_in + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool other = blockIdx.x >= first.rows;
+    const Join& j = other ? second : first;
+    const int64_t row = other ? blockIdx.x - first.rows : blockIdx.x;
+    const float f = j.scale ? *j.scale : 1.0f;
+    const int problem = row >= j.rows_per_problem ? 1 : 0;
+    uint16_t* out = j.out16[problem] + (row - problem * j.rows_per_problem) * j.N;
+    for (int64_t c = 4ll * (blockIdx.y * blockDim.x + threadIdx.x); c < j.ld; c += 4ll * gridDim.y * blockDim.x) {
+        const int64_t at = row * j.ld + c;
+        float4 v = j.acc_in ? *reinterpret_cast<const float4*>(j.acc_in + at) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
-            const float4 w = *reinterpret_cast<const float4*>(partial + s * split_stride + at);
+        for (int s = 0; s < j.splits; ++s) {
+            const float4 w = *reinterpret_cast<const float4*>(j.partial + s * j.stride + at);
             v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
         }
-        if (acc_out) {
-            *reinterpret_cast<float4*>(acc_out + at) = v;
+        if (j.acc_out) {
+            *reinterpret_cast<float4*>(j.acc_out + at) = v;
             continue;
         }
-        const bool second = row >= rows_per_problem;
-        uint16_t* dst = (second ? out1 + (row - rows_per_problem) * N : out0 + row * N) + c;
+        uint16_t* dst = out + c;
         const uint32_t lo = pack16(f * v.x, f * v.y, bf16), hi = pack16(f * v.z, f * v.w, bf16);
-        if (c + 4 <= N && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
+        if (c + 4 <= j.N && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
             *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
         } else {
             dst[0] = static_cast<uint16_t>(lo & 0xFFFFu);
-            if (c + 1 < N) dst[1] = static_cast<uint16_t>(lo >> 16);
-            if (c + 2 < N) dst[2] = static_cast<uint16_t>(hi & 0xFFFFu);
-            if (c + 3 < N) dst[3] = static_cast<uint16_t>(hi >> 16);
+            if (c + 1 < j.N) dst[1] = static_cast<uint16_t>(lo >> 16);
+            if (c + 2 < j.N) dst[2] = static_cast<uint16_t>(hi & 0xFFFFu);
+            if (c + 3 < j.N) dst[3] = static_cast<uint16_t>(hi >> 16);
         }
     }
 }
 
 }  // namespace
 
-int run_store_product(const Product& pr, const Layout& l, const void* const a[4], int64_t lda, const void* const b[2],
-                      int64_t ldb, const StoreTarget& to, float* partial, int type, const DeviceInfo& info,
-                      cudaStream_t stream) {
+int run_store_products(const StoreProduct* sp, int n, const Layout& l, int type, const DeviceInfo& info,
+                       cudaStream_t stream) {
     Maps maps;
-    if (!encode_operands(&maps, pr, l, a, lda, b, ldb)) return GEMM_ERR_LAUNCH;
-    Params p = base_params(pr, l, type, info, stream);
-    p.ld32 = ld32_of(pr.N);
-    const bool split = l.splits > 1 || pr.halves > 1;
-    if (split) {
-        p.out32 = partial;
-        p.problem_stride = pr.M * p.ld32;
-        p.split_stride = p.problem_stride * pr.problems;
-    } else {
-        p.out32 = to.acc_out;
-        p.acc_in = to.acc_in;
-        p.scale = to.scale;
-        p.ld16 = pr.N;
-        p.tma_store = to.out16[0] != nullptr;
-        for (int i = 0; i < pr.problems; ++i) {
-            p.out16[i] = static_cast<uint16_t*>(to.out16[i]);
-            if (p.tma_store && !output_map(&maps.c[i], l, to.out16[i], pr.M, pr.N, pr.N)) p.tma_store = 0;
+    memset(&maps, 0, sizeof(maps));
+    Params p = base_params(l, type, info, stream);
+    Join join[2] = {};
+    int joins = 0;
+    for (int at = 0; at < n; ++at) {
+        const int which = n == 2 ? (at ? 1 - l.first : l.first) : 0;
+        const StoreProduct& s = sp[which];
+        const Layout::Part& part = l.part[which];
+        if (!set_job(&p, &maps, at, s.pr, l, part, s.op)) return GEMM_ERR_LAUNCH;
+        Job& j = p.job[at];
+        j.ld32 = ld32_of(s.pr.N);
+        if (part.splits > 1 || s.pr.halves > 1) {
+            j.out32 = s.partial;
+            j.problem_stride = s.pr.M * j.ld32;
+            j.split_stride = j.problem_stride * s.pr.problems;
+            // (halves: the partial sums of a split's two halves lie one after the other)
+            Join& q = join[joins++];
+            q.partial = s.partial;
+            q.stride = j.split_stride / s.pr.halves;
+            q.splits = part.splits * s.pr.halves;
+            q.N = j.N;
+            q.rows_per_problem = s.pr.M / s.pr.halves;
+            q.rows = q.rows_per_problem * s.pr.problems;
+            q.ld = j.ld32;
+            q.acc_in = s.acc_in;
+            q.acc_out = s.acc_out;
+            for (int i = 0; i < 2; ++i) q.out16[i] = static_cast<uint16_t*>(s.out16[i]);
+            q.scale = s.scale;
+            continue;
+        }
+        j.out32 = s.acc_out;
+        j.acc_in = s.acc_in;
+        j.scale = s.scale;
+        j.ld16 = s.pr.N;
+        j.tma_store = s.out16[0] != nullptr;
+        for (int i = 0; i < s.pr.problems; ++i) {
+            j.out16[i] = static_cast<uint16_t*>(s.out16[i]);
+            if (j.tma_store && !output_map(&maps.c[j.c_map + i], l, s.out16[i], s.pr.M, s.pr.N, s.pr.N)) j.tma_store = 0;
         }
     }
-    int rc;
-    if (pr.amn && pr.bmn) rc = launch_product<kEpiStore, true, true>(l, maps, p, info, stream);
-    else if (!pr.amn && pr.bmn) rc = launch_product<kEpiStore, false, true>(l, maps, p, info, stream);
-    else return GEMM_ERR_INVALID_ARG;
-    if (rc != GEMM_OK || !split) return rc;
-    // (halves: the partial sums of the two halves of a split lie one after the other)
-    const int64_t rows = pr.M / pr.halves * pr.problems;
-    int64_t across = cdiv(p.ld32, 4 * 128);
+    const int rc = launch_product<kEpiStore>(l, maps, p, info, stream);
+    if (rc != GEMM_OK || joins == 0) return rc;
+    const int64_t ld = join[1].ld > join[0].ld ? join[1].ld : join[0].ld;
+    int64_t across = cdiv(ld, 4 * 128);
     if (across > 65535) across = 65535;
-    if (launch_pdl(join_splits_kernel, dim3(static_cast<unsigned>(rows), static_cast<unsigned>(across)), dim3(128), 0, stream,
-                   static_cast<const float*>(partial), l.splits * pr.halves, p.split_stride / pr.halves, pr.M,
-                   static_cast<int>(pr.N), p.ld32, to.acc_in, to.acc_out, static_cast<uint16_t*>(to.out16[0]),
-                   static_cast<uint16_t*>(to.out16[1]), to.scale, p.bf16) != cudaSuccess) {
+    if (launch_pdl(join_splits_kernel, dim3(static_cast<unsigned>(join[0].rows + join[1].rows),
+                                            static_cast<unsigned>(across)),
+                   dim3(128), 0, stream, join[0], join[1], p.bf16) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
@@ -187,10 +218,10 @@ int run_store_product(const Product& pr, const Layout& l, const void* const a[4]
 namespace {
 
 struct BwdPlan {
-    Product dx, dw;
-    Layout ldx, ldw;
+    StoreProduct sp[2];             // dx and dW, those that are wanted
+    int n = 0;
+    Layout l;
     Source dy, x, w;
-    float* partial = nullptr;
     size_t bytes = 0;
 };
 
@@ -199,19 +230,27 @@ BwdPlan plan_bwd(int64_t M, int64_t N, int64_t K, const void* dy, const void* x,
     BwdPlan pl;
     Carver c;
     c.base = static_cast<char*>(ws);
-    pl.dx.M = M; pl.dx.N = K; pl.dx.K = N;
-    pl.dx.bmn = true;
-    pl.dx.may_split = true;
-    pl.dw.M = N; pl.dw.N = K; pl.dw.K = M;
-    pl.dw.amn = pl.dw.bmn = true;
-    pl.dw.may_split = true;
+    Product pr[2];
+    if (want_dx) {
+        Product& d = pr[pl.n++];
+        d.M = M; d.N = K; d.K = N;
+        d.bmn = true;
+        d.may_split = true;
+    }
+    if (want_dw) {
+        Product& d = pr[pl.n++];
+        d.M = N; d.N = K; d.K = M;
+        d.amn = d.bmn = true;
+        d.may_split = true;
+    }
     pl.dy = source_of(dy, M, N, !tma_ok(dy, N), &c);
     pl.x = source_of(x, M, K, want_dw && !tma_ok(x, K), &c);
     pl.w = source_of(w, N, K, want_dx && !tma_ok(w, K), &c);
-    pl.ldx = choose_layout(pl.dx, num_sms);
-    pl.ldw = choose_layout(pl.dw, num_sms);
-    const int64_t fx = want_dx ? split_floats(pl.dx, pl.ldx) : 0, fw = want_dw ? split_floats(pl.dw, pl.ldw) : 0;
-    pl.partial = c.take<float>(fx > fw ? fx : fw);
+    pl.l = choose_layout(pr, pl.n, num_sms);
+    for (int i = 0; i < pl.n; ++i) {
+        pl.sp[i].pr = pr[i];
+        pl.sp[i].partial = c.take<float>(split_floats(pr[i], pl.l.part[i]));
+    }
     pl.bytes = c.used;
     return pl;
 }
@@ -239,10 +278,16 @@ extern "C" int gemm_nt_bwd_workspace(int64_t M, int64_t N, int64_t K, const void
     const int rc = check_bwd(M, N, K, dy, x, w, nullptr, nullptr, type);
     if (rc != GEMM_OK) return rc;
     if (!bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = M && N && K
-                 ? static_cast<int64_t>(
-                       plan_bwd(M, N, K, dy, x, w, true, true, pws::sm_count_or_default(), nullptr).bytes)
-                 : 0;
+    *bytes = 0;
+    if (M && N && K) {
+        // one gradient alone may be split further than the two together
+        const int sms = pws::sm_count_or_default();
+        for (int want = 1; want <= 3; ++want) {
+            const int64_t b =
+                static_cast<int64_t>(plan_bwd(M, N, K, dy, x, w, want & 1, want & 2, sms, nullptr).bytes);
+            if (b > *bytes) *bytes = b;
+        }
+    }
     return GEMM_OK;
 }
 
@@ -268,20 +313,14 @@ extern "C" int gemm_nt_bwd(int64_t M, int64_t N, int64_t K, const void* dy, cons
         return GEMM_ERR_INVALID_ARG;
     if ((rc = fill_sources({{&pl.dy, M}, {}, {}}, N, stream)) != GEMM_OK) return rc;
     if ((rc = fill_sources({{&pl.x, M}, {&pl.w, N}, {}}, K, stream)) != GEMM_OK) return rc;
-    if (dx) {
-        const void* a[4] = {pl.dy.ptr};
-        const void* b[2] = {pl.w.ptr, nullptr};
-        StoreTarget to;
-        to.out16[0] = dx;
-        rc = run_store_product(pl.dx, pl.ldx, a, pl.dy.ld, b, pl.w.ld, to, pl.partial, type, info, stream);
-        if (rc != GEMM_OK) return rc;
+    for (int i = 0; i < pl.n; ++i) {
+        StoreProduct& s = pl.sp[i];
+        const Source& b = s.pr.amn ? pl.x : pl.w;
+        s.op.a[0] = pl.dy.ptr;
+        s.op.lda = pl.dy.ld;
+        s.op.b[0] = b.ptr;
+        s.op.ldb = b.ld;
+        s.out16[0] = s.pr.amn ? dw : dx;
     }
-    if (dw) {
-        const void* a[4] = {pl.dy.ptr};
-        const void* b[2] = {pl.x.ptr, nullptr};
-        StoreTarget to;
-        to.out16[0] = dw;
-        rc = run_store_product(pl.dw, pl.ldw, a, pl.dy.ld, b, pl.x.ld, to, pl.partial, type, info, stream);
-    }
-    return rc;
+    return run_store_products(pl.sp, pl.n, pl.l, type, info, stream);
 }

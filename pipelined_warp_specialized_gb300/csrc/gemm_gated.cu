@@ -136,13 +136,13 @@ int check_gated_bwd(int64_t M, int64_t F, int64_t K, const void* dh, const void*
 }
 
 struct GatedBwdPlan {
-    Product dx, dw;
-    Layout ldx, ldw;
+    StoreProduct sp[2];             // dx and dW, those that are wanted
+    int n = 0;
+    Layout l;
     Source x, wg, wu;
     uint16_t* dg = nullptr;
     uint16_t* du = nullptr;
     int64_t ldf = 0, lo_offset = 0;
-    float* partial = nullptr;
     size_t bytes = 0;
 };
 
@@ -156,26 +156,35 @@ GatedBwdPlan plan_gated_bwd(int64_t M, int64_t F, int64_t K, const void* x, cons
     pl.lo_offset = halves == 2 ? M * pl.ldf : 0;
     pl.dg = c.take<uint16_t>(halves * M * pl.ldf);
     pl.du = c.take<uint16_t>(halves * M * pl.ldf);
-    // dx: the gate's F and the up projection's F are two segments of K; the
-    // remainders are M more rows
-    pl.dx.M = halves * M; pl.dx.N = K; pl.dx.K = F;
-    pl.dx.halves = halves;
-    pl.dx.segments = 2;
-    pl.dx.bmn = true;
-    pl.dx.may_split = true;
-    pl.dw.M = F; pl.dw.N = K; pl.dw.K = M;
-    pl.dw.problems = 2;
-    pl.dw.segments = halves;        // dW: the remainders are M more tokens
-    pl.dw.amn = pl.dw.bmn = true;
-    pl.dw.may_split = true;
+    Product pr[2];
+    if (want_dx) {
+        // the gate's F and the up projection's F are two segments of K; the
+        // remainders are M more rows
+        Product& d = pr[pl.n++];
+        d.M = halves * M; d.N = K; d.K = F;
+        d.halves = halves;
+        d.segments = 2;
+        d.bmn = true;
+        d.may_split = true;
+    }
+    if (want_dw) {
+        // the remainders are M more tokens
+        Product& d = pr[pl.n++];
+        d.M = F; d.N = K; d.K = M;
+        d.problems = 2;
+        d.segments = halves;
+        d.amn = d.bmn = true;
+        d.may_split = true;
+    }
     pl.x = source_of(x, M, K, want_dw && !tma_ok(x, K), &c);
     const bool rw = want_dx && (!tma_ok(wg, K) || !tma_ok(wu, K));
     pl.wg = source_of(wg, F, K, rw, &c);
     pl.wu = source_of(wu, F, K, rw, &c);
-    pl.ldx = choose_layout(pl.dx, num_sms);
-    pl.ldw = choose_layout(pl.dw, num_sms);
-    const int64_t fx = want_dx ? split_floats(pl.dx, pl.ldx) : 0, fw = want_dw ? split_floats(pl.dw, pl.ldw) : 0;
-    pl.partial = c.take<float>(fx > fw ? fx : fw);
+    pl.l = choose_layout(pr, pl.n, num_sms);
+    for (int i = 0; i < pl.n; ++i) {
+        pl.sp[i].pr = pr[i];
+        pl.sp[i].partial = c.take<float>(split_floats(pr[i], pl.l.part[i]));
+    }
     pl.bytes = c.used;
     return pl;
 }
@@ -223,18 +232,24 @@ extern "C" int gemm_gated_nt(int64_t M, int64_t F, int64_t K, const void* x, con
         return GEMM_ERR_INVALID_ARG;
     if ((rc = fill_sources({{&pl.x, M}, {&pl.wg, F}, {&pl.wu, F}}, K, stream)) != GEMM_OK) return rc;
     Maps maps;
-    const void* a[4] = {pl.x.ptr};
-    const void* b[2] = {pl.wg.ptr, pl.wu.ptr};
-    if (!encode_operands(&maps, pl.pr, pl.l, a, pl.x.ld, b, pl.wg.ld)) return GEMM_ERR_LAUNCH;
-    Params p = base_params(pl.pr, pl.l, type, info, stream);
+    memset(&maps, 0, sizeof(maps));
+    Params p = base_params(pl.l, type, info, stream);
+    Operands op;
+    op.a[0] = pl.x.ptr;
+    op.lda = pl.x.ld;
+    op.b[0] = pl.wg.ptr;
+    op.b[1] = pl.wu.ptr;
+    op.ldb = pl.wg.ld;
+    if (!set_job(&p, &maps, 0, pl.pr, pl.l, pl.l.part[0], op)) return GEMM_ERR_LAUNCH;
     p.act = act;
-    p.ld16 = F;
-    p.out16[0] = static_cast<uint16_t*>(h);
+    Job& j = p.job[0];
+    j.ld16 = F;
+    j.out16[0] = static_cast<uint16_t*>(h);
     p.g_out = static_cast<uint16_t*>(g);
     p.u_out = static_cast<uint16_t*>(u);
-    p.tma_store = output_map(&maps.c[0], pl.l, h, M, F, F) &&
+    j.tma_store = output_map(&maps.c[0], pl.l, h, M, F, F) &&
                   (!g || (output_map(&maps.c[1], pl.l, g, M, F, F) && output_map(&maps.c[2], pl.l, u, M, F, F)));
-    return launch_product<kEpiGated, false, false>(pl.l, maps, p, info, stream);
+    return launch_product<kEpiGated>(pl.l, maps, p, info, stream);
 }
 
 extern "C" int gemm_gated_nt_bwd_workspace(int64_t M, int64_t F, int64_t K, const void* dh, const void* g,
@@ -244,10 +259,16 @@ extern "C" int gemm_gated_nt_bwd_workspace(int64_t M, int64_t F, int64_t K, cons
     const int rc = check_gated_bwd(M, F, K, dh, g, u, x, w_gate, w_up, nullptr, nullptr, nullptr, type, GEMM_ACT_SILU);
     if (rc != GEMM_OK) return rc;
     if (!bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = M && F && K ? static_cast<int64_t>(plan_gated_bwd(M, F, K, x, w_gate, w_up, true, true,
-                                                               pws::sm_count_or_default(), nullptr)
-                                                    .bytes)
-                         : 0;
+    *bytes = 0;
+    if (M && F && K) {
+        // one side's gradients alone may be split further than all together
+        const int sms = pws::sm_count_or_default();
+        for (int want = 1; want <= 3; ++want) {
+            const int64_t b = static_cast<int64_t>(
+                plan_gated_bwd(M, F, K, x, w_gate, w_up, want & 1, want & 2, sms, nullptr).bytes);
+            if (b > *bytes) *bytes = b;
+        }
+    }
     return GEMM_OK;
 }
 
@@ -287,21 +308,26 @@ extern "C" int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh
             return GEMM_ERR_LAUNCH;
         }
     }
-    if (dx) {
-        const void* d[4] = {pl.dg, pl.du};
-        const void* b[2] = {pl.wg.ptr, pl.wu.ptr};
-        StoreTarget to;
-        to.out16[0] = dx;
-        rc = run_store_product(pl.dx, pl.ldx, d, pl.ldf, b, pl.wg.ld, to, pl.partial, type, info, stream);
-        if (rc != GEMM_OK) return rc;
+    for (int i = 0; i < pl.n; ++i) {
+        StoreProduct& q = pl.sp[i];
+        q.op.lda = pl.ldf;
+        if (q.pr.amn) {
+            q.op.a[0] = pl.dg;
+            q.op.a[1] = pl.dg + pl.lo_offset;
+            q.op.a[2] = pl.du;
+            q.op.a[3] = pl.du + pl.lo_offset;
+            q.op.b[0] = pl.x.ptr;
+            q.op.ldb = pl.x.ld;
+            q.out16[0] = dw_gate;
+            q.out16[1] = dw_up;
+        } else {
+            q.op.a[0] = pl.dg;
+            q.op.a[1] = pl.du;
+            q.op.b[0] = pl.wg.ptr;
+            q.op.b[1] = pl.wu.ptr;
+            q.op.ldb = pl.wg.ld;
+            q.out16[0] = dx;
+        }
     }
-    if (dw_gate) {
-        const void* d[4] = {pl.dg, pl.dg + pl.lo_offset, pl.du, pl.du + pl.lo_offset};
-        const void* b[2] = {pl.x.ptr, nullptr};
-        StoreTarget to;
-        to.out16[0] = dw_gate;
-        to.out16[1] = dw_up;
-        rc = run_store_product(pl.dw, pl.ldw, d, pl.ldf, b, pl.x.ld, to, pl.partial, type, info, stream);
-    }
-    return rc;
+    return run_store_products(pl.sp, pl.n, pl.l, type, info, stream);
 }

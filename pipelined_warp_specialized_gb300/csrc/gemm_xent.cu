@@ -117,11 +117,10 @@ XentPlan plan_xent(int64_t M, int64_t V, int64_t K, const void* x, const void* w
     Carver c;
     c.base = static_cast<char*>(ws);
     pl.pr.M = M; pl.pr.N = V; pl.pr.K = K;
-    pl.pr.chunk = kStatsChunk;
     pl.l = choose_layout(pl.pr, num_sms);
     pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
     pl.w = source_of(w, V, K, !tma_ok(w, K), &c);
-    pl.stats = c.take<float2>(2ll * pl.l.tiles_n * M);
+    pl.stats = c.take<float2>(2ll * pl.l.part[0].tiles_n * M);
     pl.z_target = c.take<float>(M);
     pl.bytes = c.used;
     return pl;
@@ -140,31 +139,34 @@ struct XentBwdPlan {
     float* inv_scale = nullptr;
     uint16_t* d = nullptr;
     float* acc = nullptr;
-    float* partial = nullptr;
+    float* partial[2] = {nullptr, nullptr};
     size_t bytes = 0;
 };
 
-// The three products of a piece of `v` columns.
+// The products of a piece of `v` columns: its logits, then dx and dW, those
+// that are wanted.
 Product logits_of(int64_t M, int64_t v, int64_t K) {
     Product p;
     p.M = M; p.N = v; p.K = K;
     return p;
 }
-Product dx_of(int64_t M, int64_t v, int64_t K, int halves) {
-    Product p;
-    p.M = halves * M; p.N = K; p.K = v;
-    p.halves = halves;          // the remainders are M more rows
-    p.bmn = true;
-    p.may_split = true;
-    return p;
-}
-Product dw_of(int64_t M, int64_t v, int64_t K, int halves) {
-    Product p;
-    p.M = v; p.N = K; p.K = M;
-    p.segments = halves;        // the remainders are M more tokens
-    p.amn = p.bmn = true;
-    p.may_split = true;
-    return p;
+int grads_of(int64_t M, int64_t v, int64_t K, int halves, bool want_dx, bool want_dw, Product (&pr)[2]) {
+    int n = 0;
+    if (want_dx) {
+        Product& d = pr[n++];
+        d.M = halves * M; d.N = K; d.K = v;
+        d.halves = halves;          // the remainders are M more rows
+        d.bmn = true;
+        d.may_split = true;
+    }
+    if (want_dw) {
+        Product& d = pr[n++];
+        d.M = v; d.N = K; d.K = M;
+        d.segments = halves;        // the remainders are M more tokens
+        d.amn = d.bmn = true;
+        d.may_split = true;
+    }
+    return n;
 }
 
 XentBwdPlan plan_xent_bwd(int64_t M, int64_t V, int64_t K, const void* x, const void* w, bool want_dx, bool want_dw,
@@ -178,24 +180,27 @@ XentBwdPlan plan_xent_bwd(int64_t M, int64_t V, int64_t K, const void* x, const 
     pl.piece = round_up(cdiv(V, pl.pieces), 256);
     pl.pieces = static_cast<int>(cdiv(V, pl.piece));
     pl.ldd = pl.pieces > 1 ? pl.piece : round_up(V, 64);
+    pl.halves = M <= kFewRows ? 2 : 1;
+    pl.lo_offset = pl.halves == 2 ? M * pl.ldd : 0;
     pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
     pl.w = source_of(w, V, K, !tma_ok(w, K), &c);
     pl.coef = c.take<float>(M);
     pl.inv_scale = c.take<float>(1);
-    pl.halves = M <= kFewRows ? 2 : 1;
-    pl.lo_offset = pl.halves == 2 ? M * pl.ldd : 0;
     pl.d = c.take<uint16_t>(pl.halves * M * pl.ldd);
     if (want_dx && pl.pieces > 1) pl.acc = c.take<float>(M * ld32_of(K));
-    int64_t most = 0;
-    for (int i = 0; i < 2; ++i) {          // the pieces' width, and the last one's
-        const int64_t v = i ? V - (pl.pieces - 1) * pl.piece : (pl.pieces > 1 ? pl.piece : V);
-        const Product a = dx_of(M, v, K, pl.halves), b = dw_of(M, v, K, pl.halves);
-        const int64_t fa = want_dx ? split_floats(a, choose_layout(a, num_sms)) : 0;
-        const int64_t fb = want_dw ? split_floats(b, choose_layout(b, num_sms)) : 0;
-        if (fa > most) most = fa;
-        if (fb > most) most = fb;
+    // the pieces share the space for partial sums; the last one's width differs
+    int64_t most[2] = {0, 0};
+    for (int i = 0; i < (pl.pieces > 1 ? 2 : 1); ++i) {
+        const int64_t v = i || pl.pieces == 1 ? V - (pl.pieces - 1) * pl.piece : pl.piece;
+        Product pr[2];
+        const int n = grads_of(M, v, K, pl.halves, want_dx, want_dw, pr);
+        const Layout l = choose_layout(pr, n, num_sms);
+        for (int k = 0; k < n; ++k) {
+            const int64_t f = split_floats(pr[k], l.part[k]);
+            if (f > most[k]) most[k] = f;
+        }
     }
-    pl.partial = c.take<float>(most);
+    for (int k = 0; k < 2; ++k) pl.partial[k] = c.take<float>(most[k]);
     pl.bytes = c.used;
     return pl;
 }
@@ -240,19 +245,24 @@ extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, cons
             return GEMM_ERR_INVALID_ARG;
         if ((rc = fill_sources({{&pl.x, M}, {&pl.w, V}, {}}, K, stream)) != GEMM_OK) return rc;
         Maps maps;
-        const void* a[4] = {pl.x.ptr};
-        const void* b[2] = {pl.w.ptr, nullptr};
-        if (!encode_operands(&maps, pl.pr, pl.l, a, pl.x.ld, b, pl.w.ld)) return GEMM_ERR_LAUNCH;
-        Params p = base_params(pl.pr, pl.l, type, info, stream);
+        memset(&maps, 0, sizeof(maps));
+        Params p = base_params(pl.l, type, info, stream);
+        Operands op;
+        op.a[0] = pl.x.ptr;
+        op.lda = pl.x.ld;
+        op.b[0] = pl.w.ptr;
+        op.ldb = pl.w.ld;
+        if (!set_job(&p, &maps, 0, pl.pr, pl.l, pl.l.part[0], op)) return GEMM_ERR_LAUNCH;
+        p.chunk = kStatsChunk;
         p.target = target;
         p.stats = pl.stats;
         p.z_target = pl.z_target;
-        rc = launch_product<kEpiXentStats, false, false>(pl.l, maps, p, info, stream);
+        rc = launch_product<kEpiXentStats>(pl.l, maps, p, info, stream);
         if (rc != GEMM_OK) return rc;
     }
     if (launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>(cdiv(M, 8))), dim3(256), 0, stream,
                    static_cast<const float2*>(pl.stats), static_cast<const float*>(pl.z_target), target,
-                   static_cast<int>(M), K > 0 ? 2 * pl.l.tiles_n : 0, V, ignore_index, loss, lse) != cudaSuccess) {
+                   static_cast<int>(M), K > 0 ? 2 * pl.l.part[0].tiles_n : 0, V, ignore_index, loss, lse) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
@@ -267,9 +277,16 @@ extern "C" int gemm_xent_nt_bwd_workspace(int64_t M, int64_t V, int64_t K, const
     if (rc != GEMM_OK) return rc;
     if (too_many_tiles(M, K) || too_many_tiles(V, K)) return GEMM_ERR_INVALID_ARG;
     if (!bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = M && K ? static_cast<int64_t>(
-                          plan_xent_bwd(M, V, K, x, w, true, true, pws::sm_count_or_default(), nullptr).bytes)
-                    : 0;
+    *bytes = 0;
+    if (M && K) {
+        // one gradient alone may be split further than the two together
+        const int sms = pws::sm_count_or_default();
+        for (int want = 1; want <= 3; ++want) {
+            const int64_t b =
+                static_cast<int64_t>(plan_xent_bwd(M, V, K, x, w, want & 1, want & 2, sms, nullptr).bytes);
+            if (b > *bytes) *bytes = b;
+        }
+    }
     return GEMM_OK;
 }
 
@@ -311,48 +328,52 @@ extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, 
             const Product pr = logits_of(M, v, K);
             const Layout l = choose_layout(pr, info.num_sms);
             Maps maps;
-            const void* a[4] = {pl.x.ptr};
-            const void* b[2] = {w_piece, nullptr};
-            if (!encode_operands(&maps, pr, l, a, pl.x.ld, b, pl.w.ld)) return GEMM_ERR_LAUNCH;
-            Params p = base_params(pr, l, type, info, stream);
+            memset(&maps, 0, sizeof(maps));
+            Params p = base_params(l, type, info, stream);
+            Operands op;
+            op.a[0] = pl.x.ptr;
+            op.lda = pl.x.ld;
+            op.b[0] = w_piece;
+            op.ldb = pl.w.ld;
+            if (!set_job(&p, &maps, 0, pr, l, l.part[0], op)) return GEMM_ERR_LAUNCH;
             p.target = target;
             p.lse = lse;
             p.coef = pl.coef;
             p.col0 = v0;
-            p.out16[0] = pl.d;
-            p.ld16 = pl.ldd;
             p.lo_offset = pl.lo_offset;
-            p.tma_store = output_map(&maps.c[0], l, pl.d, M, v, pl.ldd) &&
+            Job& j = p.job[0];
+            j.out16[0] = pl.d;
+            j.ld16 = pl.ldd;
+            j.tma_store = output_map(&maps.c[0], l, pl.d, M, v, pl.ldd) &&
                           (!pl.lo_offset || output_map(&maps.c[1], l, pl.d + pl.lo_offset, M, v, pl.ldd));
-            if ((rc = launch_product<kEpiXentGrad, false, false>(l, maps, p, info, stream)) != GEMM_OK) return rc;
+            if ((rc = launch_product<kEpiXentGrad>(l, maps, p, info, stream)) != GEMM_OK) return rc;
         }
-        if (dx) {
-            const void* a[4] = {pl.d};
-            const Product pr = dx_of(M, v, K, pl.halves);
-            const void* b[2] = {w_piece, nullptr};
-            StoreTarget to;
-            to.acc_in = i ? pl.acc : nullptr;
-            if (i + 1 < pl.pieces) {
-                to.acc_out = pl.acc;
+        Product pr[2];
+        StoreProduct sp[2];
+        const int n = grads_of(M, v, K, pl.halves, dx != nullptr, dw != nullptr, pr);
+        for (int k = 0; k < n; ++k) {
+            StoreProduct& q = sp[k];
+            q.pr = pr[k];
+            q.partial = pl.partial[k];
+            q.scale = pl.inv_scale;
+            q.op.a[0] = pl.d;
+            q.op.lda = pl.ldd;
+            if (q.pr.amn) {
+                q.op.a[1] = pl.d + pl.lo_offset;
+                q.op.b[0] = pl.x.ptr;
+                q.op.ldb = pl.x.ld;
+                q.out16[0] = static_cast<uint16_t*>(dw) + v0 * K;
             } else {
-                to.out16[0] = dx;
-                to.scale = pl.inv_scale;
+                q.op.b[0] = w_piece;
+                q.op.ldb = pl.w.ld;
+                // dx is summed over the pieces in fp32 and rounded by the last one
+                q.acc_in = i ? pl.acc : nullptr;
+                if (i + 1 < pl.pieces) q.acc_out = pl.acc;
+                else q.out16[0] = dx;
             }
-            rc = run_store_product(pr, choose_layout(pr, info.num_sms), a, pl.ldd, b, pl.w.ld, to, pl.partial, type,
-                                   info, stream);
-            if (rc != GEMM_OK) return rc;
         }
-        if (dw) {
-            const void* a[4] = {pl.d, pl.d + pl.lo_offset};
-            const Product pr = dw_of(M, v, K, pl.halves);
-            const void* b[2] = {pl.x.ptr, nullptr};
-            StoreTarget to;
-            to.out16[0] = static_cast<uint16_t*>(dw) + v0 * K;
-            to.scale = pl.inv_scale;
-            rc = run_store_product(pr, choose_layout(pr, info.num_sms), a, pl.ldd, b, pl.x.ld, to, pl.partial, type,
-                                   info, stream);
-            if (rc != GEMM_OK) return rc;
-        }
+        rc = run_store_products(sp, n, choose_layout(pr, n, info.num_sms), type, info, stream);
+        if (rc != GEMM_OK) return rc;
     }
     return GEMM_OK;
 }

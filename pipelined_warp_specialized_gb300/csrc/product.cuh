@@ -11,7 +11,10 @@
 //             they lie, so nothing is ever transposed in memory.
 //   segments  the K axis may run over two operand pairs, one after the other
 //             (dx = dg Wg + du Wu is one accumulation).
-//   problems  two products of one shape may share a launch (dWg and dWu).
+//   problems  two products of one shape may be one job (dWg and dWu).
+//   jobs      two products of different shapes may share a launch (dx and dW):
+//             the groups of CTAs that the first job's last wave leaves idle
+//             start on the second one's tiles.
 //   chunks    the softmax statistics sum each logit over K in chunks of
 //             kStatsChunk blocks, each chunk's tensor-memory sum added in
 //             registers (round to nearest): the tensor core's own accumulation
@@ -29,6 +32,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -72,44 +76,59 @@ constexpr int SMEM_BYTES = OFF_BAR + BAR_BYTES + 1024;      // + slack to align 
 static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory");
 static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: each owns all of tensor memory");
 
+// A wait for what is in flight before the CTA may exit outlasts any limit a
+// caller sets: copies and multiplies already issued end in microseconds.
+constexpr unsigned long long kDrainNs = 100000000ull;
+
 enum Epilogue { kEpiStore = 0, kEpiGated = 1, kEpiXentStats = 2, kEpiXentGrad = 3 };
 
-// Epilogue warps: one per tensor-memory lane quarter, or two for the softmax
-// statistics, whose running sums take 128 registers a thread.
-constexpr int epi_warps(int epi) { return epi == kEpiXentStats ? 8 : 4; }
+// Epilogue warps: two per tensor-memory lane quarter, which take the tile's
+// 64-column chunks (32-column groups for the statistics) in turn, so that the
+// epilogue of a short K loop keeps up with the multiplies; one for the gated
+// block, whose three outputs take more registers than ten warps leave.
+constexpr int epi_warps(int epi) { return epi == kEpiGated ? 4 : 8; }
 constexpr int threads_of(int epi) { return (2 + epi_warps(epi)) * 32; }
 
 // K blocks per chunk of the softmax statistics' sums.
 constexpr int kStatsChunk = 8;
 
-struct Params {
-    int M, N;                       // output rows and columns (of the epilogue's output)
+// One product of a launch.
+struct Job {
+    int M, N;                       // output rows and columns
     int nkb0, nkb;                  // K blocks of the first segment, of all segments
     int tiles_m, tiles_n, num_tiles;    // tiles of one problem; num_tiles counts all problems
-    int splits, kb_per_split;
-    int chunk;                      // K blocks per accumulator hand-over (all of a unit's, but for the statistics)
-    int total_units;                // num_tiles * splits
-    int a_rows;                     // rows of a K-major A box (<= 128): fewer than 128 for few tokens
-    int bn;                         // accumulator columns per tile (a multiple of 16)
-    int tile_n;                     // output columns per tile (bn, or bn / 2 for the gated epilogue)
-    int stages, a_bytes, slot_bytes;
-    int tx_bytes;                   // bytes one CTA's copies bring per slot
-    uint32_t idesc;
-    int bf16;                       // output type
+    int kb_per_split;
+    int units;                      // num_tiles * splits
+    int amn;                        // A is MN-major
+    int a_map, b_map, c_map;        // a_map + 2 * problem + segment, b_map + b_seg * segment, c_map + problem
+    int b_seg;                      // 1: each K segment has its own B; 0: one for both
     int tma_store;
-    int act;
-    unsigned long long timeout_ns;
-    unsigned* status;
-    // kEpiStore: out = scale * acc, to 16 bits (out16), or to fp32 (out32,
-    // partial sums: split s of problem i at out32 + s * split_stride +
-    // i * problem_stride), plus acc_in
+    uint32_t idesc;
+    // out = scale * acc, to 16 bits (out16), or to fp32 (out32, partial sums:
+    // split s of problem i at out32 + s * split_stride + i * problem_stride),
+    // plus acc_in
     uint16_t* out16[2];
     int64_t ld16;
     float* out32;
     const float* acc_in;
     int64_t ld32, split_stride, problem_stride;
     const float* scale;             // device scalar, or null for 1
-    // kEpiGated: h = act(gate) * up, and gate, up where g_out is not null
+};
+
+struct Params {
+    Job job[2];                     // job[1].units == 0: one job
+    int extra_rounds;               // schedule of the second job's units (Schedule)
+    int chunk;                      // K blocks per accumulator hand-over
+    int bn;                         // accumulator columns per tile (a multiple of 16)
+    int tile_n;                     // output columns per tile (bn, or bn / 2 for the gated epilogue)
+    int stages, a_bytes, slot_bytes;
+    int tx_bytes;                   // bytes one CTA's copies bring per slot
+    int bf16;                       // output type
+    int act;
+    unsigned flags;                 // GEMM_DEBUG_SKIP_EMPTY_SEED is honoured
+    unsigned long long timeout_ns;
+    unsigned* status;
+    // kEpiGated: h = act(gate) * up to out16[0], and gate, up where g_out is not null
     uint16_t* g_out;
     uint16_t* u_out;
     // cross entropy
@@ -123,7 +142,33 @@ struct Params {
 };
 
 struct Maps {
-    CUtensorMap a[4], b[2], c[3];   // a[2 * problem + segment], b[segment]
+    CUtensorMap a[6], b[3], c[3];
+};
+
+// The units a group of CTAs (of `groups`) runs, in order.  The first job's are
+// dealt round by round.  Its last round leaves groups rest .. groups - 1 with a
+// unit less, so the second job's first extra_rounds rounds go to those alone,
+// then its rounds go to all, those groups first.
+struct Schedule {
+    int group, groups, units0, units1, rest, extra;
+    int i = 0, k = 0;
+    __device__ __forceinline__ Schedule(const Params& p, int g, int n)
+        : group(g), groups(n), units0(p.job[0].units), units1(p.job[1].units), rest(p.job[0].units % n),
+          extra(p.extra_rounds) {}
+    __device__ __forceinline__ bool next(int& job, int& unit) {
+        job = 0;
+        unit = i * groups + group;
+        if (unit < units0) {
+            ++i;
+            return true;
+        }
+        job = 1;
+        const int late = group >= rest ? group - rest : group + groups - rest;
+        if (group >= rest && k < extra) unit = k * (groups - rest) + late;
+        else unit = extra * (groups - rest) + (k - (group >= rest ? extra : 0)) * groups + late;
+        ++k;
+        return unit < units1;
+    }
 };
 
 // K-major operand in the 128-byte swizzle: rows of 128 bytes, 8-row atoms
@@ -131,10 +176,9 @@ struct Maps {
 // MN-major operand: a box is 64 K rows of 128 bytes (64 elements of M or N);
 // 8 K rows form an atom, atoms 1024 bytes apart along K (stride offset), boxes
 // 8192 bytes apart along M or N (leading offset).
-template <bool MN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn) {
     uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((MN ? MN_BOX : 16) >> 4) << 16;
+    d |= static_cast<uint64_t>((mn ? MN_BOX : 16) >> 4) << 16;
     d |= static_cast<uint64_t>(1024u >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
@@ -142,32 +186,31 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
 }
 
 // (address >> 4) step of one UMMA_K: 32 bytes inside the swizzle row, or 16 K rows.
-template <bool MN>
-constexpr uint32_t k_step() { return (MN ? UMMA_K * 128 : UMMA_K * 2) >> 4; }
+__device__ __forceinline__ uint32_t k_step(bool mn) { return (mn ? UMMA_K * 128 : UMMA_K * 2) >> 4; }
 
 struct Tile {
     int problem, tm, tn, kb0, kb1, split;
 };
 
-__device__ __forceinline__ Tile tile_of(int u, const Params& p) {
+__device__ __forceinline__ Tile tile_of(int u, const Job& job) {
     Tile t;
-    t.split = u / p.num_tiles;
-    int r = u - t.split * p.num_tiles;
-    const int per = p.tiles_m * p.tiles_n;
+    t.split = u / job.num_tiles;
+    int r = u - t.split * job.num_tiles;
+    const int per = job.tiles_m * job.tiles_n;
     t.problem = r / per;
     r -= t.problem * per;
     // tile rows are walked GROUP_M at a time and odd groups right to left, so
     // the CTAs at work share A and B strips in L2
-    const int group = GROUP_M * p.tiles_n;
+    const int group = GROUP_M * job.tiles_n;
     const int g = r / group;
     const int first = g * GROUP_M;
-    const int rows = min(p.tiles_m - first, GROUP_M);
+    const int rows = min(job.tiles_m - first, GROUP_M);
     const int v = r - g * group;
     t.tm = first + v % rows;
     t.tn = v / rows;
-    if (g & 1) t.tn = p.tiles_n - 1 - t.tn;
-    t.kb0 = t.split * p.kb_per_split;
-    t.kb1 = min(p.nkb, t.kb0 + p.kb_per_split);
+    if (g & 1) t.tn = job.tiles_n - 1 - t.tn;
+    t.kb0 = t.split * job.kb_per_split;
+    t.kb1 = min(job.nkb, t.kb0 + job.kb_per_split);
     return t;
 }
 
@@ -215,9 +258,13 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-template <int CG, int EPI, bool AMN, bool BMN>
+// kEpiStore serves the backward products, whose B is MN-major; the others are
+// forward (NT) products.
+template <int CG, int EPI>
 __global__ void __launch_bounds__(threads_of(EPI), 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    constexpr bool BMN = EPI == kEpiStore;
+    constexpr int EW = epi_warps(EPI);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;       // swizzle atoms are 1024-byte aligned
@@ -241,7 +288,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bTFULL + 8 * b, 1);
-            mbar_init(bTEMPTY + 8 * b, epi_warps(EPI) * CG);
+            mbar_init(bTEMPTY + 8 * b, EW * CG);
         }
         mbar_init(bDRAIN, 1);
         *abort_flag = 0u;
@@ -278,19 +325,21 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 if constexpr (CG == 1) tma_load_2d(dst, map, x, y, bar);
                 else tma_load_2d_pair(dst, map, x, y, bar);
             };
-            for (int u = group_id; ok && u < p.total_units; u += num_groups) {
-                const Tile t = tile_of(u, p);
+            Schedule sched(p, group_id, num_groups);
+            for (int jn, u; ok && sched.next(jn, u);) {
+                const Job& job = p.job[jn];
+                const Tile t = tile_of(u, job);
                 const int m_cta = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA;
                 const int b_rows = p.bn / CG;                    // B rows (accumulator columns) of this CTA
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!W.wait(bEMPTY + 8 * stage, phase)) { ok = false; break; }
                     const uint32_t a_dst = base + stage * p.slot_bytes, b_dst = a_dst + p.a_bytes;
                     const uint32_t bar = full_leader + 8 * stage;
-                    const int seg = kb >= p.nkb0 ? 1 : 0;
-                    const int k = (kb - (seg ? p.nkb0 : 0)) * BK;
-                    const CUtensorMap* ma = &maps.a[2 * t.problem + seg];
+                    const int seg = kb >= job.nkb0 ? 1 : 0;
+                    const int k = (kb - (seg ? job.nkb0 : 0)) * BK;
+                    const CUtensorMap* ma = &maps.a[job.a_map + 2 * t.problem + seg];
                     if (leader) mbar_arrive_expect_tx(bFULL + 8 * stage, CG * p.tx_bytes);
-                    if constexpr (AMN) {
+                    if (BMN && job.amn) {
                         load(a_dst, ma, m_cta, k, bar);
                         load(a_dst + MN_BOX, ma, m_cta + 64, k, bar);
                     } else {
@@ -307,7 +356,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                         }
                     } else {
                         const int n = t.tn * p.tile_n + static_cast<int>(rank) * b_rows;
-                        const CUtensorMap* mb = &maps.b[seg];
+                        const CUtensorMap* mb = &maps.b[job.b_map + job.b_seg * seg];
                         if constexpr (BMN) {
                             for (int j = 0; j < b_rows; j += 64) load(b_dst + j * (MN_BOX / 64), mb, n + j, k, bar);
                         } else {
@@ -322,7 +371,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             if (!ok && leader) {
                 // drain: wait (bounded) for the copies still in flight into this CTA
                 volatile uint32_t no_abort = 0;
-                const Waiter D{p.timeout_ns, &no_abort, p.status, kStatusRoleProducer};
+                const Waiter D{max(p.timeout_ns, kDrainNs), &no_abort, p.status, kStatusRoleProducer};
                 const uint32_t first = issued > S ? issued - S : 0u;
                 for (uint32_t it = first; it < issued; ++it)
                     if (!D.wait(bFULL + 8 * (it % S), (it / S) & 1u)) break;
@@ -336,40 +385,55 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
         __syncwarp();
     } else if (warp == 1) {
         // ======================================================== MMA issuer
-        if (lane == 0)
+        if (lane == 0 && !(p.flags & GEMM_DEBUG_SKIP_EMPTY_SEED))
             for (uint32_t s = 0; s < S; ++s) mbar_arrive(bEMPTY + 8 * s);      // every slot starts empty
         if (leader && lane == 0) {
             const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleMma};
             // descriptors of slot s: slot 0's plus s slots (addresses lie below
             // 256 KB, so the 14-bit address field never carries)
-            const uint64_t adesc0 = operand_desc<AMN>(base), bdesc0 = operand_desc<BMN>(base + p.a_bytes);
+            const uint64_t bdesc0 = operand_desc(base + p.a_bytes, BMN);
             const uint32_t slot16 = static_cast<uint32_t>(p.slot_bytes) >> 4;
             uint32_t stage = 0, phase = 0, tcount = 0;
             bool ok = true, issued_any = false;
-            for (int u = group_id; ok && u < p.total_units; u += num_groups) {
-                const Tile t = tile_of(u, p);
-                for (int c0 = t.kb0; ok && c0 < t.kb1; c0 += p.chunk, ++tcount) {
+            // One unit's multiplies.  The A operand's form is a compile-time
+            // constant: the issuing thread's own instructions between
+            // multiplies idle the tensor pipe (descriptor steps computed at
+            // run time cost 14 % at 8192 x 4096 x 8192).
+            auto unit = [&](const Tile& t, uint32_t idesc, auto a_mn) {
+                constexpr bool AMN = decltype(a_mn)::value;
+                const uint64_t adesc0 = operand_desc(base, AMN);
+                for (int c0 = t.kb0; c0 < t.kb1; c0 += p.chunk, ++tcount) {
                     const int c1 = min(t.kb1, c0 + p.chunk);
                     const uint32_t b = tcount & 1u, aph = (tcount >> 1) & 1u;
-                    if (!W.template wait<CG == 2>(bTEMPTY + 8 * b, aph)) { ok = false; break; }
+                    if (!W.template wait<CG == 2>(bTEMPTY + 8 * b, aph)) return false;
                     tc_fence_after_sync();
                     const uint32_t d_tmem = tmem_base + b * MAX_BN;
                     for (int kb = c0; kb < c1; ++kb) {
-                        if (!W.wait(bFULL + 8 * stage, phase)) { ok = false; break; }
+                        if (!W.wait(bFULL + 8 * stage, phase)) return false;
                         tc_fence_after_sync();
                         const uint64_t ad = adesc0 + stage * slot16, bd = bdesc0 + stage * slot16;
 #pragma unroll
                         for (int k = 0; k < BK / UMMA_K; ++k)
-                            tc_mma_f16<CG>(d_tmem, ad + k * k_step<AMN>(), bd + k * k_step<BMN>(), p.idesc,
+                            tc_mma_f16<CG>(d_tmem, ad + k * k_step(AMN), bd + k * k_step(BMN), idesc,
                                            kb != c0 || k != 0);
                         issued_any = true;
                         if constexpr (CG == 1) tc_commit_1(bEMPTY + 8 * stage);
                         else tc_commit_2_mc(bEMPTY + 8 * stage, 0x3);
                         if (++stage == S) { stage = 0; phase ^= 1u; }
                     }
-                    if (!ok) break;
                     if constexpr (CG == 1) tc_commit_1(bTFULL + 8 * b);
                     else tc_commit_2_mc(bTFULL + 8 * b, 0x3);
+                }
+                return true;
+            };
+            Schedule sched(p, group_id, num_groups);
+            for (int jn, u; ok && sched.next(jn, u);) {
+                const Job& job = p.job[jn];
+                const Tile t = tile_of(u, job);
+                if constexpr (BMN) {
+                    ok = job.amn ? unit(t, job.idesc, std::true_type{}) : unit(t, job.idesc, std::false_type{});
+                } else {
+                    ok = unit(t, job.idesc, std::false_type{});
                 }
             }
             if (issued_any) {
@@ -377,7 +441,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 if constexpr (CG == 1) tc_commit_1(bDRAIN);
                 else tc_commit_2_mc(bDRAIN, 0x1);
                 volatile uint32_t no_abort = 0;
-                const Waiter D{p.timeout_ns, &no_abort, p.status, kStatusRoleMma};
+                const Waiter D{max(p.timeout_ns, kDrainNs), &no_abort, p.status, kStatusRoleMma};
                 D.wait(bDRAIN, 0);
             }
         }
@@ -393,43 +457,26 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 if constexpr (CG == 1) mbar_arrive(bTEMPTY + 8 * b);
                 else mbar_arrive_cluster(tempty_leader + 8 * b);
             }
-        const uint32_t bufs = base + OFF_EPI + static_cast<uint32_t>(e) * 2 * EPI_BUF;
+        constexpr int NBUF = 8 / EW;             // staging buffers of a warp
+        const uint32_t bufs = base + OFF_EPI + static_cast<uint32_t>(e) * NBUF * EPI_BUF;
+        // with two warps per lane quarter, the chunks whose number is 1 mod 2 are the second one's
+        const int first_chunk = EW == 8 ? (e >> 2) * EPI_COLS : 0;
+        constexpr int CHUNK_STEP = EW == 8 ? 2 * EPI_COLS : EPI_COLS;
         uint32_t nbuf = 0;
         int tile_end = 0;                        // the tile's last column + 1, past N or not
         // One 64-column chunk (this lane's row, 32 packed pairs) of a 16-bit
         // output: staged in the swizzle its tensor map uses and stored by TMA
         // (the staging buffers in turn), or, where TMA cannot address the
         // output or the tile ends inside the chunk, staged and stored by the warp.
-        auto emit = [&](const uint32_t(&h)[32], const CUtensorMap* map, uint16_t* out, int64_t ld, int row0, int col0,
-                        int col_end) {
-            if (p.tma_store && col0 + EPI_COLS <= tile_end) {
-                const uint32_t buf = bufs + (nbuf & 1u) * EPI_BUF;
-                ++nbuf;
-                if (lane == 0) bulk_wait_group_read<1>();
-                __syncwarp();
-                const uint32_t row_addr = buf + static_cast<uint32_t>(lane) * 128;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t dst = row_addr + ((static_cast<uint32_t>(j) ^ static_cast<uint32_t>(lane & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[4 * j]),
-                                 "r"(h[4 * j + 1]), "r"(h[4 * j + 2]), "r"(h[4 * j + 3])
-                                 : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (row0 < p.M && col0 < p.N) tma_store_2d(map, buf, col0, row0);
-                    bulk_commit_group();
-                }
-                return;
-            }
-            // The lane's row goes through the staging buffer, so that the warp
-            // then writes one row at a time, consecutive lanes at consecutive
-            // addresses (rows of any alignment; a lane storing its own row's
-            // elements touches 32 lines an instruction: measured slower).
-            const uint32_t row_addr = bufs + static_cast<uint32_t>(lane) * 128;
-            if (p.tma_store && lane == 0) bulk_wait_group_read<0>();
+        auto emit = [&](const uint32_t(&h)[32], const Job& job, const CUtensorMap* map, uint16_t* out, int row0,
+                        int col0, int col_end) {
+            const bool by_tma = job.tma_store && col0 + EPI_COLS <= tile_end;
+            const uint32_t buf = bufs + (nbuf % NBUF) * EPI_BUF;
+            ++nbuf;
+            // the store issued from this buffer has finished reading it
+            if (lane == 0) bulk_wait_group_read<NBUF - 1>();
             __syncwarp();
+            const uint32_t row_addr = buf + static_cast<uint32_t>(lane) * 128;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t dst = row_addr + ((static_cast<uint32_t>(j) ^ static_cast<uint32_t>(lane & 7)) << 4);
@@ -437,22 +484,62 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                              "r"(h[4 * j + 1]), "r"(h[4 * j + 2]), "r"(h[4 * j + 3])
                              : "memory");
             }
+            if (by_tma) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (row0 < job.M && col0 < job.N) tma_store_2d(map, buf, col0, row0);
+                    bulk_commit_group();
+                }
+                return;
+            }
+            // The warp writes row by row, consecutive lanes at consecutive
+            // addresses: 16 bytes a lane and four rows at a time where rows
+            // start on 16-byte boundaries, else a 4-byte pair (or two
+            // elements) a lane.  Eight reads are in flight before the writes:
+            // one at a time, the 32 round trips of a chunk took longer than
+            // the multiplies of a K loop of 13 blocks.
             __syncwarp();
-            const int rows = min(32, p.M - row0);
-            const int col = col0 + 2 * lane;
-            const bool both = (reinterpret_cast<uintptr_t>(out) & 3u) == 0 && (ld & 1) == 0 && (col0 & 1) == 0;
-            for (int r = 0; r < rows; ++r) {
-                const uint32_t v = ld_shared_u32(bufs + static_cast<uint32_t>(r) * 128 +
-                                                 ((static_cast<uint32_t>(lane >> 2) ^ static_cast<uint32_t>(r & 7)) << 4) +
-                                                 static_cast<uint32_t>(lane & 3) * 4);
-                uint16_t* dst = out + static_cast<int64_t>(row0 + r) * ld + col;
-                if (both && col + 1 < col_end) {
-                    *reinterpret_cast<uint32_t*>(dst) = v;
-                } else {
-                    if (col < col_end) dst[0] = static_cast<uint16_t>(v & 0xFFFFu);
-                    if (col + 1 < col_end) dst[1] = static_cast<uint16_t>(v >> 16);
+            const int64_t ld = job.ld16;
+            if ((reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (ld & 7) == 0 && (col_end & 7) == 0) {
+                const int j = lane & 7, col = col0 + 8 * j;
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += 4) {
+                    const int r = r0 + (lane >> 3);
+                    uint32_t v[4];
+                    ld_shared_v4(buf + static_cast<uint32_t>(r) * 128 + (static_cast<uint32_t>(j ^ (r & 7)) << 4), v[0],
+                                 v[1], v[2], v[3]);
+                    if (row0 + r < job.M && col < col_end)
+                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + r) * ld + col) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            } else {
+                const int col = col0 + 2 * lane;
+                const bool pairs = (reinterpret_cast<uintptr_t>(out) & 3u) == 0 && (ld & 1) == 0;
+                const uint32_t in_row = static_cast<uint32_t>(lane & 3) * 4;
+                for (int r0 = 0; r0 < 32 && row0 + r0 < job.M; r0 += 8) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = ld_shared_u32(buf + static_cast<uint32_t>(r0 + i) * 128 +
+                                             (static_cast<uint32_t>((lane >> 2) ^ i) << 4) + in_row);
+                    uint16_t* dst = out + static_cast<int64_t>(row0 + r0) * ld + col;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i, dst += ld) {
+                        if (row0 + r0 + i >= job.M) break;
+                        if (pairs && col + 1 < col_end) {
+                            *reinterpret_cast<uint32_t*>(dst) = v[i];
+                        } else {
+                            if (col < col_end) dst[0] = static_cast<uint16_t>(v[i] & 0xFFFFu);
+                            if (col + 1 < col_end) dst[1] = static_cast<uint16_t>(v[i] >> 16);
+                        }
+                    }
                 }
             }
+            // (an empty group, so that "all but the last NBUF - 1 groups" is
+            // always about this buffer)
+            if (lane == 0) bulk_commit_group();
+            __syncwarp();
         };
         uint32_t tcount = 0;
         // waits for the next accumulator hand-over; its tensor-memory address
@@ -476,20 +563,22 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             }
             ++tcount;
         };
-        for (int u = group_id; u < p.total_units; u += num_groups) {
-            const Tile t = tile_of(u, p);
+        Schedule sched(p, group_id, num_groups);
+        for (int jn, u; sched.next(jn, u);) {
+            const Job& job = p.job[jn];
+            const Tile t = tile_of(u, job);
             const int row0 = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA + q * 32;
             const int row = row0 + lane;
             const int n0 = t.tn * p.tile_n;
             tile_end = n0 + p.tile_n;
-            const int col_end = min(p.N, tile_end);
+            const int col_end = min(job.N, tile_end);
             uint32_t tbase;
             if constexpr (EPI == kEpiXentStats) {
                 // This warp's 32-column groups are 2 j + half of the tile's.
                 // The logits are summed over K chunk by chunk, then reduced to
                 // the running maximum m and sum s = sum exp(z - m) of the row.
                 const int half = e >> 2;
-                const bool rows_live = row0 < p.M;
+                const bool rows_live = row0 < job.M;
                 float z[4][32];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -521,7 +610,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 if (!got) break;
                 if (!rows_live) continue;
                 const float inf = __int_as_float(0x7f800000);
-                const int64_t tgt = row < p.M ? p.target[row] - p.col0 : -1;
+                const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
                 float m = -inf, s = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -557,23 +646,23 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     s += (s0 + s1) + (s2 + s3);
                     m = top;
                 }
-                if (row < p.M) p.stats[static_cast<int64_t>(row) * (2 * p.tiles_n) + 2 * t.tn + half] = make_float2(m, s);
+                if (row < job.M) p.stats[static_cast<int64_t>(row) * (2 * job.tiles_n) + 2 * t.tn + half] = make_float2(m, s);
                 continue;
             }
             if (!acquire(tbase)) break;
-            if (row0 < p.M) {
+            if (row0 < job.M) {
                 if constexpr (EPI == kEpiStore) {
-                    const float scale = p.scale ? *p.scale : 1.0f;
-                    if (p.out32) {
+                    const float scale = job.scale ? *job.scale : 1.0f;
+                    if (job.out32) {
                         // fp32 partial or running sums
-                        float* out = p.out32 + t.split * p.split_stride + t.problem * p.problem_stride +
-                                     static_cast<int64_t>(row) * p.ld32;
-                        const float* in = p.acc_in ? p.acc_in + static_cast<int64_t>(row) * p.ld32 : nullptr;
-                        for (int c = n0; c < col_end; c += 32) {
+                        float* out = job.out32 + t.split * job.split_stride + t.problem * job.problem_stride +
+                                     static_cast<int64_t>(row) * job.ld32;
+                        const float* in = job.acc_in ? job.acc_in + static_cast<int64_t>(row) * job.ld32 : nullptr;
+                        for (int c = n0 + first_chunk / 2; c < col_end; c += CHUNK_STEP / 2) {
                             uint32_t v[32];
                             tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0), v);
                             tmem_ld_wait();
-                            if (row < p.M) {
+                            if (row < job.M) {
 #pragma unroll
                                 for (int i = 0; i < 32; i += 4) {
                                     if (c + i < col_end) {          // rows are padded to a multiple of 4
@@ -589,15 +678,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                             }
                         }
                     } else {
-                        const float* in = p.acc_in ? p.acc_in + static_cast<int64_t>(row) * p.ld32 : nullptr;
-                        for (int c = n0; c < col_end; c += EPI_COLS) {
+                        const float* in = job.acc_in ? job.acc_in + static_cast<int64_t>(row) * job.ld32 : nullptr;
+                        for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
                             uint32_t h[32];
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 uint32_t v[32];
                                 tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0 + 32 * half), v);
                                 tmem_ld_wait();
-                                if (in && row < p.M) {
+                                if (in && row < job.M) {
 #pragma unroll
                                     for (int i = 0; i < 32; i += 4) {
                                         if (c + 32 * half + i < col_end) {
@@ -614,11 +703,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                                     h[16 * half + i] = pack16(scale * __uint_as_float(v[2 * i]),
                                                               scale * __uint_as_float(v[2 * i + 1]), p.bf16);
                             }
-                            emit(h, &maps.c[t.problem], p.out16[t.problem], p.ld16, row0, c, col_end);
+                            emit(h, job, &maps.c[job.c_map + t.problem], job.out16[t.problem], row0, c, col_end);
                         }
                     }
                 } else if constexpr (EPI == kEpiGated) {
-                    for (int c = n0; c < col_end; c += EPI_COLS) {
+                    for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
                         uint32_t h[32], hg[32], hu[32];
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -642,18 +731,18 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                                 hu[16 * half + i] = pack16(u0, u1, p.bf16);
                             }
                         }
-                        emit(h, &maps.c[0], p.out16[0], p.ld16, row0, c, col_end);
+                        emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
                         if (p.g_out) {
-                            emit(hg, &maps.c[1], p.g_out, p.ld16, row0, c, col_end);
-                            emit(hu, &maps.c[2], p.u_out, p.ld16, row0, c, col_end);
+                            emit(hg, job, &maps.c[1], p.g_out, row0, c, col_end);
+                            emit(hu, job, &maps.c[2], p.u_out, row0, c, col_end);
                         }
                     }
                 } else if constexpr (EPI == kEpiXentGrad) {
                     // D = coef (exp(z - lse) - [column = target])
-                    const int64_t tgt = row < p.M ? p.target[row] - p.col0 : -1;
-                    const float ref = row < p.M ? p.lse[row] * kLog2e : 0.0f;
-                    const float coef = row < p.M ? p.coef[row] : 0.0f;
-                    for (int c = n0; c < col_end; c += EPI_COLS) {
+                    const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
+                    const float ref = row < job.M ? p.lse[row] * kLog2e : 0.0f;
+                    const float coef = row < job.M ? p.coef[row] : 0.0f;
+                    for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
                         uint32_t h[32], lo[32];
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -680,8 +769,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                                 lo[16 * half + i] = pack16(d0 - r.x, d1 - r.y, p.bf16);
                             }
                         }
-                        emit(h, &maps.c[0], p.out16[0], p.ld16, row0, c, col_end);
-                        if (p.lo_offset) emit(lo, &maps.c[1], p.out16[0] + p.lo_offset, p.ld16, row0, c, col_end);
+                        emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
+                        if (p.lo_offset) emit(lo, job, &maps.c[1], job.out16[0] + p.lo_offset, row0, c, col_end);
                     }
                 }
             }

@@ -25,74 +25,122 @@ struct Product {
     int halves = 1;
 };
 
-// How it runs.
+// How a launch of one or two products runs: one tile shape and ring for both.
 struct Layout {
     int cg = 1, bn = 256, tile_n = 256, a_rows = 128;
-    int tiles_m = 0, tiles_n = 0, splits = 1, kb_per_split = 0;
-    int nkb0 = 0, nkb = 0;
     int stages = 0, a_bytes = 0, slot_bytes = 0, tx_bytes = 0;
+    int first = 0;              // which product is the launch's first job
+    int extra_rounds = 0;
+    struct Part {
+        int tiles_m = 0, tiles_n = 0, splits = 1, kb_per_split = 0, nkb0 = 0, nkb = 0;
+    } part[2];
 };
 
+// Time of u0 units of t0 each followed by u1 units of t1 each, dealt to
+// `groups` groups as Schedule does.
+inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t groups, int* extra_rounds) {
+    const int64_t rounds0 = u0 / groups, rest = u0 % groups, late = groups - rest;
+    *extra_rounds = 0;
+    if (u1 == 0) return static_cast<double>(rounds0 + (rest ? 1 : 0)) * t0;
+    const int extra = rest ? static_cast<int>(t0 / t1 + 0.5) : 0;
+    *extra_rounds = extra;
+    const double early0 = static_cast<double>(rounds0 + (rest ? 1 : 0)) * t0, late0 = static_cast<double>(rounds0) * t0;
+    if (extra * late >= u1) {
+        const double b = late0 + static_cast<double>(cdiv(u1, late)) * t1;
+        return b > early0 ? b : early0;
+    }
+    const int64_t left = u1 - extra * late, rounds = left / groups, rem = left % groups;
+    const double a = rest ? early0 + static_cast<double>(rounds + (rem > late ? 1 : 0)) * t1 : 0.0;
+    const double b = late0 + static_cast<double>(extra + rounds + (rem ? 1 : 0)) * t1;
+    return a > b ? a : b;
+}
+
 // Chooses the tile (CTA pair or single CTA, accumulator width) and the K
-// split with the least estimated time, in SM clocks:
+// splits with the least estimated time, in SM clocks:
 //   per K block   the larger of the multiplies (a tile of bn columns takes
 //                 2 bn clocks), the copy into shared memory (about 60 bytes a
 //                 clock and SM from L2) and a ring slot's share of one
 //                 round trip (1500 clocks over the ring's depth);
-//   per wave      the K blocks of one unit, and 300 clocks between units;
+//   per unit      its K blocks and 300 clocks between units;
 //   per launch    a fill and a last epilogue (1500 + 4 bn);
 //   a split       the join's launch (4000) and its traffic (3000 bytes a clock).
-inline Layout choose_layout(const Product& pr, int num_sms) {
+inline Layout choose_layout(const Product* pr, int n, int num_sms) {
     Layout best;
     double best_time = 1e300;
-    const int64_t nkb0 = cdiv(pr.K, BK), nkb = nkb0 * pr.segments;
-    for (int cg = 1; cg <= (pr.M > BM_CTA ? 2 : 1); ++cg) {
+    int64_t rows = 0;
+    for (int i = 0; i < n; ++i) rows = pr[i].M > rows ? pr[i].M : rows;
+    for (int cg = 1; cg <= (rows > BM_CTA ? 2 : 1); ++cg) {
         for (int bn = MAX_BN; bn >= 16; bn -= 16) {
             if (cg == 2 && (bn % 32 != 0 || bn < 64)) continue;
-            if (pr.bmn && (bn / cg) % 64 != 0) continue;
+            if (pr[0].bmn && (bn / cg) % 64 != 0) continue;
             Layout l;
             l.cg = cg;
             l.bn = bn;
-            l.tile_n = pr.gated ? bn / 2 : bn;
-            l.a_rows = pr.amn || cg == 2 ? BM_CTA : static_cast<int>(pr.M < BM_CTA ? round_up(pr.M, 8) : BM_CTA);
-            l.a_bytes = pr.amn ? 2 * MN_BOX : l.a_rows * 128;
+            l.tile_n = pr[0].gated ? bn / 2 : bn;
+            // a short box for the tokens of a launch that has no more of them
+            l.a_rows = BM_CTA;
+            if (n == 1 && !pr[0].amn && cg == 1 && rows < BM_CTA) l.a_rows = static_cast<int>(round_up(rows, 8));
+            l.a_bytes = l.a_rows * 128;         // (an MN-major A is two boxes of 64 x 64: as many)
             const int b_bytes = bn / cg * 128;
             l.tx_bytes = l.a_bytes + b_bytes;
             l.slot_bytes = static_cast<int>(round_up(l.tx_bytes, 1024));
             // the multiply reads 128 A rows from a slot's start: past a short
-            // box it reads what follows, which must still be the ring
+            // box it reads what follows (rows of D that are not stored), which
+            // must still be the ring
             const int slack = l.a_rows < BM_CTA ? BM_CTA * 128 : 0;
             l.stages = (RING_BYTES - slack) / l.slot_bytes;
             if (l.stages > MAX_STAGES) l.stages = MAX_STAGES;
-            l.tiles_m = static_cast<int>(cdiv(pr.M, BM_CTA * cg));
-            l.tiles_n = static_cast<int>(cdiv(pr.N, l.tile_n));
-            l.nkb0 = static_cast<int>(nkb0);
-            l.nkb = static_cast<int>(nkb);
-            const int64_t tiles = static_cast<int64_t>(l.tiles_m) * l.tiles_n * pr.problems;
             const int64_t groups = num_sms / cg;
             double per_kb = 2.0 * bn;
             const double copy = l.tx_bytes / 60.0, trip = 1500.0 / l.stages;
             if (copy > per_kb) per_kb = copy;
             if (trip > per_kb) per_kb = trip;
-            // splits up to a full wave of the GPU, four K blocks each at least
-            int64_t most = !pr.may_split || tiles >= groups ? 1 : (groups / tiles < nkb / 4 ? groups / tiles : nkb / 4);
-            if (most < 1) most = 1;
-            for (int64_t s = 1; s <= most; s = s == most ? s + 1 : (2 * s < most ? 2 * s : most)) {
-                const int64_t kbps = cdiv(nkb, s), splits = cdiv(nkb, kbps);
-                const int64_t waves = cdiv(tiles * splits, groups);
-                double time = waves * (kbps * per_kb + 300.0) + 1500.0 + 4.0 * bn;
-                if (splits > 1) time += 4000.0 + 8.0 * splits * pr.M * pr.N * pr.problems / 3000.0;
-                if (time < best_time) {
-                    best_time = time;
-                    best = l;
-                    best.splits = static_cast<int>(splits);
-                    best.kb_per_split = static_cast<int>(kbps);
+            // each product's candidate splits: 1, 2, 4, ... up to a full wave of the GPU
+            int64_t tiles[2] = {0, 0}, most[2] = {1, 1};
+            for (int i = 0; i < n; ++i) {
+                Layout::Part& q = l.part[i];
+                q.tiles_m = static_cast<int>(cdiv(pr[i].M, BM_CTA * cg));
+                q.tiles_n = static_cast<int>(cdiv(pr[i].N, l.tile_n));
+                q.nkb0 = static_cast<int>(cdiv(pr[i].K, BK));
+                q.nkb = q.nkb0 * pr[i].segments;
+                tiles[i] = static_cast<int64_t>(q.tiles_m) * q.tiles_n * pr[i].problems;
+                if (pr[i].may_split && tiles[i] < groups) {
+                    most[i] = groups / tiles[i];
+                    if (most[i] > q.nkb / 4) most[i] = q.nkb / 4 > 0 ? q.nkb / 4 : 1;
+                }
+            }
+            const auto more = [](int64_t s, int64_t top) { return s >= top ? top + 1 : (2 * s < top ? 2 * s : top); };
+            for (int64_t s0 = 1; s0 <= most[0]; s0 = more(s0, most[0])) {
+                for (int64_t s1 = 1; s1 <= most[1]; s1 = more(s1, most[1])) {
+                    int64_t units[2] = {0, 0};
+                    double t[2] = {0.0, 1.0}, time = 1500.0 + 4.0 * bn;
+                    bool joins = false;
+                    for (int i = 0; i < n; ++i) {
+                        Layout::Part& q = l.part[i];
+                        q.kb_per_split = static_cast<int>(cdiv(q.nkb, i ? s1 : s0));
+                        q.splits = static_cast<int>(cdiv(q.nkb, q.kb_per_split));
+                        units[i] = tiles[i] * q.splits;
+                        t[i] = q.kb_per_split * per_kb + 300.0;
+                        if (q.splits > 1 || pr[i].halves > 1) {
+                            joins = true;
+                            time += 8.0 * q.splits * pr[i].M * pr[i].N * pr[i].problems / 3000.0;
+                        }
+                    }
+                    if (joins) time += 4000.0;
+                    l.first = n == 2 && t[1] > t[0] ? 1 : 0;
+                    const int a = l.first, b = 1 - l.first;
+                    time += makespan(units[a], t[a], units[b], t[b], groups, &l.extra_rounds);
+                    if (time < best_time) {
+                        best_time = time;
+                        best = l;
+                    }
                 }
             }
         }
     }
     return best;
 }
+inline Layout choose_layout(const Product& pr, int num_sms) { return choose_layout(&pr, 1, num_sms); }
 
 // fp32 partial sums of a split product: rows padded to 16 bytes.
 inline int64_t ld32_of(int64_t N) { return round_up(N, 4); }
@@ -108,22 +156,12 @@ inline bool operand_map(CUtensorMap* map, const void* p, bool mn_major, int64_t 
                     : encode_tmap_f16_2d(map, p, K, mn, ld * 2, BK, box_rows);
 }
 
-// The parts of Params every epilogue shares.
-inline Params base_params(const Product& pr, const Layout& l, int type, const DeviceInfo& info, cudaStream_t stream) {
+// The parts of Params that every epilogue shares.
+inline Params base_params(const Layout& l, int type, const DeviceInfo& info, cudaStream_t stream) {
     Params p;
     memset(&p, 0, sizeof(p));
-    p.M = static_cast<int>(pr.M);
-    p.N = static_cast<int>(pr.N);
-    p.nkb0 = l.nkb0;
-    p.nkb = l.nkb;
-    p.tiles_m = l.tiles_m;
-    p.tiles_n = l.tiles_n;
-    p.num_tiles = l.tiles_m * l.tiles_n * pr.problems;
-    p.splits = l.splits;
-    p.kb_per_split = l.kb_per_split;
-    p.total_units = p.num_tiles * l.splits;
-    p.chunk = pr.chunk ? pr.chunk : l.kb_per_split;
-    p.a_rows = l.a_rows;
+    p.extra_rounds = l.extra_rounds;
+    p.chunk = 1 << 30;
     p.bn = l.bn;
     p.tile_n = l.tile_n;
     p.stages = l.stages;
@@ -131,29 +169,61 @@ inline Params base_params(const Product& pr, const Layout& l, int type, const De
     p.slot_bytes = l.slot_bytes;
     p.tx_bytes = l.tx_bytes;
     p.bf16 = type == GEMM_TYPE_BFLOAT;
-    // instruction descriptor: fp32 accumulator, operand types, operands'
-    // majors, N >> 3, M >> 4
-    const uint32_t t = p.bf16 ? 1u : 0u;
-    p.idesc = (1u << 4) | (t << 7) | (t << 10) | ((pr.amn ? 1u : 0u) << 15) | ((pr.bmn ? 1u : 0u) << 16) |
-              (static_cast<uint32_t>(l.bn >> 3) << 17) | (static_cast<uint32_t>((BM_CTA * l.cg) >> 4) << 24);
+    p.flags = debug_flags();
     p.timeout_ns = wait_timeout_ns();
     p.status = status_word(info, stream);
     return p;
 }
 
-// Encodes the operands' maps: a[2 * problem + segment], b[segment]; a null
-// entry repeats the first.
-inline bool encode_operands(Maps* maps, const Product& pr, const Layout& l, const void* const a[4], int64_t lda,
-                            const void* const b[2], int64_t ldb) {
-    memset(maps, 0, sizeof(*maps));
-    for (int i = 0; i < 4; ++i) {
-        if (i > 0 && !a[i]) maps->a[i] = maps->a[0];
-        else if (!operand_map(&maps->a[i], a[i], pr.amn, pr.M, pr.K, lda, l.a_rows)) return false;
+// A product's operands: a[2 * problem + segment], and b[segment] (one b for
+// both segments where A is MN-major); a null entry repeats the first.
+struct Operands {
+    const void* a[4] = {nullptr, nullptr, nullptr, nullptr};
+    int64_t lda = 0;
+    const void* b[2] = {nullptr, nullptr};
+    int64_t ldb = 0;
+};
+
+// Fills job `at` of a launch (the first uses maps 0 on, the second those after
+// the first's).
+inline bool set_job(Params* p, Maps* maps, int at, const Product& pr, const Layout& l, const Layout::Part& part,
+                    const Operands& op) {
+    Job& j = p->job[at];
+    j.M = static_cast<int>(pr.M);
+    j.N = static_cast<int>(pr.N);
+    j.nkb0 = part.nkb0;
+    j.nkb = part.nkb;
+    j.tiles_m = part.tiles_m;
+    j.tiles_n = part.tiles_n;
+    j.num_tiles = part.tiles_m * part.tiles_n * pr.problems;
+    j.kb_per_split = part.kb_per_split;
+    j.units = j.num_tiles * part.splits;
+    j.amn = pr.amn;
+    j.b_seg = pr.amn ? 0 : 1;
+    // instruction descriptor: fp32 accumulator, operand types, operands'
+    // majors, N >> 3, M >> 4
+    const uint32_t t = p->bf16 ? 1u : 0u;
+    j.idesc = (1u << 4) | (t << 7) | (t << 10) | ((pr.amn ? 1u : 0u) << 15) | ((pr.bmn ? 1u : 0u) << 16) |
+              (static_cast<uint32_t>(l.bn >> 3) << 17) | (static_cast<uint32_t>((BM_CTA * l.cg) >> 4) << 24);
+    // the second of two jobs: MN-major A takes four A maps, one B and two
+    // outputs, K-major A two, two and one
+    if (at == 1) {
+        const Job& f = p->job[0];
+        j.a_map = f.amn ? 4 : 2;
+        j.b_map = f.amn ? 1 : 2;
+        j.c_map = f.amn ? 2 : 1;
+    }
+    const int na = at == 0 && !pr.amn ? 2 : (pr.amn ? 4 : 2), nb = pr.amn ? 1 : 2;
+    for (int i = 0; i < na; ++i) {
+        CUtensorMap* m = &maps->a[j.a_map + i];
+        if (i > 0 && !op.a[i]) *m = maps->a[j.a_map];
+        else if (!operand_map(m, op.a[i], pr.amn, pr.M, pr.K, op.lda, l.a_rows)) return false;
     }
     const int b_box = pr.gated ? l.tile_n : l.bn / l.cg;
-    for (int i = 0; i < 2; ++i) {
-        if (i > 0 && !b[i]) maps->b[i] = maps->b[0];
-        else if (!operand_map(&maps->b[i], b[i], pr.bmn, pr.N, pr.K, ldb, b_box)) return false;
+    for (int i = 0; i < nb; ++i) {
+        CUtensorMap* m = &maps->b[j.b_map + i];
+        if (i > 0 && !op.b[i]) *m = maps->b[j.b_map];
+        else if (!operand_map(m, op.b[i], pr.bmn, pr.N, pr.K, op.ldb, b_box)) return false;
     }
     return true;
 }
@@ -164,9 +234,9 @@ inline bool output_map(CUtensorMap* map, const Layout& l, const void* out, int64
     return encode_tmap_f16_2d(map, out, N, M, ld * 2, EPI_COLS, 32);
 }
 
-template <int CG, int EPI, bool AMN, bool BMN>
+template <int CG, int EPI>
 int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStream_t stream) {
-    auto kern = product_kernel<CG, EPI, AMN, BMN>;
+    auto kern = product_kernel<CG, EPI>;
     static std::atomic<int> capacity[64] = {};
     if (info.device < 0 || info.device >= 64) return GEMM_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
@@ -197,7 +267,8 @@ int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStr
         }
         capacity[info.device].store(cap, std::memory_order_relaxed);
     }
-    const int groups = p.total_units < cap ? p.total_units : cap;
+    const int units = p.job[0].units + p.job[1].units;
+    const int groups = units < cap ? units : cap;
     cfg.gridDim = dim3(CG * groups, 1, 1);
     cfg.stream = stream;
     cfg.numAttrs = 2;
@@ -208,10 +279,9 @@ int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStr
     return GEMM_OK;
 }
 
-template <int EPI, bool AMN, bool BMN>
+template <int EPI>
 int launch_product(const Layout& l, const Maps& maps, const Params& p, const DeviceInfo& info, cudaStream_t stream) {
-    return l.cg == 2 ? launch_cg<2, EPI, AMN, BMN>(maps, p, info, stream)
-                     : launch_cg<1, EPI, AMN, BMN>(maps, p, info, stream);
+    return l.cg == 2 ? launch_cg<2, EPI>(maps, p, info, stream) : launch_cg<1, EPI>(maps, p, info, stream);
 }
 
 // Hands out 256-byte aligned parts of a workspace; with no base it only counts.
@@ -263,23 +333,27 @@ int fill_sources(const Fill (&f)[3], int64_t cols, cudaStream_t stream);
 // is the weights' bytes.  Both halves' rows fit one CTA's 128.
 constexpr int64_t kFewRows = 64;
 
-// fp32 values a split product's partial sums take.
-inline int64_t split_floats(const Product& pr, const Layout& l) {
-    return l.splits > 1 || pr.halves > 1 ? static_cast<int64_t>(l.splits) * pr.problems * pr.M * ld32_of(pr.N) : 0;
+// fp32 values a product's partial sums take.
+inline int64_t split_floats(const Product& pr, const Layout::Part& part) {
+    return part.splits > 1 || pr.halves > 1 ? part.splits * pr.problems * pr.M * ld32_of(pr.N) : 0;
 }
 
-// out = scale (acc_in + A B^T) to 16 bits at out16[problem] (rows N apart), or
-// acc_out = acc_in + A B^T in fp32 (rows ld32_of(N) apart).  `partial` holds
-// split_floats() floats.
-struct StoreTarget {
+// A backward product and where it goes: scale (acc_in + A B^T) to 16 bits at
+// out16[problem] (rows N apart), or acc_in + A B^T in fp32 at acc_out (rows
+// ld32_of(N) apart).
+struct StoreProduct {
+    Product pr;
+    Operands op;
     void* out16[2] = {nullptr, nullptr};
     float* acc_out = nullptr;
     const float* acc_in = nullptr;
     const float* scale = nullptr;
+    float* partial = nullptr;       // split_floats() floats
 };
-int run_store_product(const Product& pr, const Layout& l, const void* const a[4], int64_t lda, const void* const b[2],
-                      int64_t ldb, const StoreTarget& to, float* partial, int type, const DeviceInfo& info,
-                      cudaStream_t stream);
+// One launch for the n (1 or 2) products, and one that joins their splits.
+// Of two products, one has K-major A and the other MN-major A.
+int run_store_products(const StoreProduct* sp, int n, const Layout& l, int type, const DeviceInfo& info,
+                       cudaStream_t stream);
 
 // ---- argument checks
 
