@@ -87,7 +87,11 @@ enum Epilogue { kEpiStore = 0, kEpiGated = 1, kEpiXentStats = 2, kEpiXentGrad = 
 // epilogue of a short K loop keeps up with the multiplies; one for the gated
 // block, whose three outputs take more registers than ten warps leave.
 constexpr int epi_warps(int epi) { return epi == kEpiGated ? 4 : 8; }
-constexpr int threads_of(int epi) { return (2 + epi_warps(epi)) * 32; }
+// Producer warps: A's copies and B's (an MN-major operand takes two copies a
+// slot, and one thread issuing three or four of them fell behind the
+// multiplies), then the MMA issuer.
+constexpr int kMmaWarp = 2;
+constexpr int threads_of(int epi) { return (kMmaWarp + 1 + epi_warps(epi)) * 32; }
 
 // K blocks per chunk of the softmax statistics' sums.
 constexpr int kStatsChunk = 8;
@@ -299,7 +303,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
         tma_prefetch_desc(&maps.a[0]);
         tma_prefetch_desc(&maps.b[0]);
     }
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tmem_alloc<CG>(base + OFF_TMEM, 512);
         tmem_relinquish<CG>();
     }
@@ -314,9 +318,10 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
     allow_dependent_launch();
     const bool leader = CG == 1 || rank == 0;
 
-    if (warp == 0) {
-        // ======================================================== producer
+    if (warp < kMmaWarp) {
+        // ======================================================== producers
         if (lane == 0) {
+            const bool for_a = warp == 0;
             const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
             const uint32_t full_leader = CG == 2 ? mapa_shared(bFULL, 0) : bFULL;
             uint32_t stage = 0, phase = 0, issued = 0;
@@ -337,15 +342,12 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     const uint32_t bar = full_leader + 8 * stage;
                     const int seg = kb >= job.nkb0 ? 1 : 0;
                     const int k = (kb - (seg ? job.nkb0 : 0)) * BK;
-                    const CUtensorMap* ma = &maps.a[job.a_map + 2 * t.problem + seg];
-                    if (leader) mbar_arrive_expect_tx(bFULL + 8 * stage, CG * p.tx_bytes);
-                    if (BMN && job.amn) {
-                        load(a_dst, ma, m_cta, k, bar);
-                        load(a_dst + MN_BOX, ma, m_cta + 64, k, bar);
-                    } else {
-                        load(a_dst, ma, k, m_cta, bar);
-                    }
-                    if constexpr (EPI == kEpiGated) {
+                    if (for_a) {
+                        const CUtensorMap* ma = &maps.a[job.a_map + 2 * t.problem + seg];
+                        if (leader) mbar_arrive_expect_tx(bFULL + 8 * stage, CG * p.tx_bytes);
+                        load(a_dst, ma, BMN && job.amn ? m_cta : k, BMN && job.amn ? k : m_cta, bar);
+                        if (BMN && job.amn) load(a_dst + MN_BOX, ma, m_cta + 64, k, bar);
+                    } else if constexpr (EPI == kEpiGated) {
                         // gate rows are the first half of the tile's columns, up rows the second
                         const int n = t.tn * p.tile_n;
                         if constexpr (CG == 2) {
@@ -364,11 +366,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                         }
                     }
                     ++issued;
-                    st_volatile_shared_u32(sPROGRESS, issued);
+                    if (for_a) st_volatile_shared_u32(sPROGRESS, issued);
                     if (++stage == S) { stage = 0; phase ^= 1u; }
                 }
             }
-            if (!ok && leader) {
+            if (!ok && leader && for_a) {
                 // drain: wait (bounded) for the copies still in flight into this CTA
                 volatile uint32_t no_abort = 0;
                 const Waiter D{max(p.timeout_ns, kDrainNs), &no_abort, p.status, kStatusRoleProducer};
@@ -376,14 +378,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 for (uint32_t it = first; it < issued; ++it)
                     if (!D.wait(bFULL + 8 * (it % S), (it / S) & 1u)) break;
             } else if (!ok && issued > 0) {
-                // a pair's peer cannot wait on the leader's barriers: its copies
-                // land within microseconds, so a bounded millisecond outlasts them
+                // a pair's peer cannot wait on the leader's barriers, nor B's
+                // producer on a slot that A's has not armed: copies land within
+                // microseconds, so a bounded millisecond outlasts them
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
         // ======================================================== MMA issuer
         if (lane == 0 && !(p.flags & GEMM_DEBUG_SKIP_EMPTY_SEED))
             for (uint32_t s = 0; s < S; ++s) mbar_arrive(bEMPTY + 8 * s);      // every slot starts empty
@@ -448,7 +451,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
         __syncwarp();
     } else {
         // ======================================================== epilogue
-        const int e = warp - 2;
+        const int e = warp - kMmaWarp - 1;
         const int q = warp & 3;                  // tensor-memory lane quarter of this warp
         const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleEpilogue};
         const uint32_t tempty_leader = CG == 2 ? mapa_shared(bTEMPTY, 0) : bTEMPTY;
@@ -785,7 +788,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
     tc_fence_before_sync();
     __syncthreads();
     if (CG == 2) cluster_sync();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, 512);
     }
