@@ -246,15 +246,23 @@ def gemm_f16_nt_noalloc(lhs, rhs, out=None, stages: int = 4, stream=None):
 # ---------------------------------------------------------------- the operators around the products
 
 _codes = None
+_torch = None
+
+
+def _torch_module():
+    """torch, imported by the first operator call (not with the package)."""
+    global _codes, _torch
+    import torch
+    _codes = {torch.float16: GEMM_TYPE_HALF, torch.bfloat16: GEMM_TYPE_BFLOAT}
+    _torch = torch
+    return torch
 
 
 def _type_of(name, *tensors):
     """The GEMM_TYPE_* of tensors that must share one 16-bit type, be dense
     matrices and lie on one CUDA device."""
-    global _codes
-    if _codes is None:
-        import torch
-        _codes = {torch.float16: GEMM_TYPE_HALF, torch.bfloat16: GEMM_TYPE_BFLOAT}
+    if _torch is None:
+        _torch_module()
     dtype, device = tensors[0].dtype, tensors[0].device
     code = _codes.get(dtype)
     if code is None:
@@ -294,9 +302,9 @@ def _on(stream, device):
     call's stream are current, so that outputs and workspaces are taken from
     that stream's memory and are not handed to other work while the call still
     uses them."""
-    import torch
+    torch = _torch
     if stream is None and torch.cuda.current_device() == device.index:
-        return torch.cuda.current_stream(device).cuda_stream, _HERE
+        return torch._C._cuda_getCurrentRawStream(device.index), _HERE      # current_stream() without its object
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(device))
     if stream is None:
@@ -311,11 +319,11 @@ def _on(stream, device):
 
 def _workspace(name, lib, device, *args):
     """(tensor or None, address, bytes) of the workspace the call reports."""
+    torch = _torch
     need = ctypes.c_int64()
     _check(getattr(lib, name + "_workspace")(*args, ctypes.byref(need)), name)
     if need.value == 0:
         return None, None, 0
-    import torch
     ws = torch.empty(need.value, dtype=torch.uint8, device=device)
     return ws, ws.data_ptr(), need.value
 
@@ -327,7 +335,7 @@ def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream
     act is "silu" or "gelu" (tanh form).  With save=True returns (h, g, u),
     where g and u are the two products, for gemm_gated_nt_bwd.
     """
-    import torch
+    torch = _torch or _torch_module()
     name = "gemm_gated_nt"
     code, act_code = _type_of(name, x, w_gate, w_up), _act_code(name, act)
     M, K = x.shape
@@ -343,7 +351,7 @@ def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream
         px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
         ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, F, K, px, pg, pu, code)
         _check(lib.gemm_gated_nt(M, F, K, px, pg, pu, h.data_ptr(), g.data_ptr() if save else None,
-                                            u.data_ptr() if save else None, code, act_code, ws_ptr, ws_bytes, s), name)
+                                 u.data_ptr() if save else None, code, act_code, ws_ptr, ws_bytes, s), name)
     return (h, g, u) if save else h
 
 
@@ -354,7 +362,7 @@ def gemm_gated_nt_bwd(dh, g, u, x, w_gate, w_up, act: str = "silu", need_dx: boo
     g and u are what gemm_gated_nt(..., save=True) returned.  Gradients not
     needed are None.
     """
-    import torch
+    torch = _torch or _torch_module()
     name = "gemm_gated_nt_bwd"
     code, act_code = _type_of(name, dh, g, u, x, w_gate, w_up), _act_code(name, act)
     M, K = x.shape
@@ -377,7 +385,7 @@ def gemm_gated_nt_bwd(dh, g, u, x, w_gate, w_up, act: str = "silu", need_dx: boo
 
 
 def _xent_shapes(name, x, w, target):
-    import torch
+    torch = _torch
     code = _type_of(name, x, w)
     if w.shape[1] != x.shape[1]:
         raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w.shape)} do not form [M,K], [V,K]")
@@ -391,7 +399,7 @@ def gemm_xent_nt(x, w, target, ignore_index: int = -100, stream=None):
     target is int64 [M].  Returns (loss, lse), float32 [M]: loss is 0 in rows
     whose target is ignore_index and NaN for any other target outside [0, V).
     """
-    import torch
+    torch = _torch or _torch_module()
     name = "gemm_xent_nt"
     code, M, V, K = _xent_shapes(name, x, w, target)
     lib, device = load_library(), x.device
@@ -412,7 +420,7 @@ def gemm_xent_nt_bwd(x, w, target, lse, dloss, ignore_index: int = -100, need_dx
 
     lse is gemm_xent_nt's, dloss float32 [M].  Gradients not needed are None.
     """
-    import torch
+    torch = _torch or _torch_module()
     name = "gemm_xent_nt_bwd"
     code, M, V, K = _xent_shapes(name, x, w, target)
     _vector(name, "lse", lse, M, torch.float32, x.device)
@@ -435,7 +443,7 @@ def gemm_nt_bwd(dy, x, w, need_dx: bool = True, need_dw: bool = True, stream=Non
 
     float16 or bfloat16, fp32 sums.  Gradients not needed are None.
     """
-    import torch
+    torch = _torch or _torch_module()
     name = "gemm_nt_bwd"
     code = _type_of(name, dy, x, w)
     M, N = dy.shape

@@ -14,9 +14,7 @@ namespace {
 
 // Rows of `cols` 16-bit elements at any 2-byte alignment, copied to rows ld
 // apart (ld a multiple of 64), up to three matrices in one launch.  A thread
-// writes one 16-byte chunk: it reads the one or two aligned 16-byte blocks
-// that hold it (each holds at least a byte of the row, so no load leaves the
-// operand's pages) and shifts; a row's last, ragged chunk is read element by
+// writes one 16-byte chunk; a row's last, ragged chunk is read element by
 // element and padded with zeros.  The chunks of all rows are numbered
 // through, so a row of 129 chunks wastes no threads.
 struct Rows {
@@ -36,23 +34,7 @@ align_rows_kernel(const __grid_constant__ Rows r, uint32_t chunks, int64_t cols,
     const uint16_t* src = r.src[m] + row * cols + 8 * static_cast<int64_t>(j);
     uint4 o;
     if (8 * static_cast<int64_t>(j) + 8 <= cols) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(src);
-        const uint32_t sh = static_cast<uint32_t>(at & 15u);
-        const uint4* blk = reinterpret_cast<const uint4*>(at - sh);
-        o = __ldg(blk);
-        if (sh) {
-            const uint4 hi = __ldg(blk + 1);
-            const uint32_t w[8] = {o.x, o.y, o.z, o.w, hi.x, hi.y, hi.z, hi.w};
-            const uint32_t q = sh >> 2, bits = (sh & 3u) * 8u;
-            uint32_t v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = q == 0 ? w[i] : q == 1 ? w[i + 1] : q == 2 ? w[i + 2] : w[i + 3];
-                const uint32_t up = q == 0 ? w[i + 1] : q == 1 ? w[i + 2] : q == 2 ? w[i + 3] : w[i + 4];
-                v[i] = __funnelshift_r(lo, up, bits);
-            }
-            o = make_uint4(v[0], v[1], v[2], v[3]);
-        }
+        o = load_unaligned16(src);
     } else {
         uint32_t v[4];
 #pragma unroll

@@ -248,6 +248,28 @@ __device__ __forceinline__ void act_value_slope(float g, int act, float& value, 
     slope = s + (t == 0.0f ? 0.0f : t * ds);        // (a saturated gate's s' may overflow)
 }
 
+// 16 bytes at any 2-byte alignment: the one or two aligned 16-byte blocks that
+// hold them (each holds at least one of the bytes, so no load leaves their
+// pages), shifted into place.
+__device__ __forceinline__ uint4 load_unaligned16(const uint16_t* src) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+    const uint32_t sh = static_cast<uint32_t>(at & 15u);
+    const uint4* blk = reinterpret_cast<const uint4*>(at - sh);
+    const uint4 lo = __ldg(blk);
+    if (sh == 0) return lo;
+    const uint4 hi = __ldg(blk + 1);
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const uint32_t q = sh >> 2, bits = (sh & 3u) * 8u;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = q == 0 ? w[i] : q == 1 ? w[i + 1] : q == 2 ? w[i + 2] : w[i + 3];
+        const uint32_t b = q == 0 ? w[i + 1] : q == 1 ? w[i + 2] : q == 2 ? w[i + 3] : w[i + 4];
+        v[i] = __funnelshift_r(a, b, bits);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
     if (bf16) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

@@ -19,10 +19,13 @@ struct Product {
     int segments = 1, problems = 1;
     bool gated = false, amn = false, bmn = false;
     bool may_split = false;
-    int chunk = 0;                      // K blocks per accumulator hand-over, 0: all of a unit's
     // 2: A is a 16-bit value and its rounding remainder, M rows each (M counts
     // both); the two halves' outputs are added
     int halves = 1;
+    bool operator==(const Product& o) const {
+        return M == o.M && N == o.N && K == o.K && segments == o.segments && problems == o.problems &&
+               gated == o.gated && amn == o.amn && bmn == o.bmn && may_split == o.may_split && halves == o.halves;
+    }
 };
 
 // How a launch of one or two products runs: one tile shape and ring for both.
@@ -64,7 +67,7 @@ inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t gro
 //   per unit      its K blocks and 300 clocks between units;
 //   per launch    a fill and a last epilogue (1500 + 4 bn);
 //   a split       the join's launch (4000) and its traffic (3000 bytes a clock).
-inline Layout choose_layout(const Product* pr, int n, int num_sms) {
+inline Layout best_layout(const Product* pr, int n, int num_sms) {
     Layout best;
     double best_time = 1e300;
     int64_t rows = 0;
@@ -139,6 +142,28 @@ inline Layout choose_layout(const Product* pr, int n, int num_sms) {
         }
     }
     return best;
+}
+
+// best_layout, remembered for the last few sizes a host thread asked for: the
+// search takes microseconds, as long as the launch itself.
+inline Layout choose_layout(const Product* pr, int n, int num_sms) {
+    struct Entry {
+        Product pr[2];
+        int n = 0, num_sms = 0;
+        Layout l;
+    };
+    constexpr int kEntries = 16;
+    static thread_local Entry cache[kEntries];
+    static thread_local int next = 0;
+    for (const Entry& e : cache)
+        if (e.n == n && e.num_sms == num_sms && e.pr[0] == pr[0] && (n == 1 || e.pr[1] == pr[1])) return e.l;
+    Entry& e = cache[next];
+    next = (next + 1) % kEntries;
+    e.n = n;
+    e.num_sms = num_sms;
+    for (int i = 0; i < n; ++i) e.pr[i] = pr[i];
+    e.l = best_layout(pr, n, num_sms);
+    return e.l;
 }
 inline Layout choose_layout(const Product& pr, int num_sms) { return choose_layout(&pr, 1, num_sms); }
 
