@@ -55,35 +55,38 @@ xent_rows_kernel(const int64_t* __restrict__ target, const float* __restrict__ d
     }
 }
 
-// One warp per row joins its half tiles' (maximum, sum) pairs.  tiles == 0: K == 0,
-// every logit is 0.
-__global__ void __launch_bounds__(256)
+// One block per row joins its half tiles' (maximum, sum) pairs, in an order
+// that depends on their number alone.  tiles == 0: K == 0, every logit is 0.
+__global__ void __launch_bounds__(128)
 xent_join_kernel(const float2* __restrict__ stats, const float* __restrict__ z_target,
-                 const int64_t* __restrict__ target, int M, int tiles, int64_t V, int64_t ignore_index,
+                 const int64_t* __restrict__ target, int tiles, int64_t V, int64_t ignore_index,
                  float* __restrict__ loss, float* __restrict__ lse) {
     grid_dependency_wait();
     allow_dependent_launch();
-    const int row = static_cast<int>((blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) / 32);
-    const int lane = threadIdx.x % 32;
-    if (row >= M) return;
+    __shared__ float2 part[4];
+    const int64_t row = blockIdx.x;
     const float inf = __int_as_float(0x7f800000);
-    float m = -inf, s = 0.0f;
-    for (int t = lane; t < tiles; t += 32) {
-        const float2 v = stats[static_cast<int64_t>(row) * tiles + t];
-        const float top = fmaxf(m, v.x);
+    const auto join = [&](float2 a, float2 b) {
+        const float top = fmaxf(a.x, b.x);
         const float ref = top == -inf ? 0.0f : top;
-        s = s * expf(m - ref) + v.y * expf(v.x - ref);
-        m = top;
+        return make_float2(top, a.y * expf(a.x - ref) + b.y * expf(b.x - ref));
+    };
+    float2 v = make_float2(-inf, 0.0f);
+    const float2* mine = stats + row * tiles;
+    for (int t0 = threadIdx.x; t0 < tiles; t0 += 4 * 128) {
+        float2 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = t0 + i * 128 < tiles ? mine[t0 + i * 128] : make_float2(-inf, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v = join(v, w[i]);
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        const float top = fmaxf(m, m2);
-        const float ref = top == -inf ? 0.0f : top;
-        s = s * expf(m - ref) + s2 * expf(m2 - ref);
-        m = top;
-    }
-    if (lane == 0) {
-        const float total = tiles ? m + logf(s) : logf(static_cast<float>(V));
+    for (int o = 16; o > 0; o >>= 1)
+        v = join(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        v = join(join(part[0], part[1]), join(part[2], part[3]));
+        const float total = tiles ? v.x + logf(v.y) : logf(static_cast<float>(V));
         const int64_t t = target[row];
         float l = 0.0f;
         if (t != ignore_index) l = t >= 0 && t < V ? total - (tiles ? z_target[row] : 0.0f) : __int_as_float(0x7fffffff);
@@ -260,9 +263,9 @@ extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, cons
         rc = launch_product<kEpiXentStats>(pl.l, maps, p, info, stream);
         if (rc != GEMM_OK) return rc;
     }
-    if (launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>(cdiv(M, 8))), dim3(256), 0, stream,
+    if (launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>(M)), dim3(128), 0, stream,
                    static_cast<const float2*>(pl.stats), static_cast<const float*>(pl.z_target), target,
-                   static_cast<int>(M), K > 0 ? 2 * pl.l.part[0].tiles_n : 0, V, ignore_index, loss, lse) != cudaSuccess) {
+                   K > 0 ? 2 * pl.l.part[0].tiles_n : 0, V, ignore_index, loss, lse) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }

@@ -61,7 +61,7 @@ inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t gro
 // Chooses the tile (CTA pair or single CTA, accumulator width) and the K
 // splits with the least estimated time, in SM clocks:
 //   per K block   the larger of the multiplies (a tile of bn columns takes
-//                 2 bn clocks), the copy into shared memory (about 60 bytes a
+//                 2 bn clocks), the copy into shared memory (about 50 bytes a
 //                 clock and SM from L2) and a ring slot's share of one
 //                 round trip (1500 clocks over the ring's depth);
 //   per unit      its K blocks and 300 clocks between units;
@@ -95,7 +95,7 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
             if (l.stages > MAX_STAGES) l.stages = MAX_STAGES;
             const int64_t groups = num_sms / cg;
             double per_kb = 2.0 * bn;
-            const double copy = l.tx_bytes / 60.0, trip = 1500.0 / l.stages;
+            const double copy = l.tx_bytes / 50.0, trip = 1500.0 / l.stages;
             if (copy > per_kb) per_kb = copy;
             if (trip > per_kb) per_kb = trip;
             // each product's candidate splits: 1, 2, 4, ... up to a full wave of the GPU
