@@ -47,6 +47,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
                  : "memory");
 }
 
+// The same without release: for an arrival that hands over no memory, only a
+// resource whose last use by this thread has completed.  (The release waits
+// for every earlier store and copy of the thread.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
+                 : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
