@@ -93,8 +93,11 @@ constexpr int epi_warps(int epi) { return epi == kEpiGated ? 4 : 8; }
 constexpr int kMmaWarp = 2;
 constexpr int threads_of(int epi) { return (kMmaWarp + 1 + epi_warps(epi)) * 32; }
 
-// K blocks per chunk of the softmax statistics' sums.
+// K blocks per chunk of the softmax statistics' sums (whole slots: kMaxBoxes
+// divides it).
 constexpr int kStatsChunk = 8;
+constexpr int kMaxBoxes = 4;
+static_assert(kStatsChunk % kMaxBoxes == 0, "a chunk ends with a slot");
 
 // One product of a launch.
 struct Job {
@@ -125,8 +128,9 @@ struct Params {
     int chunk;                      // K blocks per accumulator hand-over
     int bn;                         // accumulator columns per tile (a multiple of 16)
     int tile_n;                     // output columns per tile (bn, or bn / 2 for the gated epilogue)
-    int stages, a_bytes, slot_bytes;
-    int tx_bytes;                   // bytes one CTA's copies bring per slot
+    int stages, boxes;              // ring slots, K blocks in each
+    int a_bytes, box_bytes, slot_bytes;
+    int tx_bytes;                   // bytes one CTA's copies bring per K block
     int bf16;                       // output type
     int act;
     unsigned flags;                 // GEMM_DEBUG_SKIP_EMPTY_SEED is honoured
@@ -291,6 +295,8 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     constexpr bool BMN = EPI == kEpiStore;
     constexpr int EW = epi_warps(EPI);
+    // slots of several K blocks, for the narrow tiles of few rows
+    constexpr bool MULTI = CG == 1 && EPI != kEpiStore;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;       // swizzle atoms are 1024-byte aligned
@@ -346,50 +352,85 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             const bool for_a = warp == 0;
             const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
             const uint32_t full_leader = CG == 2 ? mapa_shared(bFULL, 0) : bFULL;
-            uint32_t stage = 0, phase = 0, issued = 0;
+            const bool arm = for_a && leader;
+            const uint32_t tx = static_cast<uint32_t>(CG * p.tx_bytes), slot = static_cast<uint32_t>(p.slot_bytes);
+            const int boxes = MULTI ? p.boxes : 1;
+            const uint32_t box = static_cast<uint32_t>(p.box_bytes);
+            const uint32_t dst0 = base + (for_a ? 0u : static_cast<uint32_t>(p.a_bytes));
+            uint32_t stage = 0, phase = 0, issued = 0, dst = dst0;
             bool ok = true;
-            auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-                if constexpr (CG == 1) tma_load_2d(dst, map, x, y, bar);
-                else tma_load_2d_pair(dst, map, x, y, bar);
+            auto load = [&](uint32_t to, const CUtensorMap* map, int x, int y, uint32_t bar) {
+                if constexpr (CG == 1) tma_load_2d(to, map, x, y, bar);
+                else tma_load_2d_pair(to, map, x, y, bar);
+            };
+            // `count` K blocks from element k on, `boxes` of them to a slot:
+            // copy(the block's operand in the slot, the slot's full barrier, k).
+            auto stream = [&](int count, int k, auto copy) {
+                while (count > 0) {
+                    const int n = min(count, boxes);
+                    count -= n;
+                    if (!W.wait(bEMPTY + 8 * stage, phase)) return false;
+                    if (arm) mbar_arrive_expect_tx(bFULL + 8 * stage, static_cast<uint32_t>(n) * tx);
+                    uint32_t to = dst;
+                    for (int i = 0; i < n; ++i, to += box, k += BK) copy(to, full_leader + 8 * stage, k);
+                    ++issued;
+                    if (for_a) st_volatile_shared_u32(sPROGRESS, issued);
+                    dst += slot;
+                    if (++stage == S) { stage = 0; phase ^= 1u; dst = dst0; }
+                }
+                return true;
             };
             Schedule sched(p, group_id, num_groups);
             for (int jn, u; ok && sched.next(jn, u);) {
                 const Job& job = p.job[jn];
                 const Tile t = tile_of(u, job);
-                const int m_cta = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA;
-                const int b_rows = p.bn / CG;                    // B rows (accumulator columns) of this CTA
-                for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!W.wait(bEMPTY + 8 * stage, phase)) { ok = false; break; }
-                    const uint32_t a_dst = base + stage * p.slot_bytes, b_dst = a_dst + p.a_bytes;
-                    const uint32_t bar = full_leader + 8 * stage;
-                    const int seg = kb >= job.nkb0 ? 1 : 0;
-                    const int k = (kb - (seg ? job.nkb0 : 0)) * BK;
+                // the unit's blocks of the first K segment, then of the second
+                const int nkb0 = job.nkb0;
+                for (int seg = 0; ok && seg < 2; ++seg) {
+                    const int first = seg ? max(t.kb0, nkb0) : t.kb0, last = seg ? t.kb1 : min(t.kb1, nkb0);
+                    const int count = last - first, k0 = (first - (seg ? nkb0 : 0)) * BK;
+                    if (count <= 0) continue;
                     if (for_a) {
-                        const CUtensorMap* ma = &maps.a[job.a_map + 2 * t.problem + seg];
-                        if (leader) mbar_arrive_expect_tx(bFULL + 8 * stage, CG * p.tx_bytes);
-                        load(a_dst, ma, BMN && job.amn ? m_cta : k, BMN && job.amn ? k : m_cta, bar);
-                        if (BMN && job.amn) load(a_dst + MN_BOX, ma, m_cta + 64, k, bar);
+                        const CUtensorMap* map = &maps.a[job.a_map + 2 * t.problem + seg];
+                        const int m = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA;
+                        if (BMN && job.amn) {
+                            ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) {
+                                load(to, map, m, k, bar);
+                                load(to + MN_BOX, map, m + 64, k, bar);
+                            });
+                        } else {
+                            ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) { load(to, map, k, m, bar); });
+                        }
                     } else if constexpr (EPI == kEpiGated) {
                         // gate rows are the first half of the tile's columns, up rows the second
                         const int n = t.tn * p.tile_n;
                         if constexpr (CG == 2) {
-                            load(b_dst, &maps.b[rank], k, n, bar);
+                            const CUtensorMap* map = &maps.b[rank];
+                            ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) { load(to, map, k, n, bar); });
                         } else {
-                            load(b_dst, &maps.b[0], k, n, bar);
-                            load(b_dst + p.tile_n * 128, &maps.b[1], k, n, bar);
+                            const uint32_t half = static_cast<uint32_t>(p.tile_n) * 128;
+                            ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) {
+                                load(to, &maps.b[0], k, n, bar);
+                                load(to + half, &maps.b[1], k, n, bar);
+                            });
                         }
                     } else {
+                        const int b_rows = p.bn / CG;                    // B rows (accumulator columns) of this CTA
                         const int n = t.tn * p.tile_n + static_cast<int>(rank) * b_rows;
-                        const CUtensorMap* mb = &maps.b[job.b_map + job.b_seg * seg];
-                        if constexpr (BMN) {
-                            for (int j = 0; j < b_rows; j += 64) load(b_dst + j * (MN_BOX / 64), mb, n + j, k, bar);
+                        const CUtensorMap* map = &maps.b[job.b_map + job.b_seg * seg];
+                        if (BMN && b_rows == 128) {
+                            ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) {
+                                load(to, map, n, k, bar);
+                                load(to + MN_BOX, map, n + 64, k, bar);
+                            });
+                        } else if constexpr (BMN) {
+                            ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) {
+                                for (int j = 0; j < b_rows; j += 64) load(to + j * (MN_BOX / 64), map, n + j, k, bar);
+                            });
                         } else {
-                            load(b_dst, mb, k, n, bar);
+                            ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) { load(to, map, k, n, bar); });
                         }
                     }
-                    ++issued;
-                    if (for_a) st_volatile_shared_u32(sPROGRESS, issued);
-                    if (++stage == S) { stage = 0; phase ^= 1u; }
                 }
             }
             if (!ok && leader && for_a) {
@@ -414,11 +455,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             for (uint32_t s = 0; s < S; ++s) mbar_arrive(bEMPTY + 8 * s);      // every slot starts empty
         if (leader && lane == 0) {
             const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleMma};
-            // descriptors of slot s: slot 0's plus s slots (addresses lie below
-            // 256 KB, so the 14-bit address field never carries)
-            const uint64_t bdesc0 = operand_desc(base + p.a_bytes, BMN);
+            // Descriptors of slot s: slot 0's plus s slots.  Addresses lie below
+            // 256 KB, so the 14-bit address field never carries and the sum is
+            // taken in the low words alone.
             const uint32_t slot16 = static_cast<uint32_t>(p.slot_bytes) >> 4;
-            uint32_t stage = 0, phase = 0, tcount = 0;
+            const uint64_t bdesc0 = operand_desc(base + p.a_bytes, BMN);
+            const uint32_t box16 = static_cast<uint32_t>(p.box_bytes) >> 4;
+            const int chunk = p.chunk, boxes = MULTI ? p.boxes : 1;
+            auto desc = [](uint32_t lo, uint64_t of) { return (of & 0xFFFFFFFF00000000ull) | lo; };
+            uint32_t stage = 0, phase = 0, tcount = 0, off = 0;
             bool ok = true, issued_any = false;
             // One unit's multiplies.  The A operand's form is a compile-time
             // constant: the issuing thread's own instructions between
@@ -427,24 +472,32 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             auto unit = [&](const Tile& t, uint32_t idesc, auto a_mn) {
                 constexpr bool AMN = decltype(a_mn)::value;
                 const uint64_t adesc0 = operand_desc(base, AMN);
-                for (int c0 = t.kb0; c0 < t.kb1; c0 += p.chunk, ++tcount) {
-                    const int c1 = min(t.kb1, c0 + p.chunk);
+                // (counted in what is left: a chunk may be "all")
+                for (int left = t.kb1 - t.kb0; left > 0; ++tcount) {
+                    const int count = min(left, chunk);
+                    left -= count;
                     const uint32_t b = tcount & 1u, aph = (tcount >> 1) & 1u;
                     if (!W.template wait<CG == 2>(bTEMPTY + 8 * b, aph)) return false;
                     tc_fence_after_sync();
                     const uint32_t d_tmem = tmem_base + b * MAX_BN;
-                    for (int kb = c0; kb < c1; ++kb) {
+                    for (int i = 0; i < count;) {
                         if (!W.wait(bFULL + 8 * stage, phase)) return false;
                         tc_fence_after_sync();
-                        const uint64_t ad = adesc0 + stage * slot16, bd = bdesc0 + stage * slot16;
+                        uint32_t alo = static_cast<uint32_t>(adesc0) + off, blo = static_cast<uint32_t>(bdesc0) + off;
+                        const int end = min(count, i + boxes);
+                        do {
 #pragma unroll
-                        for (int k = 0; k < BK / UMMA_K; ++k)
-                            tc_mma_f16<CG>(d_tmem, ad + k * k_step(AMN), bd + k * k_step(BMN), idesc,
-                                           kb != c0 || k != 0);
+                            for (int k = 0; k < BK / UMMA_K; ++k)
+                                tc_mma_f16<CG>(d_tmem, desc(alo + k * k_step(AMN), adesc0),
+                                               desc(blo + k * k_step(BMN), bdesc0), idesc, i != 0 || k != 0);
+                            alo += box16;
+                            blo += box16;
+                        } while (++i < end);
                         issued_any = true;
                         if constexpr (CG == 1) tc_commit_1(bEMPTY + 8 * stage);
                         else tc_commit_2_mc(bEMPTY + 8 * stage, 0x3);
-                        if (++stage == S) { stage = 0; phase ^= 1u; }
+                        off += slot16;
+                        if (++stage == S) { stage = 0; phase ^= 1u; off = 0; }
                     }
                     if constexpr (CG == 1) tc_commit_1(bTFULL + 8 * b);
                     else tc_commit_2_mc(bTFULL + 8 * b, 0x3);

@@ -31,7 +31,7 @@ struct Product {
 // How a launch of one or two products runs: one tile shape and ring for both.
 struct Layout {
     int cg = 1, bn = 256, tile_n = 256, a_rows = 128;
-    int stages = 0, a_bytes = 0, slot_bytes = 0, tx_bytes = 0;
+    int stages = 0, boxes = 1, a_bytes = 0, box_bytes = 0, slot_bytes = 0, tx_bytes = 0;
     int first = 0;              // which product is the launch's first job
     int extra_rounds = 0;
     struct Part {
@@ -63,7 +63,8 @@ inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t gro
 //   per K block   the larger of the multiplies (a tile of bn columns takes
 //                 2 bn clocks), the copy into shared memory (about 50 bytes a
 //                 clock and SM from L2) and a ring slot's share of one
-//                 round trip (1500 clocks over the ring's depth);
+//                 round trip (1500 clocks over the ring's depth), and a slot's
+//                 handling by the issuing thread (400);
 //   per unit      its K blocks and 300 clocks between units;
 //   per launch    a fill and a last epilogue (1500 + 4 bn);
 //   a split       the join's launch (4000) and its traffic (3000 bytes a clock).
@@ -86,7 +87,14 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
             l.a_bytes = l.a_rows * 128;         // (an MN-major A is two boxes of 64 x 64: as many)
             const int b_bytes = bn / cg * 128;
             l.tx_bytes = l.a_bytes + b_bytes;
-            l.slot_bytes = static_cast<int>(round_up(l.tx_bytes, 1024));
+            l.box_bytes = static_cast<int>(round_up(l.tx_bytes, 1024));
+            // Narrow tiles take several K blocks to a slot: a wait, a fence and
+            // a commit per block cost the issuing thread about 400 clocks, more
+            // than their multiplies.
+            l.boxes = 1;
+            if (cg == 1 && !pr[0].bmn)
+                while (l.boxes < kMaxBoxes && 2 * bn * l.boxes < 400) l.boxes *= 2;
+            l.slot_bytes = l.boxes * l.box_bytes;
             // the multiply reads 128 A rows from a slot's start: past a short
             // box it reads what follows (rows of D that are not stored), which
             // must still be the ring
@@ -95,9 +103,11 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
             if (l.stages > MAX_STAGES) l.stages = MAX_STAGES;
             const int64_t groups = num_sms / cg;
             double per_kb = 2.0 * bn;
-            const double copy = l.tx_bytes / 50.0, trip = 1500.0 / l.stages;
+            const double copy = l.tx_bytes / 50.0, trip = 1500.0 / (l.stages * l.boxes);
+            const double issue = 400.0 / l.boxes;
             if (copy > per_kb) per_kb = copy;
             if (trip > per_kb) per_kb = trip;
+            if (issue > per_kb) per_kb = issue;
             // each product's candidate splits: 1, 2, 4, ... up to a full wave of the GPU
             int64_t tiles[2] = {0, 0}, most[2] = {1, 1};
             for (int i = 0; i < n; ++i) {
@@ -190,6 +200,8 @@ inline Params base_params(const Layout& l, int type, const DeviceInfo& info, cud
     p.bn = l.bn;
     p.tile_n = l.tile_n;
     p.stages = l.stages;
+    p.boxes = l.boxes;
+    p.box_bytes = l.box_bytes;
     p.a_bytes = l.a_bytes;
     p.slot_bytes = l.slot_bytes;
     p.tx_bytes = l.tx_bytes;
