@@ -65,8 +65,9 @@ inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t gro
 //                 clock and SM from L2) and a ring slot's share of one
 //                 round trip (1500 clocks over the ring's depth), and a slot's
 //                 handling by the issuing thread (400);
-//   per unit      its K blocks and 300 clocks between units;
-//   per launch    a fill and a last epilogue (1500 + 4 bn);
+//   per unit      the larger of its K blocks and the epilogue of the unit
+//                 before (1000 + 10 bn), and 300 clocks between units;
+//   per launch    a fill and a last epilogue (1500 + that);
 //   a split       the join's launch (4000) and its traffic (3000 bytes a clock).
 inline Layout best_layout(const Product* pr, int n, int num_sms) {
     Layout best;
@@ -102,16 +103,18 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
             l.stages = (RING_BYTES - slack) / l.slot_bytes;
             if (l.stages > MAX_STAGES) l.stages = MAX_STAGES;
             const int64_t groups = num_sms / cg;
-            double per_kb = 2.0 * bn;
-            const double copy = l.tx_bytes / 50.0, trip = 1500.0 / (l.stages * l.boxes);
-            const double issue = 400.0 / l.boxes;
-            if (copy > per_kb) per_kb = copy;
-            if (trip > per_kb) per_kb = trip;
-            if (issue > per_kb) per_kb = issue;
+            const double trip = 1500.0 / (l.stages * l.boxes), issue = 400.0 / l.boxes, epilogue = 1000.0 + 10.0 * bn;
+            double per_kb[2] = {0.0, 0.0};
             // each product's candidate splits: 1, 2, 4, ... up to a full wave of the GPU
             int64_t tiles[2] = {0, 0}, most[2] = {1, 1};
             for (int i = 0; i < n; ++i) {
                 Layout::Part& q = l.part[i];
+                // (rows of a box past the matrix are filled, not copied)
+                const double copy = ((pr[i].M < BM_CTA ? pr[i].M : BM_CTA) * 128 + b_bytes) / 50.0;
+                per_kb[i] = 2.0 * bn;
+                if (copy > per_kb[i]) per_kb[i] = copy;
+                if (trip > per_kb[i]) per_kb[i] = trip;
+                if (issue > per_kb[i]) per_kb[i] = issue;
                 q.tiles_m = static_cast<int>(cdiv(pr[i].M, BM_CTA * cg));
                 q.tiles_n = static_cast<int>(cdiv(pr[i].N, l.tile_n));
                 q.nkb0 = static_cast<int>(cdiv(pr[i].K, BK));
@@ -126,14 +129,16 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
             for (int64_t s0 = 1; s0 <= most[0]; s0 = more(s0, most[0])) {
                 for (int64_t s1 = 1; s1 <= most[1]; s1 = more(s1, most[1])) {
                     int64_t units[2] = {0, 0};
-                    double t[2] = {0.0, 1.0}, time = 1500.0 + 4.0 * bn;
+                    double t[2] = {0.0, 1.0}, time = 1500.0 + epilogue;
                     bool joins = false;
                     for (int i = 0; i < n; ++i) {
                         Layout::Part& q = l.part[i];
                         q.kb_per_split = static_cast<int>(cdiv(q.nkb, i ? s1 : s0));
                         q.splits = static_cast<int>(cdiv(q.nkb, q.kb_per_split));
                         units[i] = tiles[i] * q.splits;
-                        t[i] = q.kb_per_split * per_kb + 300.0;
+                        t[i] = q.kb_per_split * per_kb[i];
+                        if (t[i] < epilogue) t[i] = epilogue;
+                        t[i] += 300.0;
                         if (q.splits > 1 || pr[i].halves > 1) {
                             joins = true;
                             time += 8.0 * q.splits * pr[i].M * pr[i].N * pr[i].problems / 3000.0;
