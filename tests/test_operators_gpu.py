@@ -491,3 +491,43 @@ def test_a_timed_out_wait_is_reported():
     got = pws.gemm_gated_nt(x, wg, wu)
     assert pws.gemm_device_status() == pws.GEMM_OK
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+def test_example_trains_and_scores():
+    # the operators together, as a training step and as a token's score
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "language_model_block.py")
+    spec = importlib.util.spec_from_file_location("language_model_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    x, target, masters = ex.make(300, 136, 328, 1003, seed=3)
+    w = {k: v.half() for k, v in masters.items()}
+    loss, grads = ex.forward_backward(x, target, w)
+    want, want_grads = ex.autograd(x, target, w)
+    # binary16 activations on the way: h, y, g and u are rounded to 2^-11, and a
+    # logit is a sum of 136 such products of size one
+    assert abs(float(loss) - float(want)) <= 2.0 ** -8
+    for k, g in want_grads.items():
+        # half a dozen roundings of 2^-11 each between the loss and a gradient
+        assert float((grads[k].float() - g).norm()) <= 6 * 2.0 ** -11 * float(g.norm()), k
+    losses = ex.train(x, target, masters, 6)
+    assert all(b < a for a, b in zip(losses, losses[1:]))
+    w = {k: v.half() for k, v in masters.items()}
+    one = ex.score(x[7:8], target[7:8].clamp(min=0), w)
+    many = ex.score(x, target.clamp(min=0), w)
+    assert abs(float(one) - float(many[7])) <= 2.0 ** -8
+
+
+def test_too_small_a_workspace_is_refused():
+    lib = pws.load_library()
+    p = [torch.zeros(1 << 16, device="cuda", dtype=F16).data_ptr() for _ in range(9)]
+    bad, half = pws.GEMM_ERR_INVALID_ARG, pws.GEMM_TYPE_HALF
+    for ws, size in ((None, 1 << 30), (p[8] + 2, 1 << 30), (p[8], 16)):
+        assert lib.gemm_gated_nt_bwd(4, 8, 16, *p[:6], p[6], None, None, half, 0, ws, size, None) == bad
+        assert lib.gemm_xent_nt(4, 8, 16, p[0], p[1], p[2], -100, p[3], p[4], half, ws, size, None) == bad
+        assert lib.gemm_xent_nt_bwd(4, 8, 16, p[0], p[1], p[2], -100, p[3], p[4], p[5], None, half, ws, size, None) == bad
+        # 9 columns: rows that need a copy
+        assert lib.gemm_gated_nt(4, 8, 9, *p[:3], p[3], None, None, half, 0, ws, size, None) == bad
+        assert lib.gemm_nt_bwd(4, 9, 16, *p[:3], p[3], None, half, ws, size, None) == bad
