@@ -317,15 +317,28 @@ def _on(stream, device):
     return raw, stack
 
 
-def _workspace(name, lib, device, *args):
+_ws_bytes = {}          # bytes by (entry, device, type, sizes) for operands on 16-byte boundaries
+
+
+def _workspace(name, device, code, dims, *ptrs):
     """(tensor or None, address, bytes) of the workspace the call reports."""
-    torch = _torch
-    need = ctypes.c_int64()
-    _check(getattr(lib, name + "_workspace")(*args, ctypes.byref(need)), name)
-    if need.value == 0:
+    low = 0
+    for p in ptrs:
+        low |= p
+    key = (name, device.index, code, dims)
+    size = _ws_bytes.get(key) if low & 15 == 0 else None
+    if size is None:
+        need = ctypes.c_int64()
+        _check(getattr(load_library(), name + "_workspace")(*dims, *ptrs, code, ctypes.byref(need)), name)
+        size = need.value
+        if low & 15 == 0:
+            if len(_ws_bytes) >= 4096:
+                _ws_bytes.clear()
+            _ws_bytes[key] = size
+    if size == 0:
         return None, None, 0
-    ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-    return ws, ws.data_ptr(), need.value
+    ws = _torch.empty(size, dtype=_torch.uint8, device=device)
+    return ws, ws.data_ptr(), size
 
 
 def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream=None):
@@ -349,7 +362,7 @@ def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream
         h = torch.empty((M, F), dtype=x.dtype, device=device)
         g, u = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
         px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
-        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, F, K, px, pg, pu, code)
+        ws, ws_ptr, ws_bytes = _workspace(name, device, code, (M, F, K), px, pg, pu)
         _check(lib.gemm_gated_nt(M, F, K, px, pg, pu, h.data_ptr(), g.data_ptr() if save else None,
                                  u.data_ptr() if save else None, code, act_code, ws_ptr, ws_bytes, s), name)
     return (h, g, u) if save else h
@@ -378,7 +391,7 @@ def gemm_gated_nt_bwd(dh, g, u, x, w_gate, w_up, act: str = "silu", need_dx: boo
         dx = torch.empty_like(x) if need_dx else None
         dwg, dwu = (torch.empty_like(w_gate), torch.empty_like(w_up)) if need_dw else (None, None)
         ptrs = [t.data_ptr() for t in (dh, g, u, x, w_gate, w_up)]
-        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, F, K, *ptrs, code)
+        ws, ws_ptr, ws_bytes = _workspace(name, device, code, (M, F, K), *ptrs)
         outs = [t.data_ptr() if t is not None else None for t in (dx, dwg, dwu)]
         _check(lib.gemm_gated_nt_bwd(M, F, K, *ptrs, *outs, code, act_code, ws_ptr, ws_bytes, s), name)
     return dx, dwg, dwu
@@ -408,9 +421,9 @@ def gemm_xent_nt(x, w, target, ignore_index: int = -100, stream=None):
         loss = torch.empty(M, dtype=torch.float32, device=device)
         lse = torch.empty_like(loss)
         px, pw = x.data_ptr(), w.data_ptr()
-        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, V, K, px, pw, code)
+        ws, ws_ptr, ws_bytes = _workspace(name, device, code, (M, V, K), px, pw)
         _check(lib.gemm_xent_nt(M, V, K, px, pw, target.data_ptr(), int(ignore_index), loss.data_ptr(),
-                                           lse.data_ptr(), code, ws_ptr, ws_bytes, s), name)
+                                lse.data_ptr(), code, ws_ptr, ws_bytes, s), name)
     return loss, lse
 
 
@@ -431,10 +444,10 @@ def gemm_xent_nt_bwd(x, w, target, lse, dloss, ignore_index: int = -100, need_dx
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty_like(w) if need_dw else None
         px, pw = x.data_ptr(), w.data_ptr()
-        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, V, K, px, pw, code)
+        ws, ws_ptr, ws_bytes = _workspace(name, device, code, (M, V, K), px, pw)
         _check(lib.gemm_xent_nt_bwd(M, V, K, px, pw, target.data_ptr(), int(ignore_index), lse.data_ptr(),
-                                               dloss.data_ptr(), dx.data_ptr() if need_dx else None,
-                                               dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
+                                    dloss.data_ptr(), dx.data_ptr() if need_dx else None,
+                                    dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
     return dx, dw
 
 
@@ -457,9 +470,9 @@ def gemm_nt_bwd(dy, x, w, need_dx: bool = True, need_dw: bool = True, stream=Non
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty_like(w) if need_dw else None
         ptrs = [t.data_ptr() for t in (dy, x, w)]
-        ws, ws_ptr, ws_bytes = _workspace(name, lib, device, M, N, K, *ptrs, code)
+        ws, ws_ptr, ws_bytes = _workspace(name, device, code, (M, N, K), *ptrs)
         _check(lib.gemm_nt_bwd(M, N, K, *ptrs, dx.data_ptr() if need_dx else None,
-                                          dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
+                               dw.data_ptr() if need_dw else None, code, ws_ptr, ws_bytes, s), name)
     return dx, dw
 
 
