@@ -200,25 +200,29 @@ struct Tile {
     int problem, tm, tn, kb0, kb1, split;
 };
 
-__device__ __forceinline__ Tile tile_of(int u, const Job& job) {
+// The K blocks of unit u.
+__device__ __forceinline__ void k_range(uint32_t u, const Job& job, Tile& t) {
+    t.split = job.units == job.num_tiles ? 0 : u / static_cast<uint32_t>(job.num_tiles);
+    t.kb0 = t.split * job.kb_per_split;
+    t.kb1 = min(job.nkb, t.kb0 + job.kb_per_split);
+}
+
+__device__ __forceinline__ Tile tile_of(uint32_t u, const Job& job) {
     Tile t;
-    t.split = u / job.num_tiles;
-    int r = u - t.split * job.num_tiles;
-    const int per = job.tiles_m * job.tiles_n;
-    t.problem = r / per;
+    k_range(u, job, t);
+    uint32_t r = u - t.split * static_cast<uint32_t>(job.num_tiles);
+    const uint32_t tiles_n = job.tiles_n, tiles_m = job.tiles_m, per = tiles_m * tiles_n;
+    t.problem = r >= per ? 1 : 0;
     r -= t.problem * per;
     // tile rows are walked GROUP_M at a time and odd groups right to left, so
     // the CTAs at work share A and B strips in L2
-    const int group = GROUP_M * job.tiles_n;
-    const int g = r / group;
-    const int first = g * GROUP_M;
-    const int rows = min(job.tiles_m - first, GROUP_M);
-    const int v = r - g * group;
-    t.tm = first + v % rows;
-    t.tn = v / rows;
-    if (g & 1) t.tn = job.tiles_n - 1 - t.tn;
-    t.kb0 = t.split * job.kb_per_split;
-    t.kb1 = min(job.nkb, t.kb0 + job.kb_per_split);
+    const uint32_t group = GROUP_M * tiles_n;
+    const uint32_t g = r / group;
+    const uint32_t first = g * GROUP_M, v = r - g * group;
+    const uint32_t rows = min(tiles_m - first, static_cast<uint32_t>(GROUP_M));
+    const uint32_t col = rows == GROUP_M ? v / GROUP_M : v / rows;
+    t.tm = static_cast<int>(first + v - col * rows);
+    t.tn = static_cast<int>(g & 1 ? tiles_n - 1 - col : col);
     return t;
 }
 
@@ -507,7 +511,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             Schedule sched(p, group_id, num_groups);
             for (int jn, u; ok && sched.next(jn, u);) {
                 const Job& job = p.job[jn];
-                const Tile t = tile_of(u, job);
+                Tile t;
+                k_range(u, job, t);
                 if constexpr (BMN) {
                     ok = job.amn ? unit(t, job.idesc, std::true_type{}) : unit(t, job.idesc, std::false_type{});
                 } else {
