@@ -53,7 +53,7 @@ constexpr int MAX_BN = 256;                 // accumulator columns per buffer
 constexpr int MAX_STAGES = 32;
 constexpr int EPI_COLS = 64;                // output columns per staged chunk: 128 bytes
 constexpr int EPI_BUF = 32 * EPI_COLS * 2;  // one warp's 32 rows of a chunk
-constexpr int EPI_BYTES = 4 * 2 * EPI_BUF;
+constexpr int EPI_BYTES = 8 * EPI_BUF;
 constexpr int MN_BOX = 64 * BK * 2;         // one MN-major box: 64 K rows of 64 elements
 constexpr int GROUP_M = 8;                  // tile rows walked together, so their A strips stay in L2
 
@@ -84,14 +84,13 @@ enum Epilogue { kEpiStore = 0, kEpiGated = 1, kEpiXentStats = 2, kEpiXentGrad = 
 
 // Epilogue warps: two per tensor-memory lane quarter, which take the tile's
 // 64-column chunks (32-column groups for the statistics) in turn, so that the
-// epilogue of a short K loop keeps up with the multiplies; one for the gated
-// block, whose three outputs take more registers than ten warps leave.
-constexpr int epi_warps(int epi) { return epi == kEpiGated ? 4 : 8; }
+// epilogue of a short K loop keeps up with the multiplies.
+constexpr int EPI_WARPS = 8;
 // Producer warps: A's copies and B's (an MN-major operand takes two copies a
 // slot, and one thread issuing three or four of them fell behind the
 // multiplies), then the MMA issuer.
 constexpr int kMmaWarp = 2;
-constexpr int threads_of(int epi) { return (kMmaWarp + 1 + epi_warps(epi)) * 32; }
+constexpr int THREADS = (kMmaWarp + 1 + EPI_WARPS) * 32;
 
 // K blocks per chunk of the softmax statistics' sums (whole slots: kMaxBoxes
 // divides it).
@@ -295,10 +294,9 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
 // kEpiStore serves the backward products, whose B is MN-major; the others are
 // forward (NT) products.
 template <int CG, int EPI>
-__global__ void __launch_bounds__(threads_of(EPI), 1)
+__global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     constexpr bool BMN = EPI == kEpiStore;
-    constexpr int EW = epi_warps(EPI);
     // slots of several K blocks, for the narrow tiles of few rows
     constexpr bool MULTI = CG == 1 && EPI != kEpiStore;
     extern __shared__ uint8_t smem_raw[];
@@ -324,7 +322,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bTFULL + 8 * b, 1);
-            mbar_init(bTEMPTY + 8 * b, EW * CG);
+            mbar_init(bTEMPTY + 8 * b, EPI_WARPS * CG);
         }
         mbar_init(bDRAIN, 1);
         *abort_flag = 0u;
@@ -540,24 +538,20 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 if constexpr (CG == 1) mbar_arrive(bTEMPTY + 8 * b);
                 else mbar_arrive_cluster(tempty_leader + 8 * b);
             }
-        constexpr int NBUF = 8 / EW;             // staging buffers of a warp
-        const uint32_t bufs = base + OFF_EPI + static_cast<uint32_t>(e) * NBUF * EPI_BUF;
-        // with two warps per lane quarter, the chunks whose number is 1 mod 2 are the second one's
-        const int first_chunk = EW == 8 ? (e >> 2) * EPI_COLS : 0;
-        constexpr int CHUNK_STEP = EW == 8 ? 2 * EPI_COLS : EPI_COLS;
-        uint32_t nbuf = 0;
+        const uint32_t buf = base + OFF_EPI + static_cast<uint32_t>(e) * EPI_BUF;     // this warp's staging buffer
+        // the chunks whose number is 1 mod 2 are the lane quarter's second warp's
+        const int first_chunk = (e >> 2) * EPI_COLS;
+        constexpr int CHUNK_STEP = 2 * EPI_COLS;
         int tile_end = 0;                        // the tile's last column + 1, past N or not
         // One 64-column chunk (this lane's row, 32 packed pairs) of a 16-bit
-        // output: staged in the swizzle its tensor map uses and stored by TMA
-        // (the staging buffers in turn), or, where TMA cannot address the
-        // output or the tile ends inside the chunk, staged and stored by the warp.
+        // output: staged in the swizzle its tensor map uses and stored by TMA,
+        // or, where TMA cannot address the output or the tile ends inside the
+        // chunk, staged and stored by the warp.
         auto emit = [&](const uint32_t(&h)[32], const Job& job, const CUtensorMap* map, uint16_t* out, int row0,
                         int col0, int col_end) {
             const bool by_tma = job.tma_store && col0 + EPI_COLS <= tile_end;
-            const uint32_t buf = bufs + (nbuf % NBUF) * EPI_BUF;
-            ++nbuf;
-            // the store issued from this buffer has finished reading it
-            if (lane == 0) bulk_wait_group_read<NBUF - 1>();
+            // the store issued from the buffer has finished reading it
+            if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
             const uint32_t row_addr = buf + static_cast<uint32_t>(lane) * 128;
 #pragma unroll
@@ -619,10 +613,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     }
                 }
             }
-            // (an empty group, so that "all but the last NBUF - 1 groups" is
-            // always about this buffer)
-            if (lane == 0) bulk_commit_group();
-            __syncwarp();
         };
         uint32_t tcount = 0;
         // waits for the next accumulator hand-over; its tensor-memory address
@@ -794,33 +784,50 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     }
                 } else if constexpr (EPI == kEpiGated) {
                     for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
-                        uint32_t h[32], hg[32], hu[32];
+                        const uint32_t at = tbase + static_cast<uint32_t>(c - n0);
+                        uint32_t h[32];
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             uint32_t g[32], up[32];
-                            const uint32_t off = static_cast<uint32_t>(c - n0 + 32 * half);
-                            if (off < static_cast<uint32_t>(p.tile_n)) {
-                                tmem_ld_32x32b_x32(tbase + off, g);
-                                tmem_ld_32x32b_x32(tbase + p.tile_n + off, up);
+                            if (c - n0 + 32 * half < p.tile_n) {
+                                tmem_ld_32x32b_x32(at + 32 * half, g);
+                                tmem_ld_32x32b_x32(at + p.tile_n + 32 * half, up);
                                 tmem_ld_wait();
                             } else {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) g[i] = up[i] = 0u;
                             }
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
-                                const float u0 = __uint_as_float(up[2 * i]), u1 = __uint_as_float(up[2 * i + 1]);
+                            for (int i = 0; i < 16; ++i)
                                 h[16 * half + i] =
-                                    pack16(act_value(g0, p.act) * u0, act_value(g1, p.act) * u1, p.bf16);
-                                hg[16 * half + i] = pack16(g0, g1, p.bf16);
-                                hu[16 * half + i] = pack16(u0, u1, p.bf16);
-                            }
+                                    pack16(act_value(__uint_as_float(g[2 * i]), p.act) * __uint_as_float(up[2 * i]),
+                                           act_value(__uint_as_float(g[2 * i + 1]), p.act) *
+                                               __uint_as_float(up[2 * i + 1]),
+                                           p.bf16);
                         }
                         emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
-                        if (p.g_out) {
-                            emit(hg, job, &maps.c[1], p.g_out, row0, c, col_end);
-                            emit(hu, job, &maps.c[2], p.u_out, row0, c, col_end);
+                        if (!p.g_out) continue;
+                        // gate and up themselves, read from tensor memory again:
+                        // kept from above they take more registers than eleven
+                        // warps leave a thread
+#pragma unroll 1
+                        for (int which = 0; which < 2; ++which) {
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t v[32];
+                                if (c - n0 + 32 * half < p.tile_n) {
+                                    tmem_ld_32x32b_x32(at + which * p.tile_n + 32 * half, v);
+                                    tmem_ld_wait();
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) v[i] = 0u;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    h[16 * half + i] =
+                                        pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), p.bf16);
+                            }
+                            emit(h, job, &maps.c[1 + which], which ? p.u_out : p.g_out, row0, c, col_end);
                         }
                     }
                 } else if constexpr (EPI == kEpiXentGrad) {

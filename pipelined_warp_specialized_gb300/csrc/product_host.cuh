@@ -288,7 +288,7 @@ int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStr
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1] = pdl_attribute();
-    cfg.blockDim = dim3(threads_of(EPI), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.attrs = attr;
     int cap = capacity[info.device].load(std::memory_order_relaxed);
