@@ -55,6 +55,9 @@ constexpr int EPI_COLS = 64;                // output columns per staged chunk: 
 constexpr int EPI_BUF = 32 * EPI_COLS * 2;  // one warp's 32 rows of a chunk
 constexpr int EPI_BYTES = 8 * EPI_BUF;
 constexpr int MN_BOX = 64 * BK * 2;         // one MN-major box: 64 K rows of 64 elements
+constexpr int WIDE_B = 128 * BK * 2;        // the wide tile's B halves in a slot: one CTA's 128 rows each
+constexpr int WIDE_STAGES = 4;
+constexpr int kWideBlocks = 128;
 constexpr int GROUP_M = 8;                  // tile rows walked together, so their A strips stay in L2
 
 // Shared memory: ring, epilogue staging, barriers.
@@ -291,11 +294,22 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// NW = 2, the wide tile (256 x 512, a CTA pair's): each slot carries two B
+// halves, whose accumulators are the two buffers, so an A slot written once
+// feeds twice the multiplies.  Shared memory bounds the 256 x 256 tile: a K
+// block's multiplies read 12 KB per 128 clocks of it while 32 KB are written,
+// 80 KB at 128 bytes a clock (648 clocks measured, its multiplies take 512).
+// The buffers are then not free to overlap two units, so it is for backward
+// products of at least kWideBlocks K blocks a unit.  Measured, wide against
+// 256 x 256: gated backward 8192 x 8192 x 4096 (256 and 128 blocks) 1348
+// against 1405 us; a product of 64 blocks 579 against 555; of 12, 43 against 36.
+
 // kEpiStore serves the backward products, whose B is MN-major; the others are
 // forward (NT) products.
-template <int CG, int EPI>
+template <int CG, int EPI, int NW>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+    static_assert(NW == 1 || (CG == 2 && EPI == kEpiStore), "the wide tile is a CTA pair's, for plain stores");
     constexpr bool BMN = EPI == kEpiStore;
     // slots of several K blocks, for the narrow tiles of few rows
     constexpr bool MULTI = CG == 1 && EPI != kEpiStore;
@@ -312,7 +326,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
     const uint32_t bTFULL = base + OFF_TFULL, bTEMPTY = base + OFF_TEMPTY, bDRAIN = base + OFF_DRAIN;
     const uint32_t sPROGRESS = base + OFF_PROGRESS;
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + OFF_ABORT);
-    const uint32_t S = static_cast<uint32_t>(p.stages);
+    const uint32_t S = NW == 2 ? WIDE_STAGES : static_cast<uint32_t>(p.stages);
 
     // ------------------------------------------------------------ set-up
     if (threadIdx.x == 0) {
@@ -418,12 +432,16 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                         }
                     } else {
                         const int b_rows = p.bn / CG;                    // B rows (accumulator columns) of this CTA
-                        const int n = t.tn * p.tile_n + static_cast<int>(rank) * b_rows;
+                        const int n = t.tn * NW * p.tile_n + static_cast<int>(rank) * b_rows, n2 = n + p.tile_n;
                         const CUtensorMap* map = &maps.b[job.b_map + job.b_seg * seg];
                         if (BMN && b_rows == 128) {
                             ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) {
                                 load(to, map, n, k, bar);
                                 load(to + MN_BOX, map, n + 64, k, bar);
+                                if (NW == 2) {
+                                    load(to + WIDE_B, map, n2, k, bar);
+                                    load(to + WIDE_B + MN_BOX, map, n2 + 64, k, bar);
+                                }
                             });
                         } else if constexpr (BMN) {
                             ok = stream(count, k0, [&](uint32_t to, uint32_t bar, int k) {
@@ -474,6 +492,89 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             auto unit = [&](const Tile& t, uint32_t idesc, auto a_mn) {
                 constexpr bool AMN = decltype(a_mn)::value;
                 const uint64_t adesc0 = operand_desc(base, AMN);
+                if constexpr (NW == 2) {
+                    // The K blocks of a group of J at both ends of a unit run
+                    // half 0 and then half 1 on the same, still held, slots: the
+                    // epilogue drains half 0 while the tensor pipe finishes
+                    // half 1, and half 1 while half 0 of the next unit starts.
+                    // Straight-line code: J and the slot size are constants.
+                    constexpr uint32_t J = WIDE_STAGES - 1, SLOT = (BM_CTA * 128 + 2 * WIDE_B) >> 4;
+                    const int nkb = t.kb1 - t.kb0;
+                    const uint32_t aph = tcount & 1u;
+                    ++tcount;
+                    auto slot = [](uint32_t x) { return x < WIDE_STAGES ? x : x - WIDE_STAGES; };
+                    auto mma_block = [&](uint32_t s, int h, bool first) {
+                        const uint32_t alo = static_cast<uint32_t>(adesc0) + s * SLOT;
+                        const uint32_t blo = static_cast<uint32_t>(bdesc0) + s * SLOT + h * (WIDE_B >> 4);
+#pragma unroll
+                        for (int k = 0; k < BK / UMMA_K; ++k)
+                            tc_mma_f16<CG>(tmem_base + h * MAX_BN, desc(alo + k * k_step(AMN), adesc0),
+                                           desc(blo + k * k_step(BMN), bdesc0), idesc, !(first && k == 0));
+                    };
+                    auto wait_full = [&]() {
+                        if (!W.wait(bFULL + 8 * stage, phase)) return false;
+                        if (++stage == WIDE_STAGES) { stage = 0; phase ^= 1u; }
+                        return true;
+                    };
+                    auto wait_acc = [&](int h) {
+                        if (!W.template wait<true>(bTEMPTY + 8 * h, aph)) return false;
+                        tc_fence_after_sync();
+                        return true;
+                    };
+                    if (nkb > static_cast<int>(2 * J)) {
+                        const uint32_t h0 = stage;
+#pragma unroll
+                        for (uint32_t j = 0; j < J; ++j)
+                            if (!wait_full()) return false;
+                        tc_fence_after_sync();
+                        if (!wait_acc(0)) return false;
+                        issued_any = true;
+#pragma unroll
+                        for (uint32_t j = 0; j < J; ++j) mma_block(slot(h0 + j), 0, j == 0);
+                        if (!wait_acc(1)) return false;
+#pragma unroll
+                        for (uint32_t j = 0; j < J; ++j) {
+                            mma_block(slot(h0 + j), 1, j == 0);
+                            tc_commit_2_mc(bEMPTY + 8 * slot(h0 + j), 0x3);
+                        }
+                        for (int kb = J; kb < nkb - static_cast<int>(J); ++kb) {
+                            const uint32_t s0 = stage;
+                            if (!wait_full()) return false;
+                            tc_fence_after_sync();
+                            mma_block(s0, 0, false);
+                            mma_block(s0, 1, false);
+                            tc_commit_2_mc(bEMPTY + 8 * s0, 0x3);
+                        }
+                        const uint32_t t0 = stage;
+#pragma unroll
+                        for (uint32_t j = 0; j < J; ++j)
+                            if (!wait_full()) return false;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (uint32_t j = 0; j < J; ++j) mma_block(slot(t0 + j), 0, false);
+                        tc_commit_2_mc(bTFULL, 0x3);
+#pragma unroll
+                        for (uint32_t j = 0; j < J; ++j) {
+                            mma_block(slot(t0 + j), 1, false);
+                            tc_commit_2_mc(bEMPTY + 8 * slot(t0 + j), 0x3);
+                        }
+                        tc_commit_2_mc(bTFULL + 8, 0x3);
+                    } else {
+                        for (int kb = 0; kb < nkb; ++kb) {
+                            const uint32_t s0 = stage;
+                            if (!wait_full()) return false;
+                            tc_fence_after_sync();
+                            if (kb == 0 && (!wait_acc(0) || !wait_acc(1))) return false;
+                            issued_any = true;
+                            mma_block(s0, 0, kb == 0);
+                            mma_block(s0, 1, kb == 0);
+                            tc_commit_2_mc(bEMPTY + 8 * s0, 0x3);
+                        }
+                        tc_commit_2_mc(bTFULL, 0x3);
+                        tc_commit_2_mc(bTFULL + 8, 0x3);
+                    }
+                    return true;
+                }
                 // (counted in what is left: a chunk may be "all")
                 for (int left = t.kb1 - t.kb0; left > 0; ++tcount) {
                     const int count = min(left, chunk);
@@ -645,229 +746,234 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             const Tile t = tile_of(u, job);
             const int row0 = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA + q * 32;
             const int row = row0 + lane;
-            const int n0 = t.tn * p.tile_n;
-            tile_end = n0 + p.tile_n;
-            const int col_end = min(job.N, tile_end);
-            uint32_t tbase;
-            if constexpr (EPI == kEpiXentStats) {
-                // This warp's 32-column groups are 2 j + half of the tile's.
-                // The logits are summed over K chunk by chunk, then reduced to
-                // the running maximum m and sum s = sum exp(z - m) of the row.
-                const int half = e >> 2;
-                const bool rows_live = row0 < job.M;
-                float z[4][32];
+            // (the wide tile's halves, one accumulator buffer each, in turn)
+            bool alive = true;
+            for (int wide = 0; wide < NW; ++wide) {
+                const int n0 = (t.tn * NW + wide) * p.tile_n;
+                tile_end = n0 + p.tile_n;
+                const int col_end = min(job.N, tile_end);
+                uint32_t tbase;
+                if constexpr (EPI == kEpiXentStats) {
+                    // This warp's 32-column groups are 2 j + half of the tile's.
+                    // The logits are summed over K chunk by chunk, then reduced to
+                    // the running maximum m and sum s = sum exp(z - m) of the row.
+                    const int half = e >> 2;
+                    const bool rows_live = row0 < job.M;
+                    float z[4][32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[j][i] = 0.0f;
-                bool got = true;
-                for (int c0 = t.kb0; c0 < t.kb1; c0 += p.chunk) {
-                    if (!acquire(tbase)) { got = false; break; }
-                    if (rows_live) {
+                        for (int i = 0; i < 32; ++i) z[j][i] = 0.0f;
+                    bool got = true;
+                    for (int c0 = t.kb0; c0 < t.kb1; c0 += p.chunk) {
+                        if (!acquire(tbase)) { got = false; break; }
+                        if (rows_live) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int c = 32 * (2 * j + half);
-                            if (c < p.tile_n) {
-                                // (16 columns at a time: 128 running sums leave
-                                // 40 registers of the 168 a thread can have)
+                            for (int j = 0; j < 4; ++j) {
+                                const int c = 32 * (2 * j + half);
+                                if (c < p.tile_n) {
+                                    // (16 columns at a time: 128 running sums leave
+                                    // 40 registers of the 168 a thread can have)
 #pragma unroll
-                                for (int h = 0; h < 32; h += 16) {
-                                    uint32_t v[16];
-                                    tmem_ld_32x32b_x16(tbase + static_cast<uint32_t>(c + h), v);
-                                    tmem_ld_wait();
+                                    for (int h = 0; h < 32; h += 16) {
+                                        uint32_t v[16];
+                                        tmem_ld_32x32b_x16(tbase + static_cast<uint32_t>(c + h), v);
+                                        tmem_ld_wait();
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) z[j][h + i] += __uint_as_float(v[i]);
-                                }
-                            }
-                        }
-                    }
-                    release();
-                }
-                if (!got) break;
-                if (!rows_live) continue;
-                const float inf = __int_as_float(0x7f800000);
-                const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
-                float m = -inf, s = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = n0 + 32 * (2 * j + half);
-                    if (c >= col_end) continue;
-                    if (c + 32 > col_end) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i >= col_end) z[j][i] = -inf;
-                    }
-                    const bool mine = tgt >= c && tgt < c + 32;
-                    if (__any_sync(0xffffffffu, mine)) {
-                        float zt = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (tgt == c + i) zt = z[j][i];
-                        if (mine && tgt < col_end) p.z_target[row] = zt;
-                    }
-                    float top = m;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, z[j][i]);
-                    // a row of -inf so far: any finite reference gives exp(-inf) = 0
-                    const float ref = top == -inf ? 0.0f : top * kLog2e;
-                    s *= ex2(m * kLog2e - ref);
-                    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        s0 += ex2(fmaf(z[j][i], kLog2e, -ref));
-                        s1 += ex2(fmaf(z[j][i + 1], kLog2e, -ref));
-                        s2 += ex2(fmaf(z[j][i + 2], kLog2e, -ref));
-                        s3 += ex2(fmaf(z[j][i + 3], kLog2e, -ref));
-                    }
-                    s += (s0 + s1) + (s2 + s3);
-                    m = top;
-                }
-                if (row < job.M) p.stats[static_cast<int64_t>(row) * (2 * job.tiles_n) + 2 * t.tn + half] = make_float2(m, s);
-                continue;
-            }
-            if (!acquire(tbase)) break;
-            if (row0 < job.M) {
-                if constexpr (EPI == kEpiStore) {
-                    const float scale = job.scale ? *job.scale : 1.0f;
-                    if (job.out32) {
-                        // fp32 partial or running sums
-                        float* out = job.out32 + t.split * job.split_stride + t.problem * job.problem_stride +
-                                     static_cast<int64_t>(row) * job.ld32;
-                        const float* in = job.acc_in ? job.acc_in + static_cast<int64_t>(row) * job.ld32 : nullptr;
-                        for (int c = n0 + first_chunk / 2; c < col_end; c += CHUNK_STEP / 2) {
-                            uint32_t v[32];
-                            tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0), v);
-                            tmem_ld_wait();
-                            if (row < job.M) {
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-                                    if (c + i < col_end) {          // rows are padded to a multiple of 4
-                                        float4 o = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
-                                                               __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-                                        if (in) {
-                                            const float4 a = *reinterpret_cast<const float4*>(in + c + i);
-                                            o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
-                                        }
-                                        *reinterpret_cast<float4*>(out + c + i) = o;
+                                        for (int i = 0; i < 16; ++i) z[j][h + i] += __uint_as_float(v[i]);
                                     }
                                 }
                             }
                         }
-                    } else {
-                        const float* in = job.acc_in ? job.acc_in + static_cast<int64_t>(row) * job.ld32 : nullptr;
+                        release();
+                    }
+                    if (!got) { alive = false; break; }
+                    if (!rows_live) continue;
+                    const float inf = __int_as_float(0x7f800000);
+                    const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
+                    float m = -inf, s = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = n0 + 32 * (2 * j + half);
+                        if (c >= col_end) continue;
+                        if (c + 32 > col_end) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i >= col_end) z[j][i] = -inf;
+                        }
+                        const bool mine = tgt >= c && tgt < c + 32;
+                        if (__any_sync(0xffffffffu, mine)) {
+                            float zt = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (tgt == c + i) zt = z[j][i];
+                            if (mine && tgt < col_end) p.z_target[row] = zt;
+                        }
+                        float top = m;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) top = fmaxf(top, z[j][i]);
+                        // a row of -inf so far: any finite reference gives exp(-inf) = 0
+                        const float ref = top == -inf ? 0.0f : top * kLog2e;
+                        s *= ex2(m * kLog2e - ref);
+                        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            s0 += ex2(fmaf(z[j][i], kLog2e, -ref));
+                            s1 += ex2(fmaf(z[j][i + 1], kLog2e, -ref));
+                            s2 += ex2(fmaf(z[j][i + 2], kLog2e, -ref));
+                            s3 += ex2(fmaf(z[j][i + 3], kLog2e, -ref));
+                        }
+                        s += (s0 + s1) + (s2 + s3);
+                        m = top;
+                    }
+                    if (row < job.M) p.stats[static_cast<int64_t>(row) * (2 * job.tiles_n) + 2 * t.tn + half] = make_float2(m, s);
+                    continue;
+                }
+                if (!acquire(tbase)) { alive = false; break; }
+                if (row0 < job.M) {
+                    if constexpr (EPI == kEpiStore) {
+                        const float scale = job.scale ? *job.scale : 1.0f;
+                        if (job.out32) {
+                            // fp32 partial or running sums
+                            float* out = job.out32 + t.split * job.split_stride + t.problem * job.problem_stride +
+                                         static_cast<int64_t>(row) * job.ld32;
+                            const float* in = job.acc_in ? job.acc_in + static_cast<int64_t>(row) * job.ld32 : nullptr;
+                            for (int c = n0 + first_chunk / 2; c < col_end; c += CHUNK_STEP / 2) {
+                                uint32_t v[32];
+                                tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0), v);
+                                tmem_ld_wait();
+                                if (row < job.M) {
+#pragma unroll
+                                    for (int i = 0; i < 32; i += 4) {
+                                        if (c + i < col_end) {          // rows are padded to a multiple of 4
+                                            float4 o = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                                                                   __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                                            if (in) {
+                                                const float4 a = *reinterpret_cast<const float4*>(in + c + i);
+                                                o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
+                                            }
+                                            *reinterpret_cast<float4*>(out + c + i) = o;
+                                        }
+                                    }
+                                }
+                            }
+                        } else {
+                            const float* in = job.acc_in ? job.acc_in + static_cast<int64_t>(row) * job.ld32 : nullptr;
+                            for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
+                                uint32_t h[32];
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    uint32_t v[32];
+                                    tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0 + 32 * half), v);
+                                    tmem_ld_wait();
+                                    if (in && row < job.M) {
+#pragma unroll
+                                        for (int i = 0; i < 32; i += 4) {
+                                            if (c + 32 * half + i < col_end) {
+                                                const float4 a = *reinterpret_cast<const float4*>(in + c + 32 * half + i);
+                                                v[i] = __float_as_uint(__uint_as_float(v[i]) + a.x);
+                                                v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) + a.y);
+                                                v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) + a.z);
+                                                v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + a.w);
+                                            }
+                                        }
+                                    }
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        h[16 * half + i] = pack16(scale * __uint_as_float(v[2 * i]),
+                                                                  scale * __uint_as_float(v[2 * i + 1]), p.bf16);
+                                }
+                                emit(h, job, &maps.c[job.c_map + t.problem], job.out16[t.problem], row0, c, col_end);
+                            }
+                        }
+                    } else if constexpr (EPI == kEpiGated) {
                         for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
+                            const uint32_t at = tbase + static_cast<uint32_t>(c - n0);
                             uint32_t h[32];
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
-                                uint32_t v[32];
-                                tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c - n0 + 32 * half), v);
-                                tmem_ld_wait();
-                                if (in && row < job.M) {
-#pragma unroll
-                                    for (int i = 0; i < 32; i += 4) {
-                                        if (c + 32 * half + i < col_end) {
-                                            const float4 a = *reinterpret_cast<const float4*>(in + c + 32 * half + i);
-                                            v[i] = __float_as_uint(__uint_as_float(v[i]) + a.x);
-                                            v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) + a.y);
-                                            v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) + a.z);
-                                            v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + a.w);
-                                        }
-                                    }
-                                }
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    h[16 * half + i] = pack16(scale * __uint_as_float(v[2 * i]),
-                                                              scale * __uint_as_float(v[2 * i + 1]), p.bf16);
-                            }
-                            emit(h, job, &maps.c[job.c_map + t.problem], job.out16[t.problem], row0, c, col_end);
-                        }
-                    }
-                } else if constexpr (EPI == kEpiGated) {
-                    for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
-                        const uint32_t at = tbase + static_cast<uint32_t>(c - n0);
-                        uint32_t h[32];
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t g[32], up[32];
-                            if (c - n0 + 32 * half < p.tile_n) {
-                                tmem_ld_32x32b_x32(at + 32 * half, g);
-                                tmem_ld_32x32b_x32(at + p.tile_n + 32 * half, up);
-                                tmem_ld_wait();
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) g[i] = up[i] = 0u;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                h[16 * half + i] =
-                                    pack16(act_value(__uint_as_float(g[2 * i]), p.act) * __uint_as_float(up[2 * i]),
-                                           act_value(__uint_as_float(g[2 * i + 1]), p.act) *
-                                               __uint_as_float(up[2 * i + 1]),
-                                           p.bf16);
-                        }
-                        emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
-                        if (!p.g_out) continue;
-                        // gate and up themselves, read from tensor memory again:
-                        // kept from above they take more registers than eleven
-                        // warps leave a thread
-#pragma unroll 1
-                        for (int which = 0; which < 2; ++which) {
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                uint32_t v[32];
+                                uint32_t g[32], up[32];
                                 if (c - n0 + 32 * half < p.tile_n) {
-                                    tmem_ld_32x32b_x32(at + which * p.tile_n + 32 * half, v);
+                                    tmem_ld_32x32b_x32(at + 32 * half, g);
+                                    tmem_ld_32x32b_x32(at + p.tile_n + 32 * half, up);
                                     tmem_ld_wait();
                                 } else {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) v[i] = 0u;
+                                    for (int i = 0; i < 32; ++i) g[i] = up[i] = 0u;
                                 }
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
                                     h[16 * half + i] =
-                                        pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), p.bf16);
+                                        pack16(act_value(__uint_as_float(g[2 * i]), p.act) * __uint_as_float(up[2 * i]),
+                                               act_value(__uint_as_float(g[2 * i + 1]), p.act) *
+                                                   __uint_as_float(up[2 * i + 1]),
+                                               p.bf16);
                             }
-                            emit(h, job, &maps.c[1 + which], which ? p.u_out : p.g_out, row0, c, col_end);
-                        }
-                    }
-                } else if constexpr (EPI == kEpiXentGrad) {
-                    // D = coef (exp(z - lse) - [column = target])
-                    const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
-                    const float ref = row < job.M ? p.lse[row] * kLog2e : 0.0f;
-                    const float coef = row < job.M ? p.coef[row] : 0.0f;
-                    for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
-                        uint32_t h[32], lo[32];
+                            emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
+                            if (!p.g_out) continue;
+                            // gate and up themselves, read from tensor memory again:
+                            // kept from above they take more registers than eleven
+                            // warps leave a thread
+#pragma unroll 1
+                            for (int which = 0; which < 2; ++which) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t v[32];
-                            const int cc = c + 32 * half;
-                            tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(cc - n0), v);
-                            tmem_ld_wait();
-                            float d[32];
+                                for (int half = 0; half < 2; ++half) {
+                                    uint32_t v[32];
+                                    if (c - n0 + 32 * half < p.tile_n) {
+                                        tmem_ld_32x32b_x32(at + which * p.tile_n + 32 * half, v);
+                                        tmem_ld_wait();
+                                    } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) d[i] = ex2(fmaf(__uint_as_float(v[i]), kLog2e, -ref));
-                            if (__any_sync(0xffffffffu, tgt >= cc && tgt < cc + 32)) {
+                                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                                    }
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (tgt == cc + i) d[i] -= 1.0f;
-                            }
-                            // a row that does not count is zero whatever its logits are
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float d0 = coef == 0.0f ? 0.0f : coef * d[2 * i];
-                                const float d1 = coef == 0.0f ? 0.0f : coef * d[2 * i + 1];
-                                const uint32_t hi = pack16(d0, d1, p.bf16);
-                                h[16 * half + i] = hi;
-                                const float2 r = unpack16(hi, p.bf16);
-                                lo[16 * half + i] = pack16(d0 - r.x, d1 - r.y, p.bf16);
+                                    for (int i = 0; i < 16; ++i)
+                                        h[16 * half + i] =
+                                            pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), p.bf16);
+                                }
+                                emit(h, job, &maps.c[1 + which], which ? p.u_out : p.g_out, row0, c, col_end);
                             }
                         }
-                        emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
-                        if (p.lo_offset) emit(lo, job, &maps.c[1], job.out16[0] + p.lo_offset, row0, c, col_end);
+                    } else if constexpr (EPI == kEpiXentGrad) {
+                        // D = coef (exp(z - lse) - [column = target])
+                        const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
+                        const float ref = row < job.M ? p.lse[row] * kLog2e : 0.0f;
+                        const float coef = row < job.M ? p.coef[row] : 0.0f;
+                        for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
+                            uint32_t h[32], lo[32];
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t v[32];
+                                const int cc = c + 32 * half;
+                                tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(cc - n0), v);
+                                tmem_ld_wait();
+                                float d[32];
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) d[i] = ex2(fmaf(__uint_as_float(v[i]), kLog2e, -ref));
+                                if (__any_sync(0xffffffffu, tgt >= cc && tgt < cc + 32)) {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (tgt == cc + i) d[i] -= 1.0f;
+                                }
+                                // a row that does not count is zero whatever its logits are
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float d0 = coef == 0.0f ? 0.0f : coef * d[2 * i];
+                                    const float d1 = coef == 0.0f ? 0.0f : coef * d[2 * i + 1];
+                                    const uint32_t hi = pack16(d0, d1, p.bf16);
+                                    h[16 * half + i] = hi;
+                                    const float2 r = unpack16(hi, p.bf16);
+                                    lo[16 * half + i] = pack16(d0 - r.x, d1 - r.y, p.bf16);
+                                }
+                            }
+                            emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
+                            if (p.lo_offset) emit(lo, job, &maps.c[1], job.out16[0] + p.lo_offset, row0, c, col_end);
+                        }
                     }
                 }
+                release();
             }
-            release();
+            if (!alive) break;
         }
         // the staging buffers must stay until the last stores have read them
         if (lane == 0) bulk_wait_group_read<0>();

@@ -30,7 +30,7 @@ struct Product {
 
 // How a launch of one or two products runs: one tile shape and ring for both.
 struct Layout {
-    int cg = 1, bn = 256, tile_n = 256, a_rows = 128;
+    int cg = 1, nw = 1, bn = 256, tile_n = 256, a_rows = 128;
     int stages = 0, boxes = 1, a_bytes = 0, box_bytes = 0, slot_bytes = 0, tx_bytes = 0;
     int first = 0;              // which product is the launch's first job
     int extra_rounds = 0;
@@ -61,7 +61,7 @@ inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t gro
 // Chooses the tile (CTA pair or single CTA, accumulator width) and the K
 // splits with the least estimated time, in SM clocks:
 //   per K block   the larger of the multiplies (a tile of bn columns takes
-//                 2 bn clocks), the copy into shared memory (about 50 bytes a
+//                 2 bn clocks, the wide one 1024), the copy into shared memory (about 50 bytes a
 //                 clock and SM from L2) and a ring slot's share of one
 //                 round trip (1500 clocks over the ring's depth), and a slot's
 //                 handling by the issuing thread (400);
@@ -74,19 +74,22 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
     double best_time = 1e300;
     int64_t rows = 0;
     for (int i = 0; i < n; ++i) rows = pr[i].M > rows ? pr[i].M : rows;
-    for (int cg = 1; cg <= (rows > BM_CTA ? 2 : 1); ++cg) {
-        for (int bn = MAX_BN; bn >= 16; bn -= 16) {
+    for (int kind = 0; kind < (rows > BM_CTA ? 3 : 1); ++kind) {
+        const int cg = kind ? 2 : 1, nw = kind == 2 ? 2 : 1;
+        if (nw == 2 && !pr[0].bmn) continue;
+        for (int bn = MAX_BN; bn >= (nw == 2 ? MAX_BN : 16); bn -= 16) {
             if (cg == 2 && (bn % 32 != 0 || bn < 64)) continue;
             if (pr[0].bmn && (bn / cg) % 64 != 0) continue;
             Layout l;
             l.cg = cg;
+            l.nw = nw;
             l.bn = bn;
             l.tile_n = pr[0].gated ? bn / 2 : bn;
             // a short box for the tokens of a launch that has no more of them
             l.a_rows = BM_CTA;
             if (n == 1 && !pr[0].amn && cg == 1 && rows < BM_CTA) l.a_rows = static_cast<int>(round_up(rows, 8));
             l.a_bytes = l.a_rows * 128;         // (an MN-major A is two boxes of 64 x 64: as many)
-            const int b_bytes = bn / cg * 128;
+            const int b_bytes = nw * (bn / cg) * 128;
             l.tx_bytes = l.a_bytes + b_bytes;
             l.box_bytes = static_cast<int>(round_up(l.tx_bytes, 1024));
             // Narrow tiles take several K blocks to a slot: a wait, a fence and
@@ -102,8 +105,9 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
             const int slack = l.a_rows < BM_CTA ? BM_CTA * 128 : 0;
             l.stages = (RING_BYTES - slack) / l.slot_bytes;
             if (l.stages > MAX_STAGES) l.stages = MAX_STAGES;
+            if (nw == 2) l.stages = WIDE_STAGES;
             const int64_t groups = num_sms / cg;
-            const double trip = 1500.0 / (l.stages * l.boxes), issue = 400.0 / l.boxes, epilogue = 1000.0 + 10.0 * bn;
+            const double trip = 1500.0 / (l.stages * l.boxes), issue = 400.0 / l.boxes, epilogue = 1000.0 + 10.0 * bn * nw;
             double per_kb[2] = {0.0, 0.0};
             // each product's candidate splits: 1, 2, 4, ... up to a full wave of the GPU
             int64_t tiles[2] = {0, 0}, most[2] = {1, 1};
@@ -111,12 +115,12 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
                 Layout::Part& q = l.part[i];
                 // (rows of a box past the matrix are filled, not copied)
                 const double copy = ((pr[i].M < BM_CTA ? pr[i].M : BM_CTA) * 128 + b_bytes) / 50.0;
-                per_kb[i] = 2.0 * bn;
+                per_kb[i] = 2.0 * bn * nw;
                 if (copy > per_kb[i]) per_kb[i] = copy;
                 if (trip > per_kb[i]) per_kb[i] = trip;
                 if (issue > per_kb[i]) per_kb[i] = issue;
                 q.tiles_m = static_cast<int>(cdiv(pr[i].M, BM_CTA * cg));
-                q.tiles_n = static_cast<int>(cdiv(pr[i].N, l.tile_n));
+                q.tiles_n = static_cast<int>(cdiv(pr[i].N, nw * l.tile_n));
                 q.nkb0 = static_cast<int>(cdiv(pr[i].K, BK));
                 q.nkb = q.nkb0 * pr[i].segments;
                 tiles[i] = static_cast<int64_t>(q.tiles_m) * q.tiles_n * pr[i].problems;
@@ -130,11 +134,12 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
                 for (int64_t s1 = 1; s1 <= most[1]; s1 = more(s1, most[1])) {
                     int64_t units[2] = {0, 0};
                     double t[2] = {0.0, 1.0}, time = 1500.0 + epilogue;
-                    bool joins = false;
+                    bool joins = false, long_enough = true;
                     for (int i = 0; i < n; ++i) {
                         Layout::Part& q = l.part[i];
                         q.kb_per_split = static_cast<int>(cdiv(q.nkb, i ? s1 : s0));
                         q.splits = static_cast<int>(cdiv(q.nkb, q.kb_per_split));
+                        if (q.kb_per_split < kWideBlocks) long_enough = false;
                         units[i] = tiles[i] * q.splits;
                         t[i] = q.kb_per_split * per_kb[i];
                         if (t[i] < epilogue) t[i] = epilogue;
@@ -144,6 +149,7 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
                             time += 8.0 * q.splits * pr[i].M * pr[i].N * pr[i].problems / 3000.0;
                         }
                     }
+                    if (nw == 2 && !long_enough) continue;
                     if (joins) time += 4000.0;
                     l.first = n == 2 && t[1] > t[0] ? 1 : 0;
                     const int a = l.first, b = 1 - l.first;
@@ -276,9 +282,9 @@ inline bool output_map(CUtensorMap* map, const Layout& l, const void* out, int64
     return encode_tmap_f16_2d(map, out, N, M, ld * 2, EPI_COLS, 32);
 }
 
-template <int CG, int EPI>
+template <int CG, int EPI, int NW>
 int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStream_t stream) {
-    auto kern = product_kernel<CG, EPI>;
+    auto kern = product_kernel<CG, EPI, NW>;
     static std::atomic<int> capacity[64] = {};
     if (info.device < 0 || info.device >= 64) return GEMM_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
@@ -323,7 +329,9 @@ int launch_cg(const Maps& maps, const Params& p, const DeviceInfo& info, cudaStr
 
 template <int EPI>
 int launch_product(const Layout& l, const Maps& maps, const Params& p, const DeviceInfo& info, cudaStream_t stream) {
-    return l.cg == 2 ? launch_cg<2, EPI>(maps, p, info, stream) : launch_cg<1, EPI>(maps, p, info, stream);
+    if constexpr (EPI == kEpiStore)
+        if (l.nw == 2) return launch_cg<2, EPI, 2>(maps, p, info, stream);
+    return l.cg == 2 ? launch_cg<2, EPI, 1>(maps, p, info, stream) : launch_cg<1, EPI, 1>(maps, p, info, stream);
 }
 
 // Hands out 256-byte aligned parts of a workspace; with no base it only counts.

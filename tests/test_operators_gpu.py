@@ -214,10 +214,23 @@ def test_linear_bwd(M, N, K, dtype):
     check(only_dw, d.t() @ xd, acc_error(M, d.abs().t() @ xd.abs()), dtype)
 
 
+@pytest.mark.parametrize("M,N,K", [(8200, 8200, 520), (8200, 8200, 1030), (2050, 16400, 1032)])
+def test_linear_bwd_long(M, N, K):
+    # K loops of 129 blocks and more: the wide tile alone, for both products,
+    # with stores TMA cannot make, and with a split
+    dy, x, w = rand((M, N), BF16, 44), rand((M, K), BF16, 45), rand((N, K), BF16, 46, 0.1)
+    d, xd, wd = dy.double(), x.double(), w.double()
+    want = ((d @ wd, acc_error(N, d.abs() @ wd.abs())), (d.t() @ xd, acc_error(M, d.abs().t() @ xd.abs())))
+    for needs in (dict(), dict(need_dw=False), dict(need_dx=False)):
+        for got, (ref, tol) in zip(pws.gemm_nt_bwd(dy, x, w, **needs), want):
+            if got is not None:
+                check(got, ref, tol, BF16)
+
+
 def test_linear_bwd_exact_on_small_integers():
     # sums that fp32 and binary16 hold exactly have one right answer, whatever
     # the tile, split or schedule
-    for M, N, K in [(200, 300, 130), (1024, 64, 4096), (64, 2048, 64), (3000, 200, 520), (40, 33, 2000)]:
+    for M, N, K in [(200, 300, 130), (1024, 64, 4096), (64, 2048, 64), (3000, 200, 520), (40, 33, 2000), (8200, 8256, 520)]:
         g = torch.Generator(device="cuda").manual_seed(M)
         dy, x, w = (torch.randint(-1, 2, s, generator=g, device="cuda").half() for s in ((M, N), (M, K), (N, K)))
         dx, dw = pws.gemm_nt_bwd(dy, x, w)
