@@ -290,9 +290,9 @@ extern "C" int gemm_nt_bwd(int64_t M, int64_t N, int64_t K, const void* dy, cons
         return GEMM_OK;
     }
     BwdPlan pl = plan_bwd(M, N, K, dy, x, w, dx != nullptr, dw != nullptr, info.num_sms, workspace);
-    if (pl.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
-                     workspace_bytes < static_cast<int64_t>(pl.bytes)))
-        return GEMM_ERR_INVALID_ARG;
+    const Range in[3] = {{dy, bytes16(M, N)}, {x, bytes16(M, K)}, {w, bytes16(N, K)}};
+    const Range out[2] = {{dx, bytes16(M, K)}, {dw, bytes16(N, K)}};
+    if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, out)) return GEMM_ERR_INVALID_ARG;
     if ((rc = fill_sources({{&pl.dy, M}, {}, {}}, N, stream)) != GEMM_OK) return rc;
     if ((rc = fill_sources({{&pl.x, M}, {&pl.w, N}, {}}, K, stream)) != GEMM_OK) return rc;
     for (int i = 0; i < pl.n; ++i) {

@@ -58,8 +58,8 @@ gated_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ 
             og[j] = pack16(g0, g1, bf16);
             ou[j] = pack16(u0, u1, bf16);
             const float2 cg = unpack16(og[j], bf16), cu = unpack16(ou[j], bf16);
-            rg[j] = pack16(g0 - cg.x, g1 - cg.y, bf16);
-            ru[j] = pack16(u0 - cu.x, u1 - cu.y, bf16);
+            rg[j] = pack16(remainder16(g0, cg.x), remainder16(g1, cg.y), bf16);
+            ru[j] = pack16(remainder16(u0, cu.x), remainder16(u1, cu.y), bf16);
         }
         // (a last chunk's zeros lie inside the padded row)
         *reinterpret_cast<uint4*>(dg + to) = make_uint4(og[0], og[1], og[2], og[3]);
@@ -222,9 +222,9 @@ extern "C" int gemm_gated_nt(int64_t M, int64_t F, int64_t K, const void* x, con
         return zero16(u, M, F, stream);
     }
     GatedPlan pl = plan_gated(M, F, K, x, w_gate, w_up, info.num_sms, workspace);
-    if (pl.bytes && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
-                     workspace_bytes < static_cast<int64_t>(pl.bytes)))
-        return GEMM_ERR_INVALID_ARG;
+    const Range in[3] = {{x, bytes16(M, K)}, {w_gate, bytes16(F, K)}, {w_up, bytes16(F, K)}};
+    const Range out[3] = {{h, bytes16(M, F)}, {g, bytes16(M, F)}, {u, bytes16(M, F)}};
+    if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, out)) return GEMM_ERR_INVALID_ARG;
     if ((rc = fill_sources({{&pl.x, M}, {&pl.wg, F}, {&pl.wu, F}}, K, stream)) != GEMM_OK) return rc;
     Maps maps;
     memset(&maps, 0, sizeof(maps));
@@ -286,9 +286,10 @@ extern "C" int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh
     }
     GatedBwdPlan pl = plan_gated_bwd(M, F, K, x, w_gate, w_up, dx != nullptr, dw_gate != nullptr, info.num_sms,
                                      workspace);
-    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
-        workspace_bytes < static_cast<int64_t>(pl.bytes))
-        return GEMM_ERR_INVALID_ARG;
+    const Range in[6] = {{dh, bytes16(M, F)}, {g, bytes16(M, F)},      {u, bytes16(M, F)},
+                         {x, bytes16(M, K)},  {w_gate, bytes16(F, K)}, {w_up, bytes16(F, K)}};
+    const Range out[3] = {{dx, bytes16(M, K)}, {dw_gate, bytes16(F, K)}, {dw_up, bytes16(F, K)}};
+    if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, out)) return GEMM_ERR_INVALID_ARG;
     if ((rc = fill_sources({{&pl.x, M}, {&pl.wg, F}, {&pl.wu, F}}, K, stream)) != GEMM_OK) return rc;
     {
         int64_t across = cdiv(F, 8 * 256);

@@ -243,9 +243,7 @@ extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, cons
     XentPlan pl;
     if (K > 0) {
         pl = plan_xent(M, V, K, x, w, info.num_sms, workspace);
-        if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
-            workspace_bytes < static_cast<int64_t>(pl.bytes))
-            return GEMM_ERR_INVALID_ARG;
+        if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, out)) return GEMM_ERR_INVALID_ARG;
         if ((rc = fill_sources({{&pl.x, M}, {&pl.w, V}, {}}, K, stream)) != GEMM_OK) return rc;
         Maps maps;
         memset(&maps, 0, sizeof(maps));
@@ -315,9 +313,7 @@ extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, 
     if (M == 0)
         return !dw || cudaMemsetAsync(dw, 0, bytes16(V, K), stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
     XentBwdPlan pl = plan_xent_bwd(M, V, K, x, w, dx != nullptr, dw != nullptr, info.num_sms, workspace);
-    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
-        workspace_bytes < static_cast<int64_t>(pl.bytes))
-        return GEMM_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, out)) return GEMM_ERR_INVALID_ARG;
     if ((rc = fill_sources({{&pl.x, M}, {&pl.w, V}, {}}, K, stream)) != GEMM_OK) return rc;
     if (launch_pdl(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, target, dloss, static_cast<int>(M), V,
                    ignore_index, pl.coef, pl.inv_scale) != cudaSuccess) {

@@ -294,6 +294,12 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// What rounding to 16 bits left of d, for a second 16-bit value beside it; 0
+// where the rounded value is not finite (inf - inf would make it NaN).
+__device__ __forceinline__ float remainder16(float d, float rounded) {
+    return fabsf(rounded) <= 3.4e38f ? d - rounded : 0.0f;
+}
+
 // NW = 2, the wide tile (256 x 512, a CTA pair's): each slot carries two B
 // halves, whose accumulators are the two buffers, so an A slot written once
 // feeds twice the multiplies.  Shared memory bounds the 256 x 256 tile: a K
@@ -963,7 +969,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                                     const uint32_t hi = pack16(d0, d1, p.bf16);
                                     h[16 * half + i] = hi;
                                     const float2 r = unpack16(hi, p.bf16);
-                                    lo[16 * half + i] = pack16(d0 - r.x, d1 - r.y, p.bf16);
+                                    lo[16 * half + i] = pack16(remainder16(d0, r.x), remainder16(d1, r.y), p.bf16);
                                 }
                             }
                             emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);

@@ -428,6 +428,15 @@ bool overlaps(const Range (&in)[NI], const Range (&out)[NO]) {
     }
     return false;
 }
+// Whether a call's workspace will do: there where needed, aligned, large
+// enough, and apart from what the call reads and writes.
+template <int NI, int NO>
+bool workspace_ok(const void* ws, int64_t bytes, size_t need, const Range (&in)[NI], const Range (&out)[NO]) {
+    if (need == 0) return true;
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || bytes < static_cast<int64_t>(need)) return false;
+    const Range w[1] = {{ws, need}};
+    return !overlaps(in, w) && !overlaps(out, w);
+}
 inline uint64_t bytes16(int64_t a, int64_t b) { return static_cast<uint64_t>(a) * static_cast<uint64_t>(b) * 2u; }
 
 }  // namespace fused

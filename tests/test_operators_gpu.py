@@ -165,6 +165,19 @@ def test_gated_bwd(M, F, K, dtype):
     check(only_u, du.t() @ xd, eu.t() @ xd.abs() + acc_error(2 * M, du.abs().t() @ xd.abs()), dtype)
 
 
+def test_gated_bwd_overflow_is_infinite():
+    # a dg past binary16's range is infinite, not NaN, with and without the
+    # remainders that few rows carry
+    for M in (2, 100):
+        F = K = 64
+        one = torch.ones(F, K, device="cuda", dtype=F16)
+        g, u = torch.full((M, F), 10.0, device="cuda", dtype=F16), torch.full((M, F), 100.0, device="cuda", dtype=F16)
+        dh = torch.full((M, F), 60000.0, device="cuda", dtype=F16)
+        x = torch.ones(M, K, device="cuda", dtype=F16)
+        for t in pws.gemm_gated_nt_bwd(dh, g, u, x, one, one):
+            assert torch.isposinf(t).all()
+
+
 def test_gated_gradient_against_differences():
     # the directional difference of sum(dh * h) in float64 against the gradients
     M, F, K, dtype = 24, 80, 48, F16
@@ -535,12 +548,16 @@ def test_example_trains_and_scores():
 
 def test_too_small_a_workspace_is_refused():
     lib = pws.load_library()
-    p = [torch.zeros(1 << 16, device="cuda", dtype=F16).data_ptr() for _ in range(9)]
+    held = [torch.zeros(1 << 16, device="cuda", dtype=F16) for _ in range(9)]
+    p = [t.data_ptr() for t in held]
     bad, half = pws.GEMM_ERR_INVALID_ARG, pws.GEMM_TYPE_HALF
-    for ws, size in ((None, 1 << 30), (p[8] + 2, 1 << 30), (p[8], 16)):
+    # missing, misaligned, too small, on an input (p[0]), on an output (p[3], p[6])
+    for ws, size in ((None, 1 << 30), (p[8] + 2, 1 << 30), (p[8], 16), (p[0], 1 << 30)):
         assert lib.gemm_gated_nt_bwd(4, 8, 16, *p[:6], p[6], None, None, half, 0, ws, size, None) == bad
         assert lib.gemm_xent_nt(4, 8, 16, p[0], p[1], p[2], -100, p[3], p[4], half, ws, size, None) == bad
         assert lib.gemm_xent_nt_bwd(4, 8, 16, p[0], p[1], p[2], -100, p[3], p[4], p[5], None, half, ws, size, None) == bad
         # 9 columns: rows that need a copy
         assert lib.gemm_gated_nt(4, 8, 9, *p[:3], p[3], None, None, half, 0, ws, size, None) == bad
         assert lib.gemm_nt_bwd(4, 9, 16, *p[:3], p[3], None, half, ws, size, None) == bad
+    assert lib.gemm_gated_nt_bwd(4, 8, 16, *p[:6], p[6], None, None, half, 0, p[6], 1 << 30, None) == bad
+    assert lib.gemm_nt_bwd(4, 9, 16, *p[:3], p[3], None, half, p[3], 1 << 30, None) == bad
