@@ -396,6 +396,9 @@ int gemm_f16_nt_plan(int64_t M, int64_t N, int64_t K, const gemm_f16_t* lhs, con
  *     each other.
  *   - Results depend on the arguments alone: no atomics, partial sums are
  *     joined in a fixed order.
+ *   - Waits on the device are bounded as above, and reported by
+ *     gemm_device_status.  Of the debug flags above, GEMM_DEBUG_SKIP_EMPTY_SEED
+ *     applies to these calls as well.
  *   - Return codes: GEMM_OK, GEMM_ERR_INVALID_ARG (a size out of range, a
  *     missing pointer, an unknown type or activation, an overlap, a missing,
  *     misaligned or too small workspace), GEMM_ERR_ALIGNMENT (a pointer not
