@@ -254,7 +254,7 @@ extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, cons
         op.b[0] = pl.w.ptr;
         op.ldb = pl.w.ld;
         if (!set_job(&p, &maps, 0, pl.pr, pl.l, pl.l.part[0], op)) return GEMM_ERR_LAUNCH;
-        p.chunk = kStatsChunk;
+        p.chunk = pl.l.cg == 2 ? kStatsChunk : kStatsChunkSolo;
         p.target = target;
         p.stats = pl.stats;
         p.z_target = pl.z_target;

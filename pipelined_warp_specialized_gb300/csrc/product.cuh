@@ -16,7 +16,7 @@
 //             the groups of CTAs that the first job's last wave leaves idle
 //             start on the second one's tiles.
 //   chunks    the softmax statistics sum each logit over K in chunks of
-//             kStatsChunk blocks, each chunk's tensor-memory sum added in
+//             4 or 8 blocks, each chunk's tensor-memory sum added in
 //             registers (round to nearest): the tensor core's own accumulation
 //             truncates, which over a long K shifts every logit the same way.
 //   splits    few output tiles with a long K are split over K; the fp32
@@ -95,11 +95,15 @@ constexpr int EPI_WARPS = 8;
 constexpr int kMmaWarp = 2;
 constexpr int THREADS = (kMmaWarp + 1 + EPI_WARPS) * 32;
 
-// K blocks per chunk of the softmax statistics' sums (whole slots: kMaxBoxes
-// divides it).
+// K blocks per chunk of the softmax statistics' sums, on a CTA pair and on a
+// single CTA (whole slots: kMaxBoxes divides them).  On a pair 8 take no
+// measurable time (4096 x 131072 x 4096: 2.53 ms with 8 or 64) and 4 take 4 %.
+// A single CTA's product is bound by the weights' bytes, where 4 are free, and
+// its few losses average no error out.
 constexpr int kStatsChunk = 8;
+constexpr int kStatsChunkSolo = 4;
 constexpr int kMaxBoxes = 4;
-static_assert(kStatsChunk % kMaxBoxes == 0, "a chunk ends with a slot");
+static_assert(kStatsChunk % kMaxBoxes == 0 && kStatsChunkSolo % kMaxBoxes == 0, "a chunk ends with a slot");
 
 // One product of a launch.
 struct Job {
