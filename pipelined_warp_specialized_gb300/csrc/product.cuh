@@ -58,7 +58,6 @@ constexpr int MN_BOX = 64 * BK * 2;         // one MN-major box: 64 K rows of 64
 constexpr int WIDE_B = 128 * BK * 2;        // the wide tile's B halves in a slot: one CTA's 128 rows each
 constexpr int WIDE_STAGES = 4;
 constexpr int kWideBlocks = 128;
-constexpr int GROUP_M = 8;                  // tile rows walked together, so their A strips stay in L2
 
 // Shared memory: ring, epilogue staging, barriers.
 constexpr int SMEM_LIMIT = 232448;
@@ -213,6 +212,7 @@ __device__ __forceinline__ void k_range(uint32_t u, const Job& job, Tile& t) {
     t.kb1 = min(job.nkb, t.kb0 + job.kb_per_split);
 }
 
+template <uint32_t GROUP_M>
 __device__ __forceinline__ Tile tile_of(uint32_t u, const Job& job) {
     Tile t;
     k_range(u, job, t);
@@ -225,7 +225,7 @@ __device__ __forceinline__ Tile tile_of(uint32_t u, const Job& job) {
     const uint32_t group = GROUP_M * tiles_n;
     const uint32_t g = r / group;
     const uint32_t first = g * GROUP_M, v = r - g * group;
-    const uint32_t rows = min(tiles_m - first, static_cast<uint32_t>(GROUP_M));
+    const uint32_t rows = min(tiles_m - first, GROUP_M);
     const uint32_t col = rows == GROUP_M ? v / GROUP_M : v / rows;
     t.tm = static_cast<int>(first + v - col * rows);
     t.tn = static_cast<int>(g & 1 ? tiles_n - 1 - col : col);
@@ -321,6 +321,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     static_assert(NW == 1 || (CG == 2 && EPI == kEpiStore), "the wide tile is a CTA pair's, for plain stores");
     constexpr bool BMN = EPI == kEpiStore;
+    // Tile rows walked together, so that their A strips stay in L2 while B
+    // streams by.  Forward products, whose B is the weights: with 16 the head's
+    // 131072 rows are read once for 4096 tokens (2436 us; 2520 with 8, 2591 with
+    // 4).  Backward products: 8 (8192 x 4096 x 8192 643 us; 651 with 16).
+    constexpr uint32_t GROUP_M = EPI == kEpiStore ? 8 : 16;
     // slots of several K blocks, for the narrow tiles of few rows
     constexpr bool MULTI = CG == 1 && EPI != kEpiStore;
     extern __shared__ uint8_t smem_raw[];
@@ -409,7 +414,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             Schedule sched(p, group_id, num_groups);
             for (int jn, u; ok && sched.next(jn, u);) {
                 const Job& job = p.job[jn];
-                const Tile t = tile_of(u, job);
+                const Tile t = tile_of<GROUP_M>(u, job);
                 // the unit's blocks of the first K segment, then of the second
                 const int nkb0 = job.nkb0;
                 for (int seg = 0; ok && seg < 2; ++seg) {
@@ -753,7 +758,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
         Schedule sched(p, group_id, num_groups);
         for (int jn, u; sched.next(jn, u);) {
             const Job& job = p.job[jn];
-            const Tile t = tile_of(u, job);
+            const Tile t = tile_of<GROUP_M>(u, job);
             const int row0 = t.tm * (BM_CTA * CG) + static_cast<int>(rank) * BM_CTA + q * 32;
             const int row = row0 + lane;
             // (the wide tile's halves, one accumulator buffer each, in turn)
