@@ -383,7 +383,7 @@ def gemm_gated_nt_bwd(dh, g, u, x, w_gate, w_up, act: str = "silu", need_dx: boo
     if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
         raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w_gate.shape)}, {tuple(w_up.shape)} do not form "
                          "[M,K], [F,K], [F,K]")
-    if any(tuple(t.shape) != (M, F) for t in (dh, g, u)):
+    if dh.shape != g.shape or u.shape != g.shape or tuple(g.shape) != (M, F):
         raise ValueError(f"{name}: dh, g and u must have shape {(M, F)}")
     lib, device = load_library(), x.device
     s, here = _on(stream, device)

@@ -63,7 +63,7 @@ inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t gro
 //   per K block   the larger of the multiplies (a tile of bn columns takes
 //                 2 bn clocks, the wide one 1024), the copy into shared memory (about 50 bytes a
 //                 clock and SM from L2) and a ring slot's share of one
-//                 round trip (1500 clocks over the ring's depth), and a slot's
+//                 round trip (3000 clocks over the ring's depth), and a slot's
 //                 handling by the issuing thread (400);
 //   per unit      the larger of its K blocks and the epilogue of the unit
 //                 before (1000 + 10 bn), and 300 clocks between units;
@@ -107,7 +107,7 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
             if (l.stages > MAX_STAGES) l.stages = MAX_STAGES;
             if (nw == 2) l.stages = WIDE_STAGES;
             const int64_t groups = num_sms / cg;
-            const double trip = 1500.0 / (l.stages * l.boxes), issue = 400.0 / l.boxes, epilogue = 1000.0 + 10.0 * bn * nw;
+            const double trip = 3000.0 / (l.stages * l.boxes), issue = 400.0 / l.boxes, epilogue = 1000.0 + 10.0 * bn * nw;
             double per_kb[2] = {0.0, 0.0};
             // each product's candidate splits: 1, 2, 4, ... up to a full wave of the GPU
             int64_t tiles[2] = {0, 0}, most[2] = {1, 1};
