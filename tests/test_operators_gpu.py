@@ -319,9 +319,10 @@ def test_xent_bwd(M, V, K, dtype):
     check(only, d @ wd, ed @ wd.abs() + acc_error(2 * V, d.abs() @ wd.abs()) + 2.0 ** -20 * (d.abs() @ wd.abs()), dtype)
 
 
-def test_xent_pieces():
-    # more tokens than one piece's 256 MB of gradients hold at this vocabulary
-    M, V, K = 20000, 9001, 64
+@pytest.mark.parametrize("M,V,K", [(20000, 9001, 64), (9000, 40001, 72)])
+def test_xent_pieces(M, V, K):
+    # more tokens than one piece's 256 MB of gradients hold at this vocabulary:
+    # dx is summed over two pieces, and over three whose own sums are split
     x, w, target, dloss = xent_case(M, V, K, BF16, seed=60)
     loss, lse = pws.gemm_xent_nt(x, w, target)
     dx, dw = pws.gemm_xent_nt_bwd(x, w, target, lse, dloss)
