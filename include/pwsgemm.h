@@ -433,9 +433,14 @@ int gemm_gated_nt_workspace(int64_t M, int64_t F, int64_t K, const void* x, cons
 /*
  * gemm_gated_nt_bwd -- the gradients of gemm_gated_nt from dh and the kept g, u:
  *
- *   dg = dh * u * act'(g),  du = dh * act(g)          (rounded to 16 bits)
+ *   dg = dh * u * act'(g),  du = dh * act(g)
  *   dx      : [M, K] = dg . w_gate + du . w_up        (null: not wanted)
  *   dw_gate : [F, K] = dg^T . x,  dw_up : [F, K] = du^T . x   (both or neither)
+ *
+ * dg and du are rounded to 16 bits; with up to 64 rows to twice as many.  In
+ * binary16 they are scaled first, by a power of two found from the inputs and
+ * undone in fp32, so that none overflows and each is held to half a unit or to
+ * 2^-39 of the largest finite |dh| max(1.13 |u|, g, 0.28), whichever is more.
  */
 int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh, const void* g, const void* u, const void* x,
                       const void* w_gate, const void* w_up, void* dx, void* dw_gate, void* dw_up, int type, int act,

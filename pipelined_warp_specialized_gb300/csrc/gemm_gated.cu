@@ -11,6 +11,14 @@
 // inputs' type because the tensor cores multiply 16-bit operands (the rounding
 // an unfused backward pass makes as well); then dx = dg Wg + du Wu as one
 // accumulation over both weights, and dWg = dg^T x, dWu = du^T x as one launch.
+//
+// In binary16 dh is first multiplied by the power of two that brings a bound of
+// the largest |dg| and |du| (gated_top_kernel) into [2^14, 2^15), undone in fp32
+// when dx, dWg and dWu are rounded: gradients of 1e-5 would otherwise lie below
+// its normal range and lose their bits (dx of 2048 tokens off by 2.2 times its
+// own rounding), and large ones would pass 65504 where dx and dW do not.  An element is
+// then held to half a unit, or to 2^-39 of that bound.  bfloat16 has fp32's range
+// and no scale.
 #include "product_host.cuh"
 
 namespace pws {
@@ -28,9 +36,86 @@ __device__ __forceinline__ uint4 load8(const uint16_t* src, int64_t left) {
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// Binary16: the largest finite |dh| max(1.13 |u|, g, 0.28), one value a block (of
+// kTopParts).  No |dg| or |du| is above it: |act'| < 1.13 and -0.28 < act(g) <=
+// max(g, 0) for both activations, so the pass needs no exponential and is bound by
+// its reads (the exact maximum, with one, took twice as long).  The matrices are
+// dense, so rows do not matter; they are read from the end, so that
+// gated_grad_kernel begins with what L2 still holds.  What the scale costs: the
+// backward pass of 8192 x 8192 x 4096 1444 to 1500 us, of 1000 x 2731 x 1030 38.3
+// to 43.8, of one token through 4096 x 1024 15.1 to 16.9.
+constexpr int kTopParts = 152;
+constexpr int kTopThreads = 1024;
+
+__device__ __forceinline__ float grad_bound(float dh, float g, float u) {
+    return fabsf(dh) * fmaxf(fmaxf(1.13f * fabsf(u), g), 0.28f);
+}
+// The larger of two values, `a` where b is not finite.
+__device__ __forceinline__ float finite_max(float a, float b) { return b <= 3.0e38f ? fmaxf(a, b) : a; }
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kTopThreads)
+gated_top_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g, const uint16_t* __restrict__ u,
+                 int64_t count, float* __restrict__ parts) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    __shared__ float part[kTopThreads / 32];
+    float top = 0.0f;
+    const auto load = [](const uint16_t* src) {
+        return ALIGNED ? __ldg(reinterpret_cast<const uint4*>(src)) : load_unaligned16(src);
+    };
+    const auto take = [&](const uint4& a, const uint4& b, const uint4& d) {
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w}, dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 h2 = unpack16(av[j], 0), g2 = unpack16(bv[j], 0), u2 = unpack16(dv[j], 0);
+            top = finite_max(finite_max(top, grad_bound(h2.x, g2.x, u2.x)), grad_bound(h2.y, g2.y, u2.y));
+        }
+    };
+    // two chunks of eight elements a step: six loads in flight
+    const int64_t chunks = count / 8, step = static_cast<int64_t>(kTopParts) * kTopThreads;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(kTopThreads) + threadIdx.x; i < chunks; i += 2 * step) {
+        const int64_t at = (chunks - 1 - i) * 8, next = i + step < chunks ? at - step * 8 : at;
+        const uint4 a0 = load(dh + at), b0 = load(g + at), d0 = load(u + at);
+        const uint4 a1 = load(dh + next), b1 = load(g + next), d1 = load(u + next);
+        take(a0, b0, d0);
+        take(a1, b1, d1);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0 && count % 8)
+        take(load8(dh + chunks * 8, count % 8), load8(g + chunks * 8, count % 8), load8(u + chunks * 8, count % 8));
+    top = warp_max(top);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        top = warp_max(part[threadIdx.x]);
+        if (threadIdx.x == 0) parts[blockIdx.x] = top;
+    }
+}
+
+// The power of two that brings the largest of the parts into [2^14, 2^15), and
+// its inverse (both normal: the exponent is held at 15 or more).  A warp's work.
+__device__ __forceinline__ float grad_scale(const float* parts, float& inverse) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (kTopParts + 31) / 32; ++i) {
+        const int at = i * 32 + static_cast<int>(threadIdx.x % 32);
+        if (at < kTopParts) top = fmaxf(top, parts[at]);
+    }
+    top = warp_max(top);
+    const int e = max(static_cast<int>(__float_as_uint(top) >> 23), 15);     // biased exponent
+    inverse = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+    return __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+}
+
 // dg, du [M, F] with rows ldo apart (a multiple of 64) from dh, g, u [M, F]
-// (dense); with lo_offset also what their rounding left, that many elements
-// further.  Memory bound: reads three and writes two 16-bit matrices.  Eight
+// (dense), times a power of two (grad_scale) where `parts` is given; with lo_offset
+// also what their rounding left, that many elements further.  Memory bound: reads three and writes two 16-bit matrices.  Eight
 // elements a thread; a block takes one row's next 256 threads' worth, so
 // nothing divides.  Rows that do not start on 16-byte boundaries (odd F) are
 // shifted into place from aligned loads: an element a thread took 14 us
@@ -38,10 +123,16 @@ __device__ __forceinline__ uint4 load8(const uint16_t* src, int64_t left) {
 __global__ void __launch_bounds__(256)
 gated_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g, const uint16_t* __restrict__ u,
                   uint16_t* __restrict__ dg, uint16_t* __restrict__ du, int F, int64_t ldo, int64_t lo_offset, int act,
-                  int bf16) {
+                  int bf16, const float* __restrict__ parts, float* __restrict__ inv_scale) {
     grid_dependency_wait();
     allow_dependent_launch();
     const int64_t row = blockIdx.x;
+    float scale = 1.0f;
+    if (parts) {
+        float inverse;
+        scale = grad_scale(parts, inverse);
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *inv_scale = inverse;
+    }
     for (int64_t c = (blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x) * 8; c < F;
          c += static_cast<int64_t>(gridDim.y) * blockDim.x * 8) {
         const int64_t at = row * F + c, to = row * ldo + c;
@@ -54,7 +145,8 @@ gated_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ 
             float v0, s0, v1, s1;
             act_value_slope(g2.x, act, v0, s0);
             act_value_slope(g2.y, act, v1, s1);
-            const float g0 = h2.x * u2.x * s0, g1 = h2.y * u2.y * s1, u0 = h2.x * v0, u1 = h2.y * v1;
+            const float h0 = scale * h2.x, h1 = scale * h2.y;
+            const float g0 = h0 * u2.x * s0, g1 = h1 * u2.y * s1, u0 = h0 * v0, u1 = h1 * v1;
             og[j] = pack16(g0, g1, bf16);
             ou[j] = pack16(u0, u1, bf16);
             const float2 cg = unpack16(og[j], bf16), cu = unpack16(ou[j], bf16);
@@ -137,12 +229,14 @@ struct GatedBwdPlan {
     Source x, wg, wu;
     uint16_t* dg = nullptr;
     uint16_t* du = nullptr;
+    float* top_parts = nullptr;     // binary16: kTopParts, and the scale's inverse
+    float* inv_scale = nullptr;
     int64_t ldf = 0, lo_offset = 0;
     size_t bytes = 0;
 };
 
 GatedBwdPlan plan_gated_bwd(int64_t M, int64_t F, int64_t K, const void* x, const void* wg, const void* wu,
-                            bool want_dx, bool want_dw, int num_sms, void* ws) {
+                            bool want_dx, bool want_dw, int type, int num_sms, void* ws) {
     GatedBwdPlan pl;
     Carver c;
     c.base = static_cast<char*>(ws);
@@ -151,6 +245,10 @@ GatedBwdPlan plan_gated_bwd(int64_t M, int64_t F, int64_t K, const void* x, cons
     pl.lo_offset = halves == 2 ? M * pl.ldf : 0;
     pl.dg = c.take<uint16_t>(halves * M * pl.ldf);
     pl.du = c.take<uint16_t>(halves * M * pl.ldf);
+    if (type == GEMM_TYPE_HALF) {
+        pl.top_parts = c.take<float>(kTopParts);
+        pl.inv_scale = c.take<float>(1);
+    }
     Product pr[2];
     if (want_dx) {
         // the gate's F and the up projection's F are two segments of K; the
@@ -260,7 +358,7 @@ extern "C" int gemm_gated_nt_bwd_workspace(int64_t M, int64_t F, int64_t K, cons
         const int sms = pws::sm_count_or_default();
         for (int want = 1; want <= 3; ++want) {
             const int64_t b = static_cast<int64_t>(
-                plan_gated_bwd(M, F, K, x, w_gate, w_up, want & 1, want & 2, sms, nullptr).bytes);
+                plan_gated_bwd(M, F, K, x, w_gate, w_up, want & 1, want & 2, type, sms, nullptr).bytes);
             if (b > *bytes) *bytes = b;
         }
     }
@@ -284,26 +382,37 @@ extern "C" int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh
         if ((rc = zero16(dw_gate, F, K, stream)) != GEMM_OK) return rc;
         return zero16(dw_up, F, K, stream);
     }
-    GatedBwdPlan pl = plan_gated_bwd(M, F, K, x, w_gate, w_up, dx != nullptr, dw_gate != nullptr, info.num_sms,
-                                     workspace);
+    GatedBwdPlan pl = plan_gated_bwd(M, F, K, x, w_gate, w_up, dx != nullptr, dw_gate != nullptr, type,
+                                     info.num_sms, workspace);
     const Range in[6] = {{dh, bytes16(M, F)}, {g, bytes16(M, F)},      {u, bytes16(M, F)},
                          {x, bytes16(M, K)},  {w_gate, bytes16(F, K)}, {w_up, bytes16(F, K)}};
     const Range out[3] = {{dx, bytes16(M, K)}, {dw_gate, bytes16(F, K)}, {dw_up, bytes16(F, K)}};
     if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, out)) return GEMM_ERR_INVALID_ARG;
     if ((rc = fill_sources({{&pl.x, M}, {&pl.wg, F}, {&pl.wu, F}}, K, stream)) != GEMM_OK) return rc;
+    if (pl.top_parts) {
+        const auto kern = tma_ok(dh, 0) && tma_ok(g, 0) && tma_ok(u, 0) ? gated_top_kernel<true> : gated_top_kernel<false>;
+        if (launch_pdl(kern, dim3(kTopParts), dim3(kTopThreads), 0, stream, static_cast<const uint16_t*>(dh),
+                       static_cast<const uint16_t*>(g), static_cast<const uint16_t*>(u), M * F, pl.top_parts) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+    }
     {
         int64_t across = cdiv(F, 8 * 256);
         if (across > 65535) across = 65535;
         if (launch_pdl(gated_grad_kernel, dim3(static_cast<unsigned>(M), static_cast<unsigned>(across)), dim3(256), 0, stream,
                        static_cast<const uint16_t*>(dh), static_cast<const uint16_t*>(g),
                        static_cast<const uint16_t*>(u), pl.dg, pl.du, static_cast<int>(F), pl.ldf,
-                       pl.lo_offset, act, type == GEMM_TYPE_BFLOAT ? 1 : 0) != cudaSuccess) {
+                       pl.lo_offset, act, type == GEMM_TYPE_BFLOAT ? 1 : 0,
+                       static_cast<const float*>(pl.top_parts), pl.inv_scale) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_LAUNCH;
         }
     }
     for (int i = 0; i < pl.n; ++i) {
         StoreProduct& q = pl.sp[i];
+        q.scale = pl.inv_scale;
         q.op.lda = pl.ldf;
         if (q.pr.amn) {
             q.op.a[0] = pl.dg;

@@ -1,0 +1,100 @@
+"""Where the operators around the products could lose accuracy without the
+bounds of their other tests showing it: gradients far below and above
+binary16's range, confident targets over a long K, large logits, rows whose
+loss gradient is zero; the wide tile's forms; gradients against differences
+along themselves; sizes at the limit; tensors that require gradients.
+
+Tolerances are derived beside each test, from the rounding of each type (half a
+unit: 2^-11 relative in binary16, 2^-8 in bfloat16, 2^-24 in fp32).
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import pipelined_warp_specialized_gb300 as pws  # noqa: E402
+from test_operators_gpu import BF16, F16, IGNORE, TYPES, acc_error, act64, check, half_unit, rand, xent64  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _no_timeouts():
+    yield
+    if torch.cuda.is_available():
+        assert pws.gemm_device_status() == pws.GEMM_OK
+
+
+# ---------------------------------------------------------------- gated gradients of any size
+
+def gated_grads64(dh, g, u, x, wg, wu, act):
+    value, slope = act64(g.double(), act)
+    dg, du = dh.double() * u.double() * slope, dh.double() * value
+    return dg, du, (dg @ wg.double() + du @ wu.double(), dg.t() @ x.double(), du.t() @ x.double())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("std", [0.02, 1e-4, 1e-5, 1e-6])
+@pytest.mark.parametrize("M", [1, 64, 65, 2048])
+def test_gated_bwd_of_small_gradients(M, std):
+    # Against the error of rounding the exact gradient once, in norm.  Above 64
+    # rows the sums' terms are rounded to as many bits as their result: terms
+    # of random sign, so both errors are the same part of the result's norm
+    # and add as squares: sqrt(2).  Up to 64 rows the terms keep twice the bits.
+    F, K = 1024, 512
+    x, wg, wu = rand((M, K), F16, 1), rand((F, K), F16, 2, K ** -0.5), rand((F, K), F16, 3, K ** -0.5)
+    g, u, dh = rand((M, F), F16, 4), rand((M, F), F16, 5), rand((M, F), torch.float32, 6, std).half()
+    got = pws.gemm_gated_nt_bwd(dh, g, u, x, wg, wu)
+    for have, want in zip(got, gated_grads64(dh, g, u, x, wg, wu, "silu")[2]):
+        once = (want.half().double() - want).norm()
+        assert float((have.double() - want).norm()) <= (1.5 if M > 64 else 1.1) * float(once)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [9, 100])
+def test_gated_bwd_of_gradients_past_the_range(M):
+    # one row's dg is past binary16's range, its products with the weights and
+    # the tokens are within it; the other rows keep what 2^-39 of the largest
+    # |dh| max(1.13 |u|, g, 0.28) leaves them (half of binary16's smallest step,
+    # where that lies in [2^14, 2^15))
+    F, K = 320, 136
+    x, wg, wu = rand((M, K), F16, 11), rand((F, K), F16, 12, 0.004), rand((F, K), F16, 13, 0.004)
+    g, u, dh = rand((M, F), F16, 14), rand((M, F), F16, 15), rand((M, F), F16, 16, 0.02)
+    dh[3] = rand((F,), F16, 17, 1e4).clamp(-3e4, 3e4)
+    u[3] = 20.0
+    x[3] = 0.002
+    for act in ("silu", "gelu"):
+        got = pws.gemm_gated_nt_bwd(dh, g, u, x, wg, wu, act=act)
+        dg, du, want = gated_grads64(dh, g, u, x, wg, wu, act)
+        top = float((dh.double().abs() * torch.maximum(1.13 * u.double().abs(), g.double().clamp(min=0.28))).max())
+        assert float(dg.abs().max()) > 65504 and all(float(t.abs().max()) < 60000 for t in want)
+        # fp32's own error of dg and du, as for the other sizes
+        small = 2.0 ** -19 * dh.double().abs() * (u.double().abs() + 1) * (1 + g.double().abs())
+        bits = 2.0 ** -11 if M > 64 else 2.0 ** -22
+        eg, eu = (small + t.abs() * bits + 2.0 ** -39 * top for t in (dg, du))
+        wgd, wud, xd = wg.double().abs(), wu.double().abs(), x.double().abs()
+        check(got[0], want[0], eg @ wgd + eu @ wud + acc_error(4 * F, dg.abs() @ wgd + du.abs() @ wud), F16)
+        check(got[1], want[1], eg.t() @ xd + acc_error(2 * M, dg.abs().t() @ xd), F16)
+        check(got[2], want[2], eu.t() @ xd + acc_error(2 * M, du.abs().t() @ xd), F16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [3, 80])
+def test_gated_bwd_of_zeros_and_of_what_is_not_finite(M, dtype):
+    # zero gradients give zeros; an infinite or NaN dh stays in its row of dx and
+    # leaves the other rows' bits alone
+    F, K = 96, 72
+    x, wg, wu = rand((M, K), dtype, 21), rand((F, K), dtype, 22, 0.1), rand((F, K), dtype, 23, 0.1)
+    g, u, dh = rand((M, F), dtype, 24), rand((M, F), dtype, 25), rand((M, F), dtype, 26, 0.02)
+    for t in pws.gemm_gated_nt_bwd(torch.zeros_like(dh), g, u, x, wg, wu):
+        assert (t == 0).all()
+    dh[0, 0], u[0, 0], g[0, 0] = 1.0, 3.0, 3.0          # (the largest dg and du, which set their scale)
+    want = pws.gemm_gated_nt_bwd(dh, g, u, x, wg, wu)[0]
+    others = torch.arange(M, device="cuda") != 2
+    for bad in (float("inf"), float("nan")):
+        broken = dh.clone()
+        broken[2, 5] = bad
+        dx, dwg, dwu = pws.gemm_gated_nt_bwd(broken, g, u, x, wg, wu)
+        assert not torch.isfinite(dx[2]).any() and not torch.isfinite(dwg[5]).any()
+        assert torch.isfinite(dwg[4]).all() and torch.isfinite(dwu[4]).all()
+        assert torch.equal(dx[others].view(torch.int16), want[others].view(torch.int16))
