@@ -7,7 +7,8 @@
 // order:  lse = m + log sum_t s_t exp(m_t - m),  loss = lse - z_target.
 //
 // Backward: the vocabulary is taken in pieces.  For each piece the logits are
-// computed again, the epilogue turns them into D = dloss (exp(z - lse) -
+// computed again, summed over K in the forward pass's chunks (in one run, a
+// confident target's 1 - p of 9e-4 was off by 3.5e-4 over K = 8192), the epilogue turns them into D = dloss (exp(z - lse) -
 // onehot) in 16 bits, and the piece's two products follow: dx += D W (fp32
 // between pieces) and the piece's rows of dW = D^T x.  The largest buffer is
 // one piece of D.
@@ -115,11 +116,20 @@ struct XentPlan {
     size_t bytes = 0;
 };
 
+// The logits of `v` columns.  Their chunk goes by the rows alone, so that the
+// forward and the backward pass, whose tiles differ, sum a logit alike.
+Product logits_of(int64_t M, int64_t v, int64_t K) {
+    Product p;
+    p.M = M; p.N = v; p.K = K;
+    p.chunk = M > BM_CTA ? kLogitsChunk : kLogitsChunkFew;
+    return p;
+}
+
 XentPlan plan_xent(int64_t M, int64_t V, int64_t K, const void* x, const void* w, int num_sms, void* ws) {
     XentPlan pl;
     Carver c;
     c.base = static_cast<char*>(ws);
-    pl.pr.M = M; pl.pr.N = V; pl.pr.K = K;
+    pl.pr = logits_of(M, V, K);
     pl.l = choose_layout(pl.pr, num_sms);
     pl.x = source_of(x, M, K, !tma_ok(x, K), &c);
     pl.w = source_of(w, V, K, !tma_ok(w, K), &c);
@@ -146,13 +156,8 @@ struct XentBwdPlan {
     size_t bytes = 0;
 };
 
-// The products of a piece of `v` columns: its logits, then dx and dW, those
-// that are wanted.
-Product logits_of(int64_t M, int64_t v, int64_t K) {
-    Product p;
-    p.M = M; p.N = v; p.K = K;
-    return p;
-}
+// The gradients' products of a piece of `v` columns: dx and dW, those that are
+// wanted.
 int grads_of(int64_t M, int64_t v, int64_t K, int halves, bool want_dx, bool want_dw, Product (&pr)[2]) {
     int n = 0;
     if (want_dx) {
@@ -254,7 +259,6 @@ extern "C" int gemm_xent_nt(int64_t M, int64_t V, int64_t K, const void* x, cons
         op.b[0] = pl.w.ptr;
         op.ldb = pl.w.ld;
         if (!set_job(&p, &maps, 0, pl.pr, pl.l, pl.l.part[0], op)) return GEMM_ERR_LAUNCH;
-        p.chunk = pl.l.cg == 2 ? kStatsChunk : kStatsChunkSolo;
         p.target = target;
         p.stats = pl.stats;
         p.z_target = pl.z_target;

@@ -15,10 +15,12 @@
 //   jobs      two products of different shapes may share a launch (dx and dW):
 //             the groups of CTAs that the first job's last wave leaves idle
 //             start on the second one's tiles.
-//   chunks    the softmax statistics sum each logit over K in chunks of
+//   chunks    the cross entropy's epilogues sum each logit over K in chunks of
 //             4 or 8 blocks, each chunk's tensor-memory sum added in
 //             registers (round to nearest): the tensor core's own accumulation
 //             truncates, which over a long K shifts every logit the same way.
+//             Forward and backward take the same chunks, so that z - lse holds
+//             no difference between two sums of one logit.
 //   splits    few output tiles with a long K are split over K; the fp32
 //             partial sums are joined in a fixed order by a later kernel, so a
 //             result never depends on the order in which CTAs finish.
@@ -94,15 +96,16 @@ constexpr int EPI_WARPS = 8;
 constexpr int kMmaWarp = 2;
 constexpr int THREADS = (kMmaWarp + 1 + EPI_WARPS) * 32;
 
-// K blocks per chunk of the softmax statistics' sums, on a CTA pair and on a
-// single CTA (whole slots: kMaxBoxes divides them).  On a pair 8 take no
-// measurable time (4096 x 131072 x 4096: 2.53 ms with 8 or 64) and 4 take 4 %.
-// A single CTA's product is bound by the weights' bytes, where 4 are free, and
-// its few losses average no error out.
-constexpr int kStatsChunk = 8;
-constexpr int kStatsChunkSolo = 4;
+// K blocks per chunk of the logits' sums, for more rows than a CTA's and for no
+// more (whole slots: kMaxBoxes divides them).  For many rows 8 take no
+// measurable time (loss of 4096 x 131072 x 4096: 2.53 ms with 8 or 64) and 4 take
+// 4 %.  For few rows the product is bound by the weights' bytes, where 4 are
+// free, and few losses average no error out.  In the backward pass they take 0
+// to 2 % (64 tokens over 131072 x 4096 581 to 588 us).
+constexpr int kLogitsChunk = 8;
+constexpr int kLogitsChunkFew = 4;
 constexpr int kMaxBoxes = 4;
-static_assert(kStatsChunk % kMaxBoxes == 0 && kStatsChunkSolo % kMaxBoxes == 0, "a chunk ends with a slot");
+static_assert(kLogitsChunk % kMaxBoxes == 0 && kLogitsChunkFew % kMaxBoxes == 0, "a chunk ends with a slot");
 
 // One product of a launch.
 struct Job {
@@ -768,11 +771,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 tile_end = n0 + p.tile_n;
                 const int col_end = min(job.N, tile_end);
                 uint32_t tbase;
-                if constexpr (EPI == kEpiXentStats) {
-                    // This warp's 32-column groups are 2 j + half of the tile's.
-                    // The logits are summed over K chunk by chunk, then reduced to
-                    // the running maximum m and sum s = sum exp(z - m) of the row.
+                if constexpr (EPI == kEpiXentStats || EPI == kEpiXentGrad) {
+                    // This warp's four 32-column groups: 2 j + half of the tile's, or
+                    // for the gradient those of its 64-column chunks.  The logits
+                    // are summed over K chunk by chunk first.
                     const int half = e >> 2;
+                    const auto group = [&](int j) {
+                        return EPI == kEpiXentStats ? 32 * (2 * j + half)
+                                                    : first_chunk + CHUNK_STEP * (j >> 1) + 32 * (j & 1);
+                    };
                     const bool rows_live = row0 < job.M;
                     float z[4][32];
 #pragma unroll
@@ -785,7 +792,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                         if (rows_live) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const int c = 32 * (2 * j + half);
+                                const int c = group(j);
                                 if (c < p.tile_n) {
                                     // (16 columns at a time: 128 running sums leave
                                     // 40 registers of the 168 a thread can have)
@@ -804,8 +811,49 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     }
                     if (!got) { alive = false; break; }
                     if (!rows_live) continue;
-                    const float inf = __int_as_float(0x7f800000);
                     const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
+                    if constexpr (EPI == kEpiXentGrad) {
+                        // D = coef (exp(z - lse) - [column = target])
+                        const float ref = row < job.M ? p.lse[row] * kLog2e : 0.0f;
+                        const float coef = row < job.M ? p.coef[row] : 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int c = n0 + first_chunk + CHUNK_STEP * k;
+                            if (c >= col_end) continue;
+                            uint32_t h[32], lo[32];
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                float(&d)[32] = z[2 * k + s];
+                                const int cc = c + 32 * s;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) d[i] = ex2(fmaf(d[i], kLog2e, -ref));
+                                if (__any_sync(0xffffffffu, tgt >= cc && tgt < cc + 32)) {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (tgt == cc + i) d[i] -= 1.0f;
+                                }
+                                // a row that does not count is zero whatever its logits are
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float d0 = coef == 0.0f ? 0.0f : coef * d[2 * i];
+                                    const float d1 = coef == 0.0f ? 0.0f : coef * d[2 * i + 1];
+                                    const uint32_t hi = pack16(d0, d1, p.bf16);
+                                    h[16 * s + i] = hi;
+                                    if constexpr (CG == 1) {
+                                        const float2 r = unpack16(hi, p.bf16);
+                                        lo[16 * s + i] = pack16(remainder16(d0, r.x), remainder16(d1, r.y), p.bf16);
+                                    }
+                                }
+                            }
+                            emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
+                            // (remainders are few rows', which a single CTA holds)
+                            if (CG == 1 && p.lo_offset)
+                                emit(lo, job, &maps.c[1], job.out16[0] + p.lo_offset, row0, c, col_end);
+                        }
+                        continue;
+                    }
+                    // Statistics: the running maximum m and sum s = sum exp(z - m) of the row.
+                    const float inf = __int_as_float(0x7f800000);
                     float m = -inf, s = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -948,41 +996,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                                 }
                                 emit(h, job, &maps.c[1 + which], which ? p.u_out : p.g_out, row0, c, col_end);
                             }
-                        }
-                    } else if constexpr (EPI == kEpiXentGrad) {
-                        // D = coef (exp(z - lse) - [column = target])
-                        const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
-                        const float ref = row < job.M ? p.lse[row] * kLog2e : 0.0f;
-                        const float coef = row < job.M ? p.coef[row] : 0.0f;
-                        for (int c = n0 + first_chunk; c < col_end; c += CHUNK_STEP) {
-                            uint32_t h[32], lo[32];
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                uint32_t v[32];
-                                const int cc = c + 32 * half;
-                                tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(cc - n0), v);
-                                tmem_ld_wait();
-                                float d[32];
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) d[i] = ex2(fmaf(__uint_as_float(v[i]), kLog2e, -ref));
-                                if (__any_sync(0xffffffffu, tgt >= cc && tgt < cc + 32)) {
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i)
-                                        if (tgt == cc + i) d[i] -= 1.0f;
-                                }
-                                // a row that does not count is zero whatever its logits are
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float d0 = coef == 0.0f ? 0.0f : coef * d[2 * i];
-                                    const float d1 = coef == 0.0f ? 0.0f : coef * d[2 * i + 1];
-                                    const uint32_t hi = pack16(d0, d1, p.bf16);
-                                    h[16 * half + i] = hi;
-                                    const float2 r = unpack16(hi, p.bf16);
-                                    lo[16 * half + i] = pack16(remainder16(d0, r.x), remainder16(d1, r.y), p.bf16);
-                                }
-                            }
-                            emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
-                            if (p.lo_offset) emit(lo, job, &maps.c[1], job.out16[0] + p.lo_offset, row0, c, col_end);
                         }
                     }
                 }

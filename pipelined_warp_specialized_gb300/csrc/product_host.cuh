@@ -22,9 +22,11 @@ struct Product {
     // 2: A is a 16-bit value and its rounding remainder, M rows each (M counts
     // both); the two halves' outputs are added
     int halves = 1;
+    int chunk = 0;                      // K blocks per accumulator hand-over; 0: a unit's
     bool operator==(const Product& o) const {
         return M == o.M && N == o.N && K == o.K && segments == o.segments && problems == o.problems &&
-               gated == o.gated && amn == o.amn && bmn == o.bmn && may_split == o.may_split && halves == o.halves;
+               gated == o.gated && amn == o.amn && bmn == o.bmn && may_split == o.may_split && halves == o.halves &&
+               chunk == o.chunk;
     }
 };
 
@@ -63,8 +65,10 @@ inline double makespan(int64_t u0, double t0, int64_t u1, double t1, int64_t gro
 //   per K block   the larger of the multiplies (a tile of bn columns takes
 //                 2 bn clocks, the wide one 1024), the copy into shared memory (about 50 bytes a
 //                 clock and SM from L2) and a ring slot's share of one
-//                 round trip (3000 clocks over the ring's depth), and a slot's
-//                 handling by the issuing thread (400);
+//                 round trip (3000 clocks over the ring's depth), a slot's
+//                 handling by the issuing thread (400), and a chunk's share of its
+//                 hand-over to the epilogue (1200: one token's head of 50001 x 2048
+//                 takes 37 us with the 112 columns this gives it, 50 with 48);
 //   per unit      the larger of its K blocks and the epilogue of the unit
 //                 before (1000 + 10 bn), and 300 clocks between units;
 //   per launch    a fill and a last epilogue (1500 + that);
@@ -119,6 +123,7 @@ inline Layout best_layout(const Product* pr, int n, int num_sms) {
                 if (copy > per_kb[i]) per_kb[i] = copy;
                 if (trip > per_kb[i]) per_kb[i] = trip;
                 if (issue > per_kb[i]) per_kb[i] = issue;
+                if (pr[i].chunk && 1200.0 / pr[i].chunk > per_kb[i]) per_kb[i] = 1200.0 / pr[i].chunk;
                 q.tiles_m = static_cast<int>(cdiv(pr[i].M, BM_CTA * cg));
                 q.tiles_n = static_cast<int>(cdiv(pr[i].N, nw * l.tile_n));
                 q.nkb0 = static_cast<int>(cdiv(pr[i].K, BK));
@@ -207,7 +212,6 @@ inline Params base_params(const Layout& l, int type, const DeviceInfo& info, cud
     Params p;
     memset(&p, 0, sizeof(p));
     p.extra_rounds = l.extra_rounds;
-    p.chunk = 1 << 30;
     p.bn = l.bn;
     p.tile_n = l.tile_n;
     p.stages = l.stages;
@@ -236,6 +240,7 @@ struct Operands {
 // the first's).
 inline bool set_job(Params* p, Maps* maps, int at, const Product& pr, const Layout& l, const Layout::Part& part,
                     const Operands& op) {
+    p->chunk = pr.chunk ? pr.chunk : 1 << 30;
     Job& j = p->job[at];
     j.M = static_cast<int>(pr.M);
     j.N = static_cast<int>(pr.N);

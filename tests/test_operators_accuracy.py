@@ -98,3 +98,33 @@ def test_gated_bwd_of_zeros_and_of_what_is_not_finite(M, dtype):
         assert not torch.isfinite(dx[2]).any() and not torch.isfinite(dwg[5]).any()
         assert torch.isfinite(dwg[4]).all() and torch.isfinite(dwu[4]).all()
         assert torch.equal(dx[others].view(torch.int16), want[others].view(torch.int16))
+
+
+# ---------------------------------------------------------------- cross entropy
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [1, 64, 65, 300])
+def test_xent_bwd_of_confident_targets_over_a_long_k(M, dtype):
+    # Two classes with logits 7 and 0: D's entries are -(1 - p) and 1 - p with
+    # 1 - p = 9e-4, so their sum (read off a column that is 1 in every class and 0
+    # in every token) shows any difference between the logits here and those in
+    # lse.  What is left is lse's rounding (2^-22 for [4, 8)), that of the sum
+    # of exponentials and of the exponential itself (2^-21 each), and D's own
+    # rounding above 64 rows; an accumulator that loses half a unit at each of
+    # the K / 16 additions is off by 512 of them.
+    K = 8192
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    x = (torch.rand((M, K), generator=gen, device="cuda") + 0.5).to(dtype)
+    w = torch.zeros((2, K), device="cuda", dtype=dtype)
+    w[1] = ((torch.rand(K, generator=gen, device="cuda") + 0.5) * (7.0 / K)).to(dtype)
+    x[:, 5], w[:, 5] = 0.0, 1.0
+    target = torch.ones(M, dtype=torch.int64, device="cuda")
+    _, lse = pws.gemm_xent_nt(x, w, target)
+    dx, _ = pws.gemm_xent_nt_bwd(x, w, target, lse, torch.ones(M, device="cuda"))
+    z = x.double() @ w.double().t()
+    assert (z[:, 0] == 0).all() and (z[:, 1] > 6).all() and (lse < 8).all()
+    rest = torch.sigmoid(z[:, 0] - z[:, 1])
+    bits = {F16: 2.0 ** -11, BF16: 2.0 ** -8}[dtype]
+    tol = 2.0 ** -22 + 3 * 2.0 ** -21 + (2 * bits * rest if M > 64 else 0.0)
+    assert (dx[:, 5].double().abs() <= tol * (1 + bits) + 2.0 ** -25).all(), float(dx[:, 5].abs().max())
