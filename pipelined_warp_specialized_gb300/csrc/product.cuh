@@ -243,6 +243,10 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// exp(x - ref).  The difference comes first: it is exact where x is near ref, which
+// the fused x log2 e - round(ref log2 e) is not (at 100 it is off by 5e-6).
+__device__ __forceinline__ float exp_from(float x, float ref) { return ex2((x - ref) * kLog2e); }
+
 // Both activations are g * sigma(s(g)): silu with s = g, gelu (tanh form)
 // with s = 2 sqrt(2/pi) (g + 0.044715 g^3), since (1 + tanh y) / 2 = sigma(2 y).
 constexpr float kGeluC = 1.5957691216057308f;       // 2 sqrt(2 / pi)
@@ -814,7 +818,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     const int64_t tgt = row < job.M ? p.target[row] - p.col0 : -1;
                     if constexpr (EPI == kEpiXentGrad) {
                         // D = coef (exp(z - lse) - [column = target])
-                        const float ref = row < job.M ? p.lse[row] * kLog2e : 0.0f;
+                        const float lse = row < job.M ? p.lse[row] : 0.0f;
                         const float coef = row < job.M ? p.coef[row] : 0.0f;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -826,7 +830,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                                 float(&d)[32] = z[2 * k + s];
                                 const int cc = c + 32 * s;
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) d[i] = ex2(fmaf(d[i], kLog2e, -ref));
+                                for (int i = 0; i < 32; ++i) d[i] = exp_from(d[i], lse);
                                 if (__any_sync(0xffffffffu, tgt >= cc && tgt < cc + 32)) {
 #pragma unroll
                                     for (int i = 0; i < 32; ++i)
@@ -876,15 +880,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
 #pragma unroll
                         for (int i = 0; i < 32; ++i) top = fmaxf(top, z[j][i]);
                         // a row of -inf so far: any finite reference gives exp(-inf) = 0
-                        const float ref = top == -inf ? 0.0f : top * kLog2e;
-                        s *= ex2(m * kLog2e - ref);
+                        const float ref = top == -inf ? 0.0f : top;
+                        s *= exp_from(m, ref);
                         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
-                            s0 += ex2(fmaf(z[j][i], kLog2e, -ref));
-                            s1 += ex2(fmaf(z[j][i + 1], kLog2e, -ref));
-                            s2 += ex2(fmaf(z[j][i + 2], kLog2e, -ref));
-                            s3 += ex2(fmaf(z[j][i + 3], kLog2e, -ref));
+                            s0 += exp_from(z[j][i], ref);
+                            s1 += exp_from(z[j][i + 1], ref);
+                            s2 += exp_from(z[j][i + 2], ref);
+                            s3 += exp_from(z[j][i + 3], ref);
                         }
                         s += (s0 + s1) + (s2 + s3);
                         m = top;

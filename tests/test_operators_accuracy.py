@@ -128,3 +128,50 @@ def test_xent_bwd_of_confident_targets_over_a_long_k(M, dtype):
     bits = {F16: 2.0 ** -11, BF16: 2.0 ** -8}[dtype]
     tol = 2.0 ** -22 + 3 * 2.0 ** -21 + (2 * bits * rest if M > 64 else 0.0)
     assert (dx[:, 5].double().abs() <= tol * (1 + bits) + 2.0 ** -25).all(), float(dx[:, 5].abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [200, 700, 20003])
+def test_lse_of_large_logits(V):
+    # z = t_i + s_i c_v, multiples of 2^-14 below 2^7 that every sum holds exactly:
+    # what is off in lse is its own rounding (half a unit of [64, 128): 2^-18) and
+    # the relative error of the sum of exponentials: 2^-22 each from the
+    # exponential, its argument (z - max, exact, times log2 e, below 2^4) and the
+    # maximum's rescaling, 2^-24 for each of some 20 levels of sums, and the
+    # logarithm's last place: 2^-19 in all
+    M, K = 300, 16
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    x, w = torch.zeros((M, K), device="cuda", dtype=F16), torch.zeros((V, K), device="cuda", dtype=F16)
+    x[:, 0] = torch.randint(70 * 16, 110 * 16, (M,), generator=gen, device="cuda") / 16
+    w[:, 0] = 1.0
+    x[:, 1] = torch.randint(32, 65, (M,), generator=gen, device="cuda") / 64
+    w[:, 1] = torch.randint(-4 * 256, 4 * 256, (V,), generator=gen, device="cuda") / 256
+    target = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    z, want, _, loss64 = xent64(x, w, target)
+    assert float(want.max()) < 128
+    for rows in (M, 7):
+        loss, lse = pws.gemm_xent_nt(x[:rows].contiguous(), w, target[:rows])
+        assert ((lse.double() - want[:rows]).abs() <= 2.0 ** -18 + 2.0 ** -19).all()
+        # (the loss is exact in lse and a logit that fp32 holds)
+        assert ((loss.double() - loss64[:rows]).abs() <= 2.0 ** -18 + 2.0 ** -19).all()
+
+
+@pytest.mark.gpu
+def test_xent_bwd_of_large_logits():
+    # D of the target is exp(z - lse) - 1, here with lse = z + 2^-8 handed in:
+    # z and lse are exact, so are their difference and D up to the exponential's
+    # 2^-22 and the argument's rounding; read off columns of w that are one class each
+    M, V = 64, 40
+    K = 8 + V
+    x, w = torch.zeros((M, K), device="cuda", dtype=F16), torch.zeros((V, K), device="cuda", dtype=F16)
+    x[:, 0] = 70.0 + torch.arange(M, device="cuda") / 2
+    w[:, 0] = 1.0
+    w[torch.arange(V), 8 + torch.arange(V)] = 1.0
+    target = torch.arange(M, device="cuda") % V
+    lse = x[:, 0].float() + 2.0 ** -8
+    dx, _ = pws.gemm_xent_nt_bwd(x, w, target, lse, torch.ones(M, device="cuda"))
+    p = math.exp(-2.0 ** -8)
+    want = torch.full((M, V), p, device="cuda", dtype=torch.float64)
+    want[torch.arange(M), target] = math.expm1(-2.0 ** -8)
+    err = (dx[:, 8:].double() - want).abs()
+    assert (err <= half_unit(want, F16) + 2.0 ** -21).all(), float((err / half_unit(want, F16)).max())
