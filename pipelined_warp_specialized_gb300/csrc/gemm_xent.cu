@@ -342,6 +342,7 @@ extern "C" int gemm_xent_nt_bwd(int64_t M, int64_t V, int64_t K, const void* x, 
             p.target = target;
             p.lse = lse;
             p.coef = pl.coef;
+            p.ignore_index = ignore_index;
             p.col0 = v0;
             p.lo_offset = pl.lo_offset;
             Job& j = p.job[0];

@@ -152,7 +152,8 @@ struct Params {
     float2* stats;                  // [M][2 tiles_n]: maximum and sum of exponentials of half a tile's columns
     float* z_target;                // [M]
     const float* lse;
-    const float* coef;              // [M]: scaled loss gradient; 0 for a row that does not count
+    const float* coef;              // [M]: scaled loss gradient
+    int64_t ignore_index;           // a target of a row that does not count: D is 0 there
     int64_t col0;                   // vocabulary index of column 0
     int64_t lo_offset;              // elements from D to its rounding remainder, 0 for none
 };
@@ -820,6 +821,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                         // D = coef (exp(z - lse) - [column = target])
                         const float lse = row < job.M ? p.lse[row] : 0.0f;
                         const float coef = row < job.M ? p.coef[row] : 0.0f;
+                        const bool counts = row < job.M && p.target[row] != p.ignore_index;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int c = n0 + first_chunk + CHUNK_STEP * k;
@@ -839,8 +841,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                                 // a row that does not count is zero whatever its logits are
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
-                                    const float d0 = coef == 0.0f ? 0.0f : coef * d[2 * i];
-                                    const float d1 = coef == 0.0f ? 0.0f : coef * d[2 * i + 1];
+                                    const float d0 = counts ? coef * d[2 * i] : 0.0f;
+                                    const float d1 = counts ? coef * d[2 * i + 1] : 0.0f;
                                     const uint32_t hi = pack16(d0, d1, p.bf16);
                                     h[16 * s + i] = hi;
                                     if constexpr (CG == 1) {

@@ -175,3 +175,25 @@ def test_xent_bwd_of_large_logits():
     want[torch.arange(M), target] = math.expm1(-2.0 ** -8)
     err = (dx[:, 8:].double() - want).abs()
     assert (err <= half_unit(want, F16) + 2.0 ** -21).all(), float((err / half_unit(want, F16)).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [6, 130])
+def test_xent_bwd_of_rows_with_no_loss_gradient(M, dtype):
+    # dloss = 0 gives zero times D: 0 for finite logits, NaN where the row
+    # counts and a logit is NaN or infinite, 0 where the row does not count
+    V, K = 300, 72
+    x, w = rand((M, K), dtype, 31), rand((V, K), dtype, 32, 0.2)
+    target = torch.randint(0, V, (M,), generator=torch.Generator(device="cuda").manual_seed(33), device="cuda")
+    dloss = torch.ones(M, device="cuda")
+    dloss[1] = dloss[2] = dloss[3] = 0.0
+    dloss[3] *= -1.0
+    x[2, 7] = x[4, 7] = float("nan")
+    target[4] = IGNORE
+    _, lse = pws.gemm_xent_nt(x, w, target)
+    assert torch.isnan(lse[2]) and torch.isnan(lse[4])
+    dx, _ = pws.gemm_xent_nt_bwd(x, w, target, lse, dloss, need_dw=False)
+    assert torch.isnan(dx[2]).all()
+    assert (dx[1] == 0).all() and (dx[3] == 0).all() and (dx[4] == 0).all()
+    assert torch.isfinite(dx[5:]).all() and (dx[5:] != 0).any(1).all()
