@@ -382,7 +382,7 @@ int gemm_f16_nt_plan(int64_t M, int64_t N, int64_t K, const gemm_f16_t* lhs, con
  *
  * Conventions beyond the ones above:
  *   - Matrices are dense, row-major, of 16-bit elements of one type
- *     (gemm_type), 2-byte aligned; any size from 0 below 2^31.  Sums,
+ *     (gemm_type), 2-byte aligned; any size from 0 to 2^31 - 1024.  Sums,
  *     activations, softmax statistics and losses are fp32; an output is
  *     rounded once from its fp32 value (nearest, ties to even).
  *   - `workspace` is device memory of the caller, 256-byte aligned, of at

@@ -412,7 +412,10 @@ int run_store_products(const StoreProduct* sp, int n, const Layout& l, int type,
 
 // ---- argument checks
 
-inline bool bad_size(int64_t n) { return n < 0 || n >= (1ll << 31); }
+// Rows and columns are counted in an int, and a tile's end may lie up to 512
+// past the last of them.
+constexpr int64_t kMaxSize = (1ll << 31) - 1024;
+inline bool bad_size(int64_t n) { return n < 0 || n > kMaxSize; }
 inline bool odd_address(const void* p) { return reinterpret_cast<uintptr_t>(p) & 1u; }
 // accumulator tiles are counted in an int
 inline bool too_many_tiles(int64_t rows, int64_t cols) { return cdiv(rows, 128) * cdiv(cols, 16) >= (1ll << 31); }

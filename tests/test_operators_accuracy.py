@@ -7,6 +7,7 @@ along themselves; sizes at the limit; tensors that require gradients.
 Tolerances are derived beside each test, from the rounding of each type (half a
 unit: 2^-11 relative in binary16, 2^-8 in bfloat16, 2^-24 in fp32).
 """
+import ctypes
 import math
 
 import pytest
@@ -197,3 +198,42 @@ def test_xent_bwd_of_rows_with_no_loss_gradient(M, dtype):
     assert torch.isnan(dx[2]).all()
     assert (dx[1] == 0).all() and (dx[3] == 0).all() and (dx[4] == 0).all()
     assert torch.isfinite(dx[5:]).all() and (dx[5:] != 0).any(1).all()
+
+
+# ---------------------------------------------------------------- the largest sizes
+
+# fake, 256-byte aligned addresses far apart: never read, the calls below are
+# refused or only count a workspace
+AT = [(i + 1) << 48 for i in range(12)]
+LARGEST = 2 ** 31 - 1024
+
+
+def test_sizes_whose_tiles_would_pass_32_bits_are_refused():
+    # Columns are counted in 32 bits, and the last tile's end, up to 512 past the
+    # last column, has to fit: above 2^31 - 1024 it wrapped, and the tile's
+    # columns were not written (or, between widths, others were)
+    from pipelined_warp_specialized_gb300 import build as libbuild
+    libbuild.build()
+    lib = pws.load_library()
+    H, bad = pws.GEMM_TYPE_HALF, pws.GEMM_ERR_INVALID_ARG
+    calls = {
+        "gemm_gated_nt": lambda d: (*d, *AT[:4], None, None, H, 0, None, 0, None),
+        "gemm_gated_nt_bwd": lambda d: (*d, *AT[:6], *AT[6:9], H, 0, AT[9], 1 << 47, None),
+        "gemm_xent_nt": lambda d: (*d, *AT[:3], -100, *AT[3:5], H, AT[5], 1 << 47, None),
+        "gemm_xent_nt_bwd": lambda d: (*d, *AT[:3], -100, *AT[3:7], H, AT[7], 1 << 47, None),
+        "gemm_nt_bwd": lambda d: (*d, *AT[:5], H, AT[5], 1 << 47, None),
+    }
+    for name, args in calls.items():
+        for i in range(3):
+            for size in (LARGEST + 1, 2 ** 31 - 1):
+                dims = [4, 8, 16]
+                dims[i] = size
+                assert getattr(lib, name)(*args(dims)) == bad, (name, dims)
+    # the largest sizes themselves are taken
+    pointers = {"gemm_gated_nt": 3, "gemm_gated_nt_bwd": 6, "gemm_xent_nt": 2, "gemm_xent_nt_bwd": 2, "gemm_nt_bwd": 3}
+    for name, count in pointers.items():
+        for i in range(3):
+            dims = [4, 8, 16]
+            dims[i] = LARGEST
+            n = ctypes.c_int64()
+            assert getattr(lib, name + "_workspace")(*dims, *AT[:count], H, ctypes.byref(n)) == pws.GEMM_OK, (name, dims)
