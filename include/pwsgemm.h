@@ -467,9 +467,17 @@ int gemm_xent_nt_workspace(int64_t M, int64_t V, int64_t K, const void* x, const
  *
  *   D[i][v] = dloss[i] (exp(z[i][v] - lse[i]) - [v == target[i]]), 0 in rows
  *             whose target is ignore_index, NaN in rows of any other target
- *             outside [0, V); rounded to 16 bits at a scale that keeps it in range
+ *             outside [0, V)
  *   dx : [M, K] = D . w   (null: not wanted)
  *   dw : [V, K] = D^T . x (null: not wanted)
+ *
+ * D is rounded to 16 bits; with up to 64 rows to twice as many.  In binary16 it
+ * is scaled first, for all rows alike, so that the largest finite |dloss| of a
+ * row that counts becomes 2^13: an element is held to half a unit or to 2^-38 of
+ * that |dloss|, whichever is more.  A row whose dloss is 2^-20 of the largest so
+ * keeps its target's entry whole, but its probabilities in steps of 2^-17 only:
+ * where losses are weighted that far apart, take bfloat16 or one call for each
+ * size of weights.
  *
  * lse is gemm_xent_nt's.  The vocabulary is taken in pieces and the logits of
  * a piece are computed again; the workspace holds one piece of D.

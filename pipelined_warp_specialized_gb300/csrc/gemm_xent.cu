@@ -17,8 +17,9 @@
 // operands of one type.  It is scaled so that the largest |dloss| becomes 2^13,
 // undone in fp32 when dx and dW are rounded: without it binary16 would lose
 // the probabilities below 6e-8 / dloss, and with it the usual uniform dloss
-// adds no rounding of its own (2^13 (p - 1) rounds as p - 1 does).  With few
-// rows D keeps its rounding remainder too (kFewRows).
+// adds no rounding of its own (2^13 (p - 1) rounds as p - 1 does).  One scale serves
+// all rows, since dW sums over them: an element keeps half a unit or 2^-38 of the
+// largest |dloss|.  With few rows D keeps its rounding remainder too (kFewRows).
 #include "product_host.cuh"
 
 namespace pws {

@@ -200,6 +200,35 @@ def test_xent_bwd_of_rows_with_no_loss_gradient(M, dtype):
     assert torch.isfinite(dx[5:]).all() and (dx[5:] != 0).any(1).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [40, 200])
+def test_xent_bwd_of_loss_gradients_of_many_sizes(M, dtype):
+    # dloss over 24 powers of two.  Binary16 holds an element of D to half a
+    # unit of its own, or to half its smallest step at the scale that brings
+    # the largest |dloss| to 2^13: 2^-38 of that; bfloat16 to half a unit.
+    V, K = 1000, 72
+    x, w = rand((M, K), dtype, 41), rand((V, K), dtype, 42, 0.5 * K ** -0.5)
+    target = torch.randint(0, V, (M,), generator=torch.Generator(device="cuda").manual_seed(43), device="cuda")
+    dloss = 1024.0 * 2.0 ** -(torch.arange(M, device="cuda") % 25).float()
+    _, lse = pws.gemm_xent_nt(x, w, target)
+    dx, dw = pws.gemm_xent_nt_bwd(x, w, target, lse, dloss)
+    z, lse64, _, _ = xent64(x, w, target)
+    p = torch.exp(z - lse64[:, None])
+    hit = torch.zeros_like(p)
+    hit[torch.arange(M), target] = 1.0
+    c = dloss.double()[:, None]
+    d = c * (p - hit)
+    xd, wd = x.double(), w.double()
+    ez = acc_error(K, xd.abs() @ wd.abs().t())
+    ed = c * p * (ez + ez.max(1, keepdim=True).values + 2.0 ** -18)
+    bits = {F16: 2.0 ** -11, BF16: 2.0 ** -8}[dtype]
+    ed = ed + d.abs() * (bits if M > 64 else bits * bits) + (2.0 ** -38 * 1024 if dtype == F16 else 0.0)
+    check(dx, d @ wd, ed @ wd.abs() + acc_error(2 * V, d.abs() @ wd.abs()) + 2.0 ** -20 * (d.abs() @ wd.abs()), dtype)
+    check(dw, d.t() @ xd, ed.t() @ xd.abs() + acc_error(2 * M, d.abs().t() @ xd.abs()) +
+          2.0 ** -20 * (d.abs().t() @ xd.abs()), dtype)
+
+
 # ---------------------------------------------------------------- the largest sizes
 
 # fake, 256-byte aligned addresses far apart: never read, the calls below are
