@@ -229,6 +229,89 @@ def test_xent_bwd_of_loss_gradients_of_many_sizes(M, dtype):
           2.0 ** -20 * (d.abs().t() @ xd.abs()), dtype)
 
 
+# ---------------------------------------------------------------- gradients against differences
+
+def along(value, at, grads):
+    """For each argument i: the central difference of value in float64 along
+    grads[i] / |grads[i]|, and |grads[i]|.  For exact gradients they are equal;
+    errors of root sum square e move their difference by no more than e."""
+    out = []
+    for i, grad in enumerate(grads):
+        grad = grad.double()
+        size = float(grad.norm())
+        e = 1e-5
+        hi, lo = list(at), list(at)
+        hi[i], lo[i] = at[i] + e * grad / size, at[i] - e * grad / size
+        out.append((float(value(*hi) - value(*lo)) / (2 * e), size))
+    return out
+
+
+def gated_value(dh, act):
+    def value(x, wg, wu):
+        return (dh.double() * act64(x @ wg.t(), act)[0] * (x @ wu.t())).sum()
+    return value
+
+
+# Each gradient is rounded once (2^-11 of itself) and comes from g and u rounded
+# to binary16: relative errors of 2^-11 in u and, times |g act''| <= 1.2 |act'| in
+# norm over N(0, 1) gates, in act'; independent, over sums of dozens of
+# terms, so they stay at a few 2^-11 of the norm.
+GATED_ALONG = 8 * 2.0 ** -11
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [24, 100])
+def test_gated_gradient_along_itself(M, act):
+    F, K = 80, 48
+    x, wg, wu, dh = rand((M, K), F16, 51), rand((F, K), F16, 52, 0.15), rand((F, K), F16, 53, 0.15), rand((M, F), F16, 54)
+    _, g, u = pws.gemm_gated_nt(x, wg, wu, act=act, save=True)
+    grads = pws.gemm_gated_nt_bwd(dh, g, u, x, wg, wu, act=act)
+    at = [x.double(), wg.double(), wu.double()]
+    for diff, size in along(gated_value(dh, act), at, grads):
+        assert abs(diff - size) <= GATED_ALONG * size
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_a_wrong_slope_shows_along_the_gradient(act):
+    # the comparison itself, on the host: exact gradients pass by far; slopes
+    # without their second term or of the other activation do not (dWg), nor does
+    # the other activation's value (dWu)
+    M, F, K = 24, 80, 48
+    gen = torch.Generator().manual_seed(55)
+
+    def normal(rows, cols, std=1.0):
+        return torch.randn(rows, cols, generator=gen, dtype=torch.float64) * std
+
+    x, wg, wu, dh = normal(M, K), normal(F, K, 0.15), normal(F, K, 0.15), normal(M, F)
+    g, u = x @ wg.t(), x @ wu.t()
+    value, slope = act64(g, act)
+    sigma = torch.where(g == 0, torch.full_like(g, 0.5), value / g)     # act(g) = g sigma(s(g))
+    other_value, other_slope = act64(g, "gelu" if act == "silu" else "silu")
+    for v, s, wrong in ((value, slope, None), (value, sigma, 1), (value, other_slope, 1), (other_value, slope, 2)):
+        dg, du = dh * u * s, dh * v
+        off = [abs(d - n) / n for d, n in along(gated_value(dh, act), [x, wg, wu],
+                                                (dg @ wg + du @ wu, dg.t() @ x, du.t() @ x))]
+        assert max(off) <= 1e-6 if wrong is None else off[wrong] > 1.5 * GATED_ALONG, off
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [20, 90])
+def test_xent_gradient_along_itself(M):
+    # the gradients' own rounding (2^-11) and, above 64 rows, D's (2^-11): twice
+    # 2^-11 of the norm if all of it lay along the gradient
+    V, K = 90, 32
+    x, w = rand((M, K), F16, 61), rand((V, K), F16, 62, 0.4)
+    gen = torch.Generator(device="cuda").manual_seed(63)
+    target = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    target[::5] = IGNORE
+    dloss = torch.rand(M, generator=gen, device="cuda")
+    _, lse = pws.gemm_xent_nt(x, w, target)
+    grads = pws.gemm_xent_nt_bwd(x, w, target, lse, dloss)
+    for diff, size in along(lambda a, b: (xent64(a, b, target)[3] * dloss.double()).sum(), [x.double(), w.double()], grads):
+        assert abs(diff - size) <= 2 * 2.0 ** -11 * size
+
+
 # ---------------------------------------------------------------- the largest sizes
 
 # fake, 256-byte aligned addresses far apart: never read, the calls below are
