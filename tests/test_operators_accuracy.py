@@ -312,6 +312,52 @@ def test_xent_gradient_along_itself(M):
         assert abs(diff - size) <= 2 * 2.0 ** -11 * size
 
 
+# ---------------------------------------------------------------- the wide tile's forms
+
+@pytest.mark.gpu
+def test_gated_bwd_on_the_wide_tile():
+    # 129 K blocks and more in both products: dx accumulates over two segments,
+    # both weights' gradients are one job, and the last tile is ragged
+    M, F, K = 8200, 4168, 264
+    x, wg, wu = rand((M, K), BF16, 71), rand((F, K), BF16, 72, 0.05), rand((F, K), BF16, 73, 0.05)
+    g, u, dh = rand((M, F), BF16, 74), rand((M, F), BF16, 75), rand((M, F), BF16, 76, 0.02)
+    dg, du, want = gated_grads64(dh, g, u, x, wg, wu, "gelu")
+    small = 2.0 ** -19 * dh.double().abs() * (u.double().abs() + 1) * (1 + g.double().abs())
+    eg, eu = small + half_unit(dg.abs() + small, BF16), small + half_unit(du.abs() + small, BF16)
+    wgd, wud, xd = wg.double().abs(), wu.double().abs(), x.double().abs()
+    tols = (eg @ wgd + eu @ wud + acc_error(2 * F, dg.abs() @ wgd + du.abs() @ wud),
+            eg.t() @ xd + acc_error(M, dg.abs().t() @ xd), eu.t() @ xd + acc_error(M, du.abs().t() @ xd))
+    for needs in (dict(), dict(need_dw=False), dict(need_dx=False)):
+        for got, ref, tol in zip(pws.gemm_gated_nt_bwd(dh, g, u, x, wg, wu, act="gelu", **needs), want, tols):
+            if got is not None:
+                check(got, ref, tol, BF16)
+
+
+@pytest.mark.gpu
+def test_xent_bwd_on_the_wide_tile_over_pieces():
+    # 8200 tokens over two pieces of the vocabulary of 129 K blocks and more: dx
+    # is a running fp32 sum between them
+    M, V, K = 8200, 20003, 264
+    x, w = rand((M, K), BF16, 81), rand((V, K), BF16, 82, 2.0 * K ** -0.5)
+    gen = torch.Generator(device="cuda").manual_seed(83)
+    target = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    target[::7] = IGNORE
+    dloss = torch.rand(M, generator=gen, device="cuda") / M
+    _, lse = pws.gemm_xent_nt(x, w, target)
+    dx, dw = pws.gemm_xent_nt_bwd(x, w, target, lse, dloss)
+    z, lse64, keep, _ = xent64(x, w, target)
+    d = torch.exp(z - lse64[:, None])
+    del z
+    rows = torch.nonzero(keep).squeeze(1)
+    d[rows, target[rows]] -= 1.0
+    d *= (dloss.double() * keep)[:, None]
+    xd, wd = x.double(), w.double()
+    # a logit's error is far below D's rounding to bfloat16, 2^-8 of each entry
+    ed = d.abs() * (2.0 ** -8 + 2.0 ** -13) + 2.0 ** -20 * dloss.double()[:, None] / V
+    check(dx, d @ wd, ed @ wd.abs() + acc_error(2 * V, d.abs() @ wd.abs()), BF16)
+    check(dw, d.t() @ xd, ed.t() @ xd.abs() + acc_error(2 * M, d.abs().t() @ xd.abs()), BF16)
+
+
 # ---------------------------------------------------------------- the largest sizes
 
 # fake, 256-byte aligned addresses far apart: never read, the calls below are
