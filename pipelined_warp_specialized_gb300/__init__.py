@@ -191,7 +191,10 @@ def gemm_s32_nn_ring(lhs, rhs, out=None, stages: int = 4, stream=None):
 
 
 def gemm_f16_nt(lhs, rhs, out=None, stages: int = 4, stream=None):
-    """out[M,N] = f16(lhs[M,K] @ rhs[N,K].T) with fp32 accumulation, S = `stages` ring slots."""
+    """out[M,N] = f16(lhs[M,K] @ rhs[N,K].T) with fp32 accumulation, S = `stages` ring slots.
+
+    Not recorded by autograd: the gradients are gemm_nt_bwd's.
+    """
     import torch
     if lhs.dtype != torch.float16 or rhs.dtype != torch.float16:
         raise TypeError("gemm_f16_nt takes float16 tensors")
@@ -200,6 +203,7 @@ def gemm_f16_nt(lhs, rhs, out=None, stages: int = 4, stream=None):
     if not (lhs.is_cuda and rhs.is_cuda) or not lhs.is_contiguous() or not rhs.is_contiguous():
         raise ValueError("gemm_f16_nt takes contiguous CUDA tensors")
     _same_device("gemm_f16_nt", lhs, rhs, out)
+    _not_recorded("gemm_f16_nt", "gemm_nt_bwd", lhs, rhs)
     M, K = lhs.shape
     N = rhs.shape[0]
     if out is None:
@@ -279,6 +283,26 @@ def _type_of(name, *tensors):
     return code
 
 
+_warned = set()
+
+
+def _not_recorded(name, backward, *tensors):
+    """Warns, once for each entry, where autograd would expect this call's
+    output to carry a gradient: the calls are not recorded, their gradients are
+    calls of their own."""
+    for t in tensors:
+        if t.requires_grad and name not in _warned:
+            break
+    else:
+        return
+    import torch
+    if torch.is_grad_enabled():
+        import warnings
+        _warned.add(name)
+        warnings.warn(f"{name} is not recorded by autograd: its output carries no gradient although an operand "
+                      f"requires one; the gradients are those of {backward}", stacklevel=3)
+
+
 def _act_code(name, act):
     if act not in _ACTS:
         raise ValueError(f"{name}: act must be one of {sorted(_ACTS)}, got {act!r}")
@@ -346,7 +370,8 @@ def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream
 
     float16 or bfloat16; sums, activation and product in fp32, h rounded once.
     act is "silu" or "gelu" (tanh form).  With save=True returns (h, g, u),
-    where g and u are the two products, for gemm_gated_nt_bwd.
+    where g and u are the two products, for gemm_gated_nt_bwd.  Not recorded
+    by autograd.
     """
     torch = _torch or _torch_module()
     name = "gemm_gated_nt"
@@ -356,6 +381,7 @@ def gemm_gated_nt(x, w_gate, w_up, act: str = "silu", save: bool = False, stream
     if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
         raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w_gate.shape)}, {tuple(w_up.shape)} do not form "
                          "[M,K], [F,K], [F,K]")
+    _not_recorded(name, "gemm_gated_nt_bwd", x, w_gate, w_up)
     lib, device = load_library(), x.device
     s, here = _on(stream, device)
     with here:
@@ -411,10 +437,12 @@ def gemm_xent_nt(x, w, target, ignore_index: int = -100, stream=None):
 
     target is int64 [M].  Returns (loss, lse), float32 [M]: loss is 0 in rows
     whose target is ignore_index and NaN for any other target outside [0, V).
+    Not recorded by autograd: the gradients are gemm_xent_nt_bwd's.
     """
     torch = _torch or _torch_module()
     name = "gemm_xent_nt"
     code, M, V, K = _xent_shapes(name, x, w, target)
+    _not_recorded(name, "gemm_xent_nt_bwd", x, w)
     lib, device = load_library(), x.device
     s, here = _on(stream, device)
     with here:

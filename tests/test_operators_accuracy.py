@@ -395,3 +395,38 @@ def test_sizes_whose_tiles_would_pass_32_bits_are_refused():
             dims[i] = LARGEST
             n = ctypes.c_int64()
             assert getattr(lib, name + "_workspace")(*dims, *AT[:count], H, ctypes.byref(n)) == pws.GEMM_OK, (name, dims)
+
+
+# ---------------------------------------------------------------- tensors that require gradients
+
+@pytest.fixture
+def _warnings_again():
+    before = set(pws._warned)
+    pws._warned.clear()
+    yield
+    pws._warned.update(before)
+
+
+def test_unrecorded_calls_say_so_once(_warnings_again, recwarn):
+    plain, leaf = torch.zeros(2, 2), torch.zeros(2, 2, requires_grad=True)
+    pws._not_recorded("gemm_gated_nt", "gemm_gated_nt_bwd", plain, plain)
+    with torch.no_grad():
+        pws._not_recorded("gemm_gated_nt", "gemm_gated_nt_bwd", plain, leaf)
+    assert not recwarn.list
+    with pytest.warns(UserWarning, match="gemm_gated_nt is not recorded by autograd.*gemm_gated_nt_bwd"):
+        pws._not_recorded("gemm_gated_nt", "gemm_gated_nt_bwd", plain, leaf)
+    pws._not_recorded("gemm_gated_nt", "gemm_gated_nt_bwd", plain, leaf)
+    assert not recwarn.list
+
+
+@pytest.mark.gpu
+def test_forward_calls_warn_of_gradients_they_do_not_carry(_warnings_again):
+    x, w = rand((4, 16), F16, 91), rand((8, 16), F16, 92)
+    target = torch.zeros(4, dtype=torch.int64, device="cuda")
+    calls = {"gemm_gated_nt": lambda w: pws.gemm_gated_nt(x, w, w), "gemm_f16_nt": lambda w: pws.gemm_f16_nt(x, w),
+             "gemm_xent_nt": lambda w: pws.gemm_xent_nt(x, w, target)[0]}
+    for name, call in calls.items():
+        want = call(w)
+        with pytest.warns(UserWarning, match=f"{name} is not recorded"):
+            got = call(w.clone().requires_grad_())
+        assert not got.requires_grad and torch.equal(got, want)
