@@ -749,9 +749,10 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_BN;
             return got;
         };
-        // This warp's reads of the accumulator are complete (tcgen05.wait::ld):
-        // nothing in memory is handed over, so the arrival at the leader's
-        // barrier is relaxed.  A releasing one waits for the warp's output
+        // This warp's reads of the accumulator are complete (tcgen05.wait::ld after
+        // every load) and fenced: tensor memory is all that is handed over, so the
+        // arrival at the leader's barrier is relaxed (ptx.cuh gives the rule; the
+        // MMA thread's side is its wait and tc_fence_after_sync).  A releasing one waits for the warp's output
         // stores: 1800 to 3100 clocks a tile, of about 6600.
         auto release = [&]() {
             const uint32_t b = tcount & 1u;

@@ -47,9 +47,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
                  : "memory");
 }
 
-// The same without release: for an arrival that hands over no memory, only a
-// resource whose last use by this thread has completed.  (The release waits
-// for every earlier store and copy of the thread.)
+// The same without release (which waits for every earlier store and copy of
+// the thread).  Relaxed, it orders no memory access, so it may hand over tensor
+// memory alone, and only in the pattern the PTX ISA gives for that (tcgen05
+// memory consistency, synchronisation between threads):
+//   reader:  tcgen05.ld; tcgen05.wait::ld; tcgen05.fence::before_thread_sync;
+//            mbarrier.arrive.relaxed.cluster
+//   next:    mbarrier try_wait; tcgen05.fence::after_thread_sync; tcgen05.mma
+// wait::ld completes the reads, and the two fences order them before the multiplies
+// that overwrite the accumulator; the barrier carries execution order only.  A
+// warp's lanes fence and meet (__syncwarp) before the one that arrives.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t remote_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
                  : "memory");
