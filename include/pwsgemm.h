@@ -440,7 +440,7 @@ int gemm_gated_nt_workspace(int64_t M, int64_t F, int64_t K, const void* x, cons
  * dg and du are rounded to 16 bits; with up to 64 rows to twice as many.  In
  * binary16 they are scaled first, by a power of two found from the inputs and
  * undone in fp32, so that none overflows and each is held to half a unit or to
- * 2^-39 of the largest finite |dh| max(1.13 |u|, g, 0.28), whichever is more.
+ * 2^-39 of the largest finite 1.13 |dh u| or |dh| max(g, 0.28), whichever is more.
  */
 int gemm_gated_nt_bwd(int64_t M, int64_t F, int64_t K, const void* dh, const void* g, const void* u, const void* x,
                       const void* w_gate, const void* w_up, void* dx, void* dw_gate, void* dw_up, int type, int act,

@@ -42,8 +42,8 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// Binary16: the largest finite |dh| max(1.13 |u|, g, 0.28), one value a block (of
-// kTopParts).  No |dg| or |du| is above it: |act'| < 1.13 and -0.28 < act(g) <=
+// Binary16: the largest finite 1.13 |dh u| or |dh| max(g, 0.28), one value a block
+// (of kTopParts).  No |dg| or |du| is above it: |act'| < 1.13 and -0.28 < act(g) <=
 // max(g, 0) for both activations, so the pass needs no exponential and is bound by
 // its reads (the exact maximum, with one, took twice as long).  The matrices are
 // dense, so rows do not matter; they are read from the end, so that
@@ -53,11 +53,12 @@ __device__ __forceinline__ float warp_max(float v) {
 constexpr int kTopParts = 152;
 constexpr int kTopThreads = 1024;
 
-__device__ __forceinline__ float grad_bound(float dh, float g, float u) {
-    return fabsf(dh) * fmaxf(fmaxf(1.13f * fabsf(u), g), 0.28f);
-}
 // The larger of two values, `a` where b is not finite.
 __device__ __forceinline__ float finite_max(float a, float b) { return b <= 3.0e38f ? fmaxf(a, b) : a; }
+// dg's bound and du's apart: an infinite u leaves du finite.
+__device__ __forceinline__ float grad_bound(float top, float dh, float g, float u) {
+    return finite_max(finite_max(top, fabsf(1.13f * dh * u)), fabsf(dh) * fmaxf(g, 0.28f));
+}
 
 template <bool ALIGNED>
 __global__ void __launch_bounds__(kTopThreads)
@@ -75,7 +76,7 @@ gated_top_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 h2 = unpack16(av[j], 0), g2 = unpack16(bv[j], 0), u2 = unpack16(dv[j], 0);
-            top = finite_max(finite_max(top, grad_bound(h2.x, g2.x, u2.x)), grad_bound(h2.y, g2.y, u2.y));
+            top = grad_bound(grad_bound(top, h2.x, g2.x, u2.x), h2.y, g2.y, u2.y);
         }
     };
     // two chunks of eight elements a step: six loads in flight

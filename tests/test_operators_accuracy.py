@@ -101,6 +101,26 @@ def test_gated_bwd_of_zeros_and_of_what_is_not_finite(M, dtype):
         assert torch.equal(dx[others].view(torch.int16), want[others].view(torch.int16))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [8, 80])
+def test_gated_bwd_of_an_infinite_up_projection(M, act):
+    # where u is infinite dg is and du is not: du = 240000 is the largest finite
+    # element, past binary16's range, and its products with the tokens are within
+    F, K = 96, 72
+    x, wg, wu = rand((M, K), F16, 27), rand((F, K), F16, 28, 0.1), rand((F, K), F16, 29, 0.1)
+    g, u, dh = rand((M, F), F16, 30), rand((M, F), F16, 31), rand((M, F), F16, 32, 0.02)
+    dh[4, 5], g[4, 5], u[4, 5] = 30000.0, 8.0, float("inf")
+    x[4] = 0.01
+    _, dwg, dwu = pws.gemm_gated_nt_bwd(dh, g, u, x, wg, wu, act=act)
+    du = dh.double() * act64(g.double(), act)[0]
+    xd, top = x.double(), 30000.0 * 8
+    bits = 2.0 ** -11 if M > 64 else 2.0 ** -22
+    eu = 2.0 ** -19 * dh.double().abs() * (1 + g.double().abs()) + du.abs() * bits + 2.0 ** -39 * top
+    check(dwu, du.t() @ xd, eu.t() @ xd.abs() + acc_error(2 * M, du.abs().t() @ xd.abs()), F16)
+    assert not torch.isfinite(dwg[5]).any() and torch.isfinite(dwg[6]).all()
+
+
 # ---------------------------------------------------------------- cross entropy
 
 @pytest.mark.gpu
