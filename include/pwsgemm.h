@@ -406,7 +406,8 @@ int gemm_f16_nt_plan(int64_t M, int64_t N, int64_t K, const gemm_f16_t* lhs, con
  */
 typedef enum {
     GEMM_TYPE_HALF = 0,   /* IEEE binary16 */
-    GEMM_TYPE_BFLOAT = 1  /* bfloat16      */
+    GEMM_TYPE_BFLOAT = 1, /* bfloat16      */
+    GEMM_TYPE_BYTE = 2    /* 8-bit integers with a float scale for each row: gemm_moe_nt's weights alone */
 } gemm_type;
 
 typedef enum {
@@ -498,6 +499,71 @@ int gemm_xent_nt_bwd_workspace(int64_t M, int64_t V, int64_t K, const void* x, c
 int gemm_nt_bwd(int64_t M, int64_t N, int64_t K, const void* dy, const void* x, const void* w, void* dx, void* dw,
                 int type, void* workspace, int64_t workspace_bytes, cudaStream_t stream);
 int gemm_nt_bwd_workspace(int64_t M, int64_t N, int64_t K, const void* dy, const void* x, const void* w, int type,
+                          int64_t* bytes);
+
+/*
+ * Serving operators: 8-bit integer matrices, and a mixture of experts.
+ *
+ * An 8-bit matrix is int8 [rows, K], dense and row-major at any address, with a
+ * float scale for each row: element (r, k) stands for scale[r] q[r][k].  A
+ * token's activations and a weight's output channels are both rows of that form.
+ * The conventions of the operators above hold, but for the types named here.
+ */
+
+/*
+ * gemm_i8_quantize -- a 16-bit matrix as an 8-bit one.
+ *
+ *   x     : [M, K] of `type`
+ *   q     : int8 [M, K], the integer nearest to 127 x[i][k] / top[i], ties to even,
+ *           where top[i] is the largest |x[i][k]|
+ *   scale : float [M], top[i] / 127
+ *
+ * q is the correctly rounded quotient, whatever the magnitudes.  A row of zeros
+ * has scale 0 and zeros; so has a row of no elements (K == 0).  A row that holds
+ * an infinity or a NaN has scale NaN and zeros, so that its products are NaN.
+ */
+int gemm_i8_quantize(int64_t M, int64_t K, const void* x, int8_t* q, float* scale, int type, cudaStream_t stream);
+
+/*
+ * gemm_i8_nt -- out[M,N] = a_scale[M] b_scale[N] (a[M,K] . b[N,K]^T).
+ *
+ *   a, b    : int8 [M, K], [N, K]
+ *   a_scale : float [M]        b_scale : float [N]
+ *   out     : [M, N] of `type` (16 bits), written
+ *
+ * The sum of products is exact (K at most 131071, so that it fits 32 bits); its
+ * fp32 value times a_scale, times b_scale, is rounded once.  K == 0 gives zeros.
+ */
+int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, const int8_t* b, const float* a_scale,
+               const float* b_scale, void* out, int type, void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+int gemm_i8_nt_workspace(int64_t M, int64_t N, int64_t K, const int8_t* a, const int8_t* b, int type, int64_t* bytes);
+
+/*
+ * gemm_moe_nt -- a mixture-of-experts layer, made for a few tokens (M up to 64
+ * read each chosen expert's weights once; more are taken 64 at a time).
+ *
+ *   x        : [M, K] of `type`         w_router : [E, K] of `type`
+ *   w_gate, w_up : [E, F, K]            w_down   : [E, K, F]
+ *              of `type`, or int8 with weight_type GEMM_TYPE_BYTE and the scales
+ *              s_gate, s_up [E, F] and s_down [E, K] (null otherwise)
+ *   experts  : int32 [M, top_k], written: the top_k largest of z = x . w_router^T,
+ *              largest first, ties to the lower index
+ *   weights  : float [M, top_k], written: softmax(z) at those, over all E, or over
+ *              the chosen ones alone where normalize is 1
+ *   y        : [M, K] of `type`, written:
+ *              sum_j weights[j] (act(x . w_gate[e_j]^T) * (x . w_up[e_j]^T)) . w_down[e_j]^T
+ *
+ * 1 <= top_k <= E, E <= 1024, top_k <= 32.  A NaN logit counts as the largest;
+ * a token's weights and output are then NaN.  Logits are summed to about twice
+ * fp32's precision, so that near ones are taken in their true order.  The weighted
+ * activations between the projections are held to twice 16 bits (in binary16:
+ * infinite above 131008, and to 2^-25 below its normal range).
+ */
+int gemm_moe_nt(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k, const void* x, const void* w_router,
+                const void* w_gate, const void* w_up, const void* w_down, const float* s_gate, const float* s_up,
+                const float* s_down, void* y, int32_t* experts, float* weights, int type, int weight_type, int act,
+                int normalize, void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+int gemm_moe_nt_workspace(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k, int type, int weight_type,
                           int64_t* bytes);
 
 #if defined(__GNUC__)

@@ -48,6 +48,7 @@ GEMM_DEBUG_IN_PLACE = 16384
 
 GEMM_TYPE_HALF = 0
 GEMM_TYPE_BFLOAT = 1
+GEMM_TYPE_BYTE = 2
 GEMM_ACT_SILU = 0
 GEMM_ACT_GELU = 1
 _ACTS = {"silu": GEMM_ACT_SILU, "gelu": GEMM_ACT_GELU}
@@ -103,7 +104,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             ("gemm_xent_nt_bwd", [i64] * 3 + [vp] * 3 + [i64] + [vp] * 4 + [i32, vp, i64, vp]),
             ("gemm_xent_nt_bwd_workspace", [i64] * 3 + [vp] * 2 + [i32, pi64]),
             ("gemm_nt_bwd", [i64] * 3 + [vp] * 5 + [i32, vp, i64, vp]),
-            ("gemm_nt_bwd_workspace", [i64] * 3 + [vp] * 3 + [i32, pi64])):
+            ("gemm_nt_bwd_workspace", [i64] * 3 + [vp] * 3 + [i32, pi64]),
+            ("gemm_i8_quantize", [i64] * 2 + [vp] * 3 + [i32, vp]),
+            ("gemm_i8_nt", [i64] * 3 + [vp] * 5 + [i32, vp, i64, vp]),
+            ("gemm_i8_nt_workspace", [i64] * 3 + [vp] * 2 + [i32, pi64]),
+            ("gemm_moe_nt", [i64] * 5 + [vp] * 11 + [i32] * 4 + [vp, i64, vp]),
+            ("gemm_moe_nt_workspace", [i64] * 5 + [i32, i32, pi64])):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = i32
@@ -344,16 +350,16 @@ def _on(stream, device):
 _ws_bytes = {}          # bytes by (entry, device, type, sizes) for operands on 16-byte boundaries
 
 
-def _workspace(name, device, code, dims, *ptrs):
+def _workspace(name, device, code, dims, *ptrs, extra=()):
     """(tensor or None, address, bytes) of the workspace the call reports."""
     low = 0
     for p in ptrs:
         low |= p
-    key = (name, device.index, code, dims)
+    key = (name, device.index, code, dims, extra)
     size = _ws_bytes.get(key) if low & 15 == 0 else None
     if size is None:
         need = ctypes.c_int64()
-        _check(getattr(load_library(), name + "_workspace")(*dims, *ptrs, code, ctypes.byref(need)), name)
+        _check(getattr(load_library(), name + "_workspace")(*dims, *ptrs, code, *extra, ctypes.byref(need)), name)
         size = need.value
         if low & 15 == 0:
             if len(_ws_bytes) >= 4096:
@@ -504,6 +510,130 @@ def gemm_nt_bwd(dy, x, w, need_dx: bool = True, need_dw: bool = True, stream=Non
     return dx, dw
 
 
+# ---------------------------------------------------------------- serving: 8-bit matrices, a mixture of experts
+
+
+def _dense(name, what, t, shape, dtype, device):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} takes contiguous CUDA tensors")
+    if t.device != device:
+        raise ValueError(f"{name}: all tensors must be on one device, got {device} and {t.device}")
+
+
+def gemm_i8_quantize(x, stream=None):
+    """A float16 or bfloat16 matrix x[M,K] as (q, scale): int8 [M,K] and float32 [M].
+
+    scale[i] = max |x[i]| / 127 and q[i][k] is the integer nearest to
+    127 x[i][k] / max |x[i]| (ties to even), so x is about scale[:, None] * q.  A row
+    of zeros has scale 0; a row with an infinity or a NaN has scale NaN and q 0.
+    Quantizes tokens before gemm_i8_nt, and weights once: rows are a product's
+    output channels (for gemm_moe_nt, of all experts: w.view(E * F, K)).
+    """
+    torch = _torch or _torch_module()
+    name = "gemm_i8_quantize"
+    code = _type_of(name, x)
+    M, K = x.shape
+    lib, device = load_library(), x.device
+    s, here = _on(stream, device)
+    with here:
+        q = torch.empty((M, K), dtype=torch.int8, device=device)
+        scale = torch.empty(M, dtype=torch.float32, device=device)
+        _check(lib.gemm_i8_quantize(M, K, x.data_ptr(), q.data_ptr(), scale.data_ptr(), code, s), name)
+    return q, scale
+
+
+def gemm_i8_nt(a, b, a_scale, b_scale, dtype=None, stream=None):
+    """out[M,N] = a_scale[:, None] * b_scale * (a[M,K] @ b[N,K].T) of int8 a and b.
+
+    The sum is exact (K at most 131071) and the result rounded once, to `dtype`:
+    float16 or bfloat16 (the default).  The scales are float32 [M] and [N].
+    """
+    torch = _torch or _torch_module()
+    name = "gemm_i8_nt"
+    dtype = torch.bfloat16 if dtype is None else dtype
+    code = _codes.get(dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype must be float16 or bfloat16, got {dtype}")
+    for t in (a, b):
+        if t.dtype != torch.int8:
+            raise TypeError(f"{name} takes int8 matrices, got {t.dtype}")
+        if t.dim() != 2:
+            raise ValueError(f"{name} takes matrices, got a tensor of shape {tuple(t.shape)}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} takes contiguous CUDA tensors")
+    device = a.device
+    if b.device != device:
+        raise ValueError(f"{name}: all tensors must be on one device, got {device} and {b.device}")
+    M, K = a.shape
+    N = b.shape[0]
+    if b.shape[1] != K:
+        raise ValueError(f"{name}: shapes {tuple(a.shape)}, {tuple(b.shape)} do not form [M,K], [N,K]")
+    _vector(name, "a_scale", a_scale, M, torch.float32, device)
+    _vector(name, "b_scale", b_scale, N, torch.float32, device)
+    lib = load_library()
+    s, here = _on(stream, device)
+    with here:
+        out = torch.empty((M, N), dtype=dtype, device=device)
+        pa, pb = a.data_ptr(), b.data_ptr()
+        ws, ws_ptr, ws_bytes = _workspace(name, device, code, (M, N, K), pa, pb)
+        _check(lib.gemm_i8_nt(M, N, K, pa, pb, a_scale.data_ptr(), b_scale.data_ptr(), out.data_ptr(), code, ws_ptr,
+                              ws_bytes, s), name)
+    return out
+
+
+def gemm_moe_nt(x, w_router, w_gate, w_up, w_down, top_k, scales=None, act: str = "silu", normalize: bool = True,
+                stream=None):
+    """A mixture-of-experts layer for a few tokens: (y[M,K], experts, weights).
+
+    x [M,K] and w_router [E,K] are float16 or bfloat16; w_gate, w_up [E,F,K] and
+    w_down [E,K,F] have their type, or are int8 with scales = (gate [E,F], up [E,F],
+    down [E,K]) in float32.  experts (int32 [M, top_k]) are those of the top_k
+    largest x @ w_router.T, largest first, ties to the lower index; weights (float32)
+    their softmax probabilities, over the chosen experts with normalize, else over all;
+    y[i] = sum_j weights[i,j] * w_down[e] @ (act(w_gate[e] @ x[i]) * (w_up[e] @ x[i])), e = experts[i,j].
+
+    Made for up to 64 tokens (more are taken 64 at a time); E <= 1024, top_k <= 32.
+    Not recorded by autograd, and without a backward pass.
+    """
+    torch = _torch or _torch_module()
+    name = "gemm_moe_nt"
+    code, act_code = _type_of(name, x, w_router), _act_code(name, act)
+    M, K = x.shape
+    E = w_router.shape[0]
+    if w_router.shape[1] != K or w_gate.dim() != 3:
+        raise ValueError(f"{name}: shapes {tuple(x.shape)}, {tuple(w_router.shape)}, {tuple(w_gate.shape)} do not form "
+                         "[M,K], [E,K], [E,F,K]")
+    F, device = w_gate.shape[1], x.device
+    kind = x.dtype if scales is None else torch.int8
+    _dense(name, "w_gate", w_gate, (E, F, K), kind, device)
+    _dense(name, "w_up", w_up, (E, F, K), kind, device)
+    _dense(name, "w_down", w_down, (E, K, F), kind, device)
+    pg = pu = pd = None
+    if scales is not None:
+        if len(scales) != 3:
+            raise ValueError(f"{name}: scales must be those of w_gate, w_up and w_down")
+        for what, t, cols in zip(("gate", "up", "down"), scales, (F, F, K)):
+            _dense(name, f"the scales of w_{what}", t, (E, cols), torch.float32, device)
+        pg, pu, pd = (t.data_ptr() for t in scales)
+    top_k = int(top_k)
+    lib = load_library()
+    s, here = _on(stream, device)
+    with here:
+        wcode = code if scales is None else GEMM_TYPE_BYTE
+        ws, ws_ptr, ws_bytes = _workspace(name, device, code, (M, K, F, E, top_k), extra=(wcode,))
+        y = torch.empty((M, K), dtype=x.dtype, device=device)
+        experts = torch.empty((M, top_k), dtype=torch.int32, device=device)
+        weights = torch.empty((M, top_k), dtype=torch.float32, device=device)
+        _check(lib.gemm_moe_nt(M, K, F, E, top_k, x.data_ptr(), w_router.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                               w_down.data_ptr(), pg, pu, pd, y.data_ptr(), experts.data_ptr(), weights.data_ptr(), code,
+                               wcode, act_code, int(bool(normalize)), ws_ptr, ws_bytes, s), name)
+    return y, experts, weights
+
+
 def gemm_device_status(stream=None) -> int:
     """Synchronizes the stream; returns and clears the device status word."""
     return load_library().gemm_device_status(_stream_ptr(stream, None))
@@ -543,4 +673,5 @@ __all__ = [
     "gemm_status_string", "gemm_set_wait_timeout_ns", "gemm_set_debug_flags", "gemm_set_scratch_pool",
     "gemm_f16_nt_plan", "gemm_f16_nt_noalloc", "gemm_s32_nn_ring",
     "gemm_gated_nt", "gemm_gated_nt_bwd", "gemm_xent_nt", "gemm_xent_nt_bwd", "gemm_nt_bwd",
+    "gemm_i8_quantize", "gemm_i8_nt", "gemm_moe_nt",
 ]

@@ -1,0 +1,281 @@
+// gemm_i8.cu -- products of 8-bit integer matrices with a scale for each row,
+// and the quantization that makes such matrices.
+//
+// sm_103a's tensor cores multiply no 8-bit integers (tcgen05's kind::i8 does not
+// exist there), but every 8-bit integer is a binary16 value, their products are
+// exact in the fp32 accumulator, and so are sums of up to 1024 of them: 128 * 128 *
+// 1024 = 2^24.  The product therefore runs at the 16-bit rate and is exact: the
+// accumulator is handed over every 1024 of K and added up in integers.
+#include "few.cuh"
+#include "product_host.cuh"
+
+namespace pws {
+namespace i8 {
+
+using namespace fused;
+
+constexpr int64_t kMaxK = 131071;           // 128 * 128 * K < 2^31
+constexpr int kChunk = 16;                  // K blocks of 64 whose sum fp32 holds exactly
+static_assert(kChunk % kMaxBoxes == 0, "a chunk ends with a slot");
+
+// ---------------------------------------------------------------- quantization
+
+constexpr float kMagic = 12582912.0f;       // 1.5 * 2^23: adding it rounds to a whole number
+
+// rint(127 x / top) exactly, from q = x * fl(127 / top), which is off by less than
+// 2^-22 of its power of two.  A quotient of two 16-bit values that is not halfway
+// between two integers is at least 2^-19 of its power of two from there (the
+// values have at most 11 significant bits), so only near a half can the product
+// mislead, and there the division, correctly rounded, does not: halves are exact.
+__device__ __forceinline__ int quantized(float x, float top, float inverse) {
+    const float q = x * inverse;
+    const float n = __fsub_rn(__fadd_rn(q, kMagic), kMagic);
+    if (fabsf(q - n) > 0.49996f) return __float2int_rn(__fdiv_rn(127.0f * x, top));
+    return static_cast<int>(n);
+}
+
+// A row of x by LANES threads (a warp, or the block): its largest magnitude, then
+// its integers.  Each thread keeps its first four chunks of eight elements in
+// registers, so rows up to 32 LANES are read once; longer ones again, from L2.
+// Bound by memory: 2 bytes read and 1 written per element.
+template <int LANES, bool BF16, bool ALIGNED>
+__global__ void __launch_bounds__(LANES < 256 ? 256 : LANES)
+quantize_kernel(const uint8_t* __restrict__ x, int8_t* __restrict__ q, float* __restrict__ scale, int64_t M, int64_t K) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    constexpr int KEEP = 4;
+    __shared__ uint32_t part[32];
+    const int lane = threadIdx.x % LANES;
+    const int64_t row = LANES < 256 ? blockIdx.x * static_cast<int64_t>(256 / LANES) + threadIdx.x / LANES : blockIdx.x;
+    if (LANES < 256 && row >= M) return;
+    const uint8_t* src = x + row * K * 2;
+    const int64_t chunks = (K + 7) / 8;
+    const auto load = [&](int64_t i) { return few::load_row<ALIGNED, true>(src + 16 * i, 2 * (K - 8 * i)); };
+    uint4 kept[KEEP];
+    // magnitudes are ordered as their bits are, NaN above infinity
+    uint32_t top = 0u;
+    const auto take = [&](const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    };
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+        const int64_t i = lane + static_cast<int64_t>(j) * LANES;
+        kept[j] = i < chunks ? load(i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) take(kept[j]);
+    for (int64_t i = lane + static_cast<int64_t>(KEEP) * LANES; i < chunks; i += LANES) take(load(i));
+    top = max(top & 0xFFFFu, top >> 16);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (LANES > 32) {
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+        __syncthreads();
+        top = threadIdx.x % 32 < LANES / 32 ? part[threadIdx.x % 32] : 0u;
+        top = __reduce_max_sync(0xffffffffu, top);
+    }
+    float most = unpack16(top, BF16).x;
+    const bool finite = most <= 3.4e38f;
+    if (lane == 0) scale[row] = finite ? __fdiv_rn(most, 127.0f) : __int_as_float(0x7fffffff);
+    // bfloat16's range: brought to where neither 127 x nor 127 / top leaves fp32's.  (What
+    // becomes zero on the way is below 2^-60 of the largest.)
+    float by = 1.0f;
+    if (BF16) by = most > 0x1p64f ? 0x1p-64f : (most < 0x1p-64f ? 0x1p64f : 1.0f);
+    most *= by;
+    const float inverse = finite && most > 0.0f ? __fdiv_rn(127.0f, most) : 0.0f;
+    int8_t* dst = q + row * K;
+    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 7u) == 0;
+    const auto put = [&](int64_t i, const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t b[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float2 f = unpack16(w[j], BF16);
+            // (a row with an infinity or a NaN is zeros)
+            if (!finite) f = make_float2(0.0f, 0.0f);
+            if (BF16) { f.x *= by; f.y *= by; }
+            b[2 * j] = static_cast<uint32_t>(quantized(f.x, most, inverse));
+            b[2 * j + 1] = static_cast<uint32_t>(quantized(f.y, most, inverse));
+        }
+        if (wide && 8 * i + 8 <= K) {
+            const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+            const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+            *reinterpret_cast<uint2*>(dst + 8 * i) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (8 * i + j < K) dst[8 * i + j] = static_cast<int8_t>(b[j]);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+        const int64_t i = lane + static_cast<int64_t>(j) * LANES;
+        if (i < chunks) put(i, kept[j]);
+    }
+    for (int64_t i = lane + static_cast<int64_t>(KEEP) * LANES; i < chunks; i += LANES) put(i, load(i));
+}
+
+template <int LANES, bool BF16>
+int launch_quantize(int64_t M, int64_t K, const void* x, int8_t* q, float* scale, cudaStream_t stream) {
+    const bool aligned = reinterpret_cast<uintptr_t>(x) % 16 == 0 && K % 8 == 0;
+    const int64_t blocks = LANES < 256 ? cdiv(M, 256 / LANES) : M;
+    const auto kern = aligned ? quantize_kernel<LANES, BF16, true> : quantize_kernel<LANES, BF16, false>;
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(LANES < 256 ? 256 : LANES), 0, stream,
+                   static_cast<const uint8_t*>(x), q, scale, M, K) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+// ---------------------------------------------------------------- widening
+
+// Rows of 8-bit integers at any address as binary16 rows ld apart (a multiple of
+// 64, the rest of the last 16 elements zeros), two matrices in one launch.  16
+// elements a thread: 16 bytes read, 32 written.
+struct Widen {
+    const uint8_t* src[2];
+    uint16_t* dst[2];
+    int64_t rows[2];
+};
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(256)
+widen_kernel(const __grid_constant__ Widen p, int64_t K, int64_t ld) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t chunks = (K + 15) / 16, total = (p.rows[0] + p.rows[1]) * chunks;
+    for (int64_t id = blockIdx.x * 256ll + threadIdx.x; id < total; id += gridDim.x * 256ll) {
+        int64_t row = id / chunks;
+        const int64_t c = (id - row * chunks) * 16;
+        const int m = row >= p.rows[0] ? 1 : 0;
+        row -= m * p.rows[0];
+        const uint4 w = few::load_row<ALIGNED, true>(p.src[m] + row * K + c, K - c);
+        uint32_t v[8];
+        few::widen<few::kI8Half>(w, v);
+        uint4* to = reinterpret_cast<uint4*>(p.dst[m] + row * ld + c);
+        to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// ---------------------------------------------------------------- product
+
+int check(int64_t M, int64_t N, int64_t K, const void* a, const void* b, const float* sa, const float* sb,
+          const void* out, int type) {
+    if (bad_size(M) || bad_size(N) || K < 0 || K > kMaxK) return GEMM_ERR_INVALID_ARG;
+    if (type != GEMM_TYPE_HALF && type != GEMM_TYPE_BFLOAT) return GEMM_ERR_INVALID_ARG;
+    if (too_many_tiles(M, N)) return GEMM_ERR_INVALID_ARG;
+    if (odd_address(out) || reinterpret_cast<uintptr_t>(sa) % 4 != 0 || reinterpret_cast<uintptr_t>(sb) % 4 != 0)
+        return GEMM_ERR_ALIGNMENT;
+    if (M > 0 && N > 0 && K > 0 && (!a || !b)) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+struct Plan {
+    Product pr;
+    Layout l;
+    uint16_t *a = nullptr, *b = nullptr;
+    int64_t ld = 0;
+    size_t bytes = 0;
+};
+
+// num_sms 0: the workspace only.
+Plan plan_of(int64_t M, int64_t N, int64_t K, int num_sms, void* ws) {
+    Plan pl;
+    Carver c;
+    c.base = static_cast<char*>(ws);
+    pl.pr.M = M; pl.pr.N = N; pl.pr.K = K;
+    pl.pr.chunk = kChunk;
+    if (num_sms) pl.l = choose_layout(pl.pr, num_sms);
+    pl.ld = round_up(K, 64);
+    pl.a = c.take<uint16_t>(M * pl.ld);
+    pl.b = c.take<uint16_t>(N * pl.ld);
+    pl.bytes = c.used;
+    return pl;
+}
+
+}  // namespace i8
+}  // namespace pws
+
+extern "C" int gemm_i8_quantize(int64_t M, int64_t K, const void* x, int8_t* q, float* scale, int type,
+                                cudaStream_t stream) {
+    using namespace pws;
+    using namespace pws::i8;
+    if (bad_size(M) || bad_size(K)) return GEMM_ERR_INVALID_ARG;
+    if (type != GEMM_TYPE_HALF && type != GEMM_TYPE_BFLOAT) return GEMM_ERR_INVALID_ARG;
+    if (odd_address(x) || reinterpret_cast<uintptr_t>(scale) % 4 != 0) return GEMM_ERR_ALIGNMENT;
+    if (M == 0) return GEMM_OK;
+    if (!scale || (K > 0 && (!x || !q))) return GEMM_ERR_INVALID_ARG;
+    const Range in[1] = {{x, bytes16(M, K)}};
+    const Range out[2] = {{q, static_cast<uint64_t>(M) * K}, {scale, 4ull * M}};
+    if (overlaps(in, out)) return GEMM_ERR_INVALID_ARG;
+    DeviceInfo info;
+    const int rc = current_device(&info);
+    if (rc != GEMM_OK) return rc;
+    const bool bf16 = type == GEMM_TYPE_BFLOAT;
+    if (K <= 1024)
+        return bf16 ? launch_quantize<32, true>(M, K, x, q, scale, stream) : launch_quantize<32, false>(M, K, x, q, scale, stream);
+    if (K <= 8192)
+        return bf16 ? launch_quantize<256, true>(M, K, x, q, scale, stream) : launch_quantize<256, false>(M, K, x, q, scale, stream);
+    return bf16 ? launch_quantize<1024, true>(M, K, x, q, scale, stream) : launch_quantize<1024, false>(M, K, x, q, scale, stream);
+}
+
+extern "C" int gemm_i8_nt_workspace(int64_t M, int64_t N, int64_t K, const int8_t* a, const int8_t* b, int type,
+                                    int64_t* bytes) {
+    using namespace pws::i8;
+    const int rc = check(M, N, K, a, b, nullptr, nullptr, nullptr, type);
+    if (rc != GEMM_OK) return rc;
+    if (!bytes) return GEMM_ERR_INVALID_ARG;
+    *bytes = M && N && K ? static_cast<int64_t>(plan_of(M, N, K, 0, nullptr).bytes) : 0;
+    return GEMM_OK;
+}
+
+extern "C" int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, const int8_t* b, const float* a_scale,
+                          const float* b_scale, void* out, int type, void* workspace, int64_t workspace_bytes,
+                          cudaStream_t stream) {
+    using namespace pws;
+    using namespace pws::i8;
+    int rc = check(M, N, K, a, b, a_scale, b_scale, out, type);
+    if (rc != GEMM_OK) return rc;
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (!out || !a_scale || !b_scale) return GEMM_ERR_INVALID_ARG;
+    const Range in[4] = {{a, static_cast<uint64_t>(M) * K}, {b, static_cast<uint64_t>(N) * K}, {a_scale, 4ull * M}, {b_scale, 4ull * N}};
+    const Range outs[1] = {{out, bytes16(M, N)}};
+    if (overlaps(in, outs)) return GEMM_ERR_INVALID_ARG;
+    DeviceInfo info;
+    rc = current_device(&info);
+    if (rc != GEMM_OK) return rc;
+    if (K == 0) return cudaMemsetAsync(out, 0, bytes16(M, N), stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    Plan pl = plan_of(M, N, K, info.num_sms, workspace);
+    if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, outs)) return GEMM_ERR_INVALID_ARG;
+    const bool aligned = reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0 && K % 16 == 0;
+    {
+        const Widen w = {{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b)}, {pl.a, pl.b}, {M, N}};
+        int64_t blocks = cdiv((M + N) * cdiv(K, 16), 256);
+        if (blocks > (1 << 30)) blocks = 1 << 30;
+        if (launch_pdl(aligned ? widen_kernel<true> : widen_kernel<false>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                       stream, w, K, pl.ld) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+    }
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    Params p = base_params(pl.l, GEMM_TYPE_HALF, info, stream);
+    Operands op;
+    op.a[0] = pl.a;
+    op.lda = pl.ld;
+    op.b[0] = pl.b;
+    op.ldb = pl.ld;
+    if (!set_job(&p, &maps, 0, pl.pr, pl.l, pl.l.part[0], op)) return GEMM_ERR_LAUNCH;
+    p.bf16 = type == GEMM_TYPE_BFLOAT;          // (the output's; the operands are binary16)
+    p.a_scale = a_scale;
+    p.b_scale = b_scale;
+    Job& j = p.job[0];
+    j.ld16 = N;
+    j.out16[0] = static_cast<uint16_t*>(out);
+    j.tma_store = output_map(&maps.c[0], pl.l, out, M, N, N);
+    return launch_product<kEpiI8>(pl.l, maps, p, info, stream);
+}

@@ -20,7 +20,9 @@
 //             registers (round to nearest): the tensor core's own accumulation
 //             truncates, which over a long K shifts every logit the same way.
 //             Forward and backward take the same chunks, so that z - lse holds
-//             no difference between two sums of one logit.
+//             no difference between two sums of one logit.  The 8-bit product's
+//             takes chunks of 16 blocks, whose sums of whole numbers are exact,
+//             and adds them in integers.
 //   splits    few output tiles with a long K are split over K; the fp32
 //             partial sums are joined in a fixed order by a later kernel, so a
 //             result never depends on the order in which CTAs finish.
@@ -84,7 +86,7 @@ static_assert(SMEM_BYTES > 120 * 1024, "one CTA per SM: each owns all of tensor 
 // caller sets: copies and multiplies already issued end in microseconds.
 constexpr unsigned long long kDrainNs = 100000000ull;
 
-enum Epilogue { kEpiStore = 0, kEpiGated = 1, kEpiXentStats = 2, kEpiXentGrad = 3 };
+enum Epilogue { kEpiStore = 0, kEpiGated = 1, kEpiXentStats = 2, kEpiXentGrad = 3, kEpiI8 = 4 };
 
 // Epilogue warps: two per tensor-memory lane quarter, which take the tile's
 // 64-column chunks (32-column groups for the statistics) in turn, so that the
@@ -156,6 +158,9 @@ struct Params {
     int64_t ignore_index;           // a target of a row that does not count: D is 0 there
     int64_t col0;                   // vocabulary index of column 0
     int64_t lo_offset;              // elements from D to its rounding remainder, 0 for none
+    // kEpiI8: out16[0] = (whole-number sum) a_scale[row] b_scale[column]
+    const float* a_scale;
+    const float* b_scale;
 };
 
 struct Maps {
@@ -304,6 +309,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
 __device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
     if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// An element of the 8-bit product from its sum of whole numbers.  The scales one
+// after the other: their product could leave fp32's range where the element does not.
+__device__ __forceinline__ float i8_value(int sum, float a_scale, float b_scale) {
+    return static_cast<float>(sum) * a_scale * b_scale;
 }
 
 // What rounding to 16 bits left of d, for a second 16-bit value beside it; 0
@@ -777,6 +788,57 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                 tile_end = n0 + p.tile_n;
                 const int col_end = min(job.N, tile_end);
                 uint32_t tbase;
+                if constexpr (EPI == kEpiI8) {
+                    // This warp's two 64-column chunks.  128 * 128 * 1024 = 2^24: a chunk's
+                    // sum of products of 8-bit integers is a whole number that fp32 holds,
+                    // as is every partial sum of it, and chunks are added as integers.
+                    const bool rows_live = row0 < job.M;
+                    int z[4][32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) z[j][i] = 0;
+                    bool got = true;
+                    for (int c0 = t.kb0; c0 < t.kb1; c0 += p.chunk) {
+                        if (!acquire(tbase)) { got = false; break; }
+                        if (rows_live) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int c = first_chunk + CHUNK_STEP * (j >> 1) + 32 * (j & 1);
+                                if (c < p.tile_n) {
+#pragma unroll
+                                    for (int h = 0; h < 32; h += 16) {
+                                        uint32_t v[16];
+                                        tmem_ld_32x32b_x16(tbase + static_cast<uint32_t>(c + h), v);
+                                        tmem_ld_wait();
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i) z[j][h + i] += __float2int_rn(__uint_as_float(v[i]));
+                                    }
+                                }
+                            }
+                        }
+                        release();
+                    }
+                    if (!got) { alive = false; break; }
+                    if (!rows_live) continue;
+                    const float sa = row < job.M ? __ldg(p.a_scale + row) : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int c = n0 + first_chunk + CHUNK_STEP * k;
+                        if (c >= col_end) continue;
+                        uint32_t h[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int col = c + 2 * i;
+                            const float s0 = col < col_end ? __ldg(p.b_scale + col) : 0.0f;
+                            const float s1 = col + 1 < col_end ? __ldg(p.b_scale + col + 1) : 0.0f;
+                            const int(&v)[32] = z[2 * k + i / 16];
+                            h[i] = pack16(i8_value(v[2 * i % 32], sa, s0), i8_value(v[2 * i % 32 + 1], sa, s1), p.bf16);
+                        }
+                        emit(h, job, &maps.c[0], job.out16[0], row0, c, col_end);
+                    }
+                    continue;
+                }
                 if constexpr (EPI == kEpiXentStats || EPI == kEpiXentGrad) {
                     // This warp's four 32-column groups: 2 j + half of the tile's, or
                     // for the gradient those of its 64-column chunks.  The logits

@@ -1,0 +1,516 @@
+"""The 8-bit operators and the mixture of experts on the GPU, against their
+formulas in 64 bits.
+
+Every tolerance is an error bound of the computation, elementwise:
+
+* 8-bit integers: the quantization is exact (whole numbers and a correctly
+  rounded scale), and so is the product's sum; its fp32 value, two products with
+  scales and the rounding to 16 bits are four roundings: 3 * 2^-24 relative and half
+  a unit;
+* a sum of K products on the tensor cores adds 16 of them at a time into an fp32
+  accumulator.  Each of the K/16 additions loses at most one unit in the last place
+  of a partial sum no larger than S = sum |a b|, and the sum inside a group of
+  16 at most 8 more: (K/16 + 8) 2^-23 S; joining eight warps' sums stays below
+  what their shorter sums save;
+* h' as two 16-bit values: 2^-16 relative in bfloat16 (its remainder rounded to
+  8 bits more), 2^-22 and 2^-25 absolute in binary16;
+* exp2, the fast division and the routing weights are good to 2^-20 relative, for
+  arguments below 32 in magnitude.
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import pipelined_warp_specialized_gb300 as pws  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+TYPES = [F16, BF16]
+
+
+@pytest.fixture(autouse=True)
+def _no_timeouts():
+    yield
+    assert pws.gemm_device_status() == pws.GEMM_OK
+
+
+def half_unit(y, dtype):
+    y = y.abs()
+    return y * 2.0 ** -11 + 2.0 ** -25 if dtype == F16 else y * 2.0 ** -8 + 2.0 ** -134
+
+
+def acc_error(K, s):
+    return (K / 16 + 8) * 2.0 ** -23 * s
+
+
+def rand(shape, dtype, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def rand_i8(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-128, 128, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+def off_by_one(t):
+    """The same values at an address one element past a 16-byte boundary."""
+    flat = torch.empty(t.numel() + 16, dtype=t.dtype, device=t.device)
+    out = flat[1:1 + t.numel()].view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 16 == t.element_size()
+    return out
+
+
+def same_bits(a, b):
+    kind = {1: torch.int8, 2: torch.int16, 4: torch.int32}[a.element_size()]
+    return torch.equal(a.view(kind), b.view(kind))
+
+
+# ---------------------------------------------------------------- quantization
+
+
+def quantized64(x):
+    xd = x.double()
+    top = xd.abs().amax(dim=1) if x.shape[1] else torch.zeros(x.shape[0], device=x.device, dtype=torch.float64)
+    fine = torch.isfinite(top)
+    q = torch.round(127 * xd / torch.where(top > 0, top, torch.ones_like(top))[:, None])
+    q = torch.where(fine[:, None], q, torch.zeros_like(q)).to(torch.int8)
+    # (a tensor over a number is a product with its reciprocal: over a tensor, and rounded once)
+    scale = (top / torch.full_like(top, 127)).float()
+    return q, torch.where(fine, scale, torch.full_like(scale, math.nan))
+
+
+def same_scales(a, b):
+    return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 7), (3, 8), (9, 64), (5, 257), (33, 1024), (7, 1025), (64, 4096), (2, 8191),
+                                 (3, 8192), (2, 8200), (2, 32768), (2, 32777), (1, 70001), (4000, 2050), (1000, 96)])
+def test_quantize(M, K, dtype):
+    for x in (rand((M, K), dtype, M + K), rand((M, K), dtype, K) * torch.exp(3 * rand((M, 1), torch.float32, 1)).to(dtype)):
+        for y in (x, off_by_one(x)):
+            q, scale = pws.gemm_i8_quantize(y)
+            want, want_scale = quantized64(x)
+            assert torch.equal(q, want) and same_scales(scale, want_scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_every_value(dtype):
+    """Every finite value beside every tenth of a set of largest ones, at three magnitudes."""
+    bits = torch.arange(0, 1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(dtype)
+    bits = bits[torch.isfinite(bits)]
+    g = torch.Generator().manual_seed(5)
+    for exponent in ((-20, 0, 15) if dtype == F16 else (-130, -70, 0, 70, 127)):
+        tops = (1 + torch.randint(0, 1024, (40,), generator=g).double() / 1024) * 2.0 ** exponent
+        for top in tops.to(dtype).unique():
+            x = bits[bits.abs() <= top.to("cuda")]
+            x = torch.cat([x, top.to("cuda").view(1)]).view(1, -1)
+            q, scale = pws.gemm_i8_quantize(x)
+            want, want_scale = quantized64(x)
+            assert torch.equal(q, want) and same_scales(scale, want_scale), (exponent, top)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_halves_go_to_even(dtype):
+    # 127 x / top halfway between integers: top = 127 * 2^k and x = (n + 1/2) 2^k, and x = top / 2
+    n = torch.arange(-127, 127, device="cuda").double() + 0.5
+    for top in (127.0, 127 * 2.0 ** -12):
+        x = torch.cat([n * top / 127, torch.tensor([top], device="cuda")]).to(dtype).view(1, -1)
+        q, _ = pws.gemm_i8_quantize(x)
+        assert torch.equal(q, torch.round(x.double() * 127 / top).to(torch.int8))
+    x = rand((50, 64), dtype, 3)
+    x[:, 1] = x.abs().amax(dim=1)
+    x[:, 2] = x[:, 1] / 2
+    q, _ = pws.gemm_i8_quantize(x)
+    assert (q[:, 2] == 64).all()                    # 63.5
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_zero_and_nonfinite_rows(dtype):
+    for K in (5, 64, 3000, 9000):
+        x = rand((6, K), dtype, K)
+        x[0] = 0
+        x[1, K - 1] = math.inf
+        x[2, 0] = -math.inf
+        x[3, K // 2] = math.nan
+        q, scale = pws.gemm_i8_quantize(x)
+        assert not q[:4].any() and scale[0] == 0 and torch.isnan(scale[1:4]).all()
+        want, want_scale = quantized64(x[4:])
+        assert torch.equal(q[4:], want) and torch.equal(scale[4:], want_scale)
+
+
+def test_quantize_empty():
+    q, scale = pws.gemm_i8_quantize(torch.empty(3, 0, device="cuda", dtype=F16))
+    assert q.shape == (3, 0) and torch.equal(scale, torch.zeros(3, device="cuda"))
+    q, scale = pws.gemm_i8_quantize(torch.empty(0, 5, device="cuda", dtype=F16))
+    assert q.shape == (0, 5) and scale.shape == (0,)
+
+
+# ---------------------------------------------------------------- 8-bit product
+
+I8 = [(1, 1, 1), (1, 16, 64), (1, 4096, 1000), (1, 333, 4096), (2, 100, 17), (3, 1000, 2048), (4, 129, 1023), (5, 40, 16),
+      (7, 4096, 4096), (8, 500, 1030), (9, 64, 1024), (15, 77, 1025), (16, 2048, 512), (17, 256, 2050), (32, 1000, 8192),
+      (33, 100, 96), (64, 300, 4100), (65, 3000, 640), (100, 128, 131071), (128, 129, 1040), (129, 640, 3000),
+      (300, 2052, 2050), (1000, 1000, 1), (700, 5, 333), (2048, 1536, 768), (4000, 300, 2049)]
+
+
+def i8_want(a, b, sa, sb):
+    total = (a.double() @ b.double().t())
+    assert total.abs().max() < 2 ** 53
+    return total * sa.double()[:, None] * sb.double()
+
+
+def i8_check(out, want, dtype):
+    assert out.dtype == dtype and out.shape == want.shape
+    tol = want.abs() * 3 * 2.0 ** -24
+    err = (out.double() - want).abs()
+    assert (err <= tol + half_unit(want.abs() + tol, dtype)).all(), float((err / want.abs()).max())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", I8)
+def test_i8(M, N, K, dtype):
+    a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+    # (binary16: the largest sum, K * 2^14, times the scales stays below 65504)
+    sa, sb = rand((M,), torch.float32, 3).abs() * 0.02 + 0.001, rand((N,), torch.float32, 4).abs() * 0.02 + 0.001
+    want = i8_want(a, b, sa, sb)
+    out = pws.gemm_i8_nt(a, b, sa, sb, dtype=dtype)
+    i8_check(out, want, dtype)
+    for i in range(2):
+        ops = [off_by_one(t) if i == j else t for j, t in enumerate((a, b))]
+        assert same_bits(pws.gemm_i8_nt(*ops, sa, sb, dtype=dtype), out)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 131071), (8, 33, 131071), (12, 33, 131071), (40, 24, 131071), (300, 300, 131071), (2, 64, 4096),
+                                   (200, 64, 4096)])
+def test_i8_sums_are_exact(M, N, K):
+    """Sums near 2^31 that differ in their last bits: the difference of two of
+    them is exact only if each is."""
+    a = torch.full((M, K), -128, device="cuda", dtype=torch.int8)
+    b = torch.full((N, K), -128, device="cuda", dtype=torch.int8)
+    a[:, -1] = torch.arange(M, device="cuda").to(torch.int8) % 100
+    b[:, K // 2] = torch.arange(N, device="cuda").to(torch.int8) % 100 - 50
+    total = (a.double() @ b.double().t())
+    # 2^-16 of the largest sum is 32768: in binary16 units of 16 or 32; so look at the sum in
+    # pieces through the scale, whose fp32 product is exact for powers of two
+    out = pws.gemm_i8_nt(a, b, torch.full((M,), 2.0 ** -16, device="cuda"), torch.ones(N, device="cuda"), dtype=F16)
+    i8_check(out, total * 2.0 ** -16, F16)
+    # one more column cancels all but the last bits: -128 * 128 each, with opposite sign
+    half = K // 2
+    c = a.clone()
+    c[:, :half] = 127
+    d = b.clone()
+    d[:, :2 * half] = -128
+    c[:, half:2 * half] = -127
+    want = c.double() @ d.double().t()
+    assert want.abs().max() < 2 ** 15
+    ones = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    i8_check(pws.gemm_i8_nt(c, d, *ones, dtype=F16), want, F16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_i8_scales(dtype):
+    """Zero, infinite and NaN scales act on their own row and column; scales whose
+    product leaves fp32's range act one after the other."""
+    for M, N, K in ((1, 64, 64), (20, 96, 256), (300, 260, 128)):
+        a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+        a[:, 0] = b[:, 0] = 1
+        sa, sb = torch.full((M,), 1e-3, device="cuda"), torch.full((N,), 1e-3, device="cuda")
+        sb[3], sb[5], sb[7] = 0.0, math.nan, math.inf
+        want = i8_want(a, b, sa, sb)
+        out = pws.gemm_i8_nt(a, b, sa, sb, dtype=dtype)
+        assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(torch.isinf(out), torch.isinf(want))
+        fine = torch.isfinite(want)
+        assert ((out.double() - want).abs() <= want.abs() * 3 * 2.0 ** -24 + half_unit(want, dtype))[fine].all()
+        tiny = pws.gemm_i8_nt(a, b, torch.full((M,), 1e-30, device="cuda"), torch.full((N,), 1e30, device="cuda"), dtype=dtype)
+        total = a.double() @ b.double().t()
+        err = (tiny.double() - total).abs()
+        ok = total.abs() < 60000
+        assert (err <= total.abs() * 2.0 ** -20 + half_unit(total, dtype))[ok].all()
+
+
+def test_i8_empty():
+    f = torch.zeros(0, device="cuda")
+    e = lambda *s: torch.empty(*s, device="cuda", dtype=torch.int8)  # noqa: E731
+    one = torch.ones(3, device="cuda")
+    assert not pws.gemm_i8_nt(e(3, 0), e(4, 0), one, torch.ones(4, device="cuda")).any()
+    assert pws.gemm_i8_nt(e(0, 8), e(3, 8), f, one).shape == (0, 3)
+    assert pws.gemm_i8_nt(e(3, 8), e(0, 8), one, f).shape == (3, 0)
+
+
+def test_i8_writes_its_rows_alone():
+    for M, N, K in ((3, 70, 100), (20, 33, 64), (200, 65, 128)):
+        a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+        ones = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+        want = pws.gemm_i8_nt(a, b, *ones, dtype=F16)
+        room = torch.full((M * N + 64,), 7.0, device="cuda", dtype=F16)
+        need = pws.ctypes.c_int64()
+        lib = pws.load_library()
+        assert lib.gemm_i8_nt_workspace(M, N, K, a.data_ptr(), b.data_ptr(), 0, pws.ctypes.byref(need)) == 0
+        ws = torch.full((need.value + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+        rc = lib.gemm_i8_nt(M, N, K, a.data_ptr(), b.data_ptr(), ones[0].data_ptr(), ones[1].data_ptr(),
+                            room[32:].data_ptr(), 0, ws.data_ptr() if need.value else None, need.value,
+                            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        assert same_bits(room[32:32 + M * N].view(M, N), want)
+        assert (room[:32] == 7).all() and (room[32 + M * N:] == 7).all() and (ws[need.value:] == 0xFF).all()
+
+
+# ---------------------------------------------------------------- mixture of experts
+
+
+def act64(g, act):
+    if act == "silu":
+        return g * torch.sigmoid(g)
+    return 0.5 * g * (1 + torch.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)))
+
+
+def layer(M, K, F, E, dtype, i8, seed=0, logits=1.5):
+    """x, router, the three weights as the call takes them, scales or None, and their values in 64 bits."""
+    x = rand((M, K), dtype, seed + 1)
+    wr = rand((E, K), dtype, seed + 2, logits * max(1, K) ** -0.5)
+    ws, scales, values = [], [], []
+    for i, shape in enumerate(((E, F, K), (E, F, K), (E, K, F))):
+        w = rand(shape, dtype, seed + 3 + i, max(1, shape[2]) ** -0.5)
+        if i8:
+            q, s = pws.gemm_i8_quantize(w.view(-1, shape[2]))
+            ws.append(q.view(shape))
+            scales.append(s.view(shape[:2]))
+            values.append(ws[-1].double() * scales[-1].double()[..., None])
+        else:
+            ws.append(w)
+            values.append(w.double())
+    return x, wr, ws, tuple(scales) if i8 else None, values
+
+
+def moe_want(x, wr, values, top_k, act, normalize, dtype):
+    """(y, experts, weights, bound on y's error before its rounding) in 64 bits."""
+    xd = x.double()
+    M, K = x.shape
+    F = values[0].shape[1]
+    z = xd @ wr.double().t()
+    order = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :top_k]
+    chosen = z.gather(1, order)
+    p = torch.exp(chosen - torch.logsumexp(chosen if normalize else z, dim=1, keepdim=True))
+    y, bound = torch.zeros_like(xd), torch.zeros_like(xd)
+    for m in range(M):
+        for j in range(top_k):
+            e = int(order[m, j])
+            wg, wu, wd = (v[e] for v in values)
+            g, u = wg @ xd[m], wu @ xd[m]
+            eg, eu = acc_error(K, wg.abs() @ xd[m].abs()), acc_error(K, wu.abs() @ xd[m].abs())
+            h = p[m, j] * act64(g, act) * u
+            # |act'| <= 1.13; act, p and the scales to 2^-19 relative together
+            eh = p[m, j] * (1.13 * eg * (u.abs() + eu) + act64(g, act).abs() * eu) + 2.0 ** -19 * h.abs()
+            eh = eh + (2.0 ** -16 * h.abs() if dtype == BF16 else 2.0 ** -22 * h.abs() + 2.0 ** -25)
+            y[m] += wd @ h
+            bound[m] += wd.abs() @ eh + acc_error(F, wd.abs() @ h.abs()) * 2
+    # (all experts' sums of a token are one more sum of top_k terms)
+    return y, order.int(), p, bound + top_k * 2.0 ** -23 * y.abs()
+
+
+MOE = [(1, 64, 64, 4, 2), (1, 1024, 512, 32, 4), (1, 1030, 333, 12, 3), (1, 8, 1, 1, 1), (2, 96, 40, 5, 5), (3, 257, 129, 64, 6),
+       (5, 512, 768, 16, 1), (7, 1030, 731, 12, 3), (8, 640, 256, 128, 8), (9, 130, 66, 7, 2), (16, 1024, 320, 64, 8),
+       (17, 72, 96, 3, 2), (31, 500, 100, 33, 4), (32, 256, 512, 8, 2), (64, 192, 80, 6, 3), (65, 128, 64, 4, 2),
+       (130, 64, 48, 9, 4), (4, 16, 4100, 3, 2), (4, 4104, 16, 3, 2), (6, 48, 32, 1024, 32)]
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["16bit", "8bit"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F,E,top_k", MOE)
+def test_moe(M, K, F, E, top_k, dtype, i8):
+    act, normalize = ("gelu" if (M + F) % 2 else "silu"), bool((M + E) % 2)
+    x, wr, ws, scales, values = layer(M, K, F, E, dtype, i8)
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, top_k, scales=scales, act=act, normalize=normalize)
+    want, order, p, bound = moe_want(x, wr, values, top_k, act, normalize, dtype)
+    assert experts.dtype == torch.int32 and torch.equal(experts, order)
+    assert weights.dtype == torch.float32 and ((weights.double() - p).abs() <= 2.0 ** -20 * p + 1e-30).all()
+    assert y.dtype == dtype and y.shape == x.shape
+    err = (y.double() - want).abs()
+    ok = err <= bound + half_unit(want.abs() + bound, dtype)
+    assert ok.all(), f"{int((~ok).sum())} off, worst {float((err / (bound + half_unit(want, dtype))).max()):.3f}"
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["16bit", "8bit"])
+def test_moe_any_alignment(i8):
+    for M, K, F in ((3, 128, 64), (20, 64, 128)):
+        x, wr, ws, scales, _ = layer(M, K, F, 6, BF16, i8)
+        want = pws.gemm_moe_nt(x, wr, *ws, 2, scales=scales)
+        for i in range(5):
+            ops = [off_by_one(t) if i == j else t for j, t in enumerate((x, wr, *ws))]
+            got = pws.gemm_moe_nt(*ops, 2, scales=scales)
+            assert all(same_bits(a, b) for a, b in zip(got, want)), i
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_moe_ties_go_to_the_lower_index(dtype):
+    M, K, F, E = 5, 96, 32, 24
+    x, wr, ws, _, _ = layer(M, K, F, E, dtype, False)
+    wr[7], wr[3], wr[20] = wr[11], wr[11], wr[11]
+    _, experts, weights = pws.gemm_moe_nt(x, wr, *ws, E)
+    for m in range(M):
+        where = [experts[m].tolist().index(e) for e in (3, 7, 11, 20)]
+        assert where == list(range(where[0], where[0] + 4))
+        assert len(set(weights[m, where[0]:where[0] + 4].tolist())) == 1
+    assert torch.equal(experts.sort(dim=1).values, torch.arange(E, device="cuda", dtype=torch.int32).expand(M, E))
+    _, experts, weights = pws.gemm_moe_nt(x, torch.zeros_like(wr), *ws, 4)
+    assert torch.equal(experts, torch.arange(4, device="cuda", dtype=torch.int32).expand(M, 4)) and (weights == 0.25).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_moe_near_logits_go_by_their_true_order(dtype):
+    """Logits that differ by one part in 2^33 of the terms they are sums of."""
+    K, E = 2048, 8
+    x = rand((4, K), dtype, 1)
+    x[:, -1] = 2.0 ** -11
+    row = rand((1, K), dtype, 2)
+    wr = row.repeat(E, 1)
+    wr[:, -1] = torch.tensor([3.0, 1.0, 7.0, 0.0, 6.0, 2.0, 5.0, 4.0], device="cuda") * 2.0 ** -12
+    _, _, ws, _, _ = layer(1, K, 8, E, dtype, False)
+    _, experts, _ = pws.gemm_moe_nt(x, wr.to(dtype), *ws, E)
+    assert experts.tolist() == [[2, 4, 6, 7, 0, 5, 1, 3]] * 4
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_moe_nonfinite_stays_in_its_row(dtype):
+    M, K, F, E = 10, 64, 48, 8
+    x, wr, ws, _, _ = layer(M, K, F, E, dtype, False)
+    clean = pws.gemm_moe_nt(x, wr, *ws, 2)
+    x[3, 5], x[7, 0] = math.nan, math.inf
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, 2)
+    good = [m for m in range(M) if m not in (3, 7)]
+    for a, b in zip((y, experts, weights), clean):
+        assert same_bits(a[good], b[good])
+    assert torch.isnan(y[3]).all() and torch.isnan(weights[3]).all() and ((experts >= 0) & (experts < E)).all()
+    assert all(len(set(r)) == 2 for r in experts.tolist())
+    assert not torch.isfinite(y[7]).any()
+    # experts that no token chose may hold anything
+    x, wr, ws, _, _ = layer(1, 120, 100, E, dtype, False)
+    want, experts, _ = pws.gemm_moe_nt(x, wr, *ws, 2)
+    for e in set(range(E)) - set(experts[0].tolist()):
+        for w in ws:
+            w[e] = math.nan
+    assert same_bits(pws.gemm_moe_nt(x, wr, *ws, 2)[0], want)
+
+
+def test_moe_ragged_rows_do_not_meet_their_neighbours():
+    """Odd rows followed by others' infinities: what lies behind a row's end never reaches its sum."""
+    for K, F in ((33, 70), (70, 33), (1023, 15)):
+        x, wr, ws, _, values = layer(2, K, F, 3, F16, False)
+        want, experts, _ = pws.gemm_moe_nt(x[:1], wr, *ws, 1)
+        keep = int(experts[0, 0])
+        for w in ws:
+            for e in range(3):
+                if e != keep:
+                    w[e] = math.inf
+        both = torch.cat([x[:1], torch.full_like(x[:1], math.inf)])
+        y, experts, _ = pws.gemm_moe_nt(both[:1].contiguous(), wr, *ws, 1)
+        assert same_bits(y, want) and int(experts[0, 0]) == keep
+
+
+def test_moe_large_values():
+    """bfloat16 activations beyond binary16's range, and their 8-bit weights."""
+    for i8 in (False, True):
+        x, wr, ws, scales, values = layer(4, 128, 96, 6, BF16, i8)
+        x = x * 256
+        wr = wr / 256
+        y, experts, _ = pws.gemm_moe_nt(x, wr, *ws, 2, scales=scales)
+        want, order, _, bound = moe_want(x, wr, values, 2, "silu", True, BF16)
+        assert torch.equal(experts, order) and want.abs().max() > 1e4
+        assert ((y.double() - want).abs() <= bound + half_unit(want.abs() + bound, BF16)).all()
+
+
+def test_moe_empty():
+    x, wr, ws, _, _ = layer(3, 64, 0, 4, F16, False)
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, 2)
+    assert not y.any() and experts.shape == (3, 2) and ((weights.sum(1) - 1).abs() < 1e-6).all()
+    x, wr, ws, _, _ = layer(3, 0, 8, 4, F16, False)
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, 2)
+    assert y.shape == (3, 0) and experts.tolist() == [[0, 1]] * 3 and (weights == 0.5).all()
+    x, wr, ws, _, _ = layer(0, 16, 8, 4, F16, False)
+    assert [t.shape[0] for t in pws.gemm_moe_nt(x, wr, *ws, 2)] == [0, 0, 0]
+
+
+# ---------------------------------------------------------------- as they are used
+
+
+def serve(x, p):
+    """A block as it is served in 8 bits: a quantized projection, then the experts, then the head's projection."""
+    q, s = pws.gemm_i8_quantize(x)
+    a = pws.gemm_i8_nt(q, p["proj"][0], s, p["proj"][1], dtype=x.dtype)
+    y, experts, weights = pws.gemm_moe_nt(a, p["router"], *p["w"], 2, scales=p["scales"])
+    q, s = pws.gemm_i8_quantize(y)
+    return pws.gemm_i8_nt(q, p["head"][0], s, p["head"][1], dtype=x.dtype), a, y, experts, weights
+
+
+def block(K, F, E, dtype):
+    _, wr, ws, scales, values = layer(1, K, F, E, dtype, True)
+    return {"proj": pws.gemm_i8_quantize(rand((K, K), dtype, 50, K ** -0.5)), "router": wr, "w": ws, "scales": scales,
+            "head": pws.gemm_i8_quantize(rand((777, K), dtype, 51, K ** -0.5)), "values": values}
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [1, 6, 40])
+def test_run_together(M, dtype):
+    K, F, E = 256, 192, 10
+    p = block(K, F, E, dtype)
+    x = rand((M, K), dtype, 60)
+    out, a, y, experts, _ = serve(x, p)
+    q, s = quantized64(x)
+    i8_check(a, i8_want(q, p["proj"][0], s, p["proj"][1]), dtype)
+    want, order, _, bound = moe_want(a, p["router"], p["values"], 2, "silu", True, dtype)
+    assert torch.equal(experts, order)
+    assert ((y.double() - want).abs() <= bound + half_unit(want.abs() + bound, dtype)).all()
+    q, s = quantized64(y)
+    i8_check(out, i8_want(q, p["head"][0], s, p["head"][1]), dtype)
+
+
+def test_graph_replay_and_streams():
+    """Captured and replayed on new inputs, on a stream of its own and while another stream runs the same layer:
+    the same bits as one call after the other."""
+    for M in (1, 12, 40):
+        p = block(128, 96, 8, BF16)
+        xs = [rand((M, 128), BF16, 70 + i) for i in range(3)]
+        want = [[t.clone() for t in serve(x, p)] for x in xs]
+        static = xs[0].clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            serve(static, p)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = serve(static, p)
+        for x, w in zip(xs, want):
+            static.copy_(x)
+            graph.replay()
+            assert all(same_bits(a, b) for a, b in zip(got, w))
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        outs = []
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, x in zip(streams, xs):
+                with torch.cuda.stream(s):
+                    outs.append(serve(x, p))
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            assert all(same_bits(a, b) for a, b in zip(o, want[i % 3]))
+
+
+def test_stream_argument():
+    s = torch.cuda.Stream()
+    x, wr, ws, _, _ = layer(2, 64, 32, 4, F16, False)
+    torch.cuda.synchronize()
+    want = pws.gemm_moe_nt(x, wr, *ws, 2)
+    got = pws.gemm_moe_nt(x, wr, *ws, 2, stream=s)
+    q, sc = pws.gemm_i8_quantize(x, stream=s)
+    out = pws.gemm_i8_nt(q, q, sc, sc, stream=s)
+    s.synchronize()
+    assert all(same_bits(a, b) for a, b in zip(got, want))
+    assert same_bits(out, pws.gemm_i8_nt(q, q, sc, sc))
+    assert pws.gemm_device_status(s) == pws.GEMM_OK
