@@ -24,10 +24,10 @@ enum Form { kHalf = 0, kBfloat = 1, kI8Half = 2, kI8Bfloat = 3 };
 
 constexpr bool is_bf16(int form) { return form & 1; }
 constexpr bool is_i8(int form) { return form >= kI8Half; }
-// k of a step, bytes of a weight, 32-bit registers of 16-bit values a lane holds of a row
+// k of a step, bytes of a weight, and the halves of a step that 8-bit weights are widened in
 constexpr int step_k(int form) { return is_i8(form) ? 64 : 32; }
 constexpr int weight_bytes(int form) { return is_i8(form) ? 1 : 2; }
-constexpr int pairs_of(int form) { return is_i8(form) ? 8 : 4; }
+constexpr int halves_of(int form) { return is_i8(form) ? 2 : 1; }
 
 template <bool BF16>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -46,14 +46,12 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One step's multiplies of a 16-row weight tile (rows g and g + 8 of this
-// lane) by one tile of eight tokens.
-template <int FORM>
-__device__ __forceinline__ void mma_step(float (&d)[4], const uint32_t (&lo)[pairs_of(FORM)],
-                                         const uint32_t (&hi)[pairs_of(FORM)], const uint32_t (&x)[pairs_of(FORM)]) {
-#pragma unroll
-    for (int i = 0; i < pairs_of(FORM); i += 2)
-        mma_16x8x16<is_bf16(FORM)>(d, lo[i], hi[i], lo[i + 1], hi[i + 1], x[i], x[i + 1]);
+// 32 k of a 16-row weight tile (rows g and g + 8 of this lane) by one tile of
+// eight tokens.
+template <bool BF16>
+__device__ __forceinline__ void mma_step(float (&d)[4], const uint32_t (&lo)[4], const uint32_t (&hi)[4], const uint32_t (&x)[4]) {
+    mma_16x8x16<BF16>(d, lo[0], hi[0], lo[1], hi[1], x[0], x[1]);
+    mma_16x8x16<BF16>(d, lo[2], hi[2], lo[3], hi[3], x[2], x[3]);
 }
 
 // Four 8-bit integers as two pairs of 16-bit values, exactly.
@@ -83,17 +81,38 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     }
 }
 
-// A step's 16 bytes of a weight row as the pairs the multiply takes.
+// A step's 16 bytes of a weight row (or half of them) as the pairs the multiply takes.
 template <int FORM>
-__device__ __forceinline__ void widen(const uint4& w, uint32_t (&v)[pairs_of(FORM)]) {
+__device__ __forceinline__ void widen(const uint4& w, int half, uint32_t (&v)[4]) {
     if constexpr (is_i8(FORM)) {
-        widen4<is_bf16(FORM)>(w.x, v[0], v[1]);
-        widen4<is_bf16(FORM)>(w.y, v[2], v[3]);
-        widen4<is_bf16(FORM)>(w.z, v[4], v[5]);
-        widen4<is_bf16(FORM)>(w.w, v[6], v[7]);
+        widen4<is_bf16(FORM)>(half ? w.z : w.x, v[0], v[1]);
+        widen4<is_bf16(FORM)>(half ? w.w : w.y, v[2], v[3]);
     } else {
         v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
     }
+}
+
+// Bytes shift .. shift + 15 of two 16-byte blocks.
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint32_t shift) {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const uint32_t q = shift >> 2, bits = (shift & 3u) * 8u;
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t a = q == 0 ? w[k] : q == 1 ? w[k + 1] : q == 2 ? w[k + 2] : w[k + 3];
+        const uint32_t b = q == 0 ? w[k + 1] : q == 1 ? w[k + 2] : q == 2 ? w[k + 3] : w[k + 4];
+        v[k] = __funnelshift_r(a, b, bits);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// The first `n` bytes of 16, and zeros.
+__device__ __forceinline__ uint4 cleared(const uint4& b, int n) {
+    if (n >= 16) return b;
+    uint32_t v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = n >= 4 * i + 4 ? v[i] : n > 4 * i ? v[i] & ((1u << (8 * (n - 4 * i))) - 1u) : 0u;
+    return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // 16 bytes read once: past L1.
@@ -105,29 +124,147 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
     return v;
 }
 
-// 16 bytes of a row at any alignment; `left` of them are the row's, the rest
-// are zeros, whatever follows in memory (a neighbour's infinity times a zero
-// would be NaN).
-static __device__ __noinline__ uint4 load_ragged_end(const uint8_t* p, int left) {
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < left) v[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-// 16 bytes of a row, `left` bytes before its end.  ALIGNED: rows start on
-// 16-byte boundaries and are a multiple of 16 bytes long.
+// 16 bytes of a row, `left` bytes before its end; what lies behind the end is
+// zeros, whatever follows in memory (a neighbour's infinity times a zero would be
+// NaN).  ALIGNED: rows start on 16-byte boundaries and are a multiple of 16
+// bytes long.  Otherwise the one or two aligned blocks that hold bytes of the row
+// are read and shifted together; a block that holds none is not touched.
 template <bool ALIGNED, bool STREAM>
 __device__ __forceinline__ uint4 load_row(const uint8_t* p, int64_t left) {
+    const auto load = [](const void* q) { return STREAM ? load_stream(q) : __ldg(static_cast<const uint4*>(q)); };
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (ALIGNED) {
-        if (left <= 0) return make_uint4(0u, 0u, 0u, 0u);
-        return STREAM ? load_stream(p) : __ldg(reinterpret_cast<const uint4*>(p));
+        if (left > 0) v = load(p);
     } else {
-        if (left >= 16) return fused::load_unaligned16(reinterpret_cast<const uint16_t*>(p));
-        return left <= 0 ? make_uint4(0u, 0u, 0u, 0u) : load_ragged_end(p, static_cast<int>(left));
+        const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+        const uint8_t* block = p - shift;
+        uint4 w = v;
+        if (left > 0) v = load(block);
+        if (shift != 0 && left > 16 - static_cast<int>(shift)) w = load(block + 16);
+        v = shifted(v, w, shift);
+        v = cleared(v, left < 16 ? static_cast<int>(left) : 16);
     }
+    return v;
 }
+
+// The way of weights and tokens into registers: a ring of a few steps in shared
+// memory for each warp alone, filled by 16-byte asynchronous copies.  A lane
+// reads what it copied itself, so no other warp is waited for, and the
+// ring runs on over the borders of row blocks and experts, so that memory is
+// never idle while sums are joined.  The tokens come the same way: they are L2's, but
+// behind the weights' traffic an L2 load takes as long as a whole step (loaded one step
+// ahead into registers, 16 tokens over 56 experts of 1536 x 4096 read 4.9 TB/s; with
+// no token loads at all 5.9).
+//
+// Rows that do not start on 16-byte boundaries: the two aligned blocks that
+// hold the lane's 16 bytes, shifted together when they are read and cleared behind
+// the row's end.  The second one is the next lane's first (the last of a row's four
+// lanes copies its own).  A block that holds none of the row's bytes is not touched.
+constexpr int kLoads = 4;               // weight rows a lane reads a step
+
+__device__ __forceinline__ void cp_async_l1(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// TOKENS: 16-byte pieces of token rows a lane takes a step.
+constexpr int ring_slot(bool aligned, int tokens) { return (kLoads + (aligned ? 0 : 1) + tokens) * 512; }
+// As many stages, up to four, as leave room for two blocks of eight warps an SM;
+// where that is less than three, for one block with 64 KB of sums.
+constexpr int ring_stages(bool aligned, int tokens) {
+    const int stage = 8 * ring_slot(aligned, tokens), two = 92160 / stage, one = 150000 / stage;
+    return two >= 3 ? (two < 4 ? two : 4) : one < 4 ? one : 4;
+}
+constexpr int ring_bytes(bool aligned, int tokens, int warps) { return warps * ring_stages(aligned, tokens) * ring_slot(aligned, tokens); }
+
+template <bool ALIGNED, int TOKENS>
+struct Ring {
+    static constexpr int STAGES = ring_stages(ALIGNED, TOKENS), WEIGHTS = kLoads + (ALIGNED ? 0 : 1);
+    static constexpr uint32_t BLOCK = 512, SLOT = ring_slot(ALIGNED, TOKENS);
+    uint32_t first, fill, read;
+
+    __device__ __forceinline__ Ring(uint32_t warp_base) : first(warp_base + (threadIdx.x % 32) * 16), fill(first), read(first) {}
+    __device__ __forceinline__ uint32_t after(uint32_t at) const { return at == first + (STAGES - 1) * SLOT ? first : at + SLOT; }
+
+    // The block behind the last lane's of row i.
+    __device__ __forceinline__ uint32_t after_row(uint32_t stage, int i) const {
+        return stage - (threadIdx.x % 32) * 16 + kLoads * BLOCK + i * 128 + (threadIdx.x % 32) / 4 * 16;
+    }
+    // The lane's 16 bytes of each row into the next stage; `left` bytes of the
+    // rows from there on (none or less: zeros).
+    __device__ __forceinline__ void copy(const uint8_t* const (&at)[kLoads], int left) {
+        if (ALIGNED && left <= 0) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(fill + i * BLOCK), "r"(0) : "memory");
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            if constexpr (ALIGNED) {
+                cp_async<16>(fill + i * BLOCK, at[i], 16u);
+            } else {
+                const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at[i]) & 15u);
+                // (the lane before may want what its block holds of the row's end; what none wants is cleared)
+                if (left > -shift) cp_async<16>(fill + i * BLOCK, at[i] - shift, 16u);
+                if (threadIdx.x % 4 == 3 && left > 16 - shift) cp_async<16>(after_row(fill, i), at[i] - shift + 16, 16u);
+            }
+        }
+    }
+    // Piece i of the tokens: 16 bytes at `at`, through L1 (past it, every block of the GPU asks the
+    // same few lines of L2: 78 us instead of 44 for one token's gate).
+    __device__ __forceinline__ void copy_token(int i, const uint16_t* at) { cp_async_l1(fill + (WEIGHTS + i) * BLOCK, at); }
+    // Ends a stage (an empty one too: stages are counted).
+    __device__ __forceinline__ void commit() {
+        cp_async_commit();
+        fill = after(fill);
+    }
+    // The oldest stage has landed, of STAGES - 1 in flight.
+    __device__ __forceinline__ void wait() {
+        cp_async_wait_group<STAGES - 2>();
+        __syncwarp();               // (ragged rows read each other's blocks)
+    }
+    // Row i's 16 bytes of the oldest stage.  `row`: any address of the row's that is a multiple of 16
+    // bytes from its start; `left`: as it was copied.
+    __device__ __forceinline__ uint4 get(int i, const uint8_t* row, int left) const {
+        uint4 lo, hi;
+        ld_shared_v4(read + i * BLOCK, lo.x, lo.y, lo.z, lo.w);
+        if constexpr (ALIGNED) return lo;
+        ld_shared_v4(threadIdx.x % 4 == 3 ? after_row(read, i) : read + i * BLOCK + 16, hi.x, hi.y, hi.z, hi.w);
+        return cleared(shifted(lo, hi, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u)), left);
+    }
+    __device__ __forceinline__ void get_token(int i, uint32_t (&v)[4]) const {
+        ld_shared_v4(read + (WEIGHTS + i) * BLOCK, v[0], v[1], v[2], v[3]);
+    }
+    __device__ __forceinline__ void pop() { read = after(read); }
+};
+
+// Units of work handed out to the blocks of a grid as they get to them: memory's
+// bandwidth is not shared evenly between SMs, and with equal parts the GPU waited
+// for its slowest (SMs busy for 73 % of the kernel, 4.3 TB/s).  A block's first
+// unit is its number; later ones come from a counter that starts at zero.
+//
+// Rings run on into the next units, so a block knows `ahead` units beyond the one
+// at work: unit i + ahead + 1 is claimed at the start of unit i and put into
+// the queue before a barrier of unit i.  A warp with n steps a unit looks at
+// unit i + ahead + 1 when it copies the last step before it, which is in unit i + 1
+// or later if ahead * n >= the ring's stages.
+struct Claims {
+    static constexpr int QUEUE = 16;
+    int* queue;                 // [QUEUE], shared
+    int* counter;
+    int ahead;
+
+    // steps: the fewest a warp that has any takes of a unit
+    static __device__ __forceinline__ int ahead_of(int64_t steps, int stages) { return steps >= stages ? 1 : stages; }
+    __device__ __forceinline__ int claim() const { return static_cast<int>(gridDim.x) + atomicAdd(counter, 1); }
+    // One thread, before a barrier.
+    __device__ __forceinline__ void start() const {
+        queue[0] = static_cast<int>(blockIdx.x);
+        for (int i = 1; i <= ahead; ++i) queue[i] = claim();
+    }
+    __device__ __forceinline__ void put(int i, int unit) const { queue[(i + ahead + 1) % QUEUE] = unit; }
+    __device__ __forceinline__ int unit(int i) const { return queue[i % QUEUE]; }
+};
 
 }  // namespace few
 }  // namespace pws

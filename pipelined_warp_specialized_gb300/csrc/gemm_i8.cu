@@ -152,11 +152,13 @@ widen_kernel(const __grid_constant__ Widen p, int64_t K, int64_t ld) {
         const int m = row >= p.rows[0] ? 1 : 0;
         row -= m * p.rows[0];
         const uint4 w = few::load_row<ALIGNED, true>(p.src[m] + row * K + c, K - c);
-        uint32_t v[8];
-        few::widen<few::kI8Half>(w, v);
         uint4* to = reinterpret_cast<uint4*>(p.dst[m] + row * ld + c);
-        to[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t v[4];
+            few::widen<few::kI8Half>(w, half, v);
+            to[half] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
     }
 }
 

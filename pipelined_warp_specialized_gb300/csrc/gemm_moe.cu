@@ -26,8 +26,10 @@ using namespace few;
 constexpr int kTokens = 64;             // tokens a pass: more are taken 64 at a time
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
+constexpr int64_t kMaxWidth = 1 << 24;  // of K and F
 constexpr int kRouteCtas = 8;           // CTAs of a cluster that share a token's experts
-constexpr int kRouteTokens = 4;         // tokens a cluster
+constexpr int kRouteTokens = 4;         // tokens a cluster, where there are many
+constexpr int route_threads(int tokens) { return tokens == 1 ? 1024 : 512; }
 constexpr int kWarps = 8;
 
 // ---------------------------------------------------------------- router
@@ -39,119 +41,175 @@ __device__ __forceinline__ void two_sum(float& s, float& c, float p) {
     s = t;
 }
 
-// Doubles in an order of unsigned integers: larger values first, NaN before all,
-// both zeros alike, never 0.
-__device__ __forceinline__ unsigned long long key_of(double z) {
-    if (z != z) return ~0ull;
-    const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(z + 0.0));
-    return b >> 63 ? ~b : b | (1ull << 63);
-}
-__device__ __forceinline__ double value_of(unsigned long long key) {
-    if (key == ~0ull) return __longlong_as_double(0x7ff8000000000000ll);
-    return __longlong_as_double(static_cast<long long>(key >> 63 ? key & ~(1ull << 63) : ~key));
+// A sum and its error as one value and what it lacks: hi = fl(s + c), lo the rest.
+// (FP64 has few units here: a row's last sums in doubles took as long as the row.)
+__device__ __forceinline__ float2 settled(float s, float c) {
+    const float hi = __fadd_rn(s, c);
+    // (an infinite or NaN sum's error terms mean nothing)
+    return fabsf(s) <= 3.4e38f ? make_float2(hi, __fadd_rn(__fsub_rn(s, hi), c)) : make_float2(s, 0.0f);
 }
 
-// The logits of up to kRouteTokens tokens by a cluster of kRouteCtas CTAs, a warp
-// an expert; the first CTA then chooses.  A product of two 16-bit values is exact
-// in fp32, and the sum is carried with its error, so logits are good to about
-// 2^-45 of sum |x w| and only a true tie is one (it goes to the lower index).
-// 7 additions and multiplications a product: 64 tokens x 128 experts x 4096 take
-// about 9 us of the GPU, where their experts' weights take hundreds.
-template <bool BF16, bool ALIGNED>
-__global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
-moe_route_kernel(const uint8_t* __restrict__ x, const uint8_t* __restrict__ w, int M, int64_t K, int E, int top_k,
-                 int normalize, int* __restrict__ experts, float* __restrict__ weights, int per_cluster) {
-    extern __shared__ unsigned long long keys[];        // [per_cluster][E], the first CTA's
+// Floats in the order of unsigned integers: larger values first, NaN before all,
+// both zeros alike, never 0.
+__device__ __forceinline__ uint32_t key32(float v) {
+    if (v != v) return 0xFFFFFFFFu;
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value32(uint32_t key) {
+    return key == 0xFFFFFFFFu ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key);
+}
+__device__ __forceinline__ unsigned long long key_of(float2 z) {
+    return static_cast<unsigned long long>(key32(z.x)) << 32 | key32(z.y);
+}
+__device__ __forceinline__ float2 value_of(unsigned long long key) {
+    return make_float2(value32(static_cast<uint32_t>(key >> 32)), value32(static_cast<uint32_t>(key)));
+}
+__device__ __forceinline__ float exp_difference(float2 z, float2 top) { return expf((z.x - top.x) + (z.y - top.y)); }
+
+// The logits of TOKENS tokens by a cluster of kRouteCtas CTAs, a warp a part of
+// an expert's row; the first CTA then adds the parts and chooses.  A product of two
+// 16-bit values is exact in fp32, and the sum is carried with its error, so logits are good to about
+// 2^-44 of sum |x w| and only a true tie is one (it goes to the lower index).
+// Seven additions and multiplications a product, latency for few tokens: every
+// lane has eight or more loads in flight.
+// What the router hands to the experts' kernels besides the choice.
+struct Handover {
+    int* counters;
+    uint16_t* x;
+    int64_t num_counters, ldx;
+};
+
+template <bool BF16, bool ALIGNED, int TOKENS>
+__global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(route_threads(TOKENS))
+moe_route_kernel(const uint8_t* __restrict__ x, const uint8_t* __restrict__ w, int M, int64_t K, int E, int parts, int top_k,
+                 int normalize, int* __restrict__ experts, float* __restrict__ weights, const __grid_constant__ Handover out) {
+    constexpr int UNROLL = TOKENS == 1 ? 4 : 2, THREADS = route_threads(TOKENS);
+    extern __shared__ unsigned long long sums[];        // [TOKENS][E][parts] pairs, then keys; the first CTA's
     grid_dependency_wait();
     allow_dependent_launch();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
-    const int token0 = static_cast<int>(blockIdx.x / kRouteCtas) * per_cluster;
-    const int count = min(per_cluster, M - token0);
-    const uint32_t keys0 = mapa_shared(smem_u32(keys), 0);
-    for (int e = static_cast<int>(rank) * kWarps + warp; e < E; e += kRouteCtas * kWarps) {
-        float s[kRouteTokens][2], c[kRouteTokens][2];
+    cluster_arrive_release();           // (no store to a CTA that has not begun)
+    const int token0 = static_cast<int>(blockIdx.x / kRouteCtas) * TOKENS;
+    const int count = min(TOKENS, M - token0);
+    const uint32_t sums0 = mapa_shared(smem_u32(sums), 0);
+    bool begun = false;
+    const int64_t span = ((K + parts - 1) / parts + 255) / 256 * 256;
+    for (int task = static_cast<int>(rank) * (THREADS / 32) + warp; task < E * parts; task += kRouteCtas * (THREADS / 32)) {
+        const int e = task / parts, part = task - e * parts;
+        float s[TOKENS][2], c[TOKENS][2];
 #pragma unroll
-        for (int t = 0; t < kRouteTokens; ++t) s[t][0] = s[t][1] = c[t][0] = c[t][1] = 0.0f;
+        for (int t = 0; t < TOKENS; ++t) s[t][0] = s[t][1] = c[t][0] = c[t][1] = 0.0f;
         const uint8_t* wr = w + static_cast<int64_t>(e) * K * 2;
-        for (int64_t k = lane * 8; k < K; k += 256) {
-            const uint4 wv = load_row<ALIGNED, false>(wr + 2 * k, 2 * (K - k));
-            const uint32_t wp[4] = {wv.x, wv.y, wv.z, wv.w};
+        const uint8_t* xr = x + static_cast<int64_t>(token0) * K * 2;
+        const int64_t end = min(K, (part + 1) * span);
+        for (int64_t k0 = part * span + lane * 8; k0 < end; k0 += 256 * UNROLL) {
+            uint4 wv[UNROLL], xv[TOKENS][UNROLL];
 #pragma unroll
-            for (int t = 0; t < kRouteTokens; ++t) {
-                if (t >= count) break;
-                const uint4 xv = load_row<ALIGNED, false>(x + (static_cast<int64_t>(token0 + t) * K + k) * 2, 2 * (K - k));
-                const uint32_t xp[4] = {xv.x, xv.y, xv.z, xv.w};
+            for (int u = 0; u < UNROLL; ++u) {
+                const int64_t k = k0 + 256 * u, left = k < end ? 2 * (K - k) : 0;
+                wv[u] = load_row<ALIGNED, false>(wr + 2 * k, left);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 a = fused::unpack16(wp[i], BF16), b = fused::unpack16(xp[i], BF16);
-                    two_sum(s[t][0], c[t][0], __fmul_rn(a.x, b.x));
-                    two_sum(s[t][1], c[t][1], __fmul_rn(a.y, b.y));
+                for (int t = 0; t < TOKENS; ++t)
+                    xv[t][u] = load_row<ALIGNED, false>(xr + (t * K + k) * 2, t < count ? left : 0);
+            }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const uint32_t wp[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+#pragma unroll
+                for (int t = 0; t < TOKENS; ++t) {
+                    const uint32_t xp[4] = {xv[t][u].x, xv[t][u].y, xv[t][u].z, xv[t][u].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = fused::unpack16(wp[i], BF16), b = fused::unpack16(xp[i], BF16);
+                        two_sum(s[t][0], c[t][0], __fmul_rn(a.x, b.x));
+                        two_sum(s[t][1], c[t][1], __fmul_rn(a.y, b.y));
+                    }
                 }
             }
         }
+        if (!begun) cluster_wait_acquire();
+        begun = true;
 #pragma unroll
-        for (int t = 0; t < kRouteTokens; ++t) {
-            if (t >= count) break;
-            const float top = __fadd_rn(s[t][0], s[t][1]);
-            // (an infinite sum's error terms are NaN)
-            double z = fabsf(top) <= 3.4e38f
-                           ? (static_cast<double>(s[t][0]) + c[t][0]) + (static_cast<double>(s[t][1]) + c[t][1])
-                           : static_cast<double>(top);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-            if (lane == 0) {
-                const unsigned long long key = key_of(z);
-                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(keys0 + 8u * static_cast<uint32_t>(t * E + e)), "l"(key)
-                             : "memory");
-            }
-        }
-    }
-    cluster_sync();
-    if (rank != 0) return;
-    for (int t = warp; t < count; t += kWarps) {
-        unsigned long long* row = keys + t * E;
-        double z_top = 0.0;
-        float mine = 0.0f, total = 0.0f;        // lane j's chosen expert's exponential
-        int my_expert = 0;
-        for (int j = 0; j < top_k; ++j) {
-            unsigned long long best = 0;
-            int at = 0;
-            for (int e = lane; e < E; e += 32)
-                if (row[e] > best) { best = row[e]; at = e; }
+        for (int t = 0; t < TOKENS; ++t) {
+            // (both pairs, then all lanes', with every error kept)
+            float sum = s[t][0], err = __fadd_rn(c[t][0], c[t][1]);
+            two_sum(sum, err, s[t][1]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
-                const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-                const int where = __shfl_xor_sync(0xffffffffu, at, o);
-                if (other > best || (other == best && where < at)) { best = other; at = where; }
+                const float other = __shfl_xor_sync(0xffffffffu, sum, o), more = __shfl_xor_sync(0xffffffffu, err, o);
+                err = __fadd_rn(err, more);
+                two_sum(sum, err, other);
             }
-            if (j == 0) z_top = value_of(best);
-            if (lane == j) {
-                my_expert = at;
-                mine = expf(static_cast<float>(value_of(best) - z_top));
-            }
-            __syncwarp();
-            if (lane == 0) row[at] = 0ull;
-            __syncwarp();
+            if (lane == 0 && t < count)
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(sums0 + 8u * static_cast<uint32_t>((t * E + e) * parts + part)),
+                             "f"(sum), "f"(err)
+                             : "memory");
         }
-        if (lane < top_k) total = mine;
-        if (!normalize)
-            for (int e = lane; e < E; e += 32)
-                if (row[e]) total += expf(static_cast<float>(value_of(row[e]) - z_top));
+    }
+    if (!begun) cluster_wait_acquire();
+    // what the experts' kernels start from: counters at zero, and the tokens in rows of a
+    // multiple of 64, padded with zeros, whatever x's alignment is
+    const int64_t thread = blockIdx.x * static_cast<int64_t>(THREADS) + threadIdx.x, threads = static_cast<int64_t>(gridDim.x) * THREADS;
+    for (int64_t i = thread; i < out.num_counters; i += threads) out.counters[i] = 0;
+    for (int64_t i = thread; i < M * (out.ldx / 8); i += threads) {
+        const int64_t m = i / (out.ldx / 8), k = (i - m * (out.ldx / 8)) * 8;
+        *reinterpret_cast<uint4*>(out.x + m * out.ldx + k) = load_row<ALIGNED, false>(x + (m * K + k) * 2, 2 * (K - k));
+    }
+    __syncthreads();            // (the cluster barrier wants whole warps, and the loops above part them)
+    cluster_sync();
+    if (rank != 0) return;
+    if (warp >= count) return;
+    // a warp a token: keys in place of the first parts
+    unsigned long long* row = sums + warp * E * parts;
+    const auto key_at = [&](int e) { return row + e * parts; };
+    for (int e = lane; e < E; e += 32) {
+        const float2* part = reinterpret_cast<const float2*>(row + e * parts);
+        float sum = part[0].x, err = part[0].y;
+        for (int i = 1; i < parts; ++i) {
+            err = __fadd_rn(err, part[i].y);
+            two_sum(sum, err, part[i].x);
+        }
+        *key_at(e) = key_of(settled(sum, err));
+    }
+    float2 z_top = make_float2(0.0f, 0.0f);
+    float mine = 0.0f, total = 0.0f;            // lane j's chosen expert's exponential
+    int my_expert = 0;
+    for (int j = 0; j < top_k; ++j) {
+        // the largest key: its high word, then its low word, then its lowest index
+        unsigned long long best = 0;
+        int at = 0;
+        for (int e = lane; e < E; e += 32)
+            if (*key_at(e) > best) { best = *key_at(e); at = e; }
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
+        const unsigned long long top = static_cast<unsigned long long>(hi) << 32 | lo;
+        at = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(at) : 0xffffffffu));
+        if (j == 0) z_top = value_of(top);
+        if (lane == j) {
+            my_expert = at;
+            mine = exp_difference(value_of(top), z_top);
+        }
+        if (at % 32 == lane) *key_at(at) = 0ull;
+    }
+    if (lane < top_k) total = mine;
+    if (!normalize)
+        for (int e = lane; e < E; e += 32)
+            if (*key_at(e)) total += exp_difference(value_of(*key_at(e)), z_top);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane < top_k) {
-            const int64_t to = static_cast<int64_t>(token0 + t) * top_k + lane;
-            experts[to] = my_expert;
-            weights[to] = mine / total;
-        }
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane < top_k) {
+        const int64_t to = static_cast<int64_t>(token0 + warp) * top_k + lane;
+        experts[to] = my_expert;
+        weights[to] = mine / total;
     }
 }
 
 // ---------------------------------------------------------------- experts
 
 struct Params {
-    const uint8_t* x;                   // [M, K]
+    const uint16_t* x;                  // [M][ldx], padded with zeros
     const uint8_t* w_gate;              // [E, F, K]
     const uint8_t* w_up;
     const uint8_t* w_down;              // [E, K, F]
@@ -162,292 +220,494 @@ struct Params {
     const float* weights;
     uint16_t* h;                        // [2][M top_k][ldh]: h' rounded, and what that left
     uint16_t* y;                        // [M, K]
-    int64_t K, F, ldh, lo_offset;
+    int64_t K, F, ldx, ldh, lo_offset;
     int M, E, top_k, act;
+    int* counters;                      // claims of gate and of down units, then each row block's arrivals; zero at first
+    float* partial;                     // [row blocks of 32][kMaxParts][32][ldy]
 };
 
-// The distinct experts of M * top_k choices, as a bit mask (a warp's lane holds a
-// word of it).  Every thread of the block.
-__device__ __forceinline__ void mark_experts(uint32_t* mask, const int* experts, int choices) {
-    if (threadIdx.x < 32) mask[threadIdx.x] = 0u;
+// What a block of the experts' kernels knows of the routing.  A kernel's entries
+// hold up to 8 NT tokens of an expert (NT tiles): an expert with more is taken once for
+// each 8 NT of them, its weights coming from L2 again, and the accumulators stay few.
+constexpr int kMaxEntries = kMaxExperts + kTokens * kMaxTopK / 8;
+struct alignas(16) Routing {
+    uint16_t experts[kTokens * kMaxTopK];       // each choice's
+    uint16_t active[kMaxEntries];               // an entry's expert, in ascending order
+    uint8_t tokens[kMaxExperts];                // of each expert
+    int entries;
+    uint16_t list[kWarps][2][16];     // choices of the entry a warp copies, and of the one it multiplies
+};
+
+// Every thread of the block.
+template <int SIZE>
+__device__ __forceinline__ void read_routing(Routing& r, const int* experts, int choices, int num_experts) {
+    const int lane = threadIdx.x % 32;
+    for (int i = threadIdx.x; i < (num_experts + 3) / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(r.tokens)[i] = 0u;
     __syncthreads();
     for (int i = threadIdx.x; i < choices; i += blockDim.x) {
         const int e = experts[i];
-        atomicOr(&mask[e >> 5], 1u << (e & 31));
+        r.experts[i] = static_cast<uint16_t>(e);
+        // (a byte holds an expert's tokens: each of 64 at most once)
+        atomicAdd(reinterpret_cast<uint32_t*>(r.tokens) + e / 4, 1u << (8 * (e % 4)));
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int before = 0;
+        for (int e0 = 0; e0 < num_experts; e0 += 32) {
+            const int e = e0 + lane, passes = e < num_experts ? (r.tokens[e] + SIZE - 1) / SIZE : 0;
+            int at = passes;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += v;
+            }
+            const int total = __shfl_sync(0xffffffffu, at, 31);
+            at += before - passes;
+            for (int i = 0; i < passes; ++i) r.active[at + i] = static_cast<uint16_t>(e);
+            before += total;
+        }
+        if (lane == 0) r.entries = before;
     }
     __syncthreads();
 }
 
-// The n-th marked expert, and how many there are; a whole warp.
-__device__ __forceinline__ int nth_expert(const uint32_t* mask, int n, int& total) {
-    const int lane = threadIdx.x % 32;
-    const uint32_t word = mask[lane];
-    int before = __popc(word);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
+// The choices of one entry in ascending order, to a warp's list; their number.
+template <int SIZE>
+__device__ __forceinline__ int list_tokens(const Routing& r, uint16_t* list, int entry, int choices) {
+    const int lane = threadIdx.x % 32, expert = r.active[entry];
+    // (an expert's entries follow one another)
+    int n = 0;
+    for (int i = entry; i > 0 && r.active[i - 1] == expert; --i) n -= SIZE;
+    __syncwarp();
+    for (int i = lane; i - lane < choices && n < SIZE; i += 32) {
+        const bool match = i < choices && r.experts[i] == expert;
+        const uint32_t b = __ballot_sync(0xffffffffu, match);
+        const int at = n + __popc(b & ((1u << lane) - 1u));
+        if (match && at >= 0 && at < SIZE) list[at] = static_cast<uint16_t>(i);
+        n += __popc(b);
     }
-    total = __shfl_sync(0xffffffffu, before, 31);
-    before -= __popc(word);
-    int at = -1;
-    if (n >= before && n < before + __popc(word)) {
-        uint32_t rest = word;
-        for (int i = before; i < n; ++i) rest &= rest - 1;
-        at = lane * 32 + __ffs(static_cast<int>(rest)) - 1;
-    }
-    const uint32_t has = __ballot_sync(0xffffffffu, at >= 0);
-    return has ? __shfl_sync(0xffffffffu, at, __ffs(static_cast<int>(has)) - 1) : -1;
+    __syncwarp();
+    return min(n, SIZE);
 }
 
-// h' = p act(Wg x) (Wu x) of one expert's tokens, 16 rows of F a block: eight
+// h' = p act(Wg x) (Wu x), 16 rows of F of one entry's tokens at a time: eight
 // warps take the steps of K in turn and their sums are joined in warp order.
-// Block (b, a): rows 16 b .., the a-th distinct expert.
 template <int FORM, bool ALIGNED, int NT>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
 moe_gate_kernel(const __grid_constant__ Params p) {
-    constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), NP = pairs_of(FORM);
-    constexpr int UNROLL = NT <= 2 ? 4 : 2;
-    __shared__ uint32_t mask[32];
-    __shared__ int list[kTokens];
-    __shared__ int shared_expert, shared_count;
-    __shared__ float part[kWarps][2][16][8];
+    constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), LANE = 16 / WB, HALVES = halves_of(FORM);
+    constexpr int XB = NT * HALVES, STAGES = ring_stages(ALIGNED, XB);
+    constexpr bool BF16 = is_bf16(FORM);
+    extern __shared__ uint4 ring_smem[];
+    __shared__ Routing routing;
+    __shared__ __align__(16) int queue[Claims::QUEUE];
+    __shared__ __align__(16) float part[kWarps][2][16][8];      // (read and written in pairs)
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     grid_dependency_wait();
     allow_dependent_launch();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int choices = p.M * p.top_k;
-    mark_experts(mask, p.experts, choices);
-    if (warp == 0) {
-        int total;
-        const int e = nth_expert(mask, static_cast<int>(blockIdx.y), total);
-        int n = 0;
-        if (e >= 0)
-            for (int i0 = 0; i0 < choices; i0 += 32) {
-                const bool match = i0 + lane < choices && p.experts[i0 + lane] == e;
-                const uint32_t b = __ballot_sync(0xffffffffu, match);
-                if (match) list[n + __popc(b & ((1u << lane) - 1u))] = i0 + lane;
-                n += __popc(b);
-            }
-        if (lane == 0) {
-            shared_expert = e;
-            shared_count = n;
-        }
-    }
-    __syncthreads();
-    const int expert = shared_expert, count = shared_count;
-    if (expert < 0) return;
-    const int row0 = static_cast<int>(blockIdx.x) * 16;
-    const int tiles = (count + 7) / 8;
-    float acc[NT][2][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][0][j] = acc[i][1][j] = 0.0f;
-
+    read_routing<8 * NT>(routing, p.experts, choices, p.E);
     const int64_t F = p.F, K = p.K;
-    if (row0 < F) {
-        // (a row past F reads the last one; its results are dropped)
-        const int64_t r0 = min(static_cast<int64_t>(row0 + g), F - 1), r1 = min(static_cast<int64_t>(row0 + g + 8), F - 1);
-        const int64_t first = static_cast<int64_t>(expert) * F;
-        const uint8_t* wp[4] = {p.w_gate + (first + r0) * K * WB, p.w_gate + (first + r1) * K * WB,
-                                p.w_up + (first + r0) * K * WB, p.w_up + (first + r1) * K * WB};
-        const uint8_t* xp[NT];
+    const int blocks = static_cast<int>(p.ldh / 16), units = routing.entries * blocks;
+    const int steps = static_cast<int>((K + STEP - 1) / STEP);
+    const int mine = (steps - warp + kWarps - 1) / kWarps;      // of a row block; may be none
+    const Claims claims{queue, p.counters, Claims::ahead_of(steps / kWarps, STAGES)};
+    if (threadIdx.x == 0) claims.start();
+    __syncthreads();
+
+    // this lane's 16 bytes of rows g and g + 8 of gate and up, and what the rows have left from
+    // there on (a row past F reads the last one; its results are dropped)
+    struct Rows {
+        const uint8_t* at[kLoads];
+        int left;
+    };
+    const int row_bytes = static_cast<int>(K) * WB, offset = (warp * STEP + t * LANE) * WB;
+    const auto rows_of = [&](int u) {
+        const int a = u / blocks;
+        const int64_t row0 = (u - a * blocks) * 16, first = routing.active[a] * F;
+        Rows r;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t at = (first + min(row0 + g + 8 * i, F - 1)) * row_bytes + offset;
+            r.at[i] = p.w_gate + at;
+            r.at[2 + i] = p.w_up + at;
+        }
+        r.left = row_bytes - offset;
+        return r;
+    };
+    Ring<ALIGNED, XB> ring(smem_u32(ring_smem) + warp * ring_bytes(ALIGNED, XB, 1));
+    int next_i = 0, next_j = 0, next_entry = -1, next_count = 0;
+    Rows next = {{p.w_gate, p.w_gate, p.w_up, p.w_up}, 0};
+    const uint16_t* xp[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) xp[i] = p.x;
+    bool more = mine > 0;
+    const auto enter = [&](int u) {
+        more = more && u >= 0 && u < units;
+        if (!more) return;
+        next = rows_of(u);
+        const int a = u / blocks;
+        if (a != next_entry) {
+            next_entry = a;
+            next_count = list_tokens<8 * NT>(routing, routing.list[warp][0], a, choices);
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
+            // (columns past the entry's tokens are the first one's once more, and not looked at)
             const int at = 8 * i + g;
-            xp[i] = at < count ? p.x + static_cast<int64_t>(list[at] / p.top_k) * K * 2 : nullptr;
+            xp[i] = p.x + routing.list[warp][0][at < next_count ? at : 0] / p.top_k * p.ldx + warp * STEP + t * LANE;
         }
-        constexpr int LANE = 16 / WB;                   // k of a lane's 16 bytes
-        for (int64_t k0 = static_cast<int64_t>(warp) * STEP; k0 < K; k0 += static_cast<int64_t>(kWarps) * STEP * UNROLL) {
-            uint4 w[UNROLL][4];
+    };
+    enter(claims.unit(0));
+    const auto fill = [&]() {
+        if (more) {
+            ring.copy(next.at, next.left);
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int64_t k = k0 + static_cast<int64_t>(u) * kWarps * STEP + t * LANE;
+            for (int i = 0; i < NT; ++i) {
+                if (8 * i >= next_count) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[u][i] = load_row<ALIGNED, true>(wp[i] + k * WB, (K - k) * WB);
+                for (int half = 0; half < HALVES; ++half) ring.copy_token(i * HALVES + half, xp[i] + 8 * half);
+                xp[i] += kWarps * STEP;
             }
+            if (++next_j == mine) {
+                next_j = 0;
+                enter(claims.unit(++next_i));
+            } else {
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int64_t k = k0 + static_cast<int64_t>(u) * kWarps * STEP + t * LANE;
-                uint32_t v[4][NP];
+                for (int i = 0; i < kLoads; ++i) next.at[i] += kWarps * STEP * WB;
+                next.left -= kWarps * STEP * WB;
+            }
+        }
+        ring.commit();
+    };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) widen<FORM>(w[u][i], v[i]);
+    for (int i = 0; i < STAGES - 1; ++i) fill();
+
+    int entry = -1, count = 0, tiles = 0;
+    uint16_t* const list = routing.list[warp][1];
+    for (int i_unit = 0;; ++i_unit) {
+        const int u = claims.unit(i_unit);
+        if (u < 0 || u >= units) break;
+        const int claimed = threadIdx.x == 0 ? claims.claim() : 0;
+        const int a = u / blocks, row0 = (u - a * blocks) * 16, expert = routing.active[a];
+        if (a != entry) {
+            entry = a;
+            count = list_tokens<8 * NT>(routing, list, a, choices);
+            tiles = (count + 7) / 8;
+        }
+        Rows rows = rows_of(u);
+        float acc[NT][2][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][0][j] = acc[i][1][j] = 0.0f;
+        for (int j = 0; j < mine; ++j) {
+            ring.wait();
+            uint4 w[kLoads];
+            uint32_t xv[XB][4];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) w[i] = ring.get(i, rows.at[i], rows.left);
+            rows.left -= kWarps * STEP * WB;
+#pragma unroll
+            for (int i = 0; i < XB; ++i)
+                if (i / HALVES < tiles) ring.get_token(i, xv[i]);
+            ring.pop();
+            fill();
+#pragma unroll
+            for (int half = 0; half < HALVES; ++half) {
+                uint32_t v[kLoads][4];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) widen<FORM>(w[i], half, v[i]);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if (i >= tiles) break;
-                    uint32_t xv[NP];
-#pragma unroll
-                    for (int j = 0; j < NP; j += 4) {
-                        const int64_t kj = k + 2 * j;
-                        const uint4 a = xp[i] ? load_row<ALIGNED, false>(xp[i] + 2 * kj, 2 * (K - kj)) : make_uint4(0u, 0u, 0u, 0u);
-                        xv[j] = a.x; xv[j + 1] = a.y; xv[j + 2] = a.z; xv[j + 3] = a.w;
-                    }
-                    mma_step<FORM>(acc[i][0], v[0], v[1], xv);
-                    mma_step<FORM>(acc[i][1], v[2], v[3], xv);
+                    mma_step<BF16>(acc[i][0], v[0], v[1], xv[i * HALVES + half]);
+                    mma_step<BF16>(acc[i][1], v[2], v[3], xv[i * HALVES + half]);
                 }
             }
         }
-    }
-    // join the warps' sums tile by tile; thread (row, token) finishes h'
-    const int r = threadIdx.x / 8 % 16, n = threadIdx.x % 8;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        if (i >= tiles) break;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            *reinterpret_cast<float2*>(&part[warp][m][g][2 * t]) = make_float2(acc[i][m][0], acc[i][m][1]);
-            *reinterpret_cast<float2*>(&part[warp][m][g + 8][2 * t]) = make_float2(acc[i][m][2], acc[i][m][3]);
-        }
-        __syncthreads();
-        if (threadIdx.x < 128 && 8 * i + n < count) {
-            float gate = 0.0f, up = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                gate += part[k][0][r][n];
-                up += part[k][1][r][n];
-            }
-            const int choice = list[8 * i + n], row = row0 + r;
-            float h = 0.0f;
-            if (row < F) {
-                if constexpr (is_i8(FORM)) {
-                    gate *= p.s_gate[static_cast<int64_t>(expert) * F + row];
-                    up *= p.s_up[static_cast<int64_t>(expert) * F + row];
-                }
-                h = p.weights[choice] * (fused::act_value(gate, p.act) * up);
-            }
-            // (columns from F to the padded row's end are zeros)
-            const uint32_t hi = fused::pack16(h, 0.0f, is_bf16(FORM));
-            const float kept = fused::unpack16(hi, is_bf16(FORM)).x;
-            uint16_t* out = p.h + static_cast<int64_t>(choice) * p.ldh + row;
-            out[0] = static_cast<uint16_t>(hi);
-            out[p.lo_offset] = static_cast<uint16_t>(fused::pack16(fused::remainder16(h, kept), 0.0f, is_bf16(FORM)));
-        }
-        __syncthreads();
-    }
-}
-
-// y = sum over the experts of Wd h', 16 rows of K a block.  The steps of all
-// experts are one long axis, cut into a contiguous part for each warp; tokens
-// keep their own accumulator columns, so one sum runs over all of a warp's experts.
-template <int FORM, bool ALIGNED, int NT>
-__global__ void __launch_bounds__(kWarps * 32)
-moe_down_kernel(const __grid_constant__ Params p) {
-    constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), NP = pairs_of(FORM);
-    constexpr int UNROLL = NT <= 2 ? 4 : 2;
-    __shared__ uint32_t mask[32];
-    extern __shared__ int choice_experts[];             // [M top_k], then the warps' sums
-    __shared__ float part[kWarps][16][8];
-    grid_dependency_wait();
-    allow_dependent_launch();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int choices = p.M * p.top_k;
-    for (int i = threadIdx.x; i < choices; i += blockDim.x) choice_experts[i] = p.experts[i];
-    mark_experts(mask, p.experts, choices);
-    const int row0 = static_cast<int>(blockIdx.x) * 16;
-    const int64_t F = p.F, K = p.K;
-    float acc[NT][4], sum[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = sum[i][j] = 0.0f;
-    int total;
-    nth_expert(mask, 0, total);
-    const int steps = static_cast<int>((F + STEP - 1) / STEP);
-    const int64_t all = static_cast<int64_t>(total) * steps;
-    int64_t s = all * warp / kWarps;
-    const int64_t end = all * (warp + 1) / kWarps;
-    const int64_t r0 = min(static_cast<int64_t>(row0 + g), K - 1), r1 = min(static_cast<int64_t>(row0 + g + 8), K - 1);
-    constexpr int LANE = 16 / WB;
-    while (s < end) {
-        const int a = static_cast<int>(s / steps);
-        int dummy;
-        const int expert = nth_expert(mask, a, dummy);
-        const int from = static_cast<int>(s - static_cast<int64_t>(a) * steps);
-        const int to = static_cast<int>(min(static_cast<int64_t>(steps), end - static_cast<int64_t>(a) * steps));
-        s += to - from;
-        const uint8_t* wp[2] = {p.w_down + (static_cast<int64_t>(expert) * K + r0) * F * WB,
-                                p.w_down + (static_cast<int64_t>(expert) * K + r1) * F * WB};
-        // each tile's row of h' of this expert, where token g of the tile chose it
-        const uint8_t* hp[NT];
-        uint32_t live = 0;
+        if (threadIdx.x == 0) claims.put(i_unit, claimed);
+        // join the warps' sums tile by tile; thread (row, token) finishes h'
+        const int r = threadIdx.x / 8 % 16, n = threadIdx.x % 8;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const int token = 8 * i + g;
-            hp[i] = nullptr;
-            if (token < p.M)
-                for (int j = 0; j < p.top_k; ++j)
-                    if (choice_experts[token * p.top_k + j] == expert)
-                        hp[i] = reinterpret_cast<const uint8_t*>(p.h + static_cast<int64_t>(token * p.top_k + j) * p.ldh);
-            if (__any_sync(0xffffffffu, hp[i] != nullptr)) live |= 1u << i;
-        }
-        for (int k0 = from; k0 < to; k0 += UNROLL) {
-            uint4 w[UNROLL][2];
+            if (i >= tiles) break;
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int64_t k = static_cast<int64_t>(k0 + u) * STEP + t * LANE;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    w[u][i] = load_row<ALIGNED, true>(wp[i] + k * WB, k0 + u < to ? (F - k) * WB : 0);
+            for (int m = 0; m < 2; ++m) {
+                *reinterpret_cast<float2*>(&part[warp][m][g][2 * t]) = make_float2(acc[i][m][0], acc[i][m][1]);
+                *reinterpret_cast<float2*>(&part[warp][m][g + 8][2 * t]) = make_float2(acc[i][m][2], acc[i][m][3]);
             }
+            __syncthreads();
+            if (threadIdx.x < 128 && 8 * i + n < count) {
+                float gate = 0.0f, up = 0.0f;
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                if (k0 + u >= to) break;
-                const int64_t k = static_cast<int64_t>(k0 + u) * STEP + t * LANE;
-                uint32_t v[2][NP];
-                widen<FORM>(w[u][0], v[0]);
-                widen<FORM>(w[u][1], v[1]);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (!(live >> i & 1u)) continue;
-                    uint32_t hi[NP], lo[NP];
-#pragma unroll
-                    for (int j = 0; j < NP; j += 4) {
-                        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                        if (hp[i]) {
-                            a = __ldcg(reinterpret_cast<const uint4*>(hp[i] + 2 * (k + 2 * j)));
-                            b = __ldcg(reinterpret_cast<const uint4*>(hp[i] + 2 * (p.lo_offset + k + 2 * j)));
-                        }
-                        hi[j] = a.x; hi[j + 1] = a.y; hi[j + 2] = a.z; hi[j + 3] = a.w;
-                        lo[j] = b.x; lo[j + 1] = b.y; lo[j + 2] = b.z; lo[j + 3] = b.w;
-                    }
-                    mma_step<FORM>(acc[i], v[0], v[1], hi);
-                    mma_step<FORM>(acc[i], v[0], v[1], lo);
+                for (int k = 0; k < kWarps; ++k) {
+                    gate += part[k][0][r][n];
+                    up += part[k][1][r][n];
                 }
+                const int choice = list[8 * i + n], row = row0 + r;
+                float h = 0.0f;
+                if (row < F) {
+                    if constexpr (is_i8(FORM)) {
+                        gate *= p.s_gate[static_cast<int64_t>(expert) * F + row];
+                        up *= p.s_up[static_cast<int64_t>(expert) * F + row];
+                    }
+                    h = p.weights[choice] * (fused::act_value(gate, p.act) * up);
+                }
+                // (columns from F to the padded row's end are zeros)
+                const uint32_t hi = fused::pack16(h, 0.0f, BF16);
+                const float kept = fused::unpack16(hi, BF16).x;
+                uint16_t* out = p.h + static_cast<int64_t>(choice) * p.ldh + row;
+                out[0] = static_cast<uint16_t>(hi);
+                out[p.lo_offset] = static_cast<uint16_t>(fused::pack16(fused::remainder16(h, kept), 0.0f, BF16));
             }
+            __syncthreads();
         }
-        if constexpr (is_i8(FORM)) {
-            const float s0 = p.s_down[static_cast<int64_t>(expert) * K + r0], s1 = p.s_down[static_cast<int64_t>(expert) * K + r1];
+    }
+    cp_async_wait_group<0>();
+}
+
+// y = sum over the experts of Wd h', 32 rows of K at a time.  The steps of all
+// entries are one long axis, cut into parts that are units of work of their own,
+// and those into a contiguous piece for each warp.  A warp adds each entry's sums to its
+// tokens' columns in shared memory; the warps' columns are added in order, and
+// the parts' by the block that finishes a row block's last one, in order too.
+constexpr int kDownRows = 32;
+constexpr int kMaxParts = 16;
+constexpr int kDownUnits = 1216;        // 4 rounds of the GPU's blocks, so that the last is short
+
+// Parts of a row block: every warp has four steps of each, or there is one part.
+__host__ __device__ inline int down_parts(int64_t steps, int64_t blocks) {
+    int64_t parts = (kDownUnits + blocks - 1) / blocks;
+    if (parts > kMaxParts) parts = kMaxParts;
+    if (parts > steps / (4 * kWarps)) parts = steps / (4 * kWarps);
+    return parts < 1 ? 1 : static_cast<int>(parts);
+}
+
+template <int FORM, bool ALIGNED, int NT>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+moe_down_kernel(const __grid_constant__ Params p) {
+    constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), LANE = 16 / WB, HALVES = halves_of(FORM);
+    constexpr int XB = NT * HALVES, STAGES = ring_stages(ALIGNED, 2 * XB);
+    constexpr bool BF16 = is_bf16(FORM);
+    extern __shared__ uint4 ring_smem[];
+    __shared__ Routing routing;
+    __shared__ __align__(16) int queue[Claims::QUEUE];
+    __shared__ int last_part;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int M = p.M, ldy = (M + 7) / 8 * 8;
+    // [kWarps][32][ldy]
+    float* const columns = reinterpret_cast<float*>(reinterpret_cast<char*>(ring_smem) + ring_bytes(ALIGNED, 2 * XB, kWarps));
+    float* const own = columns + warp * (kDownRows * ldy);
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int choices = M * p.top_k;
+    read_routing<8 * NT>(routing, p.experts, choices, p.E);
+    const int64_t F = p.F, K = p.K;
+    const int blocks = static_cast<int>((K + kDownRows - 1) / kDownRows);
+    const int steps = static_cast<int>((F + STEP - 1) / STEP);
+    const int64_t all = static_cast<int64_t>(routing.entries) * steps;
+    const int parts = down_parts(all, blocks), units = blocks * parts;
+    // warp w's piece of a part: steps [piece(part, w), piece(part, w + 1))
+    const auto piece = [&](int part, int w) { return all * (part * kWarps + w) / (parts * kWarps); };
+    const Claims claims{queue, p.counters + 1, Claims::ahead_of(all / (kWarps * parts), STAGES)};
+    if (threadIdx.x == 0) claims.start();
+    __syncthreads();
+
+    // this lane's 16 bytes of rows g, g + 8, g + 16 and g + 24, from step j on (a row past K reads
+    // the last one; its results are dropped)
+    struct Rows {
+        const uint8_t* at[kLoads];
+        int left;
+    };
+    const int row_bytes = static_cast<int>(F) * WB;
+    const auto rows_of = [&](int a, int block, int j) {
+        const int offset = (j * STEP + t * LANE) * WB;
+        Rows r;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            r.at[i] = p.w_down + (routing.active[a] * K + min(static_cast<int64_t>(block) * kDownRows + g + 8 * i, K - 1)) * row_bytes + offset;
+        r.left = row_bytes - offset;
+        return r;
+    };
+    Ring<ALIGNED, 2 * XB> ring(smem_u32(ring_smem) + warp * ring_bytes(ALIGNED, 2 * XB, 1));
+    int next_i = 0, next_block = 0, next_a = 0, next_j = 0;
+    int left = 0;                               // steps of this warp's piece still to be copied
+    int next_entry = -1, next_count = 0;
+    Rows next = {{p.w_down, p.w_down, p.w_down, p.w_down}, 0};
+    const uint16_t* hp[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) hp[i] = p.h;
+    const auto enter_entry = [&]() {
+        next = rows_of(next_a, next_block, next_j);
+        if (next_a != next_entry) {
+            next_entry = next_a;
+            next_count = list_tokens<8 * NT>(routing, routing.list[warp][0], next_a, choices);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int at = 8 * i + g;
+            hp[i] = p.h + routing.list[warp][0][at < next_count ? at : 0] * p.ldh + next_j * STEP + t * LANE;
+        }
+    };
+    const auto enter = [&](int u) {
+        if (u < 0 || u >= units) {
+            left = 0;
+            return;
+        }
+        const int part = u / blocks;
+        next_block = u - part * blocks;
+        const int64_t s0 = piece(part, warp);
+        left = static_cast<int>(piece(part, warp + 1) - s0);
+        if (left == 0) return;                  // (one part, and fewer steps than warps: never any)
+        next_a = static_cast<int>(s0 / steps);
+        next_j = static_cast<int>(s0 - static_cast<int64_t>(next_a) * steps);
+        enter_entry();
+    };
+    enter(claims.unit(0));
+    const auto fill = [&]() {
+        if (left > 0) {
+            ring.copy(next.at, next.left);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                if (!(live >> i & 1u)) continue;
-                // (a token that did not choose the expert adds nothing, whatever the scale is)
-                const uint32_t mine = __ballot_sync(0xffffffffu, hp[i] != nullptr);
+                if (8 * i >= next_count) break;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int column = 2 * t + (j & 1);
-                    if (mine >> (4 * column) & 1u) sum[i][j] += (j < 2 ? s0 : s1) * acc[i][j];
-                    acc[i][j] = 0.0f;
+                for (int half = 0; half < HALVES; ++half) {
+                    ring.copy_token(i * HALVES + half, hp[i] + 8 * half);
+                    ring.copy_token(XB + i * HALVES + half, hp[i] + p.lo_offset + 8 * half);
+                }
+                hp[i] += STEP;
+            }
+            if (--left == 0) {
+                enter(claims.unit(++next_i));
+            } else if (++next_j == steps) {
+                next_j = 0;
+                ++next_a;
+                enter_entry();
+            } else {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) next.at[i] += STEP * WB;
+                next.left -= STEP * WB;
+            }
+        }
+        ring.commit();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fill();
+
+    uint16_t* const list = routing.list[warp][1];
+    int entry = -1, count = 0, tiles = 0;
+    for (int i_unit = 0;; ++i_unit) {
+        const int u = claims.unit(i_unit);
+        if (u < 0 || u >= units) break;
+        const int claimed = threadIdx.x == 0 ? claims.claim() : 0;
+        const int part = u / blocks, block = u - part * blocks;
+        const int64_t row0 = static_cast<int64_t>(block) * kDownRows;
+        const int64_t s0 = piece(part, warp), s1 = piece(part, warp + 1);
+        for (int i = lane; i < kDownRows * ldy; i += 32) own[i] = 0.0f;
+        __syncwarp();
+        for (int64_t s = s0; s < s1;) {
+            const int a = static_cast<int>(s / steps), from = static_cast<int>(s - static_cast<int64_t>(a) * steps);
+            const int to = static_cast<int>(min(static_cast<int64_t>(steps), from + (s1 - s)));
+            s += to - from;
+            const int expert = routing.active[a];
+            if (a != entry) {
+                entry = a;
+                count = list_tokens<8 * NT>(routing, list, a, choices);
+                tiles = (count + 7) / 8;
+            }
+            Rows rows = rows_of(a, block, from);
+            float acc[NT][2][4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][0][j] = acc[i][1][j] = 0.0f;
+            for (int j = from; j < to; ++j) {
+                ring.wait();
+                uint4 w[kLoads];
+                uint32_t hi[XB][4], lo[XB][4];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) w[i] = ring.get(i, rows.at[i], rows.left);
+                rows.left -= STEP * WB;
+#pragma unroll
+                for (int i = 0; i < XB; ++i) {
+                    if (i / HALVES >= tiles) break;
+                    ring.get_token(i, hi[i]);
+                    ring.get_token(XB + i, lo[i]);
+                }
+                ring.pop();
+                fill();
+#pragma unroll
+                for (int half = 0; half < HALVES; ++half) {
+                    uint32_t v[kLoads][4];
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) widen<FORM>(w[i], half, v[i]);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        if (i >= tiles) break;
+                        mma_step<BF16>(acc[i][0], v[0], v[1], hi[i * HALVES + half]);
+                        mma_step<BF16>(acc[i][1], v[2], v[3], hi[i * HALVES + half]);
+                        mma_step<BF16>(acc[i][0], v[0], v[1], lo[i * HALVES + half]);
+                        mma_step<BF16>(acc[i][1], v[2], v[3], lo[i * HALVES + half]);
+                    }
+                }
+            }
+            // to the columns of the tokens (each has a choice of an expert once)
+            float scale[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                scale[i] = is_i8(FORM) ? p.s_down[expert * K + min(row0 + g + 8 * i, K - 1)] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if (i >= tiles) break;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int at = 8 * i + 2 * t + j;
+                    if (at >= count) continue;
+                    float* to_column = own + list[at] / p.top_k;
+#pragma unroll
+                    for (int r = 0; r < kLoads; ++r)
+                        to_column[(g + 8 * r) * ldy] += scale[r] * acc[i][r / 2][2 * (r & 1) + j];
                 }
             }
         }
-    }
-    const int r = threadIdx.x / 8 % 16, n = threadIdx.x % 8;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        if (8 * i >= p.M) break;
-        const float(&v)[4] = is_i8(FORM) ? sum[i] : acc[i];
-        *reinterpret_cast<float2*>(&part[warp][g][2 * t]) = make_float2(v[0], v[1]);
-        *reinterpret_cast<float2*>(&part[warp][g + 8][2 * t]) = make_float2(v[2], v[3]);
+        if (threadIdx.x == 0) claims.put(i_unit, claimed);
         __syncthreads();
-        if (threadIdx.x < 128 && 8 * i + n < p.M && row0 + r < K) {
-            float total_y = 0.0f;
+        float* const sums = p.partial + (static_cast<int64_t>(block) * kMaxParts + part) * (kDownRows * ldy);
+        for (int i = threadIdx.x; i < kDownRows * ldy; i += kWarps * 32) {
+            float sum = columns[i];
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) total_y += part[k][r][n];
-            p.y[static_cast<int64_t>(8 * i + n) * K + row0 + r] =
-                static_cast<uint16_t>(fused::pack16(total_y, 0.0f, is_bf16(FORM)));
+            for (int k = 1; k < kWarps; ++k) sum += columns[k * (kDownRows * ldy) + i];
+            if (parts > 1) sums[i] = sum;
+            else columns[i] = sum;
+        }
+        if (parts > 1) {
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) last_part = atomicAdd(p.counters + 2 + block, 1) == parts - 1;
+            __syncthreads();
+            if (last_part) {
+                __threadfence();
+                const float* first = p.partial + static_cast<int64_t>(block) * kMaxParts * (kDownRows * ldy);
+                for (int i = threadIdx.x; i < kDownRows * ldy; i += kWarps * 32) {
+                    float sum = 0.0f;
+                    for (int k = 0; k < parts; ++k) sum += __ldcg(first + static_cast<int64_t>(k) * (kDownRows * ldy) + i);
+                    columns[i] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        if (parts == 1 || last_part) {
+            // 32 rows of a token in a row
+            for (int i = threadIdx.x; i < M * kDownRows; i += kWarps * 32) {
+                const int m = i / kDownRows, r = i % kDownRows;
+                if (row0 + r < K)
+                    p.y[m * K + row0 + r] = static_cast<uint16_t>(fused::pack16(columns[r * ldy + m], 0.0f, BF16));
+            }
         }
         __syncthreads();
     }
+    cp_async_wait_group<0>();
 }
 
 // ---------------------------------------------------------------- host
@@ -472,14 +732,15 @@ bool odd_word(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 != 0; }
 
 // What a call refuses before it looks at the device.
 int check(const Call& c) {
-    if (bad_size(c.M) || bad_size(c.K) || bad_size(c.F)) return GEMM_ERR_INVALID_ARG;
+    // (rows of weights are counted in an int)
+    if (bad_size(c.M) || c.K < 0 || c.K > kMaxWidth || c.F < 0 || c.F > kMaxWidth) return GEMM_ERR_INVALID_ARG;
     if (c.E < 1 || c.E > kMaxExperts || c.top_k < 1 || c.top_k > kMaxTopK || c.top_k > c.E) return GEMM_ERR_INVALID_ARG;
     if (c.type != GEMM_TYPE_HALF && c.type != GEMM_TYPE_BFLOAT) return GEMM_ERR_INVALID_ARG;
     if (c.weight_type != c.type && c.weight_type != GEMM_TYPE_BYTE) return GEMM_ERR_INVALID_ARG;
     if (c.act != GEMM_ACT_SILU && c.act != GEMM_ACT_GELU) return GEMM_ERR_INVALID_ARG;
     if (c.normalize != 0 && c.normalize != 1) return GEMM_ERR_INVALID_ARG;
-    // (a row block of 16 to a block of the grid; bytes of all experts in 63 bits)
-    if (c.F && c.K > ((1ll << 48) / c.F)) return GEMM_ERR_INVALID_ARG;
+    // units of work are counted in an int
+    if (c.E * cdiv(c.F, 16) >= (1ll << 30) || cdiv(c.K, kDownRows) * kMaxParts >= (1ll << 30)) return GEMM_ERR_INVALID_ARG;
     const bool i8 = c.weight_type == GEMM_TYPE_BYTE;
     if (odd_address(c.x) || odd_address(c.w_router) || odd_address(c.y)) return GEMM_ERR_ALIGNMENT;
     if (!i8 && (odd_address(c.w_gate) || odd_address(c.w_up) || odd_address(c.w_down))) return GEMM_ERR_ALIGNMENT;
@@ -498,9 +759,26 @@ uint64_t weight_matrix_bytes(const Call& c) {
 
 int64_t pass_tokens(int64_t M) { return M < kTokens ? M : kTokens; }
 int64_t ldh_of(int64_t F) { return round_up(F, 64); }
-int64_t workspace_bytes_of(const Call& c) {
-    if (c.M == 0 || c.K == 0 || c.F == 0) return 0;
-    return round_up(2 * pass_tokens(c.M) * c.top_k * ldh_of(c.F) * 2, 256);
+struct Workspace {
+    uint16_t* x = nullptr;
+    uint16_t* h = nullptr;
+    int* counters = nullptr;
+    float* partial = nullptr;
+    size_t bytes = 0;
+};
+int64_t num_counters(int64_t K) { return 2 + cdiv(K, kDownRows); }
+Workspace workspace_of(const Call& c, void* base) {
+    Workspace w;
+    if (c.M == 0 || c.K == 0) return w;
+    fused::Carver carver;
+    carver.base = static_cast<char*>(base);
+    const int64_t tokens = pass_tokens(c.M);
+    w.x = carver.take<uint16_t>(tokens * ldh_of(c.K));
+    w.h = carver.take<uint16_t>(2 * tokens * c.top_k * ldh_of(c.F));
+    w.counters = carver.take<int>(num_counters(c.K));
+    w.partial = carver.take<float>(cdiv(c.K, kDownRows) * kMaxParts * kDownRows * round_up(tokens, 8));
+    w.bytes = carver.used;
+    return w;
 }
 
 bool rows16(const void* p, int64_t row_bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0; }
@@ -511,44 +789,99 @@ int launched(cudaError_t e) {
     return GEMM_ERR_LAUNCH;
 }
 
+// Parts of K a row of the router is cut into: all of a cluster's warps have one.
+int route_parts(int64_t E, int64_t K, int warps) {
+    int parts = 1;
+    while (parts < 8 && 2 * E * parts <= warps && K > 512 * parts) parts *= 2;
+    return parts;
+}
+
+template <bool BF16, bool ALIGNED, int TOKENS>
+int launch_route(const Call& c, const uint8_t* x, int M, int* experts, float* weights, const Workspace& ws, cudaStream_t stream) {
+    constexpr int threads = route_threads(TOKENS);
+    const int parts = route_parts(c.E, c.K, kRouteCtas * threads / 32);
+    Handover out = {ws.counters, ws.x, num_counters(c.K), ldh_of(c.K)};
+    if (!ws.counters) out.num_counters = 0;
+    return launched(launch_pdl(moe_route_kernel<BF16, ALIGNED, TOKENS>, dim3(static_cast<unsigned>(cdiv(M, TOKENS) * kRouteCtas)),
+                               dim3(threads), static_cast<size_t>(TOKENS) * c.E * parts * 8, stream, x,
+                               static_cast<const uint8_t*>(c.w_router), M, c.K, static_cast<int>(c.E), parts,
+                               static_cast<int>(c.top_k), c.normalize, experts, weights, out));
+}
+
+// 16 tokens, a cluster each, still fit the GPU at once.
 template <bool BF16, bool ALIGNED>
-int launch_route(const Call& c, const uint8_t* x, int M, int* experts, float* weights, cudaStream_t stream) {
-    // few tokens: a cluster each
-    const int per = M <= 16 ? 1 : kRouteTokens;
-    return launched(launch_pdl(moe_route_kernel<BF16, ALIGNED>, dim3(static_cast<unsigned>(cdiv(M, per) * kRouteCtas)), dim3(256),
-                               static_cast<size_t>(per) * c.E * 8, stream, x, static_cast<const uint8_t*>(c.w_router), M, c.K,
-                               static_cast<int>(c.E), static_cast<int>(c.top_k), c.normalize, experts, weights, per));
+int launch_route_tokens(const Call& c, const uint8_t* x, int M, int* experts, float* weights, const Workspace& ws, cudaStream_t stream) {
+    return M <= 16 ? launch_route<BF16, ALIGNED, 1>(c, x, M, experts, weights, ws, stream)
+                   : launch_route<BF16, ALIGNED, kRouteTokens>(c, x, M, experts, weights, ws, stream);
+}
+
+// How many blocks of a kernel fit the GPU at once, with `smem` bytes of the `most`
+// it may have; set up on the first call on a device.
+struct Fit {
+    std::atomic<int> blocks[64] = {};
+};
+template <typename Kernel>
+int blocks_at_once(Fit& fit, Kernel kern, int smem, int most, const DeviceInfo& info) {
+    if (info.device < 0 || info.device >= 64) return 0;
+    int n = fit.blocks[info.device].load(std::memory_order_relaxed);
+    if (n == 0) {
+        // concurrent first calls compute and store the same value
+        int per_sm = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWarps * 32, smem) != cudaSuccess || per_sm <= 0) {
+            cudaGetLastError();
+            return 0;
+        }
+        n = per_sm * info.num_sms;
+        fit.blocks[info.device].store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 template <int FORM, bool ALIGNED, int NT>
-int launch_experts(const Params& p, bool down, cudaStream_t stream) {
-    const int choices = p.M * p.top_k;
+int launch_experts(const Params& p, bool down, const DeviceInfo& info, cudaStream_t stream) {
+    constexpr int pieces = NT * halves_of(FORM);
+    // the most entries that the routing can give
+    const int64_t choices = static_cast<int64_t>(p.M) * p.top_k;
+    const int64_t entries = (choices < p.E ? choices : p.E) + choices / (8 * NT);
     if (!down) {
-        const dim3 grid(static_cast<unsigned>(cdiv(p.ldh, 16)), static_cast<unsigned>(choices < p.E ? choices : p.E));
-        return launched(launch_pdl(moe_gate_kernel<FORM, ALIGNED, NT>, grid, dim3(kWarps * 32), 0, stream, p));
+        const auto kern = moe_gate_kernel<FORM, ALIGNED, NT>;
+        constexpr int ring = ring_bytes(ALIGNED, pieces, kWarps);
+        static Fit fit;
+        const int64_t fits = blocks_at_once(fit, kern, ring, ring, info), units = entries * (p.ldh / 16);
+        if (fits == 0) return GEMM_ERR_LAUNCH;
+        return launched(launch_pdl(kern, dim3(static_cast<unsigned>(units < fits ? units : fits)), dim3(kWarps * 32), ring, stream, p));
     }
-    return launched(launch_pdl(moe_down_kernel<FORM, ALIGNED, NT>, dim3(static_cast<unsigned>(cdiv(p.K, 16))), dim3(kWarps * 32),
-                               static_cast<size_t>(choices) * 4, stream, p));
+    const auto kern = moe_down_kernel<FORM, ALIGNED, NT>;
+    constexpr int ring = ring_bytes(ALIGNED, 2 * pieces, kWarps);
+    static Fit fit[kTokens / 8];
+    constexpr int columns = kWarps * kDownRows * 8 * 4;         // bytes of eight tokens
+    const int eights = static_cast<int>(cdiv(p.M, 8)), smem = ring + columns * eights;
+    const int64_t fits = blocks_at_once(fit[eights - 1], kern, smem, ring + columns * (kTokens / 8), info);
+    if (fits == 0) return GEMM_ERR_LAUNCH;
+    const int64_t blocks = cdiv(p.K, kDownRows), units = blocks * down_parts(entries * cdiv(p.F, step_k(FORM)), blocks);
+    return launched(launch_pdl(kern, dim3(static_cast<unsigned>(units < fits ? units : fits)), dim3(kWarps * 32), smem, stream, p));
 }
 
+// Two tiles where an expert has more than four tokens on average: one tile's ring
+// leaves room for more blocks, two read a crowded expert's weights half as often.
 template <int FORM, bool ALIGNED>
-int launch_tiles(const Params& p, bool down, cudaStream_t stream) {
-    if (p.M <= 8) return launch_experts<FORM, ALIGNED, 1>(p, down, stream);
-    if (p.M <= 16) return launch_experts<FORM, ALIGNED, 2>(p, down, stream);
-    return launch_experts<FORM, ALIGNED, 8>(p, down, stream);
+int launch_tiles(const Params& p, bool down, const DeviceInfo& info, cudaStream_t stream) {
+    return p.M <= 8 || p.M * p.top_k <= 4 * p.E ? launch_experts<FORM, ALIGNED, 1>(p, down, info, stream)
+                                                : launch_experts<FORM, ALIGNED, 2>(p, down, info, stream);
 }
 
 template <int FORM>
-int launch_form(const Params& p, bool down, bool aligned, cudaStream_t stream) {
-    return aligned ? launch_tiles<FORM, true>(p, down, stream) : launch_tiles<FORM, false>(p, down, stream);
+int launch_form(const Params& p, bool down, bool aligned, const DeviceInfo& info, cudaStream_t stream) {
+    return aligned ? launch_tiles<FORM, true>(p, down, info, stream) : launch_tiles<FORM, false>(p, down, info, stream);
 }
 
-int launch_kernel(const Params& p, int form, bool down, bool aligned, cudaStream_t stream) {
+int launch_kernel(const Params& p, int form, bool down, bool aligned, const DeviceInfo& info, cudaStream_t stream) {
     switch (form) {
-        case kHalf: return launch_form<kHalf>(p, down, aligned, stream);
-        case kBfloat: return launch_form<kBfloat>(p, down, aligned, stream);
-        case kI8Half: return launch_form<kI8Half>(p, down, aligned, stream);
-        default: return launch_form<kI8Bfloat>(p, down, aligned, stream);
+        case kHalf: return launch_form<kHalf>(p, down, aligned, info, stream);
+        case kBfloat: return launch_form<kBfloat>(p, down, aligned, info, stream);
+        case kI8Half: return launch_form<kI8Half>(p, down, aligned, info, stream);
+        default: return launch_form<kI8Bfloat>(p, down, aligned, info, stream);
     }
 }
 
@@ -563,7 +896,7 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
                          {c.s_gate, fb}, {c.s_up, fb},                           {c.s_down, 4ull * c.E * c.K}};
     const Range out[3] = {{c.y, xb}, {c.experts, cb}, {c.weights, cb}};
     if (fused::overlaps(in, out)) return GEMM_ERR_INVALID_ARG;
-    if (!fused::workspace_ok(workspace, workspace_bytes, workspace_bytes_of(c), in, out)) return GEMM_ERR_INVALID_ARG;
+    if (!fused::workspace_ok(workspace, workspace_bytes, workspace_of(c, nullptr).bytes, in, out)) return GEMM_ERR_INVALID_ARG;
     DeviceInfo info;
     rc = current_device(&info);
     if (rc != GEMM_OK) return rc;
@@ -571,7 +904,7 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
     const bool i8 = c.weight_type == GEMM_TYPE_BYTE, bf16 = c.type == GEMM_TYPE_BFLOAT;
     const int form = (i8 ? 2 : 0) + (bf16 ? 1 : 0), wbytes = i8 ? 1 : 2;
     const bool route_aligned = rows16(c.x, 2 * c.K) && rows16(c.w_router, 2 * c.K);
-    const bool gate_aligned = rows16(c.x, 2 * c.K) && rows16(c.w_gate, wbytes * c.K) && rows16(c.w_up, wbytes * c.K);
+    const bool gate_aligned = rows16(c.w_gate, wbytes * c.K) && rows16(c.w_up, wbytes * c.K);
     const bool down_aligned = rows16(c.w_down, wbytes * c.F);
     Params p = {};
     p.w_gate = static_cast<const uint8_t*>(c.w_gate);
@@ -580,7 +913,12 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
     p.s_gate = c.s_gate;
     p.s_up = c.s_up;
     p.s_down = c.s_down;
-    p.h = static_cast<uint16_t*>(workspace);
+    const Workspace ws = workspace_of(c, workspace);
+    p.x = ws.x;
+    p.ldx = ldh_of(c.K);
+    p.h = ws.h;
+    p.counters = ws.counters;
+    p.partial = ws.partial;
     p.K = c.K;
     p.F = c.F;
     p.ldh = ldh_of(c.F);
@@ -590,22 +928,22 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
     for (int64_t m = 0; m < c.M; m += kTokens) {
         p.M = static_cast<int>(c.M - m < kTokens ? c.M - m : kTokens);
         p.lo_offset = static_cast<int64_t>(p.M) * c.top_k * p.ldh;
-        p.x = static_cast<const uint8_t*>(c.x) + m * c.K * 2;
+        const uint8_t* x = static_cast<const uint8_t*>(c.x) + m * c.K * 2;
         p.y = static_cast<uint16_t*>(c.y) + m * c.K;
         p.experts = c.experts + m * c.top_k;
         p.weights = c.weights + m * c.top_k;
         int* experts = c.experts + m * c.top_k;
         float* weights = c.weights + m * c.top_k;
         if (bf16)
-            rc = route_aligned ? launch_route<true, true>(c, p.x, p.M, experts, weights, stream)
-                               : launch_route<true, false>(c, p.x, p.M, experts, weights, stream);
+            rc = route_aligned ? launch_route_tokens<true, true>(c, x, p.M, experts, weights, ws, stream)
+                               : launch_route_tokens<true, false>(c, x, p.M, experts, weights, ws, stream);
         else
-            rc = route_aligned ? launch_route<false, true>(c, p.x, p.M, experts, weights, stream)
-                               : launch_route<false, false>(c, p.x, p.M, experts, weights, stream);
+            rc = route_aligned ? launch_route_tokens<false, true>(c, x, p.M, experts, weights, ws, stream)
+                               : launch_route_tokens<false, false>(c, x, p.M, experts, weights, ws, stream);
         if (rc != GEMM_OK) return rc;
         if (c.K == 0) continue;
-        if (c.F > 0 && (rc = launch_kernel(p, form, false, gate_aligned, stream)) != GEMM_OK) return rc;
-        if ((rc = launch_kernel(p, form, true, down_aligned, stream)) != GEMM_OK) return rc;
+        if (c.F > 0 && (rc = launch_kernel(p, form, false, gate_aligned, info, stream)) != GEMM_OK) return rc;
+        if ((rc = launch_kernel(p, form, true, down_aligned, info, stream)) != GEMM_OK) return rc;
     }
     return GEMM_OK;
 }
@@ -624,7 +962,7 @@ extern "C" int gemm_moe_nt_workspace(int64_t M, int64_t K, int64_t F, int64_t E,
     const int rc = check(c);
     if (rc != GEMM_OK) return rc;
     if (!bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = workspace_bytes_of(c);
+    *bytes = static_cast<int64_t>(workspace_of(c, nullptr).bytes);
     return GEMM_OK;
 }
 

@@ -76,7 +76,7 @@ def test_accepted_where_only_the_device_is_missing(lib):
                        ("gemm_moe_nt", swap(MOE, (4, 6))), ("gemm_moe_nt", swap(MOE, (3, 1024), (4, 32), (0, 65))),
                        ("gemm_moe_nt", swap(MOE, (16, B), (17, B), (18, 1), (19, 0))),
                        ("gemm_moe_nt", swap(MOE8, (7, P[2] + 1), (8, P[3] + 3), (9, P[4] + 5), (16, B))),
-                       ("gemm_moe_nt", swap(MOE, (2, 0), (7, 0), (8, 0), (9, 0), (20, 0), (21, 0)))):
+                       ("gemm_moe_nt", swap(MOE, (2, 0), (7, 0), (8, 0), (9, 0)))):
         assert getattr(lib, name)(*args) not in (OK, BAD, ALIGN), (name, args)
 
 
@@ -98,9 +98,12 @@ def workspace(lib, name, *args):
 
 
 def test_workspaces(lib):
-    # the experts' activations of a pass: two 16-bit values each, rows of a multiple of 64
+    # the experts' activations of a pass, two 16-bit values each in rows of a multiple of 64, and partial sums
     for M, passes in ((1, 1), (64, 64), (1000, 64)):
-        assert workspace(lib, "gemm_moe_nt", M, 512, 100, 8, 2, H, H) == 2 * passes * 2 * 128 * 2
+        need = workspace(lib, "gemm_moe_nt", M, 512, 100, 8, 2, H, H)
+        held = 2 * passes * 2 * 128 * 2 + passes * 512 * 2 + 16 * 512 * 4 * max(8, passes)
+        assert held < need < held + 16384
+    assert workspace(lib, "gemm_moe_nt", 1000, 512, 100, 8, 2, H, H) == workspace(lib, "gemm_moe_nt", 64, 512, 100, 8, 2, H, H)
     assert workspace(lib, "gemm_moe_nt", 0, 512, 100, 8, 2, H, H) == 0
     assert workspace(lib, "gemm_i8_nt", 0, 512, 100, P[0], P[1], H) == 0
     # no more than both operands in 16 bits, whatever their alignment
