@@ -212,7 +212,7 @@ struct Ring {
     }
     // Piece i of the tokens: 16 bytes at `at`, through L1 (past it, every block of the GPU asks the
     // same few lines of L2: 78 us instead of 44 for one token's gate).
-    __device__ __forceinline__ void copy_token(int i, const uint16_t* at) { cp_async_l1(fill + (WEIGHTS + i) * BLOCK, at); }
+    __device__ __forceinline__ void copy_token(int i, const void* at) { cp_async_l1(fill + (WEIGHTS + i) * BLOCK, at); }
     // Ends a stage (an empty one too: stages are counted).
     __device__ __forceinline__ void commit() {
         cp_async_commit();

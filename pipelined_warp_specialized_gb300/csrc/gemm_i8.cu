@@ -162,6 +162,210 @@ widen_kernel(const __grid_constant__ Widen p, int64_t K, int64_t ld) {
     }
 }
 
+// ---------------------------------------------------------------- few tokens
+
+// Up to kFewTokens rows of `a`: 32 rows of b at a time by a cluster of `ctas` CTAs,
+// whose warps take the steps of K in turn (few.cuh).  Bound by b's bytes.  A warp's fp32
+// sums are whole numbers and exact over 16 steps (1024 of K); they are added up
+// as integers in shared memory, whose order does not matter: the parts of a cluster
+// and of its warps are joined exactly.
+constexpr int kFewTokens = 64;
+constexpr int kFewRows32 = 32;
+constexpr int kFewWarps = 8;
+constexpr int kExactSteps = 16;
+
+struct FewParams {
+    const uint8_t* a;               // [M][lda], rows on 16-byte boundaries
+    const uint8_t* b;               // [N, K]
+    const float* a_scale;
+    const float* b_scale;
+    uint16_t* out;                  // [M, N]
+    int64_t lda, N;
+    int M, K, ctas, bf16;
+};
+
+template <bool ALIGNED, int NT>
+__global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 2 : 1)
+few_kernel(const __grid_constant__ FewParams p) {
+    using few::kLoads;
+    constexpr int STEP = 64, LDC = 8 * NT;
+    extern __shared__ uint4 ring_smem[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const uint32_t rank = cluster_ctarank();
+    // [kFewWarps][32][LDC]
+    int* const columns = reinterpret_cast<int*>(reinterpret_cast<char*>(ring_smem) + few::ring_bytes(ALIGNED, NT, kFewWarps));
+    int* const own = columns + warp * (kFewRows32 * LDC);
+    for (int i = lane; i < kFewRows32 * LDC; i += 32) own[i] = 0;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(p.ctas)) * kFewRows32;
+    const int workers = p.ctas * kFewWarps, worker = static_cast<int>(rank) * kFewWarps + warp;
+    const int steps = (p.K + STEP - 1) / STEP, mine = steps > worker ? (steps - worker + workers - 1) / workers : 0;
+    const int stride = workers * STEP;
+
+    // this lane's 16 bytes of rows g, g + 8, g + 16 and g + 24 (a row past N reads the last one; its results are dropped)
+    const uint8_t* at[kLoads];
+    const uint8_t* xp[NT];
+    int left = p.K - worker * STEP - t * 16;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        at[i] = p.b + min(row0 + g + 8 * i, p.N - 1) * p.K + worker * STEP + t * 16;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) xp[i] = p.a + min(8 * i + g, p.M - 1) * p.lda + worker * STEP + t * 16;
+    int read_left = left;
+    const uint8_t* const row[kLoads] = {at[0], at[1], at[2], at[3]};
+    few::Ring<ALIGNED, NT> ring(smem_u32(ring_smem) + warp * few::ring_bytes(ALIGNED, NT, 1));
+    grid_dependency_wait();
+    allow_dependent_launch();
+    int filled = 0;
+    const auto fill = [&]() {
+        if (filled < mine) {
+            ring.copy(at, left);
+            // (behind the row's end b's zeros meet any bytes of a's rows)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) ring.copy_token(i, left > 0 ? xp[i] : p.a);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) at[i] += stride;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) xp[i] += stride;
+            left -= stride;
+            ++filled;
+        }
+        ring.commit();
+    };
+#pragma unroll
+    for (int i = 0; i < ring.STAGES - 1; ++i) fill();
+
+    float acc[NT][2][4];
+    const auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][0][j] = acc[i][1][j] = 0.0f;
+    };
+    const auto add_up = [&]() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int r = 0; r < kLoads; ++r)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    own[(g + 8 * r) * LDC + 8 * i + 2 * t + j] += __float2int_rn(acc[i][r / 2][2 * (r & 1) + j]);
+    };
+    clear();
+    __syncwarp();
+    for (int j = 0; j < mine;) {
+        for (const int end = min(mine, j + kExactSteps); j < end; ++j) {
+            ring.wait();
+            uint4 w[kLoads];
+            uint32_t x[NT][4];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) w[i] = ring.get(i, row[i], read_left);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) ring.get_token(i, x[i]);
+            read_left -= stride;
+            ring.pop();
+            fill();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t v[kLoads][4];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) few::widen<few::kI8Half>(w[i], half, v[i]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    uint32_t xv[4];
+                    few::widen4<false>(x[i][2 * half], xv[0], xv[1]);
+                    few::widen4<false>(x[i][2 * half + 1], xv[2], xv[3]);
+                    few::mma_step<false>(acc[i][0], v[0], v[1], xv);
+                    few::mma_step<false>(acc[i][1], v[2], v[3], xv);
+                }
+            }
+        }
+        add_up();
+        clear();
+    }
+    cp_async_wait_group<0>();
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFewRows32 * LDC; i += kFewWarps * 32) {
+        int sum = columns[i];
+#pragma unroll
+        for (int k = 1; k < kFewWarps; ++k) sum += columns[k * (kFewRows32 * LDC) + i];
+        columns[i] = sum;
+    }
+    __syncthreads();
+    if (p.ctas > 1) cluster_sync();
+    // 32 rows of a token in a row, the cluster's CTAs in turn
+    for (int i = static_cast<int>(rank) * (kFewWarps * 32) + threadIdx.x; i < p.M * kFewRows32; i += p.ctas * (kFewWarps * 32)) {
+        const int m = i / kFewRows32, r = i % kFewRows32;
+        if (row0 + r >= p.N) continue;
+        int sum = 0;
+        const uint32_t from = smem_u32(columns + r * LDC + m);
+        for (int q = 0; q < p.ctas; ++q) sum += static_cast<int>(ld_relaxed_cluster_u32(mapa_shared(from, q)));
+        const float v = i8_value(sum, __ldg(p.a_scale + m), __ldg(p.b_scale + row0 + r));
+        p.out[m * p.N + row0 + r] = static_cast<uint16_t>(pack16(v, 0.0f, p.bf16));
+    }
+    if (p.ctas > 1) {
+        __syncthreads();
+        cluster_sync();         // (no CTA leaves while another reads its sums)
+    }
+}
+
+template <bool ALIGNED, int NT>
+int launch_few(FewParams p, const DeviceInfo& info, cudaStream_t stream) {
+    const auto kern = few_kernel<ALIGNED, NT>;
+    constexpr int smem = few::ring_bytes(ALIGNED, NT, kFewWarps) + kFewWarps * kFewRows32 * 8 * NT * 4;
+    static std::atomic<bool> ready[64] = {};
+    if (info.device < 0 || info.device >= 64) return GEMM_ERR_LAUNCH;
+    if (!ready[info.device].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        ready[info.device].store(true, std::memory_order_relaxed);
+    }
+    // few row blocks: K over the CTAs of a cluster, four steps a warp at least
+    const int64_t blocks = cdiv(p.N, kFewRows32);
+    int ctas = 1;
+    while (ctas < 8 && 2 * ctas * blocks <= 2 * info.num_sms && p.K >= 2 * ctas * kFewWarps * 64 * 4) ctas *= 2;
+    p.ctas = ctas;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1] = pdl_attribute();
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks * ctas));
+    cfg.blockDim = dim3(kFewWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+template <bool ALIGNED>
+int launch_few_tiles(const FewParams& p, const DeviceInfo& info, cudaStream_t stream) {
+    if (p.M <= 8) return launch_few<ALIGNED, 1>(p, info, stream);
+    if (p.M <= 16) return launch_few<ALIGNED, 2>(p, info, stream);
+    if (p.M <= 32) return launch_few<ALIGNED, 4>(p, info, stream);
+    return launch_few<ALIGNED, 8>(p, info, stream);
+}
+
+// Rows of bytes at any address in rows ld apart (a multiple of 64), padded with
+// zeros: 16 bytes a thread.
+__global__ void __launch_bounds__(256)
+align_bytes_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, int64_t rows, int64_t K, int64_t ld) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t chunks = ld / 16, i = blockIdx.x * 256ll + threadIdx.x;
+    if (i >= rows * chunks) return;
+    const int64_t row = i / chunks, c = (i - row * chunks) * 16;
+    *reinterpret_cast<uint4*>(dst + row * ld + c) = few::load_row<false, false>(src + row * K + c, K - c);
+}
+
 // ---------------------------------------------------------------- product
 
 int check(int64_t M, int64_t N, int64_t K, const void* a, const void* b, const float* sa, const float* sb,
@@ -175,7 +379,12 @@ int check(int64_t M, int64_t N, int64_t K, const void* a, const void* b, const f
     return GEMM_OK;
 }
 
+// Whether rows of K bytes start on 16-byte boundaries.
+bool rows16(const void* p, int64_t K) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && K % 16 == 0; }
+
 struct Plan {
+    bool few = false;               // a few tokens
+    uint8_t* few_a = nullptr;       // their aligned copy, where they need one
     Product pr;
     Layout l;
     uint16_t *a = nullptr, *b = nullptr;
@@ -184,14 +393,20 @@ struct Plan {
 };
 
 // num_sms 0: the workspace only.
-Plan plan_of(int64_t M, int64_t N, int64_t K, int num_sms, void* ws) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, const void* a, int num_sms, void* ws) {
     Plan pl;
     Carver c;
     c.base = static_cast<char*>(ws);
+    pl.ld = round_up(K, 64);
+    pl.few = M <= kFewTokens;
+    if (pl.few) {
+        if (!rows16(a, K)) pl.few_a = c.take<uint8_t>(M * pl.ld);
+        pl.bytes = c.used;
+        return pl;
+    }
     pl.pr.M = M; pl.pr.N = N; pl.pr.K = K;
     pl.pr.chunk = kChunk;
     if (num_sms) pl.l = choose_layout(pl.pr, num_sms);
-    pl.ld = round_up(K, 64);
     pl.a = c.take<uint16_t>(M * pl.ld);
     pl.b = c.take<uint16_t>(N * pl.ld);
     pl.bytes = c.used;
@@ -230,7 +445,7 @@ extern "C" int gemm_i8_nt_workspace(int64_t M, int64_t N, int64_t K, const int8_
     const int rc = check(M, N, K, a, b, nullptr, nullptr, nullptr, type);
     if (rc != GEMM_OK) return rc;
     if (!bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = M && N && K ? static_cast<int64_t>(plan_of(M, N, K, 0, nullptr).bytes) : 0;
+    *bytes = M && N && K ? static_cast<int64_t>(plan_of(M, N, K, a, 0, nullptr).bytes) : 0;
     return GEMM_OK;
 }
 
@@ -250,9 +465,23 @@ extern "C" int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, cons
     rc = current_device(&info);
     if (rc != GEMM_OK) return rc;
     if (K == 0) return cudaMemsetAsync(out, 0, bytes16(M, N), stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
-    Plan pl = plan_of(M, N, K, info.num_sms, workspace);
+    Plan pl = plan_of(M, N, K, a, info.num_sms, workspace);
     if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, outs)) return GEMM_ERR_INVALID_ARG;
-    const bool aligned = reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0 && K % 16 == 0;
+    if (pl.few) {
+        FewParams p = {reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b), a_scale, b_scale,
+                       static_cast<uint16_t*>(out), K, N, static_cast<int>(M), static_cast<int>(K), 1, type == GEMM_TYPE_BFLOAT};
+        if (!rows16(a, K)) {
+            if (launch_pdl(align_bytes_kernel, dim3(static_cast<unsigned>(cdiv(M * pl.ld / 16, 256))), dim3(256), 0, stream, p.a,
+                           pl.few_a, M, K, pl.ld) != cudaSuccess) {
+                cudaGetLastError();
+                return GEMM_ERR_LAUNCH;
+            }
+            p.a = pl.few_a;
+            p.lda = pl.ld;
+        }
+        return rows16(b, K) ? launch_few_tiles<true>(p, info, stream) : launch_few_tiles<false>(p, info, stream);
+    }
+    const bool aligned = rows16(a, K) && rows16(b, K);
     {
         const Widen w = {{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b)}, {pl.a, pl.b}, {M, N}};
         int64_t blocks = cdiv((M + N) * cdiv(K, 16), 256);
