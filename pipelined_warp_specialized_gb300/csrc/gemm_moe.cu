@@ -5,8 +5,8 @@
 //
 // Three kernels in a row on the stream, each launched as a programmatic
 // dependent of the one before: the router (moe_route_kernel), gate and up
-// projections with the activation (moe_gate_kernel), down projections with the
-// weighted sum (moe_down_kernel).  With few tokens the layer is bound by the
+// projections with the activation, down projections with the weighted sum (both
+// moe_experts_kernel).  With few tokens the layer is bound by the
 // bytes of the chosen experts' weights, each read once (few.cuh).
 //
 // Rounding.  Sums are fp32.  The router's logits decide between experts, so
@@ -26,7 +26,7 @@ using namespace few;
 constexpr int kTokens = 64;             // tokens a pass: more are taken 64 at a time
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
-constexpr int64_t kMaxWidth = 1 << 24;  // of K and F
+constexpr int64_t kMaxWidth = 1 << 22;  // of K and F
 constexpr int kRouteCtas = 8;           // CTAs of a cluster that share a token's experts
 constexpr int kRouteTokens = 4;         // tokens a cluster, where there are many
 constexpr int route_threads(int tokens) { return tokens == 1 ? 1024 : 512; }
@@ -223,7 +223,7 @@ struct Params {
     int64_t K, F, ldx, ldh, lo_offset;
     int M, E, top_k, act;
     int* counters;                      // claims of gate and of down units, then each row block's arrivals; zero at first
-    float* partial;                     // [row blocks of 32][kMaxParts][32][ldy]
+    float* partial;                     // [M top_k][K]: each choice's part of y
 };
 
 // What a block of the experts' kernels knows of the routing.  A kernel's entries
@@ -290,60 +290,70 @@ __device__ __forceinline__ int list_tokens(const Routing& r, uint16_t* list, int
     return min(n, SIZE);
 }
 
-// h' = p act(Wg x) (Wu x), 16 rows of F of one entry's tokens at a time: eight
-// warps take the steps of K in turn and their sums are joined in warp order.
-template <int FORM, bool ALIGNED, int NT>
+// One pass over the chosen experts' weights, 32 rows of an entry's at a time (a
+// unit): eight warps take the steps of the rows' length in turn, their sums are
+// joined in warp order, and a thread finishes a row of a token.
+//
+// Gate and up (DOWN false): 16 rows of F of each;  h' = p act(Wg x) (Wu x).
+// Down (DOWN true): 32 rows of K;  Wd h' of each choice, in fp32 to `partial`.  The
+// block that finishes the last of a row block's entries adds up every token's
+// choices in their order: y, whatever order the units were finished in.  The
+// arrival's number is looked at one unit later, so that nobody waits for it.
+//
+// A unit of 1536 or 4096 columns takes a block 4 to 9 us, its join 0.3.
+template <int FORM, bool ALIGNED, int NT, bool DOWN>
 __global__ void __launch_bounds__(kWarps * 32, 2)
-moe_gate_kernel(const __grid_constant__ Params p) {
+moe_experts_kernel(const __grid_constant__ Params p) {
     constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), LANE = 16 / WB, HALVES = halves_of(FORM);
-    constexpr int XB = NT * HALVES, STAGES = ring_stages(ALIGNED, XB);
+    constexpr int XB = NT * HALVES, PIECES = DOWN ? 2 * XB : XB, STAGES = ring_stages(ALIGNED, PIECES);
+    constexpr int ROWS = DOWN ? 32 : 16;
     constexpr bool BF16 = is_bf16(FORM);
     extern __shared__ uint4 ring_smem[];
     __shared__ Routing routing;
     __shared__ __align__(16) int queue[Claims::QUEUE];
     __shared__ __align__(16) float part[kWarps][2][16][8];      // (read and written in pairs)
+    __shared__ int finished;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     grid_dependency_wait();
     allow_dependent_launch();
     const int choices = p.M * p.top_k;
     read_routing<8 * NT>(routing, p.experts, choices, p.E);
-    const int64_t F = p.F, K = p.K;
-    const int blocks = static_cast<int>(p.ldh / 16), units = routing.entries * blocks;
-    const int steps = static_cast<int>((K + STEP - 1) / STEP);
-    const int mine = (steps - warp + kWarps - 1) / kWarps;      // of a row block; may be none
-    const Claims claims{queue, p.counters, Claims::ahead_of(steps / kWarps, STAGES)};
+    const int64_t F = p.F, K = p.K, length = DOWN ? F : K, height = DOWN ? K : F;
+    const int blocks = static_cast<int>(DOWN ? (K + ROWS - 1) / ROWS : p.ldh / ROWS), units = routing.entries * blocks;
+    const int steps = static_cast<int>((length + STEP - 1) / STEP);
+    const int mine = (steps - warp + kWarps - 1) / kWarps;      // of a unit; may be none
+    const Claims claims{queue, p.counters + (DOWN ? 1 : 0), Claims::ahead_of(steps / kWarps, STAGES)};
     if (threadIdx.x == 0) claims.start();
     __syncthreads();
 
-    // this lane's 16 bytes of rows g and g + 8 of gate and up, and what the rows have left from
-    // there on (a row past F reads the last one; its results are dropped)
+    // this lane's 16 bytes of rows g and g + 8 of gate and up, or g, g + 8, g + 16 and g + 24, and what
+    // the rows have left from there on (a row past the last reads that one; its results are dropped)
     struct Rows {
         const uint8_t* at[kLoads];
         int left;
     };
-    const int row_bytes = static_cast<int>(K) * WB, offset = (warp * STEP + t * LANE) * WB;
+    const int row_bytes = static_cast<int>(length) * WB, offset = (warp * STEP + t * LANE) * WB;
     const auto rows_of = [&](int u) {
         const int a = u / blocks;
-        const int64_t row0 = (u - a * blocks) * 16, first = routing.active[a] * F;
+        const int64_t row0 = static_cast<int64_t>(u - a * blocks) * ROWS, first = routing.active[a] * height;
         Rows r;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t at = (first + min(row0 + g + 8 * i, F - 1)) * row_bytes + offset;
-            r.at[i] = p.w_gate + at;
-            r.at[2 + i] = p.w_up + at;
+        for (int i = 0; i < kLoads; ++i) {
+            const int64_t at = (first + min(row0 + g + 8 * (DOWN ? i : i % 2), height - 1)) * row_bytes + offset;
+            r.at[i] = (DOWN ? p.w_down : i < 2 ? p.w_gate : p.w_up) + at;
         }
         r.left = row_bytes - offset;
         return r;
     };
-    Ring<ALIGNED, XB> ring(smem_u32(ring_smem) + warp * ring_bytes(ALIGNED, XB, 1));
+    Ring<ALIGNED, PIECES> ring(smem_u32(ring_smem) + warp * ring_bytes(ALIGNED, PIECES, 1));
     int next_i = 0, next_j = 0, next_entry = -1, next_count = 0;
-    Rows next = {{p.w_gate, p.w_gate, p.w_up, p.w_up}, 0};
+    Rows next = {{p.w_down, p.w_down, p.w_down, p.w_down}, 0};
     const uint16_t* xp[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) xp[i] = p.x;
     bool more = mine > 0;
     const auto enter = [&](int u) {
-        more = more && u >= 0 && u < units;
+        more = more && u < units;
         if (!more) return;
         next = rows_of(u);
         const int a = u / blocks;
@@ -354,8 +364,8 @@ moe_gate_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             // (columns past the entry's tokens are the first one's once more, and not looked at)
-            const int at = 8 * i + g;
-            xp[i] = p.x + routing.list[warp][0][at < next_count ? at : 0] / p.top_k * p.ldx + warp * STEP + t * LANE;
+            const int choice = routing.list[warp][0][8 * i + g < next_count ? 8 * i + g : 0];
+            xp[i] = (DOWN ? p.h + choice * p.ldh : p.x + choice / p.top_k * p.ldx) + warp * STEP + t * LANE;
         }
     };
     enter(claims.unit(0));
@@ -366,7 +376,10 @@ moe_gate_kernel(const __grid_constant__ Params p) {
             for (int i = 0; i < NT; ++i) {
                 if (8 * i >= next_count) break;
 #pragma unroll
-                for (int half = 0; half < HALVES; ++half) ring.copy_token(i * HALVES + half, xp[i] + 8 * half);
+                for (int half = 0; half < HALVES; ++half) {
+                    ring.copy_token(i * HALVES + half, xp[i] + 8 * half);
+                    if (DOWN) ring.copy_token(XB + i * HALVES + half, xp[i] + p.lo_offset + 8 * half);
+                }
                 xp[i] += kWarps * STEP;
             }
             if (++next_j == mine) {
@@ -383,13 +396,31 @@ moe_gate_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) fill();
 
+    // Down: the unit before's row block and the number of its arrival (thread 0's)
+    int before = -1, arrival = 0;
+    const auto add_choices = [&](int done) {
+        if (done < 0) return;
+        __threadfence();
+        const int64_t row0 = static_cast<int64_t>(done) * ROWS;
+        for (int i = threadIdx.x; i < p.M * ROWS; i += kWarps * 32) {
+            const int m = i / ROWS;
+            const int64_t row = row0 + i % ROWS;
+            if (row >= K) continue;
+            const float* from = p.partial + static_cast<int64_t>(m) * p.top_k * K + row;
+            float sum = 0.0f;
+            for (int j = 0; j < p.top_k; ++j) sum += __ldcg(from + j * K);
+            p.y[m * K + row] = static_cast<uint16_t>(fused::pack16(sum, 0.0f, BF16));
+        }
+    };
+
     int entry = -1, count = 0, tiles = 0;
     uint16_t* const list = routing.list[warp][1];
     for (int i_unit = 0;; ++i_unit) {
         const int u = claims.unit(i_unit);
-        if (u < 0 || u >= units) break;
+        if (u >= units) break;
         const int claimed = threadIdx.x == 0 ? claims.claim() : 0;
-        const int a = u / blocks, row0 = (u - a * blocks) * 16, expert = routing.active[a];
+        const int a = u / blocks, block = u - a * blocks, expert = routing.active[a];
+        const int64_t row0 = static_cast<int64_t>(block) * ROWS;
         if (a != entry) {
             entry = a;
             count = list_tokens<8 * NT>(routing, list, a, choices);
@@ -404,13 +435,13 @@ moe_gate_kernel(const __grid_constant__ Params p) {
         for (int j = 0; j < mine; ++j) {
             ring.wait();
             uint4 w[kLoads];
-            uint32_t xv[XB][4];
+            uint32_t xv[PIECES][4];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) w[i] = ring.get(i, rows.at[i], rows.left);
             rows.left -= kWarps * STEP * WB;
 #pragma unroll
-            for (int i = 0; i < XB; ++i)
-                if (i / HALVES < tiles) ring.get_token(i, xv[i]);
+            for (int i = 0; i < PIECES; ++i)
+                if (i % XB / HALVES < tiles) ring.get_token(i, xv[i]);
             ring.pop();
             fill();
 #pragma unroll
@@ -421,293 +452,77 @@ moe_gate_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if (i >= tiles) break;
-                    mma_step<BF16>(acc[i][0], v[0], v[1], xv[i * HALVES + half]);
-                    mma_step<BF16>(acc[i][1], v[2], v[3], xv[i * HALVES + half]);
+#pragma unroll
+                    for (int piece = i * HALVES + half; piece < PIECES; piece += XB) {
+                        mma_step<BF16>(acc[i][0], v[0], v[1], xv[piece]);
+                        mma_step<BF16>(acc[i][1], v[2], v[3], xv[piece]);
+                    }
                 }
             }
         }
-        if (threadIdx.x == 0) claims.put(i_unit, claimed);
-        // join the warps' sums tile by tile; thread (row, token) finishes h'
-        const int r = threadIdx.x / 8 % 16, n = threadIdx.x % 8;
+        if (threadIdx.x == 0) {
+            claims.put(i_unit, claimed);
+            finished = before >= 0 && arrival == routing.entries - 1 ? before : -1;
+        }
+        // join the warps' sums tile by tile; a thread finishes row r of token n (down: of half m)
+        const int r = threadIdx.x / 8 % 16, n = threadIdx.x % 8, m = threadIdx.x / 128;
+        int done = -1;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             if (i >= tiles) break;
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                *reinterpret_cast<float2*>(&part[warp][m][g][2 * t]) = make_float2(acc[i][m][0], acc[i][m][1]);
-                *reinterpret_cast<float2*>(&part[warp][m][g + 8][2 * t]) = make_float2(acc[i][m][2], acc[i][m][3]);
+            for (int k = 0; k < 2; ++k) {
+                *reinterpret_cast<float2*>(&part[warp][k][g][2 * t]) = make_float2(acc[i][k][0], acc[i][k][1]);
+                *reinterpret_cast<float2*>(&part[warp][k][g + 8][2 * t]) = make_float2(acc[i][k][2], acc[i][k][3]);
             }
             __syncthreads();
-            if (threadIdx.x < 128 && 8 * i + n < count) {
-                float gate = 0.0f, up = 0.0f;
+            done = finished;            // (written before this barrier, and not again before the next)
+            if (8 * i + n < count && (DOWN || m == 0)) {
+                const int choice = list[8 * i + n];
+                float sum = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    gate += part[k][0][r][n];
-                    up += part[k][1][r][n];
-                }
-                const int choice = list[8 * i + n], row = row0 + r;
-                float h = 0.0f;
-                if (row < F) {
-                    if constexpr (is_i8(FORM)) {
-                        gate *= p.s_gate[static_cast<int64_t>(expert) * F + row];
-                        up *= p.s_up[static_cast<int64_t>(expert) * F + row];
+                for (int k = 0; k < kWarps; ++k) sum += part[k][m][r][n];
+                if constexpr (DOWN) {
+                    const int64_t row = row0 + 16 * m + r;
+                    if (row < K) {
+                        if constexpr (is_i8(FORM)) sum *= p.s_down[expert * K + row];
+                        p.partial[choice * K + row] = sum;
                     }
-                    h = p.weights[choice] * (fused::act_value(gate, p.act) * up);
+                } else {
+                    const int64_t row = row0 + r;
+                    float up = 0.0f, h = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) up += part[k][1][r][n];
+                    if (row < F) {
+                        if constexpr (is_i8(FORM)) {
+                            sum *= p.s_gate[expert * F + row];
+                            up *= p.s_up[expert * F + row];
+                        }
+                        h = p.weights[choice] * (fused::act_value(sum, p.act) * up);
+                    }
+                    // (columns from F to the padded row's end are zeros)
+                    const uint32_t hi = fused::pack16(h, 0.0f, BF16);
+                    const float kept = fused::unpack16(hi, BF16).x;
+                    uint16_t* out = p.h + choice * p.ldh + row;
+                    out[0] = static_cast<uint16_t>(hi);
+                    out[p.lo_offset] = static_cast<uint16_t>(fused::pack16(fused::remainder16(h, kept), 0.0f, BF16));
                 }
-                // (columns from F to the padded row's end are zeros)
-                const uint32_t hi = fused::pack16(h, 0.0f, BF16);
-                const float kept = fused::unpack16(hi, BF16).x;
-                uint16_t* out = p.h + static_cast<int64_t>(choice) * p.ldh + row;
-                out[0] = static_cast<uint16_t>(hi);
-                out[p.lo_offset] = static_cast<uint16_t>(fused::pack16(fused::remainder16(h, kept), 0.0f, BF16));
             }
+            if (DOWN && i == tiles - 1) __threadfence();
             __syncthreads();
+        }
+        if (DOWN) {
+            if (threadIdx.x == 0) arrival = atomicAdd(p.counters + 2 + block, 1);
+            before = block;
+            add_choices(done);
         }
     }
     cp_async_wait_group<0>();
-}
-
-// y = sum over the experts of Wd h', 32 rows of K at a time.  The steps of all
-// entries are one long axis, cut into parts that are units of work of their own,
-// and those into a contiguous piece for each warp.  A warp adds each entry's sums to its
-// tokens' columns in shared memory; the warps' columns are added in order, and
-// the parts' by the block that finishes a row block's last one, in order too.
-constexpr int kDownRows = 32;
-constexpr int kMaxParts = 16;
-constexpr int kDownUnits = 1216;        // 4 rounds of the GPU's blocks, so that the last is short
-
-// Parts of a row block: every warp has four steps of each, or there is one part.
-__host__ __device__ inline int down_parts(int64_t steps, int64_t blocks) {
-    int64_t parts = (kDownUnits + blocks - 1) / blocks;
-    if (parts > kMaxParts) parts = kMaxParts;
-    if (parts > steps / (4 * kWarps)) parts = steps / (4 * kWarps);
-    return parts < 1 ? 1 : static_cast<int>(parts);
-}
-
-template <int FORM, bool ALIGNED, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-moe_down_kernel(const __grid_constant__ Params p) {
-    constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), LANE = 16 / WB, HALVES = halves_of(FORM);
-    constexpr int XB = NT * HALVES, STAGES = ring_stages(ALIGNED, 2 * XB);
-    constexpr bool BF16 = is_bf16(FORM);
-    extern __shared__ uint4 ring_smem[];
-    __shared__ Routing routing;
-    __shared__ __align__(16) int queue[Claims::QUEUE];
-    __shared__ int last_part;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int M = p.M, ldy = (M + 7) / 8 * 8;
-    // [kWarps][32][ldy]
-    float* const columns = reinterpret_cast<float*>(reinterpret_cast<char*>(ring_smem) + ring_bytes(ALIGNED, 2 * XB, kWarps));
-    float* const own = columns + warp * (kDownRows * ldy);
-    grid_dependency_wait();
-    allow_dependent_launch();
-    const int choices = M * p.top_k;
-    read_routing<8 * NT>(routing, p.experts, choices, p.E);
-    const int64_t F = p.F, K = p.K;
-    const int blocks = static_cast<int>((K + kDownRows - 1) / kDownRows);
-    const int steps = static_cast<int>((F + STEP - 1) / STEP);
-    const int64_t all = static_cast<int64_t>(routing.entries) * steps;
-    const int parts = down_parts(all, blocks), units = blocks * parts;
-    // warp w's piece of a part: steps [piece(part, w), piece(part, w + 1))
-    const auto piece = [&](int part, int w) { return all * (part * kWarps + w) / (parts * kWarps); };
-    const Claims claims{queue, p.counters + 1, Claims::ahead_of(all / (kWarps * parts), STAGES)};
-    if (threadIdx.x == 0) claims.start();
-    __syncthreads();
-
-    // this lane's 16 bytes of rows g, g + 8, g + 16 and g + 24, from step j on (a row past K reads
-    // the last one; its results are dropped)
-    struct Rows {
-        const uint8_t* at[kLoads];
-        int left;
-    };
-    const int row_bytes = static_cast<int>(F) * WB;
-    const auto rows_of = [&](int a, int block, int j) {
-        const int offset = (j * STEP + t * LANE) * WB;
-        Rows r;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            r.at[i] = p.w_down + (routing.active[a] * K + min(static_cast<int64_t>(block) * kDownRows + g + 8 * i, K - 1)) * row_bytes + offset;
-        r.left = row_bytes - offset;
-        return r;
-    };
-    Ring<ALIGNED, 2 * XB> ring(smem_u32(ring_smem) + warp * ring_bytes(ALIGNED, 2 * XB, 1));
-    int next_i = 0, next_block = 0, next_a = 0, next_j = 0;
-    int left = 0;                               // steps of this warp's piece still to be copied
-    int next_entry = -1, next_count = 0;
-    Rows next = {{p.w_down, p.w_down, p.w_down, p.w_down}, 0};
-    const uint16_t* hp[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) hp[i] = p.h;
-    const auto enter_entry = [&]() {
-        next = rows_of(next_a, next_block, next_j);
-        if (next_a != next_entry) {
-            next_entry = next_a;
-            next_count = list_tokens<8 * NT>(routing, routing.list[warp][0], next_a, choices);
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int at = 8 * i + g;
-            hp[i] = p.h + routing.list[warp][0][at < next_count ? at : 0] * p.ldh + next_j * STEP + t * LANE;
-        }
-    };
-    const auto enter = [&](int u) {
-        if (u < 0 || u >= units) {
-            left = 0;
-            return;
-        }
-        const int part = u / blocks;
-        next_block = u - part * blocks;
-        const int64_t s0 = piece(part, warp);
-        left = static_cast<int>(piece(part, warp + 1) - s0);
-        if (left == 0) return;                  // (one part, and fewer steps than warps: never any)
-        next_a = static_cast<int>(s0 / steps);
-        next_j = static_cast<int>(s0 - static_cast<int64_t>(next_a) * steps);
-        enter_entry();
-    };
-    enter(claims.unit(0));
-    const auto fill = [&]() {
-        if (left > 0) {
-            ring.copy(next.at, next.left);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                if (8 * i >= next_count) break;
-#pragma unroll
-                for (int half = 0; half < HALVES; ++half) {
-                    ring.copy_token(i * HALVES + half, hp[i] + 8 * half);
-                    ring.copy_token(XB + i * HALVES + half, hp[i] + p.lo_offset + 8 * half);
-                }
-                hp[i] += STEP;
-            }
-            if (--left == 0) {
-                enter(claims.unit(++next_i));
-            } else if (++next_j == steps) {
-                next_j = 0;
-                ++next_a;
-                enter_entry();
-            } else {
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) next.at[i] += STEP * WB;
-                next.left -= STEP * WB;
-            }
-        }
-        ring.commit();
-    };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fill();
-
-    uint16_t* const list = routing.list[warp][1];
-    int entry = -1, count = 0, tiles = 0;
-    for (int i_unit = 0;; ++i_unit) {
-        const int u = claims.unit(i_unit);
-        if (u < 0 || u >= units) break;
-        const int claimed = threadIdx.x == 0 ? claims.claim() : 0;
-        const int part = u / blocks, block = u - part * blocks;
-        const int64_t row0 = static_cast<int64_t>(block) * kDownRows;
-        const int64_t s0 = piece(part, warp), s1 = piece(part, warp + 1);
-        for (int i = lane; i < kDownRows * ldy; i += 32) own[i] = 0.0f;
-        __syncwarp();
-        for (int64_t s = s0; s < s1;) {
-            const int a = static_cast<int>(s / steps), from = static_cast<int>(s - static_cast<int64_t>(a) * steps);
-            const int to = static_cast<int>(min(static_cast<int64_t>(steps), from + (s1 - s)));
-            s += to - from;
-            const int expert = routing.active[a];
-            if (a != entry) {
-                entry = a;
-                count = list_tokens<8 * NT>(routing, list, a, choices);
-                tiles = (count + 7) / 8;
-            }
-            Rows rows = rows_of(a, block, from);
-            float acc[NT][2][4];
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][0][j] = acc[i][1][j] = 0.0f;
-            for (int j = from; j < to; ++j) {
-                ring.wait();
-                uint4 w[kLoads];
-                uint32_t hi[XB][4], lo[XB][4];
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) w[i] = ring.get(i, rows.at[i], rows.left);
-                rows.left -= STEP * WB;
-#pragma unroll
-                for (int i = 0; i < XB; ++i) {
-                    if (i / HALVES >= tiles) break;
-                    ring.get_token(i, hi[i]);
-                    ring.get_token(XB + i, lo[i]);
-                }
-                ring.pop();
-                fill();
-#pragma unroll
-                for (int half = 0; half < HALVES; ++half) {
-                    uint32_t v[kLoads][4];
-#pragma unroll
-                    for (int i = 0; i < kLoads; ++i) widen<FORM>(w[i], half, v[i]);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        if (i >= tiles) break;
-                        mma_step<BF16>(acc[i][0], v[0], v[1], hi[i * HALVES + half]);
-                        mma_step<BF16>(acc[i][1], v[2], v[3], hi[i * HALVES + half]);
-                        mma_step<BF16>(acc[i][0], v[0], v[1], lo[i * HALVES + half]);
-                        mma_step<BF16>(acc[i][1], v[2], v[3], lo[i * HALVES + half]);
-                    }
-                }
-            }
-            // to the columns of the tokens (each has a choice of an expert once)
-            float scale[kLoads];
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                scale[i] = is_i8(FORM) ? p.s_down[expert * K + min(row0 + g + 8 * i, K - 1)] : 1.0f;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                if (i >= tiles) break;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int at = 8 * i + 2 * t + j;
-                    if (at >= count) continue;
-                    float* to_column = own + list[at] / p.top_k;
-#pragma unroll
-                    for (int r = 0; r < kLoads; ++r)
-                        to_column[(g + 8 * r) * ldy] += scale[r] * acc[i][r / 2][2 * (r & 1) + j];
-                }
-            }
-        }
-        if (threadIdx.x == 0) claims.put(i_unit, claimed);
+    if (DOWN) {
+        if (threadIdx.x == 0) finished = before >= 0 && arrival == routing.entries - 1 ? before : -1;
         __syncthreads();
-        float* const sums = p.partial + (static_cast<int64_t>(block) * kMaxParts + part) * (kDownRows * ldy);
-        for (int i = threadIdx.x; i < kDownRows * ldy; i += kWarps * 32) {
-            float sum = columns[i];
-#pragma unroll
-            for (int k = 1; k < kWarps; ++k) sum += columns[k * (kDownRows * ldy) + i];
-            if (parts > 1) sums[i] = sum;
-            else columns[i] = sum;
-        }
-        if (parts > 1) {
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) last_part = atomicAdd(p.counters + 2 + block, 1) == parts - 1;
-            __syncthreads();
-            if (last_part) {
-                __threadfence();
-                const float* first = p.partial + static_cast<int64_t>(block) * kMaxParts * (kDownRows * ldy);
-                for (int i = threadIdx.x; i < kDownRows * ldy; i += kWarps * 32) {
-                    float sum = 0.0f;
-                    for (int k = 0; k < parts; ++k) sum += __ldcg(first + static_cast<int64_t>(k) * (kDownRows * ldy) + i);
-                    columns[i] = sum;
-                }
-            }
-        }
-        __syncthreads();
-        if (parts == 1 || last_part) {
-            // 32 rows of a token in a row
-            for (int i = threadIdx.x; i < M * kDownRows; i += kWarps * 32) {
-                const int m = i / kDownRows, r = i % kDownRows;
-                if (row0 + r < K)
-                    p.y[m * K + row0 + r] = static_cast<uint16_t>(fused::pack16(columns[r * ldy + m], 0.0f, BF16));
-            }
-        }
-        __syncthreads();
+        add_choices(finished);
     }
-    cp_async_wait_group<0>();
 }
 
 // ---------------------------------------------------------------- host
@@ -740,7 +555,7 @@ int check(const Call& c) {
     if (c.act != GEMM_ACT_SILU && c.act != GEMM_ACT_GELU) return GEMM_ERR_INVALID_ARG;
     if (c.normalize != 0 && c.normalize != 1) return GEMM_ERR_INVALID_ARG;
     // units of work are counted in an int
-    if (c.E * cdiv(c.F, 16) >= (1ll << 30) || cdiv(c.K, kDownRows) * kMaxParts >= (1ll << 30)) return GEMM_ERR_INVALID_ARG;
+    if ((c.E + kTokens * kMaxTopK / 8) * cdiv(c.F > c.K ? c.F : c.K, 16) >= (1ll << 30)) return GEMM_ERR_INVALID_ARG;
     const bool i8 = c.weight_type == GEMM_TYPE_BYTE;
     if (odd_address(c.x) || odd_address(c.w_router) || odd_address(c.y)) return GEMM_ERR_ALIGNMENT;
     if (!i8 && (odd_address(c.w_gate) || odd_address(c.w_up) || odd_address(c.w_down))) return GEMM_ERR_ALIGNMENT;
@@ -766,7 +581,7 @@ struct Workspace {
     float* partial = nullptr;
     size_t bytes = 0;
 };
-int64_t num_counters(int64_t K) { return 2 + cdiv(K, kDownRows); }
+int64_t num_counters(int64_t K) { return 2 + cdiv(K, 32); }
 Workspace workspace_of(const Call& c, void* base) {
     Workspace w;
     if (c.M == 0 || c.K == 0) return w;
@@ -776,7 +591,7 @@ Workspace workspace_of(const Call& c, void* base) {
     w.x = carver.take<uint16_t>(tokens * ldh_of(c.K));
     w.h = carver.take<uint16_t>(2 * tokens * c.top_k * ldh_of(c.F));
     w.counters = carver.take<int>(num_counters(c.K));
-    w.partial = carver.take<float>(cdiv(c.K, kDownRows) * kMaxParts * kDownRows * round_up(tokens, 8));
+    w.partial = carver.take<float>(tokens * c.top_k * c.K);
     w.bytes = carver.used;
     return w;
 }
@@ -815,19 +630,18 @@ int launch_route_tokens(const Call& c, const uint8_t* x, int M, int* experts, fl
                    : launch_route<BF16, ALIGNED, kRouteTokens>(c, x, M, experts, weights, ws, stream);
 }
 
-// How many blocks of a kernel fit the GPU at once, with `smem` bytes of the `most`
-// it may have; set up on the first call on a device.
+// How many blocks of a kernel fit the GPU at once; set up on the first call on a device.
 struct Fit {
     std::atomic<int> blocks[64] = {};
 };
 template <typename Kernel>
-int blocks_at_once(Fit& fit, Kernel kern, int smem, int most, const DeviceInfo& info) {
+int blocks_at_once(Fit& fit, Kernel kern, int smem, const DeviceInfo& info) {
     if (info.device < 0 || info.device >= 64) return 0;
     int n = fit.blocks[info.device].load(std::memory_order_relaxed);
     if (n == 0) {
         // concurrent first calls compute and store the same value
         int per_sm = 0;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWarps * 32, smem) != cudaSuccess || per_sm <= 0) {
             cudaGetLastError();
             return 0;
@@ -838,37 +652,26 @@ int blocks_at_once(Fit& fit, Kernel kern, int smem, int most, const DeviceInfo& 
     return n;
 }
 
-template <int FORM, bool ALIGNED, int NT>
-int launch_experts(const Params& p, bool down, const DeviceInfo& info, cudaStream_t stream) {
-    constexpr int pieces = NT * halves_of(FORM);
-    // the most entries that the routing can give
-    const int64_t choices = static_cast<int64_t>(p.M) * p.top_k;
-    const int64_t entries = (choices < p.E ? choices : p.E) + choices / (8 * NT);
-    if (!down) {
-        const auto kern = moe_gate_kernel<FORM, ALIGNED, NT>;
-        constexpr int ring = ring_bytes(ALIGNED, pieces, kWarps);
-        static Fit fit;
-        const int64_t fits = blocks_at_once(fit, kern, ring, ring, info), units = entries * (p.ldh / 16);
-        if (fits == 0) return GEMM_ERR_LAUNCH;
-        return launched(launch_pdl(kern, dim3(static_cast<unsigned>(units < fits ? units : fits)), dim3(kWarps * 32), ring, stream, p));
-    }
-    const auto kern = moe_down_kernel<FORM, ALIGNED, NT>;
-    constexpr int ring = ring_bytes(ALIGNED, 2 * pieces, kWarps);
-    static Fit fit[kTokens / 8];
-    constexpr int columns = kWarps * kDownRows * 8 * 4;         // bytes of eight tokens
-    const int eights = static_cast<int>(cdiv(p.M, 8)), smem = ring + columns * eights;
-    const int64_t fits = blocks_at_once(fit[eights - 1], kern, smem, ring + columns * (kTokens / 8), info);
+template <int FORM, bool ALIGNED, int NT, bool DOWN>
+int launch_experts(const Params& p, const DeviceInfo& info, cudaStream_t stream) {
+    constexpr int ring = ring_bytes(ALIGNED, (DOWN ? 2 : 1) * NT * halves_of(FORM), kWarps);
+    const auto kern = moe_experts_kernel<FORM, ALIGNED, NT, DOWN>;
+    static Fit fit;
+    const int64_t fits = blocks_at_once(fit, kern, ring, info);
     if (fits == 0) return GEMM_ERR_LAUNCH;
-    const int64_t blocks = cdiv(p.K, kDownRows), units = blocks * down_parts(entries * cdiv(p.F, step_k(FORM)), blocks);
-    return launched(launch_pdl(kern, dim3(static_cast<unsigned>(units < fits ? units : fits)), dim3(kWarps * 32), smem, stream, p));
+    // the most entries that the routing can give
+    const int64_t choices = static_cast<int64_t>(p.M) * p.top_k, entries = (choices < p.E ? choices : p.E) + choices / (8 * NT);
+    const int64_t units = entries * (DOWN ? cdiv(p.K, 32) : p.ldh / 16);
+    return launched(launch_pdl(kern, dim3(static_cast<unsigned>(units < fits ? units : fits)), dim3(kWarps * 32), ring, stream, p));
 }
 
 // Two tiles where an expert has more than four tokens on average: one tile's ring
 // leaves room for more blocks, two read a crowded expert's weights half as often.
 template <int FORM, bool ALIGNED>
 int launch_tiles(const Params& p, bool down, const DeviceInfo& info, cudaStream_t stream) {
-    return p.M <= 8 || p.M * p.top_k <= 4 * p.E ? launch_experts<FORM, ALIGNED, 1>(p, down, info, stream)
-                                                : launch_experts<FORM, ALIGNED, 2>(p, down, info, stream);
+    if (p.M <= 8 || p.M * p.top_k <= 4 * p.E)
+        return down ? launch_experts<FORM, ALIGNED, 1, true>(p, info, stream) : launch_experts<FORM, ALIGNED, 1, false>(p, info, stream);
+    return down ? launch_experts<FORM, ALIGNED, 2, true>(p, info, stream) : launch_experts<FORM, ALIGNED, 2, false>(p, info, stream);
 }
 
 template <int FORM>
@@ -942,7 +745,11 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
                                : launch_route_tokens<false, false>(c, x, p.M, experts, weights, ws, stream);
         if (rc != GEMM_OK) return rc;
         if (c.K == 0) continue;
-        if (c.F > 0 && (rc = launch_kernel(p, form, false, gate_aligned, info, stream)) != GEMM_OK) return rc;
+        if (c.F == 0) {
+            if (cudaMemsetAsync(p.y, 0, fused::bytes16(p.M, c.K), stream) != cudaSuccess) return GEMM_ERR_LAUNCH;
+            continue;
+        }
+        if ((rc = launch_kernel(p, form, false, gate_aligned, info, stream)) != GEMM_OK) return rc;
         if ((rc = launch_kernel(p, form, true, down_aligned, info, stream)) != GEMM_OK) return rc;
     }
     return GEMM_OK;
