@@ -168,21 +168,22 @@ __device__ __forceinline__ void cp_async_l1(uint32_t dst, const void* src) {
 
 // TOKENS: 16-byte pieces of token rows a lane takes a step.
 constexpr int ring_slot(bool aligned, int tokens) { return (kLoads + (aligned ? 0 : 1) + tokens) * 512; }
-// As many stages, up to four, as leave room for two blocks of eight warps an SM;
-// where that is less than three, for one block with 64 KB of sums.
-constexpr int ring_stages(bool aligned, int tokens) {
-    const int stage = 8 * ring_slot(aligned, tokens), two = 92160 / stage, one = 150000 / stage;
+// As many stages, up to four, as leave room for two blocks of eight warps an SM,
+// `beside` bytes of other shared memory in each; where that is less than three, for one.
+constexpr int ring_stages(bool aligned, int tokens, int beside) {
+    const int stage = 8 * ring_slot(aligned, tokens), two = (115200 - beside) / stage, one = (231424 - beside) / stage;
     return two >= 3 ? (two < 4 ? two : 4) : one < 4 ? one : 4;
 }
-constexpr int ring_bytes(bool aligned, int tokens, int warps) { return warps * ring_stages(aligned, tokens) * ring_slot(aligned, tokens); }
 
-template <bool ALIGNED, int TOKENS>
+template <bool ALIGNED, int TOKENS, int BESIDE>
 struct Ring {
-    static constexpr int STAGES = ring_stages(ALIGNED, TOKENS), WEIGHTS = kLoads + (ALIGNED ? 0 : 1);
-    static constexpr uint32_t BLOCK = 512, SLOT = ring_slot(ALIGNED, TOKENS);
+    static constexpr int STAGES = ring_stages(ALIGNED, TOKENS, BESIDE), WEIGHTS = kLoads + (ALIGNED ? 0 : 1);
+    static constexpr uint32_t BLOCK = 512, SLOT = ring_slot(ALIGNED, TOKENS), WARP_BYTES = STAGES * SLOT;
     uint32_t first, fill, read;
 
-    __device__ __forceinline__ Ring(uint32_t warp_base) : first(warp_base + (threadIdx.x % 32) * 16), fill(first), read(first) {}
+    // base: of the block's rings, one after the other.
+    __device__ __forceinline__ Ring(uint32_t base, int warp)
+        : first(base + warp * WARP_BYTES + (threadIdx.x % 32) * 16), fill(first), read(first) {}
     __device__ __forceinline__ uint32_t after(uint32_t at) const { return at == first + (STAGES - 1) * SLOT ? first : at + SLOT; }
 
     // The block behind the last lane's of row i.

@@ -20,18 +20,37 @@ static_assert(kChunk % kMaxBoxes == 0, "a chunk ends with a slot");
 
 // ---------------------------------------------------------------- quantization
 
-constexpr float kMagic = 12582912.0f;       // 1.5 * 2^23: adding it rounds to a whole number
+constexpr float kMagic = 12582912.0f;       // 1.5 * 2^23: a sum with it is rounded to a whole number, in its low bits
 
-// rint(127 x / top) exactly, from q = x * fl(127 / top), which is off by less than
-// 2^-22 of its power of two.  A quotient of two 16-bit values that is not halfway
-// between two integers is at least 2^-19 of its power of two from there (the
-// values have at most 11 significant bits), so only near a half can the product
-// mislead, and there the division, correctly rounded, does not: halves are exact.
-__device__ __forceinline__ int quantized(float x, float top, float inverse) {
-    const float q = x * inverse;
-    const float n = __fsub_rn(__fadd_rn(q, kMagic), kMagic);
-    if (fabsf(q - n) > 0.49996f) return __float2int_rn(__fdiv_rn(127.0f * x, top));
-    return static_cast<int>(n);
+// rint(127 x / top) for eight values, in the low bytes of b, from x times inverse =
+// fl(127 / top), which is off by less than 2^-16 where it is nearest to 127.  A quotient of
+// two 16-bit values that is not halfway between two integers is at least 2^-19 of
+// its power of two from there (the values have at most 11 significant bits), 16
+// times what the product is off by: only near a half can it mislead.  There the sides
+// of 127 |x| / top = m + 1/2 are compared without a division: 254 |x| and (2 m + 1) top have at
+// most 19 bits and are exact.  Five operations an element and one branch for
+// eight: with a conversion, a branch and a division for each the pass was bound
+// by them (85 us for 16384 x 8192).
+__device__ __forceinline__ void quantize8(const float (&x)[8], float top, float inverse, uint32_t (&b)[8]) {
+    float off = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float t = __fmaf_rn(x[j], inverse, kMagic), n = __fsub_rn(t, kMagic);
+        off = fmaxf(off, fabsf(__fmaf_rn(x[j], inverse, -n)));
+        b[j] = __float_as_uint(t);
+    }
+    if (off > 0.49998f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float q = fabsf(x[j]) * inverse, m = floorf(q);
+            if (fabsf(q - m - 0.5f) < 2e-5f) {
+                const float left = 254.0f * fabsf(x[j]), right = (2.0f * m + 1.0f) * top;
+                const uint32_t low = __float_as_uint(m + kMagic);
+                const uint32_t n = low + (left > right || (left == right && (low & 1u)) ? 1u : 0u);
+                b[j] = x[j] < 0.0f ? 0u - n : n;
+            }
+        }
+    }
 }
 
 // A row of x by LANES threads (a warp, or the block): its largest magnitude, then
@@ -88,15 +107,24 @@ quantize_kernel(const uint8_t* __restrict__ x, int8_t* __restrict__ q, float* __
     const bool wide = (reinterpret_cast<uintptr_t>(dst) & 7u) == 0;
     const auto put = [&](int64_t i, const uint4& v) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float f[8];
         uint32_t b[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float2 f = unpack16(w[j], BF16);
+            const float2 two = unpack16(w[j], BF16);
+            f[2 * j] = two.x;
+            f[2 * j + 1] = two.y;
+        }
+        if (BF16 && by != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= by;
+        }
+        if (finite) {
+            quantize8(f, most, inverse, b);
+        } else {
             // (a row with an infinity or a NaN is zeros)
-            if (!finite) f = make_float2(0.0f, 0.0f);
-            if (BF16) { f.x *= by; f.y *= by; }
-            b[2 * j] = static_cast<uint32_t>(quantized(f.x, most, inverse));
-            b[2 * j + 1] = static_cast<uint32_t>(quantized(f.y, most, inverse));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j] = 0u;
         }
         if (wide && 8 * i + 8 <= K) {
             const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
@@ -173,6 +201,8 @@ constexpr int kFewTokens = 64;
 constexpr int kFewRows32 = 32;
 constexpr int kFewWarps = 8;
 constexpr int kExactSteps = 16;
+// bytes of the warps' sums of NT tiles
+constexpr int few_columns(int tiles) { return kFewWarps * kFewRows32 * 8 * tiles * 4; }
 
 struct FewParams {
     const uint8_t* a;               // [M][lda], rows on 16-byte boundaries
@@ -189,11 +219,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 2 : 1)
 few_kernel(const __grid_constant__ FewParams p) {
     using few::kLoads;
     constexpr int STEP = 64, LDC = 8 * NT;
+    using Ring = few::Ring<ALIGNED, NT, few_columns(NT)>;
     extern __shared__ uint4 ring_smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const uint32_t rank = cluster_ctarank();
     // [kFewWarps][32][LDC]
-    int* const columns = reinterpret_cast<int*>(reinterpret_cast<char*>(ring_smem) + few::ring_bytes(ALIGNED, NT, kFewWarps));
+    int* const columns = reinterpret_cast<int*>(reinterpret_cast<char*>(ring_smem) + kFewWarps * Ring::WARP_BYTES);
     int* const own = columns + warp * (kFewRows32 * LDC);
     for (int i = lane; i < kFewRows32 * LDC; i += 32) own[i] = 0;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(p.ctas)) * kFewRows32;
@@ -212,7 +243,7 @@ few_kernel(const __grid_constant__ FewParams p) {
     for (int i = 0; i < NT; ++i) xp[i] = p.a + min(8 * i + g, p.M - 1) * p.lda + worker * STEP + t * 16;
     int read_left = left;
     const uint8_t* const row[kLoads] = {at[0], at[1], at[2], at[3]};
-    few::Ring<ALIGNED, NT> ring(smem_u32(ring_smem) + warp * few::ring_bytes(ALIGNED, NT, 1));
+    Ring ring(smem_u32(ring_smem), warp);
     grid_dependency_wait();
     allow_dependent_launch();
     int filled = 0;
@@ -232,7 +263,7 @@ few_kernel(const __grid_constant__ FewParams p) {
         ring.commit();
     };
 #pragma unroll
-    for (int i = 0; i < ring.STAGES - 1; ++i) fill();
+    for (int i = 0; i < Ring::STAGES - 1; ++i) fill();
 
     float acc[NT][2][4];
     const auto clear = [&]() {
@@ -311,7 +342,7 @@ few_kernel(const __grid_constant__ FewParams p) {
 template <bool ALIGNED, int NT>
 int launch_few(FewParams p, const DeviceInfo& info, cudaStream_t stream) {
     const auto kern = few_kernel<ALIGNED, NT>;
-    constexpr int smem = few::ring_bytes(ALIGNED, NT, kFewWarps) + kFewWarps * kFewRows32 * 8 * NT * 4;
+    constexpr int smem = kFewWarps * few::Ring<ALIGNED, NT, few_columns(NT)>::WARP_BYTES + few_columns(NT);
     static std::atomic<bool> ready[64] = {};
     if (info.device < 0 || info.device >= 64) return GEMM_ERR_LAUNCH;
     if (!ready[info.device].load(std::memory_order_relaxed)) {

@@ -149,17 +149,20 @@ moe_route_kernel(const uint8_t* __restrict__ x, const uint8_t* __restrict__ w, i
         }
     }
     if (!begun) cluster_wait_acquire();
-    // what the experts' kernels start from: counters at zero, and the tokens in rows of a
-    // multiple of 64, padded with zeros, whatever x's alignment is
-    const int64_t thread = blockIdx.x * static_cast<int64_t>(THREADS) + threadIdx.x, threads = static_cast<int64_t>(gridDim.x) * THREADS;
-    for (int64_t i = thread; i < out.num_counters; i += threads) out.counters[i] = 0;
-    for (int64_t i = thread; i < M * (out.ldx / 8); i += threads) {
-        const int64_t m = i / (out.ldx / 8), k = (i - m * (out.ldx / 8)) * 8;
-        *reinterpret_cast<uint4*>(out.x + m * out.ldx + k) = load_row<ALIGNED, false>(x + (m * K + k) * 2, 2 * (K - k));
-    }
     __syncthreads();            // (the cluster barrier wants whole warps, and the loops above part them)
     cluster_sync();
-    if (rank != 0) return;
+    if (rank != 0) {
+        // what the experts' kernels start from: counters at zero, and the tokens in rows of a
+        // multiple of 64, padded with zeros, whatever x's alignment is
+        const int64_t others = kRouteCtas - 1, clusters = gridDim.x / kRouteCtas;
+        const int64_t thread = (blockIdx.x / kRouteCtas * others + rank - 1) * THREADS + threadIdx.x, threads = clusters * others * THREADS;
+        for (int64_t i = thread; i < out.num_counters; i += threads) out.counters[i] = 0;
+        for (int64_t i = thread; i < M * (out.ldx / 8); i += threads) {
+            const int64_t m = i / (out.ldx / 8), k = (i - m * (out.ldx / 8)) * 8;
+            *reinterpret_cast<uint4*>(out.x + m * out.ldx + k) = load_row<ALIGNED, false>(x + (m * K + k) * 2, 2 * (K - k));
+        }
+        return;
+    }
     if (warp >= count) return;
     // a warp a token: keys in place of the first parts
     unsigned long long* row = sums + warp * E * parts;
@@ -176,22 +179,31 @@ moe_route_kernel(const uint8_t* __restrict__ x, const uint8_t* __restrict__ w, i
     float2 z_top = make_float2(0.0f, 0.0f);
     float mine = 0.0f, total = 0.0f;            // lane j's chosen expert's exponential
     int my_expert = 0;
-    for (int j = 0; j < top_k; ++j) {
-        // the largest key: its high word, then its low word, then its lowest index
-        unsigned long long best = 0;
-        int at = 0;
+    // each lane's largest key; the one that is taken looks for its next
+    unsigned long long best = 0;
+    int at = 0;
+    const auto look = [&]() {
+        best = 0;
         for (int e = lane; e < E; e += 32)
             if (*key_at(e) > best) { best = *key_at(e); at = e; }
+    };
+    look();
+    for (int j = 0; j < top_k; ++j) {
+        // the largest: its high word, then its low word, then its lowest index
         const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
         const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
         const unsigned long long top = static_cast<unsigned long long>(hi) << 32 | lo;
-        at = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(at) : 0xffffffffu));
+        const int chosen = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(at) : 0xffffffffu));
         if (j == 0) z_top = value_of(top);
         if (lane == j) {
-            my_expert = at;
+            my_expert = chosen;
             mine = exp_difference(value_of(top), z_top);
         }
-        if (at % 32 == lane) *key_at(at) = 0ull;
+        if (chosen % 32 == lane) {
+            *key_at(chosen) = 0ull;
+            look();
+        }
+        __syncwarp();
     }
     if (lane < top_k) total = mine;
     if (!normalize)
@@ -222,31 +234,39 @@ struct Params {
     uint16_t* y;                        // [M, K]
     int64_t K, F, ldx, ldh, lo_offset;
     int M, E, top_k, act;
+    int groups;                         // 32 rows a unit takes: 1, 2, 4 or 8
     int* counters;                      // claims of gate and of down units, then each row block's arrivals; zero at first
     float* partial;                     // [M top_k][K]: each choice's part of y
 };
 
+// Shared memory of a block beside its rings and the routing's arrays.
+constexpr int kBeside = 11264;
+
 // What a block of the experts' kernels knows of the routing.  A kernel's entries
 // hold up to 8 NT tokens of an expert (NT tiles): an expert with more is taken once for
 // each 8 NT of them, its weights coming from L2 again, and the accumulators stay few.
-constexpr int kMaxEntries = kMaxExperts + kTokens * kMaxTopK / 8;
 struct alignas(16) Routing {
-    uint16_t experts[kTokens * kMaxTopK];       // each choice's
-    uint16_t active[kMaxEntries];               // an entry's expert, in ascending order
-    uint8_t tokens[kMaxExperts];                // of each expert
+    uint16_t* experts;                          // each choice's
+    uint16_t* active;                           // an entry's expert, in ascending order (no more entries than choices)
     int entries;
-    uint16_t list[kWarps][2][16];     // choices of the entry a warp copies, and of the one it multiplies
+    uint8_t tokens[kMaxExperts];                // of each expert
+    uint16_t list[kWarps][2][16];               // choices of the entry a warp copies, and of the one it multiplies
 };
+constexpr int routing_bytes(int choices) { return (4 * choices + 15) / 16 * 16; }
 
 // Every thread of the block.
 template <int SIZE>
-__device__ __forceinline__ void read_routing(Routing& r, const int* experts, int choices, int num_experts) {
+__device__ __forceinline__ void read_routing(Routing& r, uint16_t* room, const int* experts, int choices, int num_experts) {
     const int lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        r.experts = room;
+        r.active = room + choices;
+    }
     for (int i = threadIdx.x; i < (num_experts + 3) / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(r.tokens)[i] = 0u;
     __syncthreads();
     for (int i = threadIdx.x; i < choices; i += blockDim.x) {
         const int e = experts[i];
-        r.experts[i] = static_cast<uint16_t>(e);
+        room[i] = static_cast<uint16_t>(e);
         // (a byte holds an expert's tokens: each of 64 at most once)
         atomicAdd(reinterpret_cast<uint32_t*>(r.tokens) + e / 4, 1u << (8 * (e % 4)));
     }
@@ -263,7 +283,7 @@ __device__ __forceinline__ void read_routing(Routing& r, const int* experts, int
             }
             const int total = __shfl_sync(0xffffffffu, at, 31);
             at += before - passes;
-            for (int i = 0; i < passes; ++i) r.active[at + i] = static_cast<uint16_t>(e);
+            for (int i = 0; i < passes; ++i) room[choices + at + i] = static_cast<uint16_t>(e);
             before += total;
         }
         if (lane == 0) r.entries = before;
@@ -290,6 +310,8 @@ __device__ __forceinline__ int list_tokens(const Routing& r, uint16_t* list, int
     return min(n, SIZE);
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // One pass over the chosen experts' weights, 32 rows of an entry's at a time (a
 // unit): eight warps take the steps of the rows' length in turn, their sums are
 // joined in warp order, and a thread finishes a row of a token.
@@ -300,13 +322,15 @@ __device__ __forceinline__ int list_tokens(const Routing& r, uint16_t* list, int
 // choices in their order: y, whatever order the units were finished in.  The
 // arrival's number is looked at one unit later, so that nobody waits for it.
 //
-// A unit of 1536 or 4096 columns takes a block 4 to 9 us, its join 0.3.
+// A unit is p.groups such 32 rows, each 8 / p.groups of the warps': short rows in
+// 8 bits are a few steps, and a join for each 64 KB took as long as reading them
+// (down of 32 tokens, 32 experts of 2048 x 4096 in 8 bits, 138 us).
 template <int FORM, bool ALIGNED, int NT, bool DOWN>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 moe_experts_kernel(const __grid_constant__ Params p) {
     constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), LANE = 16 / WB, HALVES = halves_of(FORM);
-    constexpr int XB = NT * HALVES, PIECES = DOWN ? 2 * XB : XB, STAGES = ring_stages(ALIGNED, PIECES);
-    constexpr int ROWS = DOWN ? 32 : 16;
+    constexpr int XB = NT * HALVES, PIECES = DOWN ? 2 * XB : XB, ROWS = DOWN ? 32 : 16;
+    using ExpertsRing = Ring<ALIGNED, PIECES, kBeside>;
     constexpr bool BF16 = is_bf16(FORM);
     extern __shared__ uint4 ring_smem[];
     __shared__ Routing routing;
@@ -317,12 +341,16 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     grid_dependency_wait();
     allow_dependent_launch();
     const int choices = p.M * p.top_k;
-    read_routing<8 * NT>(routing, p.experts, choices, p.E);
+    // the routing's arrays lie behind the rings
+    read_routing<8 * NT>(routing, reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(ring_smem) + kWarps * ExpertsRing::WARP_BYTES),
+                         p.experts, choices, p.E);
     const int64_t F = p.F, K = p.K, length = DOWN ? F : K, height = DOWN ? K : F;
-    const int blocks = static_cast<int>(DOWN ? (K + ROWS - 1) / ROWS : p.ldh / ROWS), units = routing.entries * blocks;
-    const int steps = static_cast<int>((length + STEP - 1) / STEP);
-    const int mine = (steps - warp + kWarps - 1) / kWarps;      // of a unit; may be none
-    const Claims claims{queue, p.counters + (DOWN ? 1 : 0), Claims::ahead_of(steps / kWarps, STAGES)};
+    // this warp's 32 rows of a unit, and its number among those that share them
+    const int split = kWarps / p.groups, group = warp / split, part_of = warp % split, unit_rows = ROWS * p.groups;
+    const int blocks = static_cast<int>(((DOWN ? K : p.ldh) + unit_rows - 1) / unit_rows), units = routing.entries * blocks;
+    const int steps = static_cast<int>((length + STEP - 1) / STEP), stride = split * STEP;
+    const int mine = (steps - part_of + split - 1) / split;     // of a unit; may be none
+    const Claims claims{queue, p.counters + (DOWN ? 1 : 0), Claims::ahead_of(steps / split, ExpertsRing::STAGES)};
     if (threadIdx.x == 0) claims.start();
     __syncthreads();
 
@@ -332,10 +360,10 @@ moe_experts_kernel(const __grid_constant__ Params p) {
         const uint8_t* at[kLoads];
         int left;
     };
-    const int row_bytes = static_cast<int>(length) * WB, offset = (warp * STEP + t * LANE) * WB;
+    const int row_bytes = static_cast<int>(length) * WB, offset = (part_of * STEP + t * LANE) * WB;
     const auto rows_of = [&](int u) {
         const int a = u / blocks;
-        const int64_t row0 = static_cast<int64_t>(u - a * blocks) * ROWS, first = routing.active[a] * height;
+        const int64_t row0 = static_cast<int64_t>(u - a * blocks) * unit_rows + group * ROWS, first = routing.active[a] * height;
         Rows r;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -345,7 +373,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
         r.left = row_bytes - offset;
         return r;
     };
-    Ring<ALIGNED, PIECES> ring(smem_u32(ring_smem) + warp * ring_bytes(ALIGNED, PIECES, 1));
+    ExpertsRing ring(smem_u32(ring_smem), warp);
     int next_i = 0, next_j = 0, next_entry = -1, next_count = 0;
     Rows next = {{p.w_down, p.w_down, p.w_down, p.w_down}, 0};
     const uint16_t* xp[NT];
@@ -365,7 +393,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
         for (int i = 0; i < NT; ++i) {
             // (columns past the entry's tokens are the first one's once more, and not looked at)
             const int choice = routing.list[warp][0][8 * i + g < next_count ? 8 * i + g : 0];
-            xp[i] = (DOWN ? p.h + choice * p.ldh : p.x + choice / p.top_k * p.ldx) + warp * STEP + t * LANE;
+            xp[i] = (DOWN ? p.h + choice * p.ldh : p.x + choice / p.top_k * p.ldx) + part_of * STEP + t * LANE;
         }
     };
     enter(claims.unit(0));
@@ -380,31 +408,31 @@ moe_experts_kernel(const __grid_constant__ Params p) {
                     ring.copy_token(i * HALVES + half, xp[i] + 8 * half);
                     if (DOWN) ring.copy_token(XB + i * HALVES + half, xp[i] + p.lo_offset + 8 * half);
                 }
-                xp[i] += kWarps * STEP;
+                xp[i] += stride;
             }
             if (++next_j == mine) {
                 next_j = 0;
                 enter(claims.unit(++next_i));
             } else {
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) next.at[i] += kWarps * STEP * WB;
-                next.left -= kWarps * STEP * WB;
+                for (int i = 0; i < kLoads; ++i) next.at[i] += stride * WB;
+                next.left -= stride * WB;
             }
         }
         ring.commit();
     };
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fill();
+    for (int i = 0; i < ExpertsRing::STAGES - 1; ++i) fill();
 
     // Down: the unit before's row block and the number of its arrival (thread 0's)
     int before = -1, arrival = 0;
     const auto add_choices = [&](int done) {
         if (done < 0) return;
         __threadfence();
-        const int64_t row0 = static_cast<int64_t>(done) * ROWS;
-        for (int i = threadIdx.x; i < p.M * ROWS; i += kWarps * 32) {
-            const int m = i / ROWS;
-            const int64_t row = row0 + i % ROWS;
+        const int64_t row0 = static_cast<int64_t>(done) * unit_rows;
+        for (int i = threadIdx.x; i < p.M * unit_rows; i += kWarps * 32) {
+            const int m = i / unit_rows;
+            const int64_t row = row0 + i % unit_rows;
             if (row >= K) continue;
             const float* from = p.partial + static_cast<int64_t>(m) * p.top_k * K + row;
             float sum = 0.0f;
@@ -420,11 +448,20 @@ moe_experts_kernel(const __grid_constant__ Params p) {
         if (u >= units) break;
         const int claimed = threadIdx.x == 0 ? claims.claim() : 0;
         const int a = u / blocks, block = u - a * blocks, expert = routing.active[a];
-        const int64_t row0 = static_cast<int64_t>(block) * ROWS;
+        const int64_t row0 = static_cast<int64_t>(block) * unit_rows;
         if (a != entry) {
             entry = a;
             count = list_tokens<8 * NT>(routing, list, a, choices);
             tiles = (count + 7) / 8;
+        }
+        if constexpr (is_i8(FORM)) {
+            // the join's scales, into L1 ahead of it
+            const int64_t row = row0 + threadIdx.x;
+            if (static_cast<int>(threadIdx.x) < unit_rows && row < height) {
+                const int64_t at = expert * height + row;
+                prefetch_l1((DOWN ? p.s_down : p.s_gate) + at);
+                if (!DOWN) prefetch_l1(p.s_up + at);
+            }
         }
         Rows rows = rows_of(u);
         float acc[NT][2][4];
@@ -438,7 +475,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
             uint32_t xv[PIECES][4];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) w[i] = ring.get(i, rows.at[i], rows.left);
-            rows.left -= kWarps * STEP * WB;
+            rows.left -= stride * WB;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i)
                 if (i % XB / HALVES < tiles) ring.get_token(i, xv[i]);
@@ -464,7 +501,8 @@ moe_experts_kernel(const __grid_constant__ Params p) {
             claims.put(i_unit, claimed);
             finished = before >= 0 && arrival == routing.entries - 1 ? before : -1;
         }
-        // join the warps' sums tile by tile; a thread finishes row r of token n (down: of half m)
+        // join the warps' sums tile by tile; a thread finishes row r of token n, of group m (gate
+        // and up) or of each group's half m (down)
         const int r = threadIdx.x / 8 % 16, n = threadIdx.x % 8, m = threadIdx.x / 128;
         int done = -1;
 #pragma unroll
@@ -477,22 +515,21 @@ moe_experts_kernel(const __grid_constant__ Params p) {
             }
             __syncthreads();
             done = finished;            // (written before this barrier, and not again before the next)
-            if (8 * i + n < count && (DOWN || m == 0)) {
+            for (int of = DOWN ? 0 : m; 8 * i + n < count && of < p.groups; of += DOWN ? 1 : 2) {
                 const int choice = list[8 * i + n];
-                float sum = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) sum += part[k][m][r][n];
+                const int64_t row = row0 + of * ROWS + (DOWN ? 16 * m : 0) + r;
+                float sum = 0.0f, up = 0.0f;
+                for (int k = of * split; k < (of + 1) * split; ++k) {
+                    sum += part[k][DOWN ? m : 0][r][n];
+                    if (!DOWN) up += part[k][1][r][n];
+                }
                 if constexpr (DOWN) {
-                    const int64_t row = row0 + 16 * m + r;
                     if (row < K) {
                         if constexpr (is_i8(FORM)) sum *= p.s_down[expert * K + row];
                         p.partial[choice * K + row] = sum;
                     }
-                } else {
-                    const int64_t row = row0 + r;
-                    float up = 0.0f, h = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < kWarps; ++k) up += part[k][1][r][n];
+                } else if (row < p.ldh) {
+                    float h = 0.0f;
                     if (row < F) {
                         if constexpr (is_i8(FORM)) {
                             sum *= p.s_gate[expert * F + row];
@@ -508,11 +545,14 @@ moe_experts_kernel(const __grid_constant__ Params p) {
                     out[p.lo_offset] = static_cast<uint16_t>(fused::pack16(fused::remainder16(h, kept), 0.0f, BF16));
                 }
             }
-            if (DOWN && i == tiles - 1) __threadfence();
             __syncthreads();
         }
         if (DOWN) {
-            if (threadIdx.x == 0) arrival = atomicAdd(p.counters + 2 + block, 1);
+            // (the barrier ordered the block's stores before this thread's fence)
+            if (threadIdx.x == 0) {
+                __threadfence();
+                arrival = atomicAdd(p.counters + 2 + block, 1);
+            }
             before = block;
             add_choices(done);
         }
@@ -630,18 +670,19 @@ int launch_route_tokens(const Call& c, const uint8_t* x, int M, int* experts, fl
                    : launch_route<BF16, ALIGNED, kRouteTokens>(c, x, M, experts, weights, ws, stream);
 }
 
-// How many blocks of a kernel fit the GPU at once; set up on the first call on a device.
+// How many blocks of a kernel fit the GPU at once, with `smem` bytes of the `most` it
+// may have; set up on the first call on a device.
 struct Fit {
     std::atomic<int> blocks[64] = {};
 };
 template <typename Kernel>
-int blocks_at_once(Fit& fit, Kernel kern, int smem, const DeviceInfo& info) {
+int blocks_at_once(Fit& fit, Kernel kern, int smem, int most, const DeviceInfo& info) {
     if (info.device < 0 || info.device >= 64) return 0;
     int n = fit.blocks[info.device].load(std::memory_order_relaxed);
     if (n == 0) {
         // concurrent first calls compute and store the same value
         int per_sm = 0;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWarps * 32, smem) != cudaSuccess || per_sm <= 0) {
             cudaGetLastError();
             return 0;
@@ -653,16 +694,24 @@ int blocks_at_once(Fit& fit, Kernel kern, int smem, const DeviceInfo& info) {
 }
 
 template <int FORM, bool ALIGNED, int NT, bool DOWN>
-int launch_experts(const Params& p, const DeviceInfo& info, cudaStream_t stream) {
-    constexpr int ring = ring_bytes(ALIGNED, (DOWN ? 2 : 1) * NT * halves_of(FORM), kWarps);
+int launch_experts(Params p, const DeviceInfo& info, cudaStream_t stream) {
+    constexpr int ring = kWarps * Ring<ALIGNED, (DOWN ? 2 : 1) * NT * halves_of(FORM), kBeside>::WARP_BYTES;
     const auto kern = moe_experts_kernel<FORM, ALIGNED, NT, DOWN>;
+    const int64_t choices = static_cast<int64_t>(p.M) * p.top_k;
     static Fit fit;
-    const int64_t fits = blocks_at_once(fit, kern, ring, info);
+    const int64_t fits = blocks_at_once(fit, kern, ring + routing_bytes(256), ring + routing_bytes(kTokens * kMaxTopK), info);
     if (fits == 0) return GEMM_ERR_LAUNCH;
     // the most entries that the routing can give
-    const int64_t choices = static_cast<int64_t>(p.M) * p.top_k, entries = (choices < p.E ? choices : p.E) + choices / (8 * NT);
-    const int64_t units = entries * (DOWN ? cdiv(p.K, 32) : p.ldh / 16);
-    return launched(launch_pdl(kern, dim3(static_cast<unsigned>(units < fits ? units : fits)), dim3(kWarps * 32), ring, stream, p));
+    const int64_t entries = (choices < p.E ? choices : p.E) + choices / (8 * NT);
+    const int64_t rows = DOWN ? p.K : p.ldh, steps = cdiv(DOWN ? p.F : p.K, step_k(FORM));
+    // units of 16 steps a warp, as long as every block has four of them (8 and 32 steps: 207 and 189
+    // against 191 us for 32 tokens over 32 experts of 2048 x 4096 in 8 bits, 378 and 394 against 380
+    // for 16 tokens over 56 of 1536 x 4096 in 16)
+    p.groups = 1;
+    while (p.groups < kWarps && steps * p.groups < 16 * kWarps && entries * cdiv(rows, 2 * p.groups * (DOWN ? 32 : 16)) >= 4 * fits) p.groups *= 2;
+    const int64_t units = entries * cdiv(rows, p.groups * (DOWN ? 32 : 16));
+    return launched(launch_pdl(kern, dim3(static_cast<unsigned>(units < fits ? units : fits)), dim3(kWarps * 32),
+                               ring + routing_bytes(static_cast<int>(choices)), stream, p));
 }
 
 // Two tiles where an expert has more than four tokens on average: one tile's ring
