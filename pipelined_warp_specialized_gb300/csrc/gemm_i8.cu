@@ -192,15 +192,21 @@ widen_kernel(const __grid_constant__ Widen p, int64_t K, int64_t ld) {
 
 // ---------------------------------------------------------------- few tokens
 
-// Up to kFewTokens rows of `a`: 32 rows of b at a time by a cluster of `ctas` CTAs,
+// A few rows of `a` (few_tokens): 32 rows of b at a time by a cluster of `ctas` CTAs,
 // whose warps take the steps of K in turn (few.cuh).  Bound by b's bytes.  A warp's fp32
 // sums are whole numbers and exact over 16 steps (1024 of K); they are added up
 // as integers in shared memory, whose order does not matter: the parts of a cluster
 // and of its warps are joined exactly.
-constexpr int kFewTokens = 64;
 constexpr int kFewRows32 = 32;
 constexpr int kFewWarps = 8;
 constexpr int kExactSteps = 16;
+// Up to 16 tokens, and up to 32 through matrices of up to 8 MB: with four token tiles a
+// warp's loads no longer run ahead of its multiplies (cold caches, 32 tokens: 35.5 us
+// through 16384 x 4096 where batch_kernel takes 29.7, 15.3 and 13.5 through 4096 x 4096),
+// but a small matrix ends before the other kernel's widened copy of the tokens, its
+// barriers and its longer epilogue pay (1024 x 8192 8.5 and 13.2 us, 4096 x 1024 6.1 and 8.6).
+constexpr int64_t kFewBytes = 8 << 20;
+bool few_tokens(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 32 && N * K <= kFewBytes); }
 // bytes of the warps' sums of NT tiles
 constexpr int few_columns(int tiles) { return kFewWarps * kFewRows32 * 8 * tiles * 4; }
 
@@ -380,9 +386,7 @@ int launch_few(FewParams p, const DeviceInfo& info, cudaStream_t stream) {
 template <bool ALIGNED>
 int launch_few_tiles(const FewParams& p, const DeviceInfo& info, cudaStream_t stream) {
     if (p.M <= 8) return launch_few<ALIGNED, 1>(p, info, stream);
-    if (p.M <= 16) return launch_few<ALIGNED, 2>(p, info, stream);
-    if (p.M <= 32) return launch_few<ALIGNED, 4>(p, info, stream);
-    return launch_few<ALIGNED, 8>(p, info, stream);
+    return p.M <= 16 ? launch_few<ALIGNED, 2>(p, info, stream) : launch_few<ALIGNED, 4>(p, info, stream);
 }
 
 // Rows of bytes at any address in rows ld apart (a multiple of 64), padded with
@@ -395,6 +399,376 @@ align_bytes_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, i
     if (i >= rows * chunks) return;
     const int64_t row = i / chunks, c = (i - row * chunks) * 16;
     *reinterpret_cast<uint4*>(dst + row * ld + c) = few::load_row<false, false>(src + row * K + c, K - c);
+}
+
+// ---------------------------------------------------------------- a batch of tokens
+
+// More tokens than registers hold and fewer than pay for widening b in memory: 128
+// rows of b are the tensor core's rows, up to NB tokens (binary16, widened before) its
+// columns.  Two groups of eight warps copy b's bytes to shared memory, widen them in
+// registers into the swizzled operand tiles of every other stage (two K blocks) and,
+// a chunk of 1024 of K behind, add the finished chunk's sums up in integers; one
+// thread copies the tokens, one multiplies.  A cluster's CTAs take a part of K each where
+// row tiles alone would not fill the GPU; integer sums are joined exactly.
+//
+// b's bytes bound it; it takes 2 to 3 times as long (cold caches, through 16384 x 4096: 32 tokens
+// 29.7 us, 64 30.3, 128 36.7, where b alone is 10; widening b in memory first takes 58 to 62).
+// One group of eight warps, whose copies, loads, fences and barriers of a stage follow one
+// another, took 1800 clocks a stage of 16 KB (32 tokens 33 us), and the issuing thread about
+// 400 a barrier, so a slot holds both K blocks of a stage.  The tokens have slots of their
+// own, more of them: a copy from L2 takes as long as two stages.  With b prefetched into
+// registers instead of shared memory 32 tokens take as long and 64 and 128 longer (35.3 and 43.2).
+constexpr int kBatchWarps = 16;
+constexpr int kBatchThreads = (kBatchWarps + 2) * 32;
+constexpr int kBatchRows = 128;
+constexpr int kStageBytes = kBatchRows * 128;           // of b, two K blocks
+constexpr int kStageChunk = kChunk / 2;                 // stages of a chunk
+constexpr int64_t kBatchTokens = 128;
+
+template <bool ALIGNED, int NB>
+struct Batch {
+    static constexpr int STAGE = kStageBytes + (ALIGNED ? 0 : kBatchRows * 16);     // (ragged: a row's last block)
+    static constexpr int STAGES = NB == 32 ? 3 : 2;                                 // of each group
+    static constexpr int TILES = 2 * kBatchRows * 128, TILE_SLOTS = NB == 128 ? 2 : 3;  // b's operand tiles of a stage
+    static constexpr int TOKENS = 2 * NB * 128;                                     // the tokens' of a stage
+    static constexpr int TOKEN_SLOTS = NB == 32 ? (ALIGNED ? 4 : 2) : NB == 64 ? (ALIGNED ? 4 : 3) : (ALIGNED ? 3 : 2);
+    static constexpr int OFF_TILES = (2 * STAGES * STAGE + 1023) / 1024 * 1024;
+    static constexpr int OFF_TOKENS = OFF_TILES + TILE_SLOTS * TILES;
+    static constexpr int OFF_BAR = OFF_TOKENS + TOKEN_SLOTS * TOKENS;
+    static constexpr int SMEM = OFF_BAR + 256 + 1024;                               // + slack to align the base to 1024
+    static_assert(SMEM <= SMEM_LIMIT, "shared memory");
+    static_assert(kBatchRows * NB * 4 <= OFF_BAR, "the sums fit where the copies were");
+};
+
+struct BatchParams {
+    const uint8_t* b;               // [N, K]
+    const float* a_scale;
+    const float* b_scale;
+    uint16_t* out;                  // [M, N]
+    int64_t N;
+    int M, K, ctas, bf16;
+    unsigned flags;
+    unsigned long long timeout_ns;
+    unsigned* status;
+};
+
+template <bool ALIGNED, int NB>
+__global__ void __launch_bounds__(kBatchThreads, 1)
+batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__ BatchParams p) {
+    using L = Batch<ALIGNED, NB>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* const gbase = smem_raw + (base - raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    // b's tiles' and the tokens' full and empty barriers, the accumulator's
+    const uint32_t bFULL = base + L::OFF_BAR, bEMPTY = bFULL + 8 * L::TILE_SLOTS;
+    const uint32_t tFULL = bEMPTY + 8 * L::TILE_SLOTS, tEMPTY = tFULL + 8 * L::TOKEN_SLOTS;
+    const uint32_t bTFULL = tEMPTY + 8 * L::TOKEN_SLOTS, bTEMPTY = bTFULL + 16;
+    const uint32_t bDRAIN = bTEMPTY + 16, sTMEM = bDRAIN + 8, sABORT = sTMEM + 4;
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + (sABORT - base));
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::TILE_SLOTS; ++s) {
+            mbar_init(bFULL + 8 * s, kBatchWarps / 2);
+            mbar_init(bEMPTY + 8 * s, 1);
+        }
+        for (int s = 0; s < L::TOKEN_SLOTS; ++s) {
+            mbar_init(tFULL + 8 * s, 1);
+            mbar_init(tEMPTY + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bTFULL + 8 * i, 1);
+            mbar_init(bTEMPTY + 8 * i, kBatchWarps);
+        }
+        mbar_init(bDRAIN, 1);
+        *abort_flag = 0u;
+        fence_mbar_init();
+        tma_prefetch_desc(&tokens);
+    }
+    if (warp == kBatchWarps + 1) {
+        tmem_alloc<1>(sTMEM, 512);
+        tmem_relinquish<1>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *reinterpret_cast<uint32_t*>(gbase + (sTMEM - base));
+    grid_dependency_wait();
+    allow_dependent_launch();
+
+    // this CTA's K blocks (an even number, but for the last part's) and stages of two
+    const int nkb = (p.K + BK - 1) / BK, per = ((nkb + p.ctas - 1) / p.ctas + 1) / 2 * 2;
+    const int kb0 = min(nkb, static_cast<int>(rank) * per), count = min(nkb - kb0, per);
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(p.ctas)) * kBatchRows;
+    const int stages = (count + 1) / 2, chunks = (stages + kStageChunk - 1) / kStageChunk;
+    int sums[NB / 4];
+#pragma unroll
+    for (int i = 0; i < NB / 4; ++i) sums[i] = 0;
+    bool ok = true;
+
+    if (warp < kBatchWarps) {
+        // ======================================================== copies and widening of b, sums
+        const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
+        const int group = warp / (kBatchWarps / 2), thread = threadIdx.x % (kBatchThreads / 2 - 32);
+        // a lane's piece j of a stage: 16 bytes at 16 c of K block j / 2, row r + 64 (j % 2)
+        const int c = lane % 4, r = thread / 4;
+        const int mine = (stages - group + 1) / 2;              // stages group, group + 2, ..
+        const uint32_t ring = base + group * (L::STAGES * L::STAGE);
+        const uint8_t* at[2];
+        int left = p.K - (kb0 + 2 * group) * BK - 16 * c;       // of a row, from piece 0 on
+#pragma unroll
+        for (int j = 0; j < 2; ++j) at[j] = p.b + min(row0 + r + 64 * j, p.N - 1) * p.K + (kb0 + 2 * group) * BK + 16 * c;
+        const int shift[2] = {static_cast<int>(reinterpret_cast<uintptr_t>(at[0]) & 15u), static_cast<int>(reinterpret_cast<uintptr_t>(at[1]) & 15u)};
+        int filled = 0, fill_stage = 0, read_stage = 0;
+        const auto fill = [&]() {
+            if (filled < mine) {
+                const uint32_t to = ring + fill_stage * L::STAGE + thread * 16;
+                if (ALIGNED && left > BK) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cp_async<16>(to + j * 4096, at[j % 2] + j / 2 * BK, 16u);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // (few.cuh's ragged rows: the lane after holds this one's second block, and the last of a
+                        // row's first K block finds it in the second)
+                        const int rest = left - j / 2 * BK, off = ALIGNED ? 0 : shift[j % 2];
+                        if (rest > -off) cp_async<16>(to + j * 4096, at[j % 2] + j / 2 * BK - off, 16u);
+                        if (!ALIGNED && j >= 2 && c == 3 && rest > 16 - off)
+                            cp_async<16>(ring + fill_stage * L::STAGE + kStageBytes + (r + 64 * (j % 2)) * 16, at[j % 2] + BK - off + 16, 16u);
+                    }
+                }
+                at[0] += 4 * BK;
+                at[1] += 4 * BK;
+                left -= 4 * BK;
+                ++filled;
+            }
+            cp_async_commit();
+            if (++fill_stage == L::STAGES) fill_stage = 0;
+        };
+        const int first_left = left;
+#pragma unroll
+        for (int i = 0; i < L::STAGES - 1; ++i) fill();
+
+        // the sums of chunk i: lane quarter warp % 4, quarter warp / 4 of the columns
+        const auto add_up = [&](int i) {
+            const int b = i & 1;
+            bool got = lane == 0 ? W.wait(bTFULL + 8 * b, (i >> 1) & 1) : true;
+            got = __shfl_sync(0xffffffffu, got, 0);
+            if (!got) return false;
+            tc_fence_after_sync();
+            const uint32_t from = tmem_base + (static_cast<uint32_t>(warp % 4 * 32) << 16) + b * 256 + warp / 4 * (NB / 4);
+#pragma unroll
+            for (int k = 0; k < NB / 4; k += 8) {
+                uint32_t v[8];
+                tmem_ld_32x32b_x8(from + k, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) sums[k + x] += __float2int_rn(__uint_as_float(v[x]));
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bTEMPTY + 8 * b);
+            return true;
+        };
+        for (int i = 0; ok && i < mine; ++i) {
+            const int st = 2 * i + group, slot = st % L::TILE_SLOTS;
+            cp_async_wait_group<L::STAGES - 2>();
+            bool got = lane == 0 ? W.wait(bEMPTY + 8 * slot, st / L::TILE_SLOTS & 1) : true;
+            got = __shfl_sync(0xffffffffu, got, 0);             // (and every lane's copies have landed)
+            if (!got) { ok = false; break; }
+            const uint32_t stage = ring + read_stage * L::STAGE, own = stage + thread * 16;
+            // (rows r and r + 1 of the lanes that store together differ in their swizzle's lowest bit: no two
+            // pieces of theirs share banks)
+            const uint32_t tile = base + L::OFF_TILES + slot * L::TILES + r * 128;
+            const uint32_t to[2] = {tile + ((2 * c ^ (r & 7)) << 4), tile + (((2 * c + 1) ^ (r & 7)) << 4)};
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ld_shared_v4(own + j * 4096, w[j].x, w[j].y, w[j].z, w[j].w);
+                if constexpr (!ALIGNED) {
+                    uint4 hi;
+                    ld_shared_v4(c < 3 ? own + j * 4096 + 16 : j < 2 ? own + (j + 2) * 4096 - 48 : stage + kStageBytes + (r + 64 * (j % 2)) * 16,
+                                 hi.x, hi.y, hi.z, hi.w);
+                    w[j] = few::shifted(w[j], hi, shift[j % 2]);
+                }
+            }
+            if (i == mine - 1) {
+                // (only K's last stage may end inside)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = few::cleared(w[j], first_left - i * 4 * BK - j / 2 * BK);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t v[4];
+                    few::widen<few::kI8Half>(w[j], half, v);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to[half] + j / 2 * (kBatchRows * 128) + j % 2 * 8192), "r"(v[0]),
+                                 "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                 : "memory");
+                }
+            fence_proxy_async_smem();
+            __syncwarp();               // (and ragged lanes have read their neighbours' blocks)
+            if (lane == 0) mbar_arrive(bFULL + 8 * slot);
+            if (++read_stage == L::STAGES) read_stage = 0;
+            fill();
+            // a chunk widened: the one before it has been multiplied, or soon
+            if ((i + 1) % (kStageChunk / 2) == 0 && i + 1 > kStageChunk / 2) ok = add_up((i + 1) / (kStageChunk / 2) - 2);
+        }
+        cp_async_wait_group<0>();
+        for (int i = max(0, mine / (kStageChunk / 2) - 1); ok && i < chunks; ++i) ok = add_up(i);
+    } else if (warp == kBatchWarps) {
+        // ======================================================== copies of the tokens
+        if (lane == 0) {
+            const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
+            for (int st = 0; st < stages; ++st) {
+                const int slot = st % L::TOKEN_SLOTS, pair = min(2, count - 2 * st);
+                if (!W.wait(tEMPTY + 8 * slot, st / L::TOKEN_SLOTS & 1)) { ok = false; break; }
+                mbar_arrive_expect_tx(tFULL + 8 * slot, pair * (L::TOKENS / 2));
+                for (int k = 0; k < pair; ++k)
+                    tma_load_2d(base + L::OFF_TOKENS + slot * L::TOKENS + k * (L::TOKENS / 2), &tokens, (kb0 + 2 * st + k) * BK, 0,
+                                tFULL + 8 * slot);
+            }
+            if (!ok) {
+                // copies in flight land within microseconds: a bounded millisecond outlasts them
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ======================================================== multiplies
+        if (lane == 0) {
+            const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleMma};
+            if (!(p.flags & GEMM_DEBUG_SKIP_EMPTY_SEED)) {
+                // every slot starts empty
+                for (int s = 0; s < L::TILE_SLOTS; ++s) mbar_arrive(bEMPTY + 8 * s);
+                for (int s = 0; s < L::TOKEN_SLOTS; ++s) mbar_arrive(tEMPTY + 8 * s);
+            }
+            const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NB >> 3) << 17) | (static_cast<uint32_t>(kBatchRows >> 4) << 24);
+            bool issued = false;
+            for (int st = 0; st < stages; ++st) {
+                const int i = st / kStageChunk, b = i & 1, pair = min(2, count - 2 * st);
+                const int slot = st % L::TILE_SLOTS, tslot = st % L::TOKEN_SLOTS;
+                const bool first = st % kStageChunk == 0;
+                // (the first two chunks' accumulators are free)
+                if (first && i >= 2 && !W.wait(bTEMPTY + 8 * b, (i / 2 - 1) & 1)) { ok = false; break; }
+                if (!W.wait(tFULL + 8 * tslot, st / L::TOKEN_SLOTS & 1)) { ok = false; break; }
+                if (!W.wait(bFULL + 8 * slot, st / L::TILE_SLOTS & 1)) { ok = false; break; }
+                tc_fence_after_sync();
+                for (int k = 0; k < pair; ++k) {
+                    const uint64_t ad = operand_desc(base + L::OFF_TILES + slot * L::TILES + k * kBatchRows * 128, false);
+                    const uint64_t bd = operand_desc(base + L::OFF_TOKENS + tslot * L::TOKENS + k * (L::TOKENS / 2), false);
+#pragma unroll
+                    for (int x = 0; x < BK / UMMA_K; ++x)
+                        tc_mma_f16<1>(tmem_base + b * 256, ad + x * k_step(false), bd + x * k_step(false), idesc, !first || k != 0 || x != 0);
+                }
+                issued = true;
+                tc_commit_1(bEMPTY + 8 * slot);
+                tc_commit_1(tEMPTY + 8 * tslot);
+                if (st == stages - 1 || st % kStageChunk == kStageChunk - 1) tc_commit_1(bTFULL + 8 * b);
+            }
+            if (issued) {
+                // all multiplies have finished before tensor memory is released
+                tc_commit_1(bDRAIN);
+                volatile uint32_t no_abort = 0;
+                const Waiter D{max(p.timeout_ns, kDrainNs), &no_abort, p.status, kStatusRoleMma};
+                D.wait(bDRAIN, 0);
+            }
+        }
+        __syncwarp();
+    }
+
+    // the sums, [NB][128], where the copies were
+    tc_fence_before_sync();
+    __syncthreads();
+    const bool alive = *abort_flag == 0u;
+    int* const shared_sums = reinterpret_cast<int*>(gbase);
+    if (warp < kBatchWarps) {
+        const int n = warp % 4 * 32 + lane, first = warp / 4 * (NB / 4);
+#pragma unroll
+        for (int i = 0; i < NB / 4; ++i) shared_sums[(first + i) * kBatchRows + n] = sums[i];
+    }
+    __syncthreads();
+    if (p.ctas > 1) cluster_sync();
+    // CTA r of a cluster takes every ctas-th token; a thread two rows of b side by side
+    const bool pairs = p.N % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3u) == 0;
+    for (int i = threadIdx.x; alive && i < NB / p.ctas * (kBatchRows / 2); i += kBatchThreads) {
+        const int m = i / (kBatchRows / 2) * p.ctas + static_cast<int>(rank), n = i % (kBatchRows / 2) * 2;
+        if (m >= p.M || row0 + n >= p.N) continue;
+        const bool both = row0 + n + 1 < p.N;
+        int s0 = 0, s1 = 0;
+        const uint32_t from = smem_u32(shared_sums + m * kBatchRows + n);
+        for (int q = 0; q < p.ctas; ++q) {
+            const uint32_t remote = mapa_shared(from, q);
+            s0 += static_cast<int>(ld_relaxed_cluster_u32(remote));
+            s1 += static_cast<int>(ld_relaxed_cluster_u32(remote + 4));
+        }
+        const float sa = __ldg(p.a_scale + m), sb0 = __ldg(p.b_scale + row0 + n), sb1 = both ? __ldg(p.b_scale + row0 + n + 1) : 0.0f;
+        const uint32_t v = pack16(i8_value(s0, sa, sb0), i8_value(s1, sa, sb1), p.bf16);
+        uint16_t* to = p.out + (m) * p.N + row0 + n;
+        if (pairs) {
+            *reinterpret_cast<uint32_t*>(to) = v;
+        } else {
+            to[0] = static_cast<uint16_t>(v & 0xFFFFu);
+            if (both) to[1] = static_cast<uint16_t>(v >> 16);
+        }
+    }
+    __syncthreads();
+    if (p.ctas > 1) cluster_sync();             // (no CTA leaves while another reads its sums)
+    if (warp == kBatchWarps + 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem_base, 512);
+    }
+}
+
+template <bool ALIGNED, int NB>
+int launch_batch(const CUtensorMap& tokens, BatchParams p, const DeviceInfo& info, cudaStream_t stream) {
+    const auto kern = batch_kernel<ALIGNED, NB>;
+    constexpr int smem = Batch<ALIGNED, NB>::SMEM;
+    static std::atomic<bool> ready[64] = {};
+    if (info.device < 0 || info.device >= 64) return GEMM_ERR_LAUNCH;
+    if (!ready[info.device].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        ready[info.device].store(true, std::memory_order_relaxed);
+    }
+    const int64_t tiles = cdiv(p.N, kBatchRows);
+    int ctas = 1;
+    while (ctas < 8 && 2 * ctas * tiles <= info.num_sms && p.K >= 2 * ctas * 4 * BK) ctas *= 2;
+    p.ctas = ctas;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1] = pdl_attribute();
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * ctas));
+    cfg.blockDim = dim3(kBatchThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, tokens, p) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+int batch_columns(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+template <bool ALIGNED>
+int launch_batch_columns(const CUtensorMap& tokens, const BatchParams& p, const DeviceInfo& info, cudaStream_t stream) {
+    switch (batch_columns(p.M)) {
+        case 32: return launch_batch<ALIGNED, 32>(tokens, p, info, stream);
+        case 64: return launch_batch<ALIGNED, 64>(tokens, p, info, stream);
+        default: return launch_batch<ALIGNED, 128>(tokens, p, info, stream);
+    }
 }
 
 // ---------------------------------------------------------------- product
@@ -415,6 +789,7 @@ bool rows16(const void* p, int64_t K) { return reinterpret_cast<uintptr_t>(p) % 
 
 struct Plan {
     bool few = false;               // a few tokens
+    bool batch = false;             // a batch of them
     uint8_t* few_a = nullptr;       // their aligned copy, where they need one
     Product pr;
     Layout l;
@@ -429,16 +804,21 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, const void* a, int num_sms, void* 
     Carver c;
     c.base = static_cast<char*>(ws);
     pl.ld = round_up(K, 64);
-    pl.few = M <= kFewTokens;
+    pl.few = few_tokens(M, N, K);
     if (pl.few) {
         if (!rows16(a, K)) pl.few_a = c.take<uint8_t>(M * pl.ld);
+        pl.bytes = c.used;
+        return pl;
+    }
+    pl.a = c.take<uint16_t>(M * pl.ld);
+    pl.batch = M <= kBatchTokens;
+    if (pl.batch) {
         pl.bytes = c.used;
         return pl;
     }
     pl.pr.M = M; pl.pr.N = N; pl.pr.K = K;
     pl.pr.chunk = kChunk;
     if (num_sms) pl.l = choose_layout(pl.pr, num_sms);
-    pl.a = c.take<uint16_t>(M * pl.ld);
     pl.b = c.take<uint16_t>(N * pl.ld);
     pl.bytes = c.used;
     return pl;
@@ -514,14 +894,23 @@ extern "C" int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, cons
     }
     const bool aligned = rows16(a, K) && rows16(b, K);
     {
-        const Widen w = {{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b)}, {pl.a, pl.b}, {M, N}};
-        int64_t blocks = cdiv((M + N) * cdiv(K, 16), 256);
+        // (a batch's b is widened on its way)
+        const int64_t rows_b = pl.batch ? 0 : N;
+        const Widen w = {{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b)}, {pl.a, pl.b}, {M, rows_b}};
+        int64_t blocks = cdiv((M + rows_b) * cdiv(K, 16), 256);
         if (blocks > (1 << 30)) blocks = 1 << 30;
-        if (launch_pdl(aligned ? widen_kernel<true> : widen_kernel<false>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+        if (launch_pdl((pl.batch ? rows16(a, K) : aligned) ? widen_kernel<true> : widen_kernel<false>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                        stream, w, K, pl.ld) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_LAUNCH;
         }
+    }
+    if (pl.batch) {
+        CUtensorMap tokens;
+        if (!encode_tmap_f16_2d(&tokens, pl.a, K, M, pl.ld * 2, BK, batch_columns(M))) return GEMM_ERR_LAUNCH;
+        const BatchParams p = {reinterpret_cast<const uint8_t*>(b), a_scale, b_scale, static_cast<uint16_t*>(out), N, static_cast<int>(M),
+                               static_cast<int>(K), 1, type == GEMM_TYPE_BFLOAT, debug_flags(), wait_timeout_ns(), status_word(info, stream)};
+        return rows16(b, K) ? launch_batch_columns<true>(tokens, p, info, stream) : launch_batch_columns<false>(tokens, p, info, stream);
     }
     Maps maps;
     memset(&maps, 0, sizeof(maps));

@@ -186,6 +186,20 @@ def test_i8(M, N, K, dtype):
         assert same_bits(pws.gemm_i8_nt(*ops, sa, sb, dtype=dtype), out)
 
 
+# a batch of tokens where its weights are large, small, split over a cluster and at the edges of tiles and chunks
+@pytest.mark.parametrize("M", [17, 24, 32, 33, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("N,K", [(1000, 8400), (4100, 2056), (20000, 449), (77, 130), (129, 64), (128, 3136), (333, 8193), (3, 5)])
+def test_i8_batches(M, N, K):
+    a, b = rand_i8((M, K), M), rand_i8((N, K), N)
+    sa, sb = rand((M,), torch.float32, 3).abs() * 0.02 + 0.001, rand((N,), torch.float32, 4).abs() * 0.02 + 0.001
+    want = i8_want(a, b, sa, sb)
+    out = pws.gemm_i8_nt(a, b, sa, sb, dtype=BF16)
+    i8_check(out, want, BF16)
+    assert same_bits(pws.gemm_i8_nt(a, off_by_one(b), sa, sb, dtype=BF16), out)
+    # a token's row is its own: alone and in the batch the same bits
+    assert same_bits(pws.gemm_i8_nt(a[M - 1:], b, sa[M - 1:], sb, dtype=BF16), out[M - 1:])
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 131071), (8, 33, 131071), (12, 33, 131071), (40, 24, 131071), (300, 300, 131071), (2, 64, 4096),
                                    (200, 64, 4096)])
 def test_i8_sums_are_exact(M, N, K):
@@ -500,6 +514,26 @@ def test_graph_replay_and_streams():
         torch.cuda.synchronize()
         for i, o in enumerate(outs):
             assert all(same_bits(a, b) for a, b in zip(o, want[i % 3]))
+
+
+def test_a_timed_out_wait_is_reported():
+    # slots that never become empty: every wait runs out, the call returns, the status word says so, and the
+    # next call is whole again
+    for M, N, K in ((40, 500, 4096), (24, 20000, 512), (128, 300, 1000), (300, 500, 1024)):
+        a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+        ones = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+        want = pws.gemm_i8_nt(a, b, *ones, dtype=BF16)
+        torch.cuda.synchronize()
+        pws.gemm_set_debug_flags(pws.GEMM_DEBUG_SKIP_EMPTY_SEED)
+        pws.gemm_set_wait_timeout_ns(20_000_000)
+        try:
+            pws.gemm_i8_nt(a, b, *ones, dtype=BF16)
+            assert pws.gemm_device_status() == pws.GEMM_ERR_TIMEOUT
+        finally:
+            pws.gemm_set_debug_flags(0)
+            pws.gemm_set_wait_timeout_ns(0)
+        assert same_bits(pws.gemm_i8_nt(a, b, *ones, dtype=BF16), want)
+        assert pws.gemm_device_status() == pws.GEMM_OK
 
 
 def test_stream_argument():
