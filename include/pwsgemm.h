@@ -507,7 +507,13 @@ int gemm_nt_bwd_workspace(int64_t M, int64_t N, int64_t K, const void* dy, const
  * An 8-bit matrix is int8 [rows, K], dense and row-major at any address, with a
  * float scale for each row: element (r, k) stands for scale[r] q[r][k].  A
  * token's activations and a weight's output channels are both rows of that form.
- * The conventions of the operators above hold, but for the types named here.
+ * The conventions of the operators above hold, but for the types named here, and
+ * gemm_moe_nt counts in its workspace: atomics hand out its work and tell which block
+ * is the last at a row, but the sums' order, and so every result, is fixed.  It waits
+ * for nothing on the device, and neither does gemm_i8_nt with a few tokens; for more,
+ * gemm_i8_nt's waits are bounded and heed GEMM_DEBUG_SKIP_EMPTY_SEED.
+ *
+ * These are calls of inference: they have no backward pass.
  */
 
 /*
@@ -539,8 +545,8 @@ int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, const int8_t* b
 int gemm_i8_nt_workspace(int64_t M, int64_t N, int64_t K, const int8_t* a, const int8_t* b, int type, int64_t* bytes);
 
 /*
- * gemm_moe_nt -- a mixture-of-experts layer, made for a few tokens (M up to 64
- * read each chosen expert's weights once; more are taken 64 at a time).
+ * gemm_moe_nt -- a mixture-of-experts layer, made for a few tokens: 64 at a time,
+ * each of which reads an expert's weights once for every 8 or 16 of its tokens.
  *
  *   x        : [M, K] of `type`         w_router : [E, K] of `type`
  *   w_gate, w_up : [E, F, K]            w_down   : [E, K, F]
@@ -553,7 +559,7 @@ int gemm_i8_nt_workspace(int64_t M, int64_t N, int64_t K, const int8_t* a, const
  *   y        : [M, K] of `type`, written:
  *              sum_j weights[j] (act(x . w_gate[e_j]^T) * (x . w_up[e_j]^T)) . w_down[e_j]^T
  *
- * 1 <= top_k <= E, E <= 1024, top_k <= 32.  A NaN logit counts as the largest;
+ * 1 <= top_k <= E, E <= 1024, top_k <= 32, and K and F at most 2^22.  A NaN logit counts as the largest;
  * a token's weights and output are then NaN.  Logits are summed to about twice
  * fp32's precision, so that near ones are taken in their true order.  The weighted
  * activations between the projections are held to twice 16 bits (in binary16:

@@ -306,7 +306,8 @@ def _not_recorded(name, backward, *tensors):
         import warnings
         _warned.add(name)
         warnings.warn(f"{name} is not recorded by autograd: its output carries no gradient although an operand "
-                      f"requires one; the gradients are those of {backward}", stacklevel=3)
+                      f"requires one; " + (f"the gradients are those of {backward}" if backward else "it has no backward pass"),
+                      stacklevel=3)
 
 
 def _act_code(name, act):
@@ -531,11 +532,13 @@ def gemm_i8_quantize(x, stream=None):
     127 x[i][k] / max |x[i]| (ties to even), so x is about scale[:, None] * q.  A row
     of zeros has scale 0; a row with an infinity or a NaN has scale NaN and q 0.
     Quantizes tokens before gemm_i8_nt, and weights once: rows are a product's
-    output channels (for gemm_moe_nt, of all experts: w.view(E * F, K)).
+    output channels (for gemm_moe_nt, of all experts: w.view(E * F, K)).  Not recorded
+    by autograd.
     """
     torch = _torch or _torch_module()
     name = "gemm_i8_quantize"
     code = _type_of(name, x)
+    _not_recorded(name, None, x)
     M, K = x.shape
     lib, device = load_library(), x.device
     s, here = _on(stream, device)
@@ -596,8 +599,8 @@ def gemm_moe_nt(x, w_router, w_gate, w_up, w_down, top_k, scales=None, act: str 
     their softmax probabilities, over the chosen experts with normalize, else over all;
     y[i] = sum_j weights[i,j] * w_down[e] @ (act(w_gate[e] @ x[i]) * (w_up[e] @ x[i])), e = experts[i,j].
 
-    Made for up to 64 tokens (more are taken 64 at a time); E <= 1024, top_k <= 32.
-    Not recorded by autograd, and without a backward pass.
+    Made for up to 64 tokens (more are taken 64 at a time); E <= 1024, top_k <= 32,
+    K and F at most 2^22.  Not recorded by autograd, and without a backward pass.
     """
     torch = _torch or _torch_module()
     name = "gemm_moe_nt"
@@ -620,6 +623,7 @@ def gemm_moe_nt(x, w_router, w_gate, w_up, w_down, top_k, scales=None, act: str 
             _dense(name, f"the scales of w_{what}", t, (E, cols), torch.float32, device)
         pg, pu, pd = (t.data_ptr() for t in scales)
     top_k = int(top_k)
+    _not_recorded(name, None, x, w_router, w_gate, w_up, w_down)
     lib = load_library()
     s, here = _on(stream, device)
     with here:

@@ -707,7 +707,7 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
         }
         const float sa = __ldg(p.a_scale + m), sb0 = __ldg(p.b_scale + row0 + n), sb1 = both ? __ldg(p.b_scale + row0 + n + 1) : 0.0f;
         const uint32_t v = pack16(i8_value(s0, sa, sb0), i8_value(s1, sa, sb1), p.bf16);
-        uint16_t* to = p.out + (m) * p.N + row0 + n;
+        uint16_t* to = p.out + m * p.N + row0 + n;
         if (pairs) {
             *reinterpret_cast<uint32_t*>(to) = v;
         } else {

@@ -536,6 +536,36 @@ def test_a_timed_out_wait_is_reported():
         assert pws.gemm_device_status() == pws.GEMM_OK
 
 
+def test_operands_that_require_a_gradient():
+    # the calls are not recorded: said once for each
+    x, wr, ws, _, _ = layer(2, 64, 32, 4, F16, False)
+    pws._warned.difference_update({"gemm_i8_quantize", "gemm_moe_nt"})
+    x.requires_grad_(True)
+    with pytest.warns(UserWarning, match="no backward pass"):
+        assert not pws.gemm_i8_quantize(x)[1].requires_grad
+    with pytest.warns(UserWarning, match="no backward pass"):
+        assert not pws.gemm_moe_nt(x, wr, *ws, 2)[0].requires_grad
+
+
+def test_more_tokens_than_a_pass_takes():
+    # each token's row is its own, in whichever pass of 64 it lies
+    x, wr, ws, scales, _ = layer(200, 136, 72, 5, BF16, True)
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, 3, scales=scales)
+    for rows in (slice(0, 64), slice(64, 128), slice(128, 192), slice(192, 200)):
+        got = pws.gemm_moe_nt(x[rows], wr, *ws, 3, scales=scales)
+        assert all(same_bits(a, b[rows]) for a, b in zip(got, (y, experts, weights)))
+
+
+def test_the_same_matrix_as_both_operands():
+    for M, K in ((7, 64), (40, 200), (200, 1030)):
+        a = rand_i8((M, K), M)
+        s = torch.rand(M, device="cuda") * 0.01
+        i8_check(pws.gemm_i8_nt(a, a, s, s), i8_want(a, a, s, s), BF16)
+    x, wr, ws, _, _ = layer(5, 96, 96, 4, F16, False)
+    y = pws.gemm_moe_nt(x, wr, ws[0], ws[0], ws[0], 2)[0]
+    assert same_bits(y, pws.gemm_moe_nt(x, wr, ws[0], ws[0].clone(), ws[0].clone(), 2)[0])
+
+
 def test_stream_argument():
     s = torch.cuda.Stream()
     x, wr, ws, _, _ = layer(2, 64, 32, 4, F16, False)

@@ -84,6 +84,15 @@ def test_top_k_is_at_most_32(lib):
     assert lib.gemm_moe_nt(*swap(MOE, (3, 64), (4, 33))) == BAD
 
 
+def test_width_is_at_most_2_to_the_22(lib):
+    top, n = 1 << 22, ctypes.c_int64()
+    for i in (1, 2):
+        assert lib.gemm_moe_nt(*swap(MOE, (i, top + 1))) == BAD
+        sizes = swap([64, 16, 8, 1024, 32, H, H], (i, top))
+        assert lib.gemm_moe_nt_workspace(*sizes, ctypes.byref(n)) == OK and n.value > 0
+        assert lib.gemm_moe_nt_workspace(*swap(sizes, (i, top + 1)), ctypes.byref(n)) == BAD
+
+
 def test_empty_calls_are_no_ops(lib):
     assert lib.gemm_i8_quantize(*swap(QUANTIZE, (0, 0), (2, 0))) == OK
     assert lib.gemm_i8_nt(*swap(PRODUCT, (0, 0), (7, 0))) == OK
