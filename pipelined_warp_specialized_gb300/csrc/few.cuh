@@ -250,27 +250,29 @@ struct Ring {
 // for its slowest (SMs busy for 73 % of the kernel, 4.3 TB/s).  A block's first
 // unit is its number; later ones come from a counter that starts at zero.
 //
-// Rings run on into the next units, so a block knows `ahead` units beyond the one
-// at work: unit i + ahead + 1 is claimed at the start of unit i and put into
-// the queue before a barrier of unit i.  A warp with n steps a unit looks at
-// unit i + ahead + 1 when it copies the last step before it, which is in unit i + 1
-// or later if ahead * n >= the ring's stages.
+// Rings run on into the next unit, so a block knows one unit beyond the one at work:
+// unit i + 2 is claimed at the start of unit i and put into the queue before a
+// barrier of unit i.  A warp with n steps a unit looks at unit i + 2 when it copies the
+// last step before it, which is in unit i + 1 or later if n >= the ring's stages.  Shorter
+// units would have to be claimed several ahead, and the first blocks would leave
+// none to the others (7 tokens over 12 experts of 736 x 1024 37 us): they go round
+// the blocks in turn (27 us).
 struct Claims {
-    static constexpr int QUEUE = 16;
+    static constexpr int QUEUE = 4;
     int* queue;                 // [QUEUE], shared
     int* counter;
-    int ahead;
+    bool in_turn;
 
     // steps: the fewest a warp that has any takes of a unit
-    static __device__ __forceinline__ int ahead_of(int64_t steps, int stages) { return steps >= stages ? 1 : stages; }
-    __device__ __forceinline__ int claim() const { return static_cast<int>(gridDim.x) + atomicAdd(counter, 1); }
-    // One thread, before a barrier.
-    __device__ __forceinline__ void start() const {
-        queue[0] = static_cast<int>(blockIdx.x);
-        for (int i = 1; i <= ahead; ++i) queue[i] = claim();
+    static __device__ __forceinline__ bool too_short(int64_t steps, int stages) { return steps < stages; }
+    __device__ __forceinline__ int claim() const { return in_turn ? 0 : static_cast<int>(gridDim.x) + atomicAdd(counter, 1); }
+    // One thread, before a barrier: the first unit, the second, unit i + 2.
+    __device__ __forceinline__ void start() const { queue[0] = static_cast<int>(blockIdx.x); }
+    __device__ __forceinline__ void second(int unit) const { queue[1] = unit; }
+    __device__ __forceinline__ void put(int i, int unit) const { queue[(i + 2) % QUEUE] = unit; }
+    __device__ __forceinline__ int unit(int i) const {
+        return in_turn ? static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x) : queue[i % QUEUE];
     }
-    __device__ __forceinline__ void put(int i, int unit) const { queue[(i + ahead + 1) % QUEUE] = unit; }
-    __device__ __forceinline__ int unit(int i) const { return queue[i % QUEUE]; }
 };
 
 }  // namespace few

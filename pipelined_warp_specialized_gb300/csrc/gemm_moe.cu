@@ -267,7 +267,7 @@ __device__ __forceinline__ void read_routing(Routing& r, uint16_t* room, const i
     for (int i = threadIdx.x; i < (num_experts + 3) / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(r.tokens)[i] = 0u;
     __syncthreads();
     for (int i = threadIdx.x; i < choices; i += blockDim.x) {
-        const int e = experts[i];
+        const int e = __ldcg(experts + i);
         room[i] = static_cast<uint16_t>(e);
         // (a byte holds an expert's tokens: each of 64 at most once)
         atomicAdd(reinterpret_cast<uint32_t*>(r.tokens) + e / 4, 1u << (8 * (e % 4)));
@@ -340,8 +340,13 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     __shared__ __align__(16) float part[kWarps][2][16][8];      // (read and written in pairs)
     __shared__ int finished;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    grid_dependency_wait();
-    allow_dependent_launch();
+    // Down reads the routing while gate and up still run: they let it start after their own wait for
+    // the router, so its results are there (one token's layer 20.6 to 17.4 us, with the second unit's claim
+    // under way while the ring fills).  h' is read, and units are claimed, behind the wait alone.
+    if (!DOWN) {
+        grid_dependency_wait();
+        allow_dependent_launch();
+    }
     const int choices = p.M * p.top_k;
     // the routing's arrays lie behind the rings
     read_routing<8 * NT>(routing, reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(ring_smem) + kWarps * ExpertsRing::WARP_BYTES),
@@ -352,7 +357,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     const int blocks = static_cast<int>(((DOWN ? K : p.ldh) + unit_rows - 1) / unit_rows), units = routing.entries * blocks;
     const int steps = static_cast<int>((length + STEP - 1) / STEP), stride = split * STEP;
     const int mine = (steps - part_of + split - 1) / split;     // of a unit; may be none
-    const Claims claims{queue, p.counters + (DOWN ? 1 : 0), Claims::ahead_of(steps / split, ExpertsRing::STAGES)};
+    const Claims claims{queue, p.counters + (DOWN ? 1 : 0), Claims::too_short(steps / split, ExpertsRing::STAGES)};
     if (threadIdx.x == 0) claims.start();
     __syncthreads();
 
@@ -423,8 +428,15 @@ moe_experts_kernel(const __grid_constant__ Params p) {
         }
         ring.commit();
     };
+    if (DOWN) {
+        grid_dependency_wait();
+        allow_dependent_launch();
+    }
+    const int second = threadIdx.x == 0 ? claims.claim() : 0;
 #pragma unroll
     for (int i = 0; i < ExpertsRing::STAGES - 1; ++i) fill();
+    if (threadIdx.x == 0) claims.second(second);
+    __syncthreads();            // (if units are claimed, the first one fills the ring)
 
     // Down: the unit before's row block and the number of its arrival (thread 0's)
     int before = -1, arrival = 0;
