@@ -200,11 +200,12 @@ widen_kernel(const __grid_constant__ Widen p, int64_t K, int64_t ld) {
 constexpr int kFewRows32 = 32;
 constexpr int kFewWarps = 8;
 constexpr int kExactSteps = 16;
-// Up to 16 tokens, and up to 32 through matrices of up to 8 MB: with four token tiles a
-// warp's loads no longer run ahead of its multiplies (cold caches, 32 tokens: 35.5 us
-// through 16384 x 4096 where batch_kernel takes 29.7, 15.3 and 13.5 through 4096 x 4096),
-// but a small matrix ends before the other kernel's widened copy of the tokens, its
-// barriers and its longer epilogue pay (1024 x 8192 8.5 and 13.2 us, 4096 x 1024 6.1 and 8.6).
+// Up to 16 tokens (16384 x 4096, cold caches: 19.7 us, batch_kernel 22.9), and up to 32
+// through matrices of up to 8 MB: with four token tiles a warp's loads no longer run
+// ahead of its multiplies (32 tokens 35.5 us through 16384 x 4096 where batch_kernel
+// takes 23.1, 15.3 and 12.2 through 4096 x 4096), but a small matrix ends before the
+// other kernel's widened copy of the tokens, its barriers and its longer epilogue pay
+// (1024 x 8192 8.5 and 12.6 us, 4096 x 1024 6.1 and 8.4).
 constexpr int64_t kFewBytes = 8 << 20;
 bool few_tokens(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 32 && N * K <= kFewBytes); }
 // bytes of the warps' sums of NT tiles
@@ -405,39 +406,42 @@ align_bytes_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, i
 
 // More tokens than registers hold and fewer than pay for widening b in memory: 128
 // rows of b are the tensor core's rows, up to NB tokens (binary16, widened before) its
-// columns.  Two groups of eight warps copy b's bytes to shared memory, widen them in
-// registers into the swizzled operand tiles of every other stage (two K blocks) and,
-// a chunk of 1024 of K behind, add the finished chunk's sums up in integers; one
-// thread copies the tokens, one multiplies.  A cluster's CTAs take a part of K each where
-// row tiles alone would not fill the GPU; integer sums are joined exactly.
+// columns.  Two groups of eight warps take the stages (two K blocks) in turn: a warp
+// copies 32 rows of one K block through a ring of its own, then a lane widens a row in
+// registers and writes it into tensor memory, where the multiply takes its left operand.
+// One thread copies the tokens, and one for each group multiplies into accumulators of the
+// group's own; after 1024 of K all warps add their sums up in integers.  A cluster's
+// CTAs take a part of K each where row tiles alone would not fill the GPU; integer sums
+// are joined exactly.
 //
-// b's bytes bound it; it takes 2 to 3 times as long (cold caches, through 16384 x 4096: 32 tokens
-// 29.7 us, 64 30.3, 128 36.7, where b alone is 10; widening b in memory first takes 58 to 62).
-// One group of eight warps, whose copies, loads, fences and barriers of a stage follow one
-// another, took 1800 clocks a stage of 16 KB (32 tokens 33 us), and the issuing thread about
-// 400 a barrier, so a slot holds both K blocks of a stage.  The tokens have slots of their
-// own, more of them: a copy from L2 takes as long as two stages.  With b prefetched into
-// registers instead of shared memory 32 tokens take as long and 64 and 128 longer (35.3 and 43.2).
+// b's bytes bound it; it takes about twice as long (cold caches, through 16384 x 4096: 32
+// tokens 23.1 us, 64 24.7, 128 31.4, where b alone is 10; widening b in memory first takes 58
+// to 62).  8 us are the tokens' widening, the prologue and the joining of sums.  Of the rest the
+// issue of multiplies and barriers is the most: a thread takes some 50 clocks a multiply and 100 or
+// more for each wait or commit, 1300 a stage, so with one for both groups 32 tokens took 30.1 us
+// wherever b was widened to (tensor or shared memory), with an arrival for each K block 33.
 constexpr int kBatchWarps = 16;
-constexpr int kBatchThreads = (kBatchWarps + 2) * 32;
+constexpr int kBatchThreads = (kBatchWarps + 3) * 32;
 constexpr int kBatchRows = 128;
-constexpr int kStageBytes = kBatchRows * 128;           // of b, two K blocks
-constexpr int kStageChunk = kChunk / 2;                 // stages of a chunk
+constexpr int kStageChunk = kChunk / 2;                 // stages of a chunk, of one group's
 constexpr int64_t kBatchTokens = 128;
 
 template <bool ALIGNED, int NB>
 struct Batch {
-    static constexpr int STAGE = kStageBytes + (ALIGNED ? 0 : kBatchRows * 16);     // (ragged: a row's last block)
-    static constexpr int STAGES = NB == 32 ? 3 : 2;                                 // of each group
-    static constexpr int TILES = 2 * kBatchRows * 128, TILE_SLOTS = NB == 128 ? 2 : 3;  // b's operand tiles of a stage
+    static constexpr int PIECE = 32 * 64 + (ALIGNED ? 0 : 32 * 16);                 // a warp's of a stage (ragged: a row's last block)
+    static constexpr int STAGES = NB == 128 && !ALIGNED ? 3 : ALIGNED && NB < 128 ? 5 : 4;  // of each warp
+    static constexpr int TILE_SLOTS = 4;                                            // b's operand tiles of a stage, in tensor memory
     static constexpr int TOKENS = 2 * NB * 128;                                     // the tokens' of a stage
-    static constexpr int TOKEN_SLOTS = NB == 32 ? (ALIGNED ? 4 : 2) : NB == 64 ? (ALIGNED ? 4 : 3) : (ALIGNED ? 3 : 2);
-    static constexpr int OFF_TILES = (2 * STAGES * STAGE + 1023) / 1024 * 1024;
-    static constexpr int OFF_TOKENS = OFF_TILES + TILE_SLOTS * TILES;
+    static constexpr int TOKEN_SLOTS = NB == 128 ? 3 : 4;
+    static constexpr int OFF_TOKENS = (kBatchWarps * STAGES * PIECE + 1023) / 1024 * 1024;
     static constexpr int OFF_BAR = OFF_TOKENS + TOKEN_SLOTS * TOKENS;
     static constexpr int SMEM = OFF_BAR + 256 + 1024;                               // + slack to align the base to 1024
     static_assert(SMEM <= SMEM_LIMIT, "shared memory");
     static_assert(kBatchRows * NB * 4 <= OFF_BAR, "the sums fit where the copies were");
+    // tensor memory: each group's accumulators, one or two in 128 columns, then the tiles, 64 columns each
+    static constexpr int BUFFERS = NB == 128 ? 1 : 2, TILES_AT = 256, TILE = 64;
+    static constexpr int acc(int group, int buffer) { return 128 * group + 64 * buffer; }
+    static_assert(TILES_AT + TILE_SLOTS * TILE <= 512 && NB * BUFFERS <= 128 && TILE_SLOTS % 2 == 0, "tensor memory");
 };
 
 struct BatchParams {
@@ -461,11 +465,11 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
     uint8_t* const gbase = smem_raw + (base - raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
-    // b's tiles' and the tokens' full and empty barriers, the accumulator's
+    // b's tiles' and the tokens' full and empty barriers, the accumulators' (buffer b of group g: b 2 + g)
     const uint32_t bFULL = base + L::OFF_BAR, bEMPTY = bFULL + 8 * L::TILE_SLOTS;
     const uint32_t tFULL = bEMPTY + 8 * L::TILE_SLOTS, tEMPTY = tFULL + 8 * L::TOKEN_SLOTS;
-    const uint32_t bTFULL = tEMPTY + 8 * L::TOKEN_SLOTS, bTEMPTY = bTFULL + 16;
-    const uint32_t bDRAIN = bTEMPTY + 16, sTMEM = bDRAIN + 8, sABORT = sTMEM + 4;
+    const uint32_t bTFULL = tEMPTY + 8 * L::TOKEN_SLOTS, bTEMPTY = bTFULL + 16 * L::BUFFERS;
+    const uint32_t bDRAIN = bTEMPTY + 16 * L::BUFFERS, sTMEM = bDRAIN + 16, sABORT = sTMEM + 4;
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + (sABORT - base));
 
     if (threadIdx.x == 0) {
@@ -477,11 +481,11 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
             mbar_init(tFULL + 8 * s, 1);
             mbar_init(tEMPTY + 8 * s, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2 * L::BUFFERS; ++i) {
             mbar_init(bTFULL + 8 * i, 1);
             mbar_init(bTEMPTY + 8 * i, kBatchWarps);
         }
-        mbar_init(bDRAIN, 1);
+        for (int g = 0; g < 2; ++g) mbar_init(bDRAIN + 8 * g, 1);
         *abort_flag = 0u;
         fence_mbar_init();
         tma_prefetch_desc(&tokens);
@@ -501,7 +505,9 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
     const int nkb = (p.K + BK - 1) / BK, per = ((nkb + p.ctas - 1) / p.ctas + 1) / 2 * 2;
     const int kb0 = min(nkb, static_cast<int>(rank) * per), count = min(nkb - kb0, per);
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(p.ctas)) * kBatchRows;
-    const int stages = (count + 1) / 2, chunks = (stages + kStageChunk - 1) / kStageChunk;
+    const int stages = (count + 1) / 2;
+    const auto stages_of = [&](int group) { return (stages - group + 1) / 2; };         // group, group + 2, ..
+    const auto chunks_of = [&](int group) { return (stages_of(group) + kStageChunk - 1) / kStageChunk; };
     int sums[NB / 4];
 #pragma unroll
     for (int i = 0; i < NB / 4; ++i) sums[i] = 0;
@@ -510,114 +516,109 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
     if (warp < kBatchWarps) {
         // ======================================================== copies and widening of b, sums
         const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
-        const int group = warp / (kBatchWarps / 2), thread = threadIdx.x % (kBatchThreads / 2 - 32);
-        // a lane's piece j of a stage: 16 bytes at 16 c of K block j / 2, row r + 64 (j % 2)
-        const int c = lane % 4, r = thread / 4;
-        const int mine = (stages - group + 1) / 2;              // stages group, group + 2, ..
-        const uint32_t ring = base + group * (L::STAGES * L::STAGE);
-        const uint8_t* at[2];
-        int left = p.K - (kb0 + 2 * group) * BK - 16 * c;       // of a row, from piece 0 on
+        // group warp / 8, K block warp / 4 % 2 of a stage, rows 32 (warp % 4) .. (the lanes this warp may write)
+        const int group = warp / (kBatchWarps / 2), block = warp / 4 % 2, rows = warp % 4 * 32;
+        // a lane copies 16 bytes at 16 c of rows r, r + 8, r + 16 and r + 24
+        const int c = lane % 4, r = lane / 4;
+        const int mine = stages_of(group);
+        const uint32_t ring = base + warp * (L::STAGES * L::PIECE);
+        const int k0 = (kb0 + 2 * group + block) * BK;          // of its first K block
+        const uint8_t* at[4];
+        int left = p.K - k0 - 16 * c;                           // of a row, from the lane's 16 bytes on
 #pragma unroll
-        for (int j = 0; j < 2; ++j) at[j] = p.b + min(row0 + r + 64 * j, p.N - 1) * p.K + (kb0 + 2 * group) * BK + 16 * c;
-        const int shift[2] = {static_cast<int>(reinterpret_cast<uintptr_t>(at[0]) & 15u), static_cast<int>(reinterpret_cast<uintptr_t>(at[1]) & 15u)};
+        for (int j = 0; j < 4; ++j) at[j] = p.b + min(row0 + rows + r + 8 * j, p.N - 1) * p.K + k0 + 16 * c;
+        // (blocks trade places in a row so that 32 lanes' reads of a row each, and a copy's writes, share no banks)
+        const auto place = [](int row, int block16) { return row * 64 + ((block16 ^ (row >> 1 & 3)) << 4); };
         int filled = 0, fill_stage = 0, read_stage = 0;
         const auto fill = [&]() {
             if (filled < mine) {
-                const uint32_t to = ring + fill_stage * L::STAGE + thread * 16;
-                if (ALIGNED && left > BK) {
+                const uint32_t to = ring + fill_stage * L::PIECE;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) cp_async<16>(to + j * 4096, at[j % 2] + j / 2 * BK, 16u);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // (few.cuh's ragged rows: the lane after holds this one's second block, and the last of a
-                        // row's first K block finds it in the second)
-                        const int rest = left - j / 2 * BK, off = ALIGNED ? 0 : shift[j % 2];
-                        if (rest > -off) cp_async<16>(to + j * 4096, at[j % 2] + j / 2 * BK - off, 16u);
-                        if (!ALIGNED && j >= 2 && c == 3 && rest > 16 - off)
-                            cp_async<16>(ring + fill_stage * L::STAGE + kStageBytes + (r + 64 * (j % 2)) * 16, at[j % 2] + BK - off + 16, 16u);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int off = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(at[j]) & 15u);
+                    // (few.cuh's ragged rows: blocks from the one below on, as far as they hold bytes of the row)
+                    if (left > -off) cp_async<16>(to + place(r + 8 * j, c), at[j] - off, 16u);
+                    if (!ALIGNED && c == 3 && left > 16 - off) cp_async<16>(to + 2048 + (r + 8 * j) * 16, at[j] - off + 16, 16u);
+                    at[j] += 4 * BK;
                 }
-                at[0] += 4 * BK;
-                at[1] += 4 * BK;
                 left -= 4 * BK;
                 ++filled;
             }
             cp_async_commit();
             if (++fill_stage == L::STAGES) fill_stage = 0;
         };
-        const int first_left = left;
+        // this lane's own row, as it is widened
+        int row_left = p.K - k0;
+        const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.b + min(row0 + rows + lane, p.N - 1) * p.K + k0) & 15u);
 #pragma unroll
         for (int i = 0; i < L::STAGES - 1; ++i) fill();
 
-        // the sums of chunk i: lane quarter warp % 4, quarter warp / 4 of the columns
+        // the sums of chunk i of both groups: lane quarter warp % 4, quarter warp / 4 of the columns
         const auto add_up = [&](int i) {
-            const int b = i & 1;
-            bool got = lane == 0 ? W.wait(bTFULL + 8 * b, (i >> 1) & 1) : true;
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got) return false;
-            tc_fence_after_sync();
-            const uint32_t from = tmem_base + (static_cast<uint32_t>(warp % 4 * 32) << 16) + b * 256 + warp / 4 * (NB / 4);
+            const int b = i % L::BUFFERS;
+            for (int g = 0; g < 2; ++g) {
+                if (i >= chunks_of(g)) continue;
+                bool got = lane == 0 ? W.wait(bTFULL + 8 * (2 * b + g), i / L::BUFFERS & 1) : true;
+                got = __shfl_sync(0xffffffffu, got, 0);
+                if (!got) return false;
+                tc_fence_after_sync();
+                const uint32_t from = tmem_base + (static_cast<uint32_t>(warp % 4 * 32) << 16) + L::acc(g, b) + warp / 4 * (NB / 4);
 #pragma unroll
-            for (int k = 0; k < NB / 4; k += 8) {
-                uint32_t v[8];
-                tmem_ld_32x32b_x8(from + k, v);
-                tmem_ld_wait();
+                for (int k = 0; k < NB / 4; k += 8) {
+                    uint32_t v[8];
+                    tmem_ld_32x32b_x8(from + k, v);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < 8; ++x) sums[k + x] += __float2int_rn(__uint_as_float(v[x]));
+                    for (int x = 0; x < 8; ++x) sums[k + x] += __float2int_rn(__uint_as_float(v[x]));
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bTEMPTY + 8 * (2 * b + g));
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bTEMPTY + 8 * b);
             return true;
         };
+        int added = 0;
         for (int i = 0; ok && i < mine; ++i) {
             const int st = 2 * i + group, slot = st % L::TILE_SLOTS;
             cp_async_wait_group<L::STAGES - 2>();
             bool got = lane == 0 ? W.wait(bEMPTY + 8 * slot, st / L::TILE_SLOTS & 1) : true;
-            got = __shfl_sync(0xffffffffu, got, 0);             // (and every lane's copies have landed)
+            got = __shfl_sync(0xffffffffu, got, 0);
+            __syncwarp();                                       // (every lane's copies have landed, and are seen)
             if (!got) { ok = false; break; }
-            const uint32_t stage = ring + read_stage * L::STAGE, own = stage + thread * 16;
-            // (rows r and r + 1 of the lanes that store together differ in their swizzle's lowest bit: no two
-            // pieces of theirs share banks)
-            const uint32_t tile = base + L::OFF_TILES + slot * L::TILES + r * 128;
-            const uint32_t to[2] = {tile + ((2 * c ^ (r & 7)) << 4), tile + (((2 * c + 1) ^ (r & 7)) << 4)};
-            uint4 w[4];
+            tc_fence_after_sync();
+            const uint32_t stage = ring + read_stage * L::PIECE;
+            uint32_t v[32];
+            uint4 w[ALIGNED ? 4 : 5];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                ld_shared_v4(own + j * 4096, w[j].x, w[j].y, w[j].z, w[j].w);
-                if constexpr (!ALIGNED) {
-                    uint4 hi;
-                    ld_shared_v4(c < 3 ? own + j * 4096 + 16 : j < 2 ? own + (j + 2) * 4096 - 48 : stage + kStageBytes + (r + 64 * (j % 2)) * 16,
-                                 hi.x, hi.y, hi.z, hi.w);
-                    w[j] = few::shifted(w[j], hi, shift[j % 2]);
-                }
-            }
-            if (i == mine - 1) {
-                // (only K's last stage may end inside)
+            for (int q = 0; q < 4; ++q) ld_shared_v4(stage + place(lane, q), w[q].x, w[q].y, w[q].z, w[q].w);
+            if constexpr (!ALIGNED) ld_shared_v4(stage + 2048 + lane * 16, w[4].x, w[4].y, w[4].z, w[4].w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = few::cleared(w[j], first_left - i * 4 * BK - j / 2 * BK);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int q = 0; q < 4; ++q) {
+                uint4 x = w[q];
+                if constexpr (!ALIGNED) x = few::shifted(x, w[q + 1], shift);
+                if (row_left < BK) x = few::cleared(x, row_left - 16 * q);      // (K's last block)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t v[4];
-                    few::widen<few::kI8Half>(w[j], half, v);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to[half] + j / 2 * (kBatchRows * 128) + j % 2 * 8192), "r"(v[0]),
-                                 "r"(v[1]), "r"(v[2]), "r"(v[3])
-                                 : "memory");
+                    uint32_t pairs[4];
+                    few::widen<few::kI8Half>(x, half, pairs);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[8 * q + 4 * half + k] = pairs[k];
                 }
-            fence_proxy_async_smem();
-            __syncwarp();               // (and ragged lanes have read their neighbours' blocks)
+            }
+            row_left -= 4 * BK;
+            tmem_st_32x32b_x32(tmem_base + (static_cast<uint32_t>(rows) << 16) + L::TILES_AT + slot * L::TILE + block * (L::TILE / 2), v);
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
             if (lane == 0) mbar_arrive(bFULL + 8 * slot);
             if (++read_stage == L::STAGES) read_stage = 0;
             fill();
-            // a chunk widened: the one before it has been multiplied, or soon
-            if ((i + 1) % (kStageChunk / 2) == 0 && i + 1 > kStageChunk / 2) ok = add_up((i + 1) / (kStageChunk / 2) - 2);
+            // a chunk widened: with two accumulators the one before it has been multiplied, or soon; with
+            // one the next cannot begin before this one's sums are taken
+            if ((i + 1) % kStageChunk == 0 && (i + 1) / kStageChunk >= L::BUFFERS) ok = add_up(added++);
         }
         cp_async_wait_group<0>();
-        for (int i = max(0, mine / (kStageChunk / 2) - 1); ok && i < chunks; ++i) ok = add_up(i);
+        for (; ok && added < chunks_of(0); ++added) ok = add_up(added);
     } else if (warp == kBatchWarps) {
         // ======================================================== copies of the tokens
         if (lane == 0) {
@@ -638,43 +639,46 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
         }
         __syncwarp();
     } else {
-        // ======================================================== multiplies
+        // ======================================================== multiplies, a warp each group's stages
+        const int group = warp - kBatchWarps - 1;
         if (lane == 0) {
             const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleMma};
-            if (!(p.flags & GEMM_DEBUG_SKIP_EMPTY_SEED)) {
+            if (group == 0 && !(p.flags & GEMM_DEBUG_SKIP_EMPTY_SEED)) {
                 // every slot starts empty
                 for (int s = 0; s < L::TILE_SLOTS; ++s) mbar_arrive(bEMPTY + 8 * s);
                 for (int s = 0; s < L::TOKEN_SLOTS; ++s) mbar_arrive(tEMPTY + 8 * s);
             }
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NB >> 3) << 17) | (static_cast<uint32_t>(kBatchRows >> 4) << 24);
+            const int mine = stages_of(group);
             bool issued = false;
-            for (int st = 0; st < stages; ++st) {
-                const int i = st / kStageChunk, b = i & 1, pair = min(2, count - 2 * st);
+            for (int i = 0; i < mine; ++i) {
+                const int st = 2 * i + group, chunk = i / kStageChunk, b = chunk % L::BUFFERS, pair = min(2, count - 2 * st);
                 const int slot = st % L::TILE_SLOTS, tslot = st % L::TOKEN_SLOTS;
-                const bool first = st % kStageChunk == 0;
-                // (the first two chunks' accumulators are free)
-                if (first && i >= 2 && !W.wait(bTEMPTY + 8 * b, (i / 2 - 1) & 1)) { ok = false; break; }
+                const bool first = i % kStageChunk == 0;
+                // (the first chunks' accumulators are free)
+                if (first && chunk >= L::BUFFERS && !W.wait(bTEMPTY + 8 * (2 * b + group), (chunk / L::BUFFERS - 1) & 1)) { ok = false; break; }
                 if (!W.wait(tFULL + 8 * tslot, st / L::TOKEN_SLOTS & 1)) { ok = false; break; }
                 if (!W.wait(bFULL + 8 * slot, st / L::TILE_SLOTS & 1)) { ok = false; break; }
                 tc_fence_after_sync();
                 for (int k = 0; k < pair; ++k) {
-                    const uint64_t ad = operand_desc(base + L::OFF_TILES + slot * L::TILES + k * kBatchRows * 128, false);
+                    const uint32_t ad = tmem_base + L::TILES_AT + slot * L::TILE + k * (L::TILE / 2);
                     const uint64_t bd = operand_desc(base + L::OFF_TOKENS + tslot * L::TOKENS + k * (L::TOKENS / 2), false);
 #pragma unroll
                     for (int x = 0; x < BK / UMMA_K; ++x)
-                        tc_mma_f16<1>(tmem_base + b * 256, ad + x * k_step(false), bd + x * k_step(false), idesc, !first || k != 0 || x != 0);
+                        tc_mma_f16_tmem_a(tmem_base + L::acc(group, b), ad + x * (UMMA_K / 2), bd + x * k_step(false), idesc,
+                                          !first || k != 0 || x != 0);
                 }
                 issued = true;
                 tc_commit_1(bEMPTY + 8 * slot);
                 tc_commit_1(tEMPTY + 8 * tslot);
-                if (st == stages - 1 || st % kStageChunk == kStageChunk - 1) tc_commit_1(bTFULL + 8 * b);
+                if (i == mine - 1 || i % kStageChunk == kStageChunk - 1) tc_commit_1(bTFULL + 8 * (2 * b + group));
             }
             if (issued) {
                 // all multiplies have finished before tensor memory is released
-                tc_commit_1(bDRAIN);
+                tc_commit_1(bDRAIN + 8 * group);
                 volatile uint32_t no_abort = 0;
                 const Waiter D{max(p.timeout_ns, kDrainNs), &no_abort, p.status, kStatusRoleMma};
-                D.wait(bDRAIN, 0);
+                D.wait(bDRAIN + 8 * group, 0);
             }
         }
         __syncwarp();
