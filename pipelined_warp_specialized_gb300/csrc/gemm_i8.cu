@@ -200,12 +200,12 @@ widen_kernel(const __grid_constant__ Widen p, int64_t K, int64_t ld) {
 constexpr int kFewRows32 = 32;
 constexpr int kFewWarps = 8;
 constexpr int kExactSteps = 16;
-// Up to 16 tokens (16384 x 4096, cold caches: 19.7 us, batch_kernel 22.9), and up to 32
+// Up to 16 tokens (16384 x 4096, cold caches: 19.7 us, batch_kernel 22.0), and up to 32
 // through matrices of up to 8 MB: with four token tiles a warp's loads no longer run
 // ahead of its multiplies (32 tokens 35.5 us through 16384 x 4096 where batch_kernel
-// takes 23.1, 15.3 and 12.2 through 4096 x 4096), but a small matrix ends before the
+// takes 22.5, 15.3 and 11.6 through 4096 x 4096), but a small matrix ends before the
 // other kernel's widened copy of the tokens, its barriers and its longer epilogue pay
-// (1024 x 8192 8.5 and 12.6 us, 4096 x 1024 6.1 and 8.4).
+// (1024 x 8192 8.4 and 11.1 us, 4096 x 1024 6.1 and 8.2).
 constexpr int64_t kFewBytes = 8 << 20;
 bool few_tokens(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 32 && N * K <= kFewBytes); }
 // bytes of the warps' sums of NT tiles
@@ -415,7 +415,7 @@ align_bytes_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, i
 // are joined exactly.
 //
 // b's bytes bound it; it takes about twice as long (cold caches, through 16384 x 4096: 32
-// tokens 23.1 us, 64 24.7, 128 31.4, where b alone is 10; widening b in memory first takes 58
+// tokens 22.5 us, 64 24.0, 128 30.3, where b alone is 10; widening b in memory first takes 58
 // to 62).  8 us are the tokens' widening, the prologue and the joining of sums.  Of the rest the
 // issue of multiplies and barriers is the most: a thread takes some 50 clocks a multiply and 100 or
 // more for each wait or commit, 1300 a stage, so with one for both groups 32 tokens took 30.1 us
@@ -498,8 +498,6 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *reinterpret_cast<uint32_t*>(gbase + (sTMEM - base));
-    grid_dependency_wait();
-    allow_dependent_launch();
 
     // this CTA's K blocks (an even number, but for the last part's) and stages of two
     const int nkb = (p.K + BK - 1) / BK, per = ((nkb + p.ctas - 1) / p.ctas + 1) / 2 * 2;
@@ -621,6 +619,10 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
         for (; ok && added < chunks_of(0); ++added) ok = add_up(added);
     } else if (warp == kBatchWarps) {
         // ======================================================== copies of the tokens
+        // The kernel before widens them; this one starts once that one's own wait is over, so b is
+        // there already, and only this warp waits.
+        grid_dependency_wait();
+        allow_dependent_launch();
         if (lane == 0) {
             const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
             for (int st = 0; st < stages; ++st) {
