@@ -566,6 +566,65 @@ def test_the_same_matrix_as_both_operands():
     assert same_bits(y, pws.gemm_moe_nt(x, wr, ws[0], ws[0].clone(), ws[0].clone(), 2)[0])
 
 
+def test_outputs_at_any_element():
+    # outputs one element past a 16-byte boundary: the same bits, and nothing beside them
+    lib, stream = pws.load_library(), torch.cuda.current_stream().cuda_stream
+    need = pws.ctypes.c_int64()
+    for M, N, K in ((3, 71, 100), (40, 130, 4096), (40, 131, 200), (200, 131, 128), (300, 256, 256)):
+        a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+        ones = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+        want = pws.gemm_i8_nt(a, b, *ones, dtype=BF16)
+        room = torch.full((M * N + 2,), 7.0, device="cuda", dtype=BF16)
+        assert lib.gemm_i8_nt_workspace(M, N, K, a.data_ptr(), b.data_ptr(), 1, pws.ctypes.byref(need)) == 0
+        ws = torch.empty(max(need.value, 1), dtype=torch.uint8, device="cuda")
+        assert lib.gemm_i8_nt(M, N, K, a.data_ptr(), b.data_ptr(), ones[0].data_ptr(), ones[1].data_ptr(), room[1:].data_ptr(), 1,
+                              ws.data_ptr(), need.value, stream) == 0
+        assert same_bits(room[1:-1].view(M, N), want) and room[0] == 7 and room[-1] == 7
+    for M, K, F, E, top_k in ((2, 71, 40, 4, 2), (70, 136, 72, 5, 3)):
+        x, wr, ws3, _, _ = layer(M, K, F, E, BF16, False)
+        want = pws.gemm_moe_nt(x, wr, *ws3, top_k)
+        y = torch.full((M * K + 2,), 7.0, device="cuda", dtype=BF16)
+        e, p = torch.full((M * top_k + 2,), 7, device="cuda", dtype=torch.int32), torch.full((M * top_k + 2,), 7.0, device="cuda")
+        assert lib.gemm_moe_nt_workspace(M, K, F, E, top_k, 1, 1, pws.ctypes.byref(need)) == 0
+        ws = torch.full((need.value + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+        assert lib.gemm_moe_nt(M, K, F, E, top_k, x.data_ptr(), wr.data_ptr(), *(w.data_ptr() for w in ws3), None, None, None,
+                               y[1:].data_ptr(), e[1:].data_ptr(), p[1:].data_ptr(), 1, 1, 0, 1, ws.data_ptr(), need.value, stream) == 0
+        for got, t in zip((y, e, p), want):
+            assert same_bits(got[1:-1].view(t.shape), t) and got[0] == 7 and got[-1] == 7
+        assert (ws[need.value:] == 0xFF).all()
+
+
+def test_weights_written_just_before_the_call():
+    # the weights' last writer is the kernel before the call, on the call's stream, captured and not
+    M, N, K = 24, 20000, 512
+    sides = [(rand_i8((M, K), i), rand_i8((N, K), 10 + i)) for i in range(2)]
+    ones = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    want = [pws.gemm_i8_nt(a, b, *ones) for a, b in sides]
+    x, wr, ws3, _, _ = layer(5, 512, 256, 6, BF16, False)
+    other = [w.flip(1).contiguous() for w in ws3]
+    want_y = [pws.gemm_moe_nt(x, wr, *w, 2)[0] for w in (ws3, other)]
+    a, b, held = sides[0][0].clone(), sides[0][1].clone(), [w.clone() for w in ws3]
+    source = [[t.clone() for t in (*side, *w)] for side, w in zip(sides, (ws3, other))]
+
+    def step(i):
+        for to, t in zip((a, b, *held), source[i]):
+            to.copy_(t)
+        return pws.gemm_i8_nt(a, b, *ones), pws.gemm_moe_nt(x, wr, *held, 2)[0]
+
+    graphs = []
+    for i in range(2):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, step(i)))
+    for turn in range(20):
+        i = turn % 2
+        got = step(i)
+        assert same_bits(got[0], want[i]) and same_bits(got[1], want_y[i])
+        graphs[i][0].replay()
+        assert same_bits(graphs[i][1][0], want[i]) and same_bits(graphs[i][1][1], want_y[i])
+
+
 def test_stream_argument():
     s = torch.cuda.Stream()
     x, wr, ws, _, _ = layer(2, 64, 32, 4, F16, False)
