@@ -625,6 +625,37 @@ def test_weights_written_just_before_the_call():
         assert same_bits(graphs[i][1][0], want[i]) and same_bits(graphs[i][1][1], want_y[i])
 
 
+def test_calls_from_several_threads():
+    import threading
+    sizes = [(1, 300, 512), (24, 20000, 512), (100, 260, 1030), (300, 512, 256)]
+    p = block(128, 96, 8, F16)
+    inputs = [(rand_i8((M, K), M), rand_i8((N, K), N), rand((3 + i, 128), F16, i)) for i, (M, N, K) in enumerate(sizes)]
+    ones = torch.ones(20000, device="cuda")
+
+    def step(a, b, x):
+        return (pws.gemm_i8_nt(a, b, ones[:a.shape[0]], ones[:b.shape[0]]),) + serve(x, p)
+
+    want = [step(*i) for i in inputs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    if not all(same_bits(g, w) for g, w in zip(step(*inputs[i]), want[i])):
+                        wrong.append(i)
+        except Exception as e:              # (a thread's exception is not the test's)
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_stream_argument():
     s = torch.cuda.Stream()
     x, wr, ws, _, _ = layer(2, 64, 32, 4, F16, False)
