@@ -317,6 +317,8 @@ def _act_code(name, act):
 
 
 def _vector(name, what, t, rows, dtype, device):
+    if t.dtype == dtype and t.shape == (rows,) and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != rows or not t.is_contiguous():
@@ -334,7 +336,7 @@ def _on(stream, device):
     that stream's memory and are not handed to other work while the call still
     uses them."""
     torch = _torch
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and torch._C._cuda_getDevice() == device.index:       # current_device(), of a context that is there
         return torch._C._cuda_getCurrentRawStream(device.index), _HERE      # current_stream() without its object
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(device))
@@ -515,6 +517,8 @@ def gemm_nt_bwd(dy, x, w, need_dx: bool = True, need_dw: bool = True, stream=Non
 
 
 def _dense(name, what, t, shape, dtype, device):
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -561,8 +565,9 @@ def gemm_i8_nt(a, b, a_scale, b_scale, dtype=None, stream=None):
     code = _codes.get(dtype)
     if code is None:
         raise TypeError(f"{name}: dtype must be float16 or bfloat16, got {dtype}")
+    int8 = torch.int8
     for t in (a, b):
-        if t.dtype != torch.int8:
+        if t.dtype != int8:
             raise TypeError(f"{name} takes int8 matrices, got {t.dtype}")
         if t.dim() != 2:
             raise ValueError(f"{name} takes matrices, got a tensor of shape {tuple(t.shape)}")
@@ -572,8 +577,8 @@ def gemm_i8_nt(a, b, a_scale, b_scale, dtype=None, stream=None):
     if b.device != device:
         raise ValueError(f"{name}: all tensors must be on one device, got {device} and {b.device}")
     M, K = a.shape
-    N = b.shape[0]
-    if b.shape[1] != K:
+    N, columns = b.shape
+    if columns != K:
         raise ValueError(f"{name}: shapes {tuple(a.shape)}, {tuple(b.shape)} do not form [M,K], [N,K]")
     _vector(name, "a_scale", a_scale, M, torch.float32, device)
     _vector(name, "b_scale", b_scale, N, torch.float32, device)

@@ -410,8 +410,8 @@ align_bytes_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, i
 // copies 32 rows of one K block through a ring of its own, then a lane widens a row in
 // registers and writes it into tensor memory, where the multiply takes its left operand.
 // One thread copies the tokens, and one for each group multiplies into accumulators of the
-// group's own; after 1024 of K all warps add their sums up in integers.  A cluster's
-// CTAs take a part of K each where row tiles alone would not fill the GPU; integer sums
+// group's own; after 1024 of K all warps add their sums up in integers.  More than 128
+// tokens are tiles of 128, each with CTAs of its own.  A cluster's CTAs take a part of K each where row tiles alone would not fill the GPU; integer sums
 // are joined exactly.
 //
 // b's bytes bound it; it takes about twice as long (cold caches, through 16384 x 4096: 32
@@ -424,7 +424,6 @@ constexpr int kBatchWarps = 16;
 constexpr int kBatchThreads = (kBatchWarps + 3) * 32;
 constexpr int kBatchRows = 128;
 constexpr int kStageChunk = kChunk / 2;                 // stages of a chunk, of one group's
-constexpr int64_t kBatchTokens = 128;
 
 template <bool ALIGNED, int NB>
 struct Batch {
@@ -450,7 +449,7 @@ struct BatchParams {
     const float* b_scale;
     uint16_t* out;                  // [M, N]
     int64_t N;
-    int M, K, ctas, bf16;
+    int M, K, ctas, bf16, token_tiles;
     unsigned flags;
     unsigned long long timeout_ns;
     unsigned* status;
@@ -502,7 +501,10 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
     // this CTA's K blocks (an even number, but for the last part's) and stages of two
     const int nkb = (p.K + BK - 1) / BK, per = ((nkb + p.ctas - 1) / p.ctas + 1) / 2 * 2;
     const int kb0 = min(nkb, static_cast<int>(rank) * per), count = min(nkb - kb0, per);
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(p.ctas)) * kBatchRows;
+    // (a row tile's token tiles lie side by side: its rows come from memory once)
+    const unsigned tile = blockIdx.x / static_cast<unsigned>(p.ctas), tiles = static_cast<unsigned>(p.token_tiles);
+    const int64_t row0 = static_cast<int64_t>(tile / tiles) * kBatchRows;
+    const int token0 = static_cast<int>(tile % tiles) * NB;
     const int stages = (count + 1) / 2;
     const auto stages_of = [&](int group) { return (stages - group + 1) / 2; };         // group, group + 2, ..
     const auto chunks_of = [&](int group) { return (stages_of(group) + kStageChunk - 1) / kStageChunk; };
@@ -630,7 +632,7 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
                 if (!W.wait(tEMPTY + 8 * slot, st / L::TOKEN_SLOTS & 1)) { ok = false; break; }
                 mbar_arrive_expect_tx(tFULL + 8 * slot, pair * (L::TOKENS / 2));
                 for (int k = 0; k < pair; ++k)
-                    tma_load_2d(base + L::OFF_TOKENS + slot * L::TOKENS + k * (L::TOKENS / 2), &tokens, (kb0 + 2 * st + k) * BK, 0,
+                    tma_load_2d(base + L::OFF_TOKENS + slot * L::TOKENS + k * (L::TOKENS / 2), &tokens, (kb0 + 2 * st + k) * BK, token0,
                                 tFULL + 8 * slot);
             }
             if (!ok) {
@@ -702,7 +704,7 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
     const bool pairs = p.N % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3u) == 0;
     for (int i = threadIdx.x; alive && i < NB / p.ctas * (kBatchRows / 2); i += kBatchThreads) {
         const int m = i / (kBatchRows / 2) * p.ctas + static_cast<int>(rank), n = i % (kBatchRows / 2) * 2;
-        if (m >= p.M || row0 + n >= p.N) continue;
+        if (token0 + m >= p.M || row0 + n >= p.N) continue;
         const bool both = row0 + n + 1 < p.N;
         int s0 = 0, s1 = 0;
         const uint32_t from = smem_u32(shared_sums + m * kBatchRows + n);
@@ -711,9 +713,9 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
             s0 += static_cast<int>(ld_relaxed_cluster_u32(remote));
             s1 += static_cast<int>(ld_relaxed_cluster_u32(remote + 4));
         }
-        const float sa = __ldg(p.a_scale + m), sb0 = __ldg(p.b_scale + row0 + n), sb1 = both ? __ldg(p.b_scale + row0 + n + 1) : 0.0f;
+        const float sa = __ldg(p.a_scale + token0 + m), sb0 = __ldg(p.b_scale + row0 + n), sb1 = both ? __ldg(p.b_scale + row0 + n + 1) : 0.0f;
         const uint32_t v = pack16(i8_value(s0, sa, sb0), i8_value(s1, sa, sb1), p.bf16);
-        uint16_t* to = p.out + m * p.N + row0 + n;
+        uint16_t* to = p.out + (token0 + m) * p.N + row0 + n;
         if (pairs) {
             *reinterpret_cast<uint32_t*>(to) = v;
         } else {
@@ -742,9 +744,13 @@ int launch_batch(const CUtensorMap& tokens, BatchParams p, const DeviceInfo& inf
         }
         ready[info.device].store(true, std::memory_order_relaxed);
     }
-    const int64_t tiles = cdiv(p.N, kBatchRows);
+    p.token_tiles = static_cast<int>(cdiv(p.M, NB));
+    const int64_t tiles = cdiv(p.N, kBatchRows) * p.token_tiles;
     int ctas = 1;
-    while (ctas < 8 && 2 * ctas * tiles <= info.num_sms && p.K >= 2 * ctas * 4 * BK) ctas *= 2;
+    // (clusters of four find places on 144 of 152 SMs, of eight on 120: with 16 of them a second round,
+    // 128 tokens through 2048 x 8192 29.6 us)
+    const auto places = [&](int n) { return n == 8 ? info.num_sms * 15 / 19 : n == 4 ? info.num_sms * 18 / 19 : info.num_sms; };
+    while (ctas < 8 && 2 * ctas * tiles <= places(2 * ctas) && p.K >= 2 * ctas * 4 * BK) ctas *= 2;
     p.ctas = ctas;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2] = {};
@@ -766,6 +772,13 @@ int launch_batch(const CUtensorMap& tokens, BatchParams p, const DeviceInfo& inf
     return GEMM_OK;
 }
 
+// Up to 256 tokens (16384 x 4096 53.9 us, widened in memory 65.2; 8192 x 1024 15.2 and 16.3),
+// and more while all tiles run at once and K is long enough for the widening to count (512
+// tokens through 4096 x 4096 28.6 and 30.6 us, through 2048 x 8192 29.1 and 44.5; 384 through
+// 8192 x 8192, more tiles than SMs, 89.0 and 80.2; 512 through 4096 x 1024 15.0 and 14.2).
+bool batch_tokens(int64_t M, int64_t N, int64_t K) {
+    return M <= 256 || (K >= 2048 && cdiv(N, kBatchRows) * cdiv(M, 128) <= 128);
+}
 int batch_columns(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 template <bool ALIGNED>
@@ -817,7 +830,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, const void* a, int num_sms, void* 
         return pl;
     }
     pl.a = c.take<uint16_t>(M * pl.ld);
-    pl.batch = M <= kBatchTokens;
+    pl.batch = batch_tokens(M, N, K);
     if (pl.batch) {
         pl.bytes = c.used;
         return pl;
@@ -915,7 +928,7 @@ extern "C" int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, cons
         CUtensorMap tokens;
         if (!encode_tmap_f16_2d(&tokens, pl.a, K, M, pl.ld * 2, BK, batch_columns(M))) return GEMM_ERR_LAUNCH;
         const BatchParams p = {reinterpret_cast<const uint8_t*>(b), a_scale, b_scale, static_cast<uint16_t*>(out), N, static_cast<int>(M),
-                               static_cast<int>(K), 1, type == GEMM_TYPE_BFLOAT, debug_flags(), wait_timeout_ns(), status_word(info, stream)};
+                               static_cast<int>(K), 1, type == GEMM_TYPE_BFLOAT, 1, debug_flags(), wait_timeout_ns(), status_word(info, stream)};
         return rows16(b, K) ? launch_batch_columns<true>(tokens, p, info, stream) : launch_batch_columns<false>(tokens, p, info, stream);
     }
     Maps maps;

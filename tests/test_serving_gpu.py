@@ -200,7 +200,18 @@ def test_i8_batches(M, N, K):
     assert same_bits(pws.gemm_i8_nt(a[M - 1:], b, sa[M - 1:], sb, dtype=BF16), out[M - 1:])
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 131071), (8, 33, 131071), (12, 33, 131071), (40, 24, 131071), (300, 300, 131071), (2, 64, 4096),
+# several tiles of tokens, the last one a few, and a count of tiles that leaves the batch's kernel
+@pytest.mark.parametrize("M,N,K", [(130, 20000, 100), (255, 129, 64), (256, 700, 8200), (257, 70, 2049), (513, 1030, 4100), (1000, 300, 2048),
+                                   (5000, 40, 2050), (300, 8000, 2050), (700, 3000, 2304)])
+def test_i8_token_tiles(M, N, K):
+    a, b = rand_i8((M, K), M), rand_i8((N, K), N)
+    sa, sb = rand((M,), torch.float32, 3).abs() * 0.02 + 0.001, rand((N,), torch.float32, 4).abs() * 0.02 + 0.001
+    out = pws.gemm_i8_nt(a, b, sa, sb, dtype=BF16)
+    i8_check(out, i8_want(a, b, sa, sb), BF16)
+    assert same_bits(pws.gemm_i8_nt(off_by_one(a), off_by_one(b), sa, sb, dtype=BF16), out)
+
+
+@pytest.mark.parametrize("M,N,K", [(2100, 1100, 131071), (1, 40, 131071), (8, 33, 131071), (12, 33, 131071), (40, 24, 131071), (300, 300, 131071), (2, 64, 4096),
                                    (200, 64, 4096)])
 def test_i8_sums_are_exact(M, N, K):
     """Sums near 2^31 that differ in their last bits: the difference of two of
