@@ -661,6 +661,9 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
                 const bool first = i % kStageChunk == 0;
                 // (the first chunks' accumulators are free)
                 if (first && chunk >= L::BUFFERS && !W.wait(bTEMPTY + 8 * (2 * b + group), (chunk / L::BUFFERS - 1) & 1)) { ok = false; break; }
+                // (an odd number of slots: the other group's stage was the slot's last one, and a parity alone would
+                // take this thread's own, two phases ago, for this one while the other's is on its way)
+                if (L::TOKEN_SLOTS % 2 && st >= L::TOKEN_SLOTS && !W.wait(tFULL + 8 * tslot, (st / L::TOKEN_SLOTS - 1) & 1)) { ok = false; break; }
                 if (!W.wait(tFULL + 8 * tslot, st / L::TOKEN_SLOTS & 1)) { ok = false; break; }
                 if (!W.wait(bFULL + 8 * slot, st / L::TILE_SLOTS & 1)) { ok = false; break; }
                 tc_fence_after_sync();

@@ -211,6 +211,24 @@ def test_i8_token_tiles(M, N, K):
     assert same_bits(pws.gemm_i8_nt(off_by_one(a), off_by_one(b), sa, sb, dtype=BF16), out)
 
 
+@pytest.mark.parametrize("M,N,K", [(5000, 40, 2050), (1000, 300, 4096), (128, 3000, 4096)])
+def test_i8_repeats(M, N, K):
+    """The same bits every time, whatever else keeps memory busy and the copies out of step."""
+    a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+    ones = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    want = (a.double() @ b.double().t()).bfloat16()
+    junk, side = torch.empty(1 << 26, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(100):
+        if i % 4 == 0:
+            with torch.cuda.stream(side):
+                junk.mul_(1.0)
+        outs.append(pws.gemm_i8_nt(a, b, *ones))
+    torch.cuda.synchronize()
+    assert all(same_bits(o, want) for o in outs)
+
+
 @pytest.mark.parametrize("M,N,K", [(2100, 1100, 131071), (1, 40, 131071), (8, 33, 131071), (12, 33, 131071), (40, 24, 131071), (300, 300, 131071), (2, 64, 4096),
                                    (200, 64, 4096)])
 def test_i8_sums_are_exact(M, N, K):
