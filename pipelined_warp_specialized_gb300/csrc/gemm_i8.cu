@@ -428,10 +428,13 @@ constexpr int kStageChunk = kChunk / 2;                 // stages of a chunk, of
 template <bool ALIGNED, int NB>
 struct Batch {
     static constexpr int PIECE = 32 * 64 + (ALIGNED ? 0 : 32 * 16);                 // a warp's of a stage (ragged: a row's last block)
-    static constexpr int STAGES = NB == 128 && !ALIGNED ? 3 : ALIGNED && NB < 128 ? 5 : 4;  // of each warp
+    static constexpr int STAGES = (NB == 128 ? 2 : 4) + (ALIGNED ? 1 : 0);            // of each warp
     static constexpr int TILE_SLOTS = 4;                                            // b's operand tiles of a stage, in tensor memory
     static constexpr int TOKENS = 2 * NB * 128;                                     // the tokens' of a stage
-    static constexpr int TOKEN_SLOTS = NB == 128 ? 3 : 4;
+    // (even numbers of slots: a group's thread then sees every phase of its slots' barriers; of one that the other
+    // group fills in between it would take a phase long past for the one that it waits for)
+    static constexpr int TOKEN_SLOTS = 4;
+    static_assert(TILE_SLOTS % 2 == 0 && TOKEN_SLOTS % 2 == 0, "a slot is one group's");
     static constexpr int OFF_TOKENS = (kBatchWarps * STAGES * PIECE + 1023) / 1024 * 1024;
     static constexpr int OFF_BAR = OFF_TOKENS + TOKEN_SLOTS * TOKENS;
     static constexpr int SMEM = OFF_BAR + 256 + 1024;                               // + slack to align the base to 1024
@@ -440,7 +443,7 @@ struct Batch {
     // tensor memory: each group's accumulators, one or two in 128 columns, then the tiles, 64 columns each
     static constexpr int BUFFERS = NB == 128 ? 1 : 2, TILES_AT = 256, TILE = 64;
     static constexpr int acc(int group, int buffer) { return 128 * group + 64 * buffer; }
-    static_assert(TILES_AT + TILE_SLOTS * TILE <= 512 && NB * BUFFERS <= 128 && TILE_SLOTS % 2 == 0, "tensor memory");
+    static_assert(TILES_AT + TILE_SLOTS * TILE <= 512 && NB * BUFFERS <= 128, "tensor memory");
 };
 
 struct BatchParams {
@@ -661,9 +664,6 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
                 const bool first = i % kStageChunk == 0;
                 // (the first chunks' accumulators are free)
                 if (first && chunk >= L::BUFFERS && !W.wait(bTEMPTY + 8 * (2 * b + group), (chunk / L::BUFFERS - 1) & 1)) { ok = false; break; }
-                // (an odd number of slots: the other group's stage was the slot's last one, and a parity alone would
-                // take this thread's own, two phases ago, for this one while the other's is on its way)
-                if (L::TOKEN_SLOTS % 2 && st >= L::TOKEN_SLOTS && !W.wait(tFULL + 8 * tslot, (st / L::TOKEN_SLOTS - 1) & 1)) { ok = false; break; }
                 if (!W.wait(tFULL + 8 * tslot, st / L::TOKEN_SLOTS & 1)) { ok = false; break; }
                 if (!W.wait(bFULL + 8 * slot, st / L::TILE_SLOTS & 1)) { ok = false; break; }
                 tc_fence_after_sync();
