@@ -697,3 +697,71 @@ def test_stream_argument():
     assert all(same_bits(a, b) for a, b in zip(got, want))
     assert same_bits(out, pws.gemm_i8_nt(q, q, sc, sc))
     assert pws.gemm_device_status(s) == pws.GEMM_OK
+
+
+# ---------------------------------------------------------------- as a served layer runs
+
+
+def moe_want_by_expert(x, wr, ws, scales, top_k, act, normalize, held):
+    """moe_want with an expert's tokens at once; held(h): how far h' may be from its value as it is held."""
+    xd = x.double()
+    M, K = x.shape
+    F = ws[0].shape[1]
+    z = xd @ wr.double().t()
+    order = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :top_k]
+    chosen = z.gather(1, order)
+    p = torch.exp(chosen - torch.logsumexp(chosen if normalize else z, dim=1, keepdim=True))
+    y, bound = torch.zeros_like(xd), torch.zeros_like(xd)
+    for e in order.unique().tolist():
+        token, slot = torch.nonzero(order == e, as_tuple=True)
+        wg, wu, wd = (w[e].double() if scales is None else w[e].double() * s[e].double()[:, None] for w, s in zip(ws, scales or ws))
+        xe, pe = xd[token], p[token, slot][:, None]
+        g, u = xe @ wg.t(), xe @ wu.t()
+        eg, eu = acc_error(K, xe.abs() @ wg.abs().t()), acc_error(K, xe.abs() @ wu.abs().t())
+        a = act64(g, act)
+        h = pe * a * u
+        # |act'| <= 1.13; act, p and the scales to 2^-19 relative together
+        eh = pe * (1.13 * eg * (u.abs() + eu) + a.abs() * eu) + 2.0 ** -19 * h.abs() + held(h)
+        size = h.abs() @ wd.abs().t()
+        y.index_add_(0, token, h @ wd.t())
+        bound.index_add_(0, token, eh @ wd.abs().t() + acc_error(F, size) * 2)
+    return y, order.int(), p, bound + top_k * 2.0 ** -23 * y.abs()
+
+
+def held_in_two(dtype):
+    """h' as two 16-bit values, as in moe_want."""
+    return (lambda h: 2.0 ** -16 * h.abs()) if dtype == BF16 else (lambda h: 2.0 ** -22 * h.abs() + 2.0 ** -25)
+
+
+# More units of work than blocks, claimed or in turn: rings that run on over units, row blocks whose last entry another block
+# finished, 1 to 8 groups of rows a unit, one and two tiles of tokens, each in rows of whole 16 bytes and in ragged ones.
+# (The groups of 32 rows of a gate and of a down unit, on 152 SMs; an expert's tokens.)
+SERVED = [(1, 4096, 2048, 64, 6, False), (1, 4096, 2048, 64, 6, True),         # 1, 1; one
+          (16, 4096, 1536, 64, 8, False), (16, 4098, 1531, 64, 8, False),      # 1, 4; two
+          (16, 4096, 1536, 64, 8, True),                                       # 2, 8; two
+          (32, 4096, 2048, 32, 4, True), (32, 4099, 2050, 32, 4, True),        # 2, 4; four
+          (64, 4096, 128, 128, 8, False),                                      # 1, 8; four
+          (48, 1024, 1056, 64, 4, False), (48, 1022, 1058, 64, 4, False),      # 4, 2; three
+          (64, 2048, 4096, 8, 2, False), (64, 2050, 4100, 8, 2, False),        # 2, 1; sixteen, in tiles of two
+          (64, 2048, 4096, 8, 2, True), (64, 2050, 4100, 8, 2, True),          # 2 or 4, 1; the same
+          (64, 1000, 2049, 64, 8, True), (64, 4096, 512, 32, 8, False)]        # 8, 4 and 1, 4; eight and sixteen
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F,E,top_k,i8", SERVED)
+def test_moe_served(M, K, F, E, top_k, i8, dtype):
+    act, normalize = ("gelu" if E % 64 else "silu"), bool(M % 32)
+    x, wr, ws, scales = layer(M, K, F, E, dtype, i8)[:4]
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, top_k, scales=scales, act=act, normalize=normalize)
+    want, order, p, bound = moe_want_by_expert(x, wr, ws, scales, top_k, act, normalize, held_in_two(dtype))
+    assert torch.equal(experts, order) and ((weights.double() - p).abs() <= 2.0 ** -20 * p + 1e-30).all()
+    err = (y.double() - want).abs()
+    ok = err <= bound + half_unit(want.abs() + bound, dtype)
+    assert ok.all(), f"{int((~ok).sum())} off, worst {float((err / (bound + half_unit(want, dtype))).max()):.3f}"
+    # units finished in another order give the same bits
+    junk, side = torch.empty(1 << 26, device="cuda"), torch.cuda.Stream()
+    for i in range(6):
+        with torch.cuda.stream(side):
+            junk.mul_(1.0)
+        assert same_bits(pws.gemm_moe_nt(x, wr, *ws, top_k, scales=scales, act=act, normalize=normalize)[0], y)
+    torch.cuda.synchronize()
