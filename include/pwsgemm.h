@@ -561,9 +561,10 @@ int gemm_i8_nt_workspace(int64_t M, int64_t N, int64_t K, const int8_t* a, const
  *
  * 1 <= top_k <= E, E <= 1024, top_k <= 32, and K and F at most 2^22.  A NaN logit counts as the largest;
  * a token's weights and output are then NaN.  Logits are summed to about twice
- * fp32's precision, so that near ones are taken in their true order.  The weighted
- * activations between the projections are held to twice 16 bits (in binary16:
- * infinite above 131008, and to 2^-25 below its normal range).
+ * fp32's precision, so that near ones are taken in their true order.  The
+ * activations act(..) * (..) between the projections are held in fp32; the down
+ * projections multiply all of its bits by bfloat16 weights, and 22 of them by binary16
+ * and 8-bit ones, less what lies below 2^-39 of the largest of that token and expert.
  */
 int gemm_moe_nt(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k, const void* x, const void* w_router,
                 const void* w_gate, const void* w_up, const void* w_down, const float* s_gate, const float* s_up,

@@ -14,9 +14,15 @@
 // Rounding.  Sums are fp32.  The router's logits decide between experts, so
 // they are summed to twice fp32's precision: two experts whose logits differ by
 // fp32's own error would else be taken in an order that no definition gives.
-// h' = p act(g) u is held as two 16-bit values, its rounding and what that left
-// (the tensor cores multiply 16-bit values): 16 bits alone would add an error as
-// large as the output's own rounding.
+// h = act(g) u is held in fp32.  The tensor cores multiply 16-bit values, so the down
+// projections take it apart as they read it: for bfloat16 weights into three bfloat16
+// values, which are all of its 24 bits; for binary16 and 8-bit weights (8-bit integers
+// are binary16 values, whatever the tokens' type) into two binary16 values of
+// h times a power of two that brings the token's largest |h| to 2^14 .. 2^15: 22 bits, and
+// 2^-39 of that largest one, whatever the magnitudes.  The power and p are taken into
+// account in fp32 when sums are joined.
+#include <type_traits>
+
 #include "few.cuh"
 #include "product_host.cuh"
 
@@ -232,12 +238,13 @@ struct Params {
     const float* s_down;
     const int* experts;                 // [M, top_k]
     const float* weights;
-    uint16_t* h;                        // [2][M top_k][ldh]: h' rounded, and what that left
+    float* h;                           // [M top_k][ldh], each step's in the order of h_place
     uint16_t* y;                        // [M, K]
-    int64_t K, F, ldx, ldh, lo_offset;
-    int M, E, top_k, act;
+    int64_t K, F, ldx, ldh;
+    int M, E, top_k, act, bf16;         // bf16: the type of y
     int groups;                         // 32 rows a unit takes: 1, 2, 4 or 8
     int* counters;                      // claims of gate and of down units, then each row block's arrivals; zero at first
+    uint32_t* tops;                     // [M top_k], the bits of each choice's largest |h|; zero at first
     float* partial;                     // [M top_k][K]: each choice's part of y
 };
 
@@ -312,14 +319,59 @@ __device__ __forceinline__ int list_tokens(const Routing& r, uint16_t* list, int
     return min(n, SIZE);
 }
 
+// h in shared memory and on its way there.  A lane multiplies 8 consecutive elements of a token (few.cuh), which
+// are two 16-byte pieces of fp32; each piece of the four lanes of a token lies side by side, so that a copy's and a
+// read's 16 bytes a lane are 64 in a row.  Element k of a row:
+template <bool I8>
+__device__ __forceinline__ int64_t h_place(int64_t k) {
+    constexpr int LANE = I8 ? 16 : 8;
+    const int in = static_cast<int>(k) & (4 * LANE - 1);
+    return k - in + in % LANE / 4 * 16 + in / LANE * 4 + in % 4;
+}
+
+// The exponent field of the power of two that brings `top` (the bits of the largest |h|) to 2^14 .. 2^15.  A largest
+// one that is infinite or NaN gives kNoScale, 2^-114: what is finite beside it stays so, and the products are what
+// the infinity or NaN makes of them.
+constexpr uint32_t kNoScale = 268u - 255u;
+__device__ __forceinline__ uint32_t scale_bits(uint32_t top) { return min(268u - (top >> 23), 253u); }
+__device__ __forceinline__ float scale_of(uint32_t bits) { return __uint_as_float(bits << 23); }
+__device__ __forceinline__ float unscale_of(uint32_t bits) { return __uint_as_float((254u - bits) << 23); }
+
+// Eight elements of h as the pairs of 16-bit values the multiply takes, the largest parts first.
+constexpr int h_parts(bool bf16) { return bf16 ? 3 : 2; }
+template <bool BF16>
+__device__ __forceinline__ void take_apart(const uint32_t (&a)[4], const uint32_t (&b)[4], uint32_t scale, uint32_t (&v)[h_parts(BF16)][4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float f0 = __uint_as_float(j < 2 ? a[2 * j] : b[2 * j - 4]), f1 = __uint_as_float(j < 2 ? a[2 * j + 1] : b[2 * j - 3]);
+        if constexpr (BF16) {
+            // 8 bits, 8 more, and the 8 that are left: every difference is exact
+            const auto high = [](float f) { return __uint_as_float(__float_as_uint(f) & 0xFFFF0000u); };
+            const auto pair = [](float x, float y) { return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632); };
+            const float m0 = __fsub_rn(f0, high(f0)), m1 = __fsub_rn(f1, high(f1));
+            const float l0 = __fsub_rn(m0, high(m0)), l1 = __fsub_rn(m1, high(m1));
+            // (an infinity has no rest: inf - inf would make it NaN)
+            const bool finite = scale != kNoScale;
+            v[0][j] = pair(f0, f1);
+            v[1][j] = finite ? pair(m0, m1) : 0u;
+            v[2][j] = finite ? pair(l0, l1) : 0u;
+        } else {
+            const float s = scale_of(scale), g0 = f0 * s, g1 = f1 * s;
+            v[0][j] = fused::pack16(g0, g1, false);
+            const float2 kept = fused::unpack16(v[0][j], false);
+            v[1][j] = scale != kNoScale ? fused::pack16(__fsub_rn(g0, kept.x), __fsub_rn(g1, kept.y), false) : 0u;
+        }
+    }
+}
+
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 // One pass over the chosen experts' weights, 32 rows of an entry's at a time (a
 // unit): eight warps take the steps of the rows' length in turn, their sums are
 // joined in warp order, and a thread finishes a row of a token.
 //
-// Gate and up (DOWN false): 16 rows of F of each;  h' = p act(Wg x) (Wu x).
-// Down (DOWN true): 32 rows of K;  Wd h' of each choice, in fp32 to `partial`.  The
+// Gate and up (DOWN false): 16 rows of F of each;  h = act(Wg x) (Wu x), and each choice's largest |h|.
+// Down (DOWN true): 32 rows of K;  p Wd h of each choice, in fp32 to `partial`.  The
 // block that finishes the last of a row block's entries adds up every token's
 // choices in their order: y, whatever order the units were finished in.  The
 // arrival's number is looked at one unit later, so that nobody waits for it.
@@ -331,6 +383,7 @@ template <int FORM, bool ALIGNED, int NT, bool DOWN>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 moe_experts_kernel(const __grid_constant__ Params p) {
     constexpr int STEP = step_k(FORM), WB = weight_bytes(FORM), LANE = 16 / WB, HALVES = halves_of(FORM);
+    // (16-byte pieces of tokens: 8 elements of x are one, of h two)
     constexpr int XB = NT * HALVES, PIECES = DOWN ? 2 * XB : XB, ROWS = DOWN ? 32 : 16;
     using ExpertsRing = Ring<ALIGNED, PIECES, kBeside>;
     constexpr bool BF16 = is_bf16(FORM);
@@ -342,7 +395,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     // Down reads the routing while gate and up still run: they let it start after their own wait for
     // the router, so its results are there (one token's layer 20.6 to 17.4 us, with the second unit's claim
-    // under way while the ring fills).  h' is read, and units are claimed, behind the wait alone.
+    // under way while the ring fills).  h is read, and units are claimed, behind the wait alone.
     if (!DOWN) {
         grid_dependency_wait();
         allow_dependent_launch();
@@ -383,9 +436,10 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     ExpertsRing ring(smem_u32(ring_smem), warp);
     int next_i = 0, next_j = 0, next_entry = -1, next_count = 0;
     Rows next = {{p.w_down, p.w_down, p.w_down, p.w_down}, 0};
-    const uint16_t* xp[NT];
+    using Token = typename std::conditional<DOWN, float, uint16_t>::type;
+    const Token* xp[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xp[i] = p.x;
+    for (int i = 0; i < NT; ++i) xp[i] = nullptr;
     bool more = mine > 0;
     const auto enter = [&](int u) {
         more = more && u < units;
@@ -400,7 +454,10 @@ moe_experts_kernel(const __grid_constant__ Params p) {
         for (int i = 0; i < NT; ++i) {
             // (columns past the entry's tokens are the first one's once more, and not looked at)
             const int choice = routing.list[warp][0][8 * i + g < next_count ? 8 * i + g : 0];
-            xp[i] = (DOWN ? p.h + choice * p.ldh : p.x + choice / p.top_k * p.ldx) + part_of * STEP + t * LANE;
+            if constexpr (DOWN)
+                xp[i] = p.h + choice * p.ldh + part_of * STEP + t * 4;
+            else
+                xp[i] = p.x + choice / p.top_k * p.ldx + part_of * STEP + t * LANE;
         }
     };
     enter(claims.unit(0));
@@ -412,8 +469,13 @@ moe_experts_kernel(const __grid_constant__ Params p) {
                 if (8 * i >= next_count) break;
 #pragma unroll
                 for (int half = 0; half < HALVES; ++half) {
-                    ring.copy_token(i * HALVES + half, xp[i] + 8 * half);
-                    if (DOWN) ring.copy_token(XB + i * HALVES + half, xp[i] + p.lo_offset + 8 * half);
+                    const int piece = i * HALVES + half;
+                    if constexpr (DOWN) {
+                        ring.copy_token(2 * piece, xp[i] + 32 * half);
+                        ring.copy_token(2 * piece + 1, xp[i] + 32 * half + 16);
+                    } else {
+                        ring.copy_token(piece, xp[i] + 8 * half);
+                    }
                 }
                 xp[i] += stride;
             }
@@ -436,6 +498,11 @@ moe_experts_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int i = 0; i < ExpertsRing::STAGES - 1; ++i) fill();
     if (threadIdx.x == 0) claims.second(second);
+    if (DOWN && static_cast<int>(threadIdx.x) * 32 < choices) {
+        // what the units and their joins ask for of each choice, into L1
+        prefetch_l1(p.tops + threadIdx.x * 32);
+        prefetch_l1(p.weights + threadIdx.x * 32);
+    }
     __syncthreads();            // (if units are claimed, the first one fills the ring)
 
     // Down: the unit before's row block and the number of its arrival (thread 0's)
@@ -451,12 +518,15 @@ moe_experts_kernel(const __grid_constant__ Params p) {
             const float* from = p.partial + static_cast<int64_t>(m) * p.top_k * K + row;
             float sum = 0.0f;
             for (int j = 0; j < p.top_k; ++j) sum += __ldcg(from + j * K);
-            p.y[m * K + row] = static_cast<uint16_t>(fused::pack16(sum, 0.0f, BF16));
+            p.y[m * K + row] = static_cast<uint16_t>(fused::pack16(sum, 0.0f, p.bf16));
         }
     };
 
     int entry = -1, count = 0, tiles = 0;
     uint16_t* const list = routing.list[warp][1];
+    uint32_t scale[NT];                 // down: of the token this lane multiplies, of each tile
+#pragma unroll
+    for (int i = 0; i < NT; ++i) scale[i] = 0u;
     for (int i_unit = 0;; ++i_unit) {
         const int u = claims.unit(i_unit);
         if (u >= units) break;
@@ -467,6 +537,10 @@ moe_experts_kernel(const __grid_constant__ Params p) {
             entry = a;
             count = list_tokens<8 * NT>(routing, list, a, choices);
             tiles = (count + 7) / 8;
+            if (DOWN) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) scale[i] = scale_bits(p.tops[list[8 * i + g < count ? 8 * i + g : 0]]);
+            }
         }
         if constexpr (is_i8(FORM)) {
             // the join's scales, into L1 ahead of it
@@ -492,7 +566,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
             rows.left -= stride * WB;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i)
-                if (i % XB / HALVES < tiles) ring.get_token(i, xv[i]);
+                if (i / (PIECES / NT) < tiles) ring.get_token(i, xv[i]);
             ring.pop();
             fill();
 #pragma unroll
@@ -503,8 +577,16 @@ moe_experts_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if (i >= tiles) break;
+                    const int piece = i * HALVES + half;
+                    if constexpr (DOWN) {
+                        uint32_t h[h_parts(BF16)][4];
+                        take_apart<BF16>(xv[2 * piece], xv[2 * piece + 1], scale[i], h);
 #pragma unroll
-                    for (int piece = i * HALVES + half; piece < PIECES; piece += XB) {
+                        for (int k = 0; k < h_parts(BF16); ++k) {
+                            mma_step<BF16>(acc[i][0], v[0], v[1], h[k]);
+                            mma_step<BF16>(acc[i][1], v[2], v[3], h[k]);
+                        }
+                    } else {
                         mma_step<BF16>(acc[i][0], v[0], v[1], xv[piece]);
                         mma_step<BF16>(acc[i][1], v[2], v[3], xv[piece]);
                     }
@@ -529,6 +611,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
             }
             __syncthreads();
             done = finished;            // (written before this barrier, and not again before the next)
+            uint32_t top = 0u;          // bits of the largest |h| (magnitudes are ordered as their bits are, NaN above infinity)
             for (int of = DOWN ? 0 : m; 8 * i + n < count && of < p.groups; of += DOWN ? 1 : 2) {
                 const int choice = list[8 * i + n];
                 const int64_t row = row0 + of * ROWS + (DOWN ? 16 * m : 0) + r;
@@ -539,8 +622,10 @@ moe_experts_kernel(const __grid_constant__ Params p) {
                 }
                 if constexpr (DOWN) {
                     if (row < K) {
-                        if constexpr (is_i8(FORM)) sum *= p.s_down[expert * K + row];
-                        p.partial[choice * K + row] = sum;
+                        // (binary16: out of the scale's units, by the weights' scale first so that neither leaves fp32's range alone)
+                        float back = BF16 ? 1.0f : unscale_of(scale_bits(p.tops[choice]));
+                        if constexpr (is_i8(FORM)) back *= p.s_down[expert * K + row];
+                        p.partial[choice * K + row] = sum * p.weights[choice] * back;
                     }
                 } else if (row < p.ldh) {
                     float h = 0.0f;
@@ -549,15 +634,18 @@ moe_experts_kernel(const __grid_constant__ Params p) {
                             sum *= p.s_gate[expert * F + row];
                             up *= p.s_up[expert * F + row];
                         }
-                        h = p.weights[choice] * (fused::act_value(sum, p.act) * up);
+                        h = fused::act_value(sum, p.act) * up;
                     }
                     // (columns from F to the padded row's end are zeros)
-                    const uint32_t hi = fused::pack16(h, 0.0f, BF16);
-                    const float kept = fused::unpack16(hi, BF16).x;
-                    uint16_t* out = p.h + choice * p.ldh + row;
-                    out[0] = static_cast<uint16_t>(hi);
-                    out[p.lo_offset] = static_cast<uint16_t>(fused::pack16(fused::remainder16(h, kept), 0.0f, BF16));
+                    p.h[choice * p.ldh + h_place<is_i8(FORM)>(row)] = h;
+                    top = max(top, __float_as_uint(h) & 0x7FFFFFFFu);
                 }
+            }
+            if (!DOWN) {
+                // this warp's rows of each token
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                if (lane < 8 && top != 0u) atomicMax(p.tops + list[8 * i + lane], top);
             }
             __syncthreads();
         }
@@ -628,11 +716,12 @@ int64_t pass_tokens(int64_t M) { return M < kTokens ? M : kTokens; }
 int64_t ldh_of(int64_t F) { return round_up(F, 64); }
 struct Workspace {
     uint16_t* x = nullptr;
-    uint16_t* h = nullptr;
+    float* h = nullptr;
     int* counters = nullptr;
     float* partial = nullptr;
     size_t bytes = 0;
 };
+// the kernels' counters, and the choices' largest |h| behind them
 int64_t num_counters(int64_t K) { return 2 + cdiv(K, 32); }
 Workspace workspace_of(const Call& c, void* base) {
     Workspace w;
@@ -641,8 +730,8 @@ Workspace workspace_of(const Call& c, void* base) {
     carver.base = static_cast<char*>(base);
     const int64_t tokens = pass_tokens(c.M);
     w.x = carver.take<uint16_t>(tokens * ldh_of(c.K));
-    w.h = carver.take<uint16_t>(2 * tokens * c.top_k * ldh_of(c.F));
-    w.counters = carver.take<int>(num_counters(c.K));
+    w.h = carver.take<float>(tokens * c.top_k * ldh_of(c.F));
+    w.counters = carver.take<int>(num_counters(c.K) + tokens * c.top_k);
     w.partial = carver.take<float>(tokens * c.top_k * c.K);
     w.bytes = carver.used;
     return w;
@@ -667,7 +756,7 @@ template <bool BF16, bool ALIGNED, int TOKENS>
 int launch_route(const Call& c, const uint8_t* x, int M, int* experts, float* weights, const Workspace& ws, cudaStream_t stream) {
     constexpr int threads = route_threads(TOKENS);
     const int parts = route_parts(c.E, c.K, kRouteCtas * threads / 32);
-    Handover out = {ws.counters, ws.x, num_counters(c.K), ldh_of(c.K)};
+    Handover out = {ws.counters, ws.x, num_counters(c.K) + M * c.top_k, ldh_of(c.K)};
     if (!ws.counters) out.num_counters = 0;
     return launched(launch_pdl(moe_route_kernel<BF16, ALIGNED, TOKENS>, dim3(static_cast<unsigned>(cdiv(M, TOKENS) * kRouteCtas)),
                                dim3(threads), static_cast<size_t>(TOKENS) * c.E * parts * 8, stream, x,
@@ -728,24 +817,25 @@ int launch_experts(Params p, const DeviceInfo& info, cudaStream_t stream) {
 
 // Two tiles where an expert has more than four tokens on average: one tile's ring
 // leaves room for more blocks, two read a crowded expert's weights half as often.
-template <int FORM, bool ALIGNED>
-int launch_tiles(const Params& p, bool down, const DeviceInfo& info, cudaStream_t stream) {
-    if (p.M <= 8 || p.M * p.top_k <= 4 * p.E)
-        return down ? launch_experts<FORM, ALIGNED, 1, true>(p, info, stream) : launch_experts<FORM, ALIGNED, 1, false>(p, info, stream);
-    return down ? launch_experts<FORM, ALIGNED, 2, true>(p, info, stream) : launch_experts<FORM, ALIGNED, 2, false>(p, info, stream);
+template <int FORM, bool ALIGNED, bool DOWN>
+int launch_tiles(const Params& p, const DeviceInfo& info, cudaStream_t stream) {
+    if (p.M <= 8 || p.M * p.top_k <= 4 * p.E) return launch_experts<FORM, ALIGNED, 1, DOWN>(p, info, stream);
+    return launch_experts<FORM, ALIGNED, 2, DOWN>(p, info, stream);
 }
 
-template <int FORM>
-int launch_form(const Params& p, bool down, bool aligned, const DeviceInfo& info, cudaStream_t stream) {
-    return aligned ? launch_tiles<FORM, true>(p, down, info, stream) : launch_tiles<FORM, false>(p, down, info, stream);
+template <int FORM, bool DOWN>
+int launch_form(const Params& p, bool aligned, const DeviceInfo& info, cudaStream_t stream) {
+    return aligned ? launch_tiles<FORM, true, DOWN>(p, info, stream) : launch_tiles<FORM, false, DOWN>(p, info, stream);
 }
 
-int launch_kernel(const Params& p, int form, bool down, bool aligned, const DeviceInfo& info, cudaStream_t stream) {
+template <bool DOWN>
+int launch_kernel(const Params& p, int form, bool aligned, const DeviceInfo& info, cudaStream_t stream) {
     switch (form) {
-        case kHalf: return launch_form<kHalf>(p, down, aligned, info, stream);
-        case kBfloat: return launch_form<kBfloat>(p, down, aligned, info, stream);
-        case kI8Half: return launch_form<kI8Half>(p, down, aligned, info, stream);
-        default: return launch_form<kI8Bfloat>(p, down, aligned, info, stream);
+        case kHalf: return launch_form<kHalf, DOWN>(p, aligned, info, stream);
+        case kBfloat: return launch_form<kBfloat, DOWN>(p, aligned, info, stream);
+        case kI8Half: return launch_form<kI8Half, DOWN>(p, aligned, info, stream);
+        // (down's h is binary16 values beside 8-bit weights, whatever the tokens are)
+        default: return launch_form<DOWN ? kI8Half : kI8Bfloat, DOWN>(p, aligned, info, stream);
     }
 }
 
@@ -782,6 +872,8 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
     p.ldx = ldh_of(c.K);
     p.h = ws.h;
     p.counters = ws.counters;
+    p.tops = reinterpret_cast<uint32_t*>(ws.counters + num_counters(c.K));
+    p.bf16 = bf16;
     p.partial = ws.partial;
     p.K = c.K;
     p.F = c.F;
@@ -791,7 +883,6 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
     p.act = c.act;
     for (int64_t m = 0; m < c.M; m += kTokens) {
         p.M = static_cast<int>(c.M - m < kTokens ? c.M - m : kTokens);
-        p.lo_offset = static_cast<int64_t>(p.M) * c.top_k * p.ldh;
         const uint8_t* x = static_cast<const uint8_t*>(c.x) + m * c.K * 2;
         p.y = static_cast<uint16_t*>(c.y) + m * c.K;
         p.experts = c.experts + m * c.top_k;
@@ -810,8 +901,8 @@ int run(const Call& c, void* workspace, int64_t workspace_bytes, cudaStream_t st
             if (cudaMemsetAsync(p.y, 0, fused::bytes16(p.M, c.K), stream) != cudaSuccess) return GEMM_ERR_LAUNCH;
             continue;
         }
-        if ((rc = launch_kernel(p, form, false, gate_aligned, info, stream)) != GEMM_OK) return rc;
-        if ((rc = launch_kernel(p, form, true, down_aligned, info, stream)) != GEMM_OK) return rc;
+        if ((rc = launch_kernel<false>(p, form, gate_aligned, info, stream)) != GEMM_OK) return rc;
+        if ((rc = launch_kernel<true>(p, form, down_aligned, info, stream)) != GEMM_OK) return rc;
     }
     return GEMM_OK;
 }

@@ -724,7 +724,8 @@ def moe_want_by_expert(x, wr, ws, scales, top_k, act, normalize, held):
         eh = pe * (1.13 * eg * (u.abs() + eu) + a.abs() * eu) + 2.0 ** -19 * h.abs() + held(h)
         size = h.abs() @ wd.abs().t()
         y.index_add_(0, token, h @ wd.t())
-        bound.index_add_(0, token, eh @ wd.abs().t() + acc_error(F, size) * 2)
+        # (h is two or three 16-bit values, each with sums of its own)
+        bound.index_add_(0, token, eh @ wd.abs().t() + acc_error(F, size) * 3)
     return y, order.int(), p, bound + top_k * 2.0 ** -23 * y.abs()
 
 
@@ -765,3 +766,140 @@ def test_moe_served(M, K, F, E, top_k, i8, dtype):
             junk.mul_(1.0)
         assert same_bits(pws.gemm_moe_nt(x, wr, *ws, top_k, scales=scales, act=act, normalize=normalize)[0], y)
     torch.cuda.synchronize()
+
+
+def held_in_fp32(dtype, i8):
+    """h in fp32, then as three bfloat16 values (all 24 bits), or as two binary16 ones of a multiple whose largest magnitude is
+    2^14 or more: 11 bits, 11 bits of the rest, and half of binary16's smallest step, 2^-25."""
+    if dtype == BF16 and not i8:
+        return lambda h: 2.0 ** -24 * h.abs()
+    return lambda h: (2.0 ** -24 + 2.0 ** -22) * h.abs() + 2.0 ** -39 * h.abs().amax(dim=1, keepdim=True)
+
+
+def moe_in_range(x, wr, ws, scales, top_k, act, dtype):
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, top_k, scales=scales, act=act, normalize=False)
+    want, order, p, bound = moe_want_by_expert(x, wr, ws, scales, top_k, act, False, held_in_fp32(dtype, scales is not None))
+    assert torch.equal(experts, order)
+    assert torch.isfinite(want).all() and want.abs().max() < 60000 and want.abs().median() > (2.0 ** -13 if dtype == F16 else 0)
+    err = (y.double() - want).abs()
+    ok = err <= bound + half_unit(want.abs() + bound, dtype)
+    assert ok.all(), f"{int((~ok).sum())} of {ok.numel()} off, worst {float((err / (bound + half_unit(want, dtype))).max()):.3f}"
+    return want
+
+
+# what x is multiplied by, and what the 8-bit gate's and up's scales are: h from 1e-20 to 1e20
+@pytest.mark.parametrize("size,more", [(400.0, 1.0), (150.0, 1.0), (1e4, 1.0), (3e-3, 1.0), (1e-2, 1.0), (1e4, 1e6), (1e-2, 1e-8)])
+@pytest.mark.parametrize("M,F", [(3, 160), (6, 1024), (40, 96)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_moe_activations_of_any_size(M, F, size, more, dtype):
+    """y is off by its rounding and fp32's sums whatever the activations between the projections are: beyond binary16's largest
+    value, and below its smallest."""
+    K, E, top_k = 128, 6, 2
+    for i8 in (False, True):
+        if more != 1.0 and not i8:
+            continue
+        act = "gelu" if M % 2 else "silu"
+        x, wr, ws, scales, _ = layer(M, K, F, E, dtype, i8, seed=M)
+        x, wr = (x.float() * size).to(dtype), (wr.float() / size).to(dtype)
+        # g and u are about size * more; an activation below 1 is about half of g
+        h = (size * more) ** 2 * (1.0 if size * more > 1 else 0.5)
+        back = (100.0 if dtype == F16 else 1.0) / h
+        if i8:
+            scales = (scales[0] * more, scales[1] * more, scales[2] * back)
+        else:
+            ws[2] = (ws[2].float() * min(back, 2000.0)).to(dtype)
+        if not i8 and min(back, 2000.0) * h < 0.05:
+            continue
+        moe_in_range(x, wr, ws, scales, top_k, act, dtype)
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["16bit", "8bit"])
+def test_moe_activations_across_the_end_of_binary16(i8):
+    """One token, one expert, one column: h a little below and above 65504, 65520 and 131008."""
+    for h in (65000.0, 65504.0, 65519.0, 65520.0, 65536.0, 70000.0, 100000.0, 131000.0, 131008.0, 131072.0, 1e6, 2.6e8):       # (u itself is binary16: below 2^28)
+        K = 16
+        x = torch.zeros(1, K, device="cuda", dtype=F16)
+        x[0, 0], x[0, 1] = 64.0, 1.0
+        one = torch.zeros(1, 1, K, device="cuda", dtype=F16)
+        one[0, 0, 0] = 1.0                                          # g = 64: silu(64) is 64 to 2^-90
+        up = torch.zeros(1, 1, K, device="cuda", dtype=F16)
+        up[0, 0, 0] = h / 64 / 64                                   # u = 64 up
+        down = torch.full((1, K, 1), 2.0 ** -14, device="cuda", dtype=F16)
+        ws, scales = [one, up, down], None
+        if i8:
+            q = [pws.gemm_i8_quantize(w.view(-1, w.shape[2])) for w in ws]
+            ws, scales = [a.view(w.shape) for (a, _), w in zip(q, ws)], tuple(c.view(w.shape[:2]) for (_, c), w in zip(q, ws))
+        want = moe_in_range(x, torch.zeros(1, K, device="cuda", dtype=F16), ws, scales, 1, "silu", F16)
+        assert abs(float(want[0, 0]) / (h * 2.0 ** -14) - 1) < 0.01
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["16bit", "8bit"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_moe_activations_of_different_tokens(dtype, i8):
+    """Each token's activations are held by their own size: rows 2^30 apart in one call, each as when it is alone."""
+    M, K, F, E = 31, 64, 200, 4
+    x, wr, ws, scales, _ = layer(M, K, F, E, dtype, i8)
+    x = (x.float() * torch.exp2(torch.arange(M, device="cuda") / 2.0 - 7.0)[:, None]).to(dtype)
+    wr = (wr.float() / 16).to(dtype)
+    ws[2], scales = (ws[2], scales[:2] + (scales[2] / 64,)) if i8 else ((ws[2].float() / 64).to(dtype), None)
+    y, experts, _ = pws.gemm_moe_nt(x, wr, *ws, 2, scales=scales)
+    want, order, _, bound = moe_want_by_expert(x, wr, ws, scales, 2, "silu", True, held_in_fp32(dtype, i8))
+    assert torch.equal(experts, order)
+    assert ((y.double() - want).abs() <= bound + half_unit(want.abs() + bound, dtype)).all()
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["16bit", "8bit"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [1, 8, 40])
+def test_moe_activations_that_cancel(M, dtype, i8):
+    """h of two columns, a part in 2^12 apart, with weights of opposite sign: what is left shows to how many bits h is held."""
+    K = 8
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.zeros(M, K, device="cuda")
+    x[:, 0] = torch.randint(33, 65, (M,), generator=g, device="cuda")
+    x[:, 1] = 1
+    x[:, 2] = torch.rand(M, generator=g, device="cuda") * 4 + 0.5
+    x = x.to(dtype)
+    wg, wu, wd = torch.zeros(1, 2, K, device="cuda"), torch.zeros(1, 2, K, device="cuda"), torch.zeros(1, K, 2, device="cuda")
+    wg[0, :, 2] = 1                                     # g = x_2
+    wu[0, :, 0], wu[0, 1, 1] = 64, 1                    # u = 64 x_0 and 64 x_0 + 1, exactly
+    wd[0, :, 0] = torch.arange(1, K + 1)
+    wd[0, :, 1] = -wd[0, :, 0]
+    kind = torch.int8 if i8 else dtype
+    scales = (torch.ones(1, 2, device="cuda"), torch.ones(1, 2, device="cuda"), torch.ones(1, K, device="cuda")) if i8 else None
+    y = pws.gemm_moe_nt(x, torch.zeros(1, K, device="cuda", dtype=dtype), *(w.to(kind) for w in (wg, wu, wd)), 1, scales=scales)[0]
+    a, u = act64(x[:, 2:3].double(), "silu"), 64 * x[:, 0:1].double()
+    want = -a * wd[0, :, 0].double()
+    # a's error is the same in both columns; each h is rounded to fp32 and held; sums as in acc_error
+    size = (a * (2 * u + 1)).abs()
+    bound = 2.0 ** -19 * want.abs() + wd[0, :, 0].double() * (2.0 ** -24 + (2.0 ** -24 if dtype == BF16 and not i8 else 2.0 ** -22)) * size
+    bound = bound + acc_error(2, wd[0, :, 0].double() * size) * 3
+    err = (y.double() - want).abs()
+    assert (err <= bound + half_unit(want.abs() + bound, dtype)).all(), float((err / (bound + half_unit(want, dtype))).max())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_moe_infinite_activations(dtype):
+    """h beyond fp32: its token's y is an infinity of the weight's sign, and NaN at a weight of zero, as products with it are; no other
+    token's changes."""
+    K, size = 16, 1e4
+    x = torch.zeros(3, K, device="cuda", dtype=dtype)
+    x[:, 0] = torch.tensor([1.0, size, 2.0], device="cuda")
+    ones = [torch.zeros(1, 40, K, device="cuda", dtype=torch.int8) for _ in range(2)]
+    for w in ones:
+        w[0, :, 0] = 1
+    down = torch.zeros(1, K, 40, device="cuda", dtype=torch.int8)
+    down[0, 0], down[0, 1] = 3, -2
+    s = torch.full((1, 40), 1e16, device="cuda")
+    scales = (s, s, torch.full((1, K), 1e-33, device="cuda"))
+    wr = torch.zeros(1, K, device="cuda", dtype=dtype)
+    y = pws.gemm_moe_nt(x, wr, *ones, down, 1, scales=scales)[0]
+    assert y[1, 0] == math.inf and y[1, 1] == -math.inf and torch.isnan(y[1, 2:]).all()
+    for m in (0, 2):
+        assert torch.isfinite(y[m]).all()
+        assert same_bits(y[m:m + 1], pws.gemm_moe_nt(x[m:m + 1], wr, *ones, down, 1, scales=scales)[0])
+    if dtype == BF16:
+        x[1, 0] = 1e20
+        w = [t.to(dtype) for t in (*ones, down)]
+        y = pws.gemm_moe_nt(x, wr, *w, 1)[0]
+        assert y[1, 0] == math.inf and y[1, 1] == -math.inf and torch.isnan(y[1, 2:]).all() and torch.isfinite(y[[0, 2]]).all()
