@@ -507,9 +507,16 @@ moe_experts_kernel(const __grid_constant__ Params p) {
 
     // Down: the unit before's row block and the number of its arrival (thread 0's)
     int before = -1, arrival = 0;
+    // Thread 0, before a barrier: that row block if its last arrival was this block's, or -1.  The fence between the
+    // counter and the barrier orders the other blocks' stores, each fenced ahead of its own arrival, before
+    // all of this block's loads behind the barrier.
+    const auto last_there = [&]() {
+        if (before < 0 || arrival != routing.entries - 1) return -1;
+        __threadfence();
+        return before;
+    };
     const auto add_choices = [&](int done) {
         if (done < 0) return;
-        __threadfence();
         const int64_t row0 = static_cast<int64_t>(done) * unit_rows;
         for (int i = threadIdx.x; i < p.M * unit_rows; i += kWarps * 32) {
             const int m = i / unit_rows;
@@ -595,7 +602,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
         }
         if (threadIdx.x == 0) {
             claims.put(i_unit, claimed);
-            finished = before >= 0 && arrival == routing.entries - 1 ? before : -1;
+            finished = last_there();
         }
         // join the warps' sums tile by tile; a thread finishes row r of token n, of group m (gate
         // and up) or of each group's half m (down)
@@ -661,7 +668,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     }
     cp_async_wait_group<0>();
     if (DOWN) {
-        if (threadIdx.x == 0) finished = before >= 0 && arrival == routing.entries - 1 ? before : -1;
+        if (threadIdx.x == 0) finished = last_there();
         __syncthreads();
         add_choices(finished);
     }
