@@ -557,7 +557,8 @@ def gemm_i8_nt(a, b, a_scale, b_scale, dtype=None, stream=None):
     """out[M,N] = a_scale[:, None] * b_scale * (a[M,K] @ b[N,K].T) of int8 a and b.
 
     The sum is exact (K at most 131071) and the result rounded once, to `dtype`:
-    float16 or bfloat16 (the default).  The scales are float32 [M] and [N].
+    float16 or bfloat16 (the default).  The scales are float32 [M] and [N].  Not
+    recorded by autograd.
     """
     torch = _torch or _torch_module()
     name = "gemm_i8_nt"
@@ -582,6 +583,7 @@ def gemm_i8_nt(a, b, a_scale, b_scale, dtype=None, stream=None):
         raise ValueError(f"{name}: shapes {tuple(a.shape)}, {tuple(b.shape)} do not form [M,K], [N,K]")
     _vector(name, "a_scale", a_scale, M, torch.float32, device)
     _vector(name, "b_scale", b_scale, N, torch.float32, device)
+    _not_recorded(name, None, a_scale, b_scale)
     lib = load_library()
     s, here = _on(stream, device)
     with here:
@@ -628,7 +630,7 @@ def gemm_moe_nt(x, w_router, w_gate, w_up, w_down, top_k, scales=None, act: str 
             _dense(name, f"the scales of w_{what}", t, (E, cols), torch.float32, device)
         pg, pu, pd = (t.data_ptr() for t in scales)
     top_k = int(top_k)
-    _not_recorded(name, None, x, w_router, w_gate, w_up, w_down)
+    _not_recorded(name, None, x, w_router, w_gate, w_up, w_down, *(scales or ()))
     lib = load_library()
     s, here = _on(stream, device)
     with here:

@@ -903,3 +903,19 @@ def test_moe_infinite_activations(dtype):
         w = [t.to(dtype) for t in (*ones, down)]
         y = pws.gemm_moe_nt(x, wr, *w, 1)[0]
         assert y[1, 0] == math.inf and y[1, 1] == -math.inf and torch.isnan(y[1, 2:]).all() and torch.isfinite(y[[0, 2]]).all()
+
+
+def test_scales_that_require_a_gradient():
+    # learned scales: the calls are not recorded for them either
+    x, wr, ws, scales, _ = layer(2, 64, 32, 4, F16, True)
+    q, s = pws.gemm_i8_quantize(x)
+    for which in range(2):
+        pws._warned.discard("gemm_i8_nt")
+        pair = [s.clone().requires_grad_(which == i) for i in range(2)]
+        with pytest.warns(UserWarning, match="no backward pass"):
+            assert not pws.gemm_i8_nt(q, q, *pair).requires_grad
+    for which in range(3):
+        pws._warned.discard("gemm_moe_nt")
+        three = tuple(c.clone().requires_grad_(which == i) for i, c in enumerate(scales))
+        with pytest.warns(UserWarning, match="no backward pass"):
+            assert not pws.gemm_moe_nt(x, wr, *ws, 2, scales=three)[0].requires_grad
