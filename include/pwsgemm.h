@@ -538,7 +538,9 @@ int gemm_i8_quantize(int64_t M, int64_t K, const void* x, int8_t* q, float* scal
  *   out     : [M, N] of `type` (16 bits), written
  *
  * The sum of products is exact (K at most 131071, so that it fits 32 bits); its
- * fp32 value times a_scale, times b_scale, is rounded once.  K == 0 gives zeros.
+ * fp32 value times a_scale, times b_scale (the other way round where |a_scale| is
+ * above 2^90), is rounded once: an element that fits `type` is right whatever the
+ * scales' sizes.  K == 0 gives zeros.
  */
 int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, const int8_t* b, const float* a_scale,
                const float* b_scale, void* out, int type, void* workspace, int64_t workspace_bytes, cudaStream_t stream);

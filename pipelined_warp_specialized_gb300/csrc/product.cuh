@@ -312,9 +312,13 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int bf16) {
 }
 
 // An element of the 8-bit product from its sum of whole numbers.  The scales one
-// after the other: their product could leave fp32's range where the element does not.
+// after the other: their product could leave fp32's range where the element does
+// not.  A whole number times a scale loses nothing to underflow (it is a multiple of
+// fp32's smallest value where it is below the normal range), and overflows with a scale
+// of 2^97 or more: such a one comes last.
 __device__ __forceinline__ float i8_value(int sum, float a_scale, float b_scale) {
-    return static_cast<float>(sum) * a_scale * b_scale;
+    const bool b_first = fabsf(a_scale) > 0x1p90f;
+    return static_cast<float>(sum) * (b_first ? b_scale : a_scale) * (b_first ? a_scale : b_scale);
 }
 
 // What rounding to 16 bits left of d, for a second 16-bit value beside it; 0

@@ -919,3 +919,23 @@ def test_scales_that_require_a_gradient():
         three = tuple(c.clone().requires_grad_(which == i) for i, c in enumerate(scales))
         with pytest.warns(UserWarning, match="no backward pass"):
             assert not pws.gemm_moe_nt(x, wr, *ws, 2, scales=three)[0].requires_grad
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 64, 256), (20, 96, 256), (40, 130, 8200), (100, 96, 256), (300, 260, 256)])
+def test_i8_scales_at_the_ends_of_their_range(M, N, K, dtype):
+    """Either scale so large that it takes the sum out of fp32's range alone, or below its normal range: the other brings the element back."""
+    a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+    a[0], b[0] = 127, 127                                   # (one sum of the largest)
+    total = (a.double() @ b.double().t()).abs().max()
+    assert total * 3e37 > 3.5e38
+    for large, small in ((3e37, 2.0 ** -140), (3.4e38, 3 * 2.0 ** -148), (1e33, 1e-35), (2.0 ** 91, 2.0 ** -93), (2.0 ** 100, 2.0 ** -126)):
+        for first in (large, small):
+            sa = torch.full((M,), first, device="cuda")
+            sb = torch.full((N,), small if first == large else large, device="cuda")
+            # (to at most 30000 in binary16)
+            if float(total) * large * small > 30000:
+                (sa if first == small else sb).mul_(2.0 ** -math.ceil(math.log2(float(total) * large * small / 30000)))
+            want = i8_want(a, b, sa, sb)
+            assert 0 < want.abs().max() < 65504
+            i8_check(pws.gemm_i8_nt(a, b, sa, sb, dtype=dtype), want, dtype)
