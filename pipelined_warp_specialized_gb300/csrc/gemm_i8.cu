@@ -630,19 +630,21 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
         allow_dependent_launch();
         if (lane == 0) {
             const Waiter W{p.timeout_ns, abort_flag, p.status, kStatusRoleProducer};
-            for (int st = 0; st < stages; ++st) {
-                const int slot = st % L::TOKEN_SLOTS, pair = min(2, count - 2 * st);
-                if (!W.wait(tEMPTY + 8 * slot, st / L::TOKEN_SLOTS & 1)) { ok = false; break; }
+            int armed = 0;
+            for (; armed < stages; ++armed) {
+                const int st = armed, slot = st % L::TOKEN_SLOTS, pair = min(2, count - 2 * st);
+                if (!W.wait(tEMPTY + 8 * slot, st / L::TOKEN_SLOTS & 1)) break;
                 mbar_arrive_expect_tx(tFULL + 8 * slot, pair * (L::TOKENS / 2));
                 for (int k = 0; k < pair; ++k)
                     tma_load_2d(base + L::OFF_TOKENS + slot * L::TOKENS + k * (L::TOKENS / 2), &tokens, (kb0 + 2 * st + k) * BK, token0,
                                 tFULL + 8 * slot);
             }
-            if (!ok) {
-                // copies in flight land within microseconds: a bounded millisecond outlasts them
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
-            }
+            // Copies in flight into this CTA land before it may end.  A slot that was armed last is not armed again, so its
+            // phase is there to be seen, whichever role gave up and however short the limit is.
+            volatile uint32_t no_abort = 0;
+            const Waiter D{max(p.timeout_ns, kDrainNs), &no_abort, p.status, kStatusRoleProducer};
+            for (int st = max(0, armed - L::TOKEN_SLOTS); st < armed; ++st)
+                if (!D.wait(tFULL + 8 * (st % L::TOKEN_SLOTS), st / L::TOKEN_SLOTS & 1)) break;
         }
         __syncwarp();
     } else {

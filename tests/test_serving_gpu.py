@@ -939,3 +939,22 @@ def test_i8_scales_at_the_ends_of_their_range(M, N, K, dtype):
             want = i8_want(a, b, sa, sb)
             assert 0 < want.abs().max() < 65504
             i8_check(pws.gemm_i8_nt(a, b, sa, sb, dtype=dtype), want, dtype)
+
+
+def test_a_limit_shorter_than_a_copy():
+    """Waits that give up while the tokens' copies are on their way: the call says so or is right, and so is the next one."""
+    for M, N, K in ((40, 500, 4096), (24, 20000, 512), (100, 300, 256), (128, 300, 1030), (200, 500, 8200)):
+        a, b = rand_i8((M, K), 1), rand_i8((N, K), 2)
+        ones = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+        want = pws.gemm_i8_nt(a, b, *ones, dtype=BF16)
+        torch.cuda.synchronize()
+        for limit in (1, 1000, 4000):
+            pws.gemm_set_wait_timeout_ns(limit)
+            try:
+                out = pws.gemm_i8_nt(a, b, *ones, dtype=BF16)
+                status = pws.gemm_device_status()
+                assert status == pws.GEMM_ERR_TIMEOUT or (status == pws.GEMM_OK and same_bits(out, want))
+            finally:
+                pws.gemm_set_wait_timeout_ns(0)
+            assert same_bits(pws.gemm_i8_nt(a, b, *ones, dtype=BF16), want)
+            assert pws.gemm_device_status() == pws.GEMM_OK
