@@ -777,12 +777,15 @@ int launch_batch(const CUtensorMap& tokens, BatchParams p, const DeviceInfo& inf
     return GEMM_OK;
 }
 
-// Up to 256 tokens (16384 x 4096 53.9 us, widened in memory 65.2; 8192 x 1024 15.2 and 16.3),
-// and more while all tiles run at once and K is long enough for the widening to count (512
-// tokens through 4096 x 4096 28.6 and 30.6 us, through 2048 x 8192 29.1 and 44.5; 384 through
-// 8192 x 8192, more tiles than SMs, 89.0 and 80.2; 512 through 4096 x 1024 15.0 and 14.2).
-bool batch_tokens(int64_t M, int64_t N, int64_t K) {
-    return M <= 256 || (K >= 2048 && cdiv(N, kBatchRows) * cdiv(M, 128) <= 128);
+// Up to 256 tokens (16384 x 4096 53.8 us, widened in memory 64.8; 4096 x 1024 13.2 and 15.0), and more while
+// all tiles run at once and K is long enough for the widening to count (512 tokens through
+// 4096 x 4096 28.5 and 30.6 us, through 2048 x 8192 29.1 and 44.3; 384 through 8192 x 8192, more tiles than
+// SMs, 89.0 and 80.2; 512 through 4096 x 1024 15.0 and 14.2).  Ragged rows of b go through rings of two
+// stages here, whose copies and widening do not overlap: half as many tiles (768 tokens through 1024 x 8200, 48
+// tiles, 40.0 and 43.5 us, 512 through 2048 x 8200, 64, 40.1 and 47.4, 768, 96, 65.9 and 48.8; 512 through 4096 x 4104, 128,
+// 39.8 and 33.7; up to 256 tokens 16384 x 4104 77.3 and 75.7, 4096 x 4104 26.6 and 32.3, 4096 x 1032 15.0 both).
+bool batch_tokens(int64_t M, int64_t N, int64_t K, bool aligned) {
+    return M <= 256 || (K >= 2048 && cdiv(N, kBatchRows) * cdiv(M, 128) <= (aligned ? 128 : 64));
 }
 int batch_columns(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
@@ -823,7 +826,7 @@ struct Plan {
 };
 
 // num_sms 0: the workspace only.
-Plan plan_of(int64_t M, int64_t N, int64_t K, const void* a, int num_sms, void* ws) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, const void* a, const void* b, int num_sms, void* ws) {
     Plan pl;
     Carver c;
     c.base = static_cast<char*>(ws);
@@ -835,7 +838,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, const void* a, int num_sms, void* 
         return pl;
     }
     pl.a = c.take<uint16_t>(M * pl.ld);
-    pl.batch = batch_tokens(M, N, K);
+    pl.batch = batch_tokens(M, N, K, rows16(b, K));
     if (pl.batch) {
         pl.bytes = c.used;
         return pl;
@@ -880,7 +883,7 @@ extern "C" int gemm_i8_nt_workspace(int64_t M, int64_t N, int64_t K, const int8_
     const int rc = check(M, N, K, a, b, nullptr, nullptr, nullptr, type);
     if (rc != GEMM_OK) return rc;
     if (!bytes) return GEMM_ERR_INVALID_ARG;
-    *bytes = M && N && K ? static_cast<int64_t>(plan_of(M, N, K, a, 0, nullptr).bytes) : 0;
+    *bytes = M && N && K ? static_cast<int64_t>(plan_of(M, N, K, a, b, 0, nullptr).bytes) : 0;
     return GEMM_OK;
 }
 
@@ -900,7 +903,7 @@ extern "C" int gemm_i8_nt(int64_t M, int64_t N, int64_t K, const int8_t* a, cons
     rc = current_device(&info);
     if (rc != GEMM_OK) return rc;
     if (K == 0) return cudaMemsetAsync(out, 0, bytes16(M, N), stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
-    Plan pl = plan_of(M, N, K, a, info.num_sms, workspace);
+    Plan pl = plan_of(M, N, K, a, b, info.num_sms, workspace);
     if (!workspace_ok(workspace, workspace_bytes, pl.bytes, in, outs)) return GEMM_ERR_INVALID_ARG;
     if (pl.few) {
         FewParams p = {reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b), a_scale, b_scale,

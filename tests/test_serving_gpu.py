@@ -958,3 +958,13 @@ def test_a_limit_shorter_than_a_copy():
                 pws.gemm_set_wait_timeout_ns(0)
             assert same_bits(pws.gemm_i8_nt(a, b, *ones, dtype=BF16), want)
             assert pws.gemm_device_status() == pws.GEMM_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(600, 1100, 2050), (700, 1500, 2050), (700, 1500, 2064), (520, 2000, 4100)])
+def test_i8_ragged_weights_on_both_sides_of_a_tile_count(M, N, K):
+    a, b = rand_i8((M, K), M), rand_i8((N, K), N)
+    sa, sb = rand((M,), torch.float32, 3).abs() * 0.02 + 0.001, rand((N,), torch.float32, 4).abs() * 0.02 + 0.001
+    out = pws.gemm_i8_nt(a, b, sa, sb, dtype=BF16)
+    i8_check(out, i8_want(a, b, sa, sb), BF16)
+    for ops in ((off_by_one(a), b), (a, off_by_one(b))):
+        assert same_bits(pws.gemm_i8_nt(*ops, sa, sb, dtype=BF16), out)

@@ -122,6 +122,17 @@ def test_workspaces(lib):
             assert need <= 2 * (300 + 512) * ((K + 63) // 64 * 64) + 512
 
 
+def test_ragged_weights_of_many_tiles_are_widened_in_memory(lib):
+    # 128 x 128 tiles: 48 and 64 of them go past memory in any rows, 96 and 128 in rows of whole 16 bytes alone
+    for M, N, K, tiles in ((768, 1024, 8200, 48), (512, 2048, 8200, 64), (768, 2048, 8200, 96), (512, 4096, 4104, 128)):
+        ld = (K + 63) // 64 * 64
+        tokens, both = 2 * M * ld, 2 * (M + N) * ld
+        need = workspace(lib, "gemm_i8_nt", M, N, K, P[0], P[1], H)
+        assert (both if tiles > 64 else tokens) <= need < (both if tiles > 64 else tokens) + 1024
+        assert tokens <= workspace(lib, "gemm_i8_nt", M, N, ld, P[0], P[1], H) < tokens + 1024
+        assert workspace(lib, "gemm_i8_nt", M, N, ld, P[0], P[1] + 1, H) == need
+
+
 def test_workspace_refusals(lib):
     n = ctypes.c_int64()
     ref = ctypes.byref(n)
