@@ -1,17 +1,19 @@
-// few.cuh -- products of a few tokens: weights stream from memory into the
-// registers of the warps that multiply them.
+// few.cuh -- products of a few tokens: weights stream through a ring of each warp's
+// own into the registers that multiply them.
 //
 //   D[r, t] = sum_k W[r, k] X[t, k]        16 weight rows r, 8 tokens t a tile
 //
 // With few tokens a product is bound by the weights' bytes, so what counts is
-// that every warp has many 16-byte loads in flight.  The operand layout of
-// mma.m16n8k16 lets a weight go from memory to the tensor core without shared
-// memory in between: the instruction's k index only has to mean the same for both
+// that every warp has many 16-byte copies in flight: they go asynchronously into
+// shared memory (Ring, below), and each lane reads its own back.  The operand
+// layout of mma.m16n8k16 needs no exchange between lanes on the way: the
+// instruction's k index only has to mean the same for both
 // operands, so lane (g, t) (g = lane / 4, t = lane % 4) takes 16 consecutive
 // bytes of rows g and g + 8, at byte 16 t of a 64-byte step, and 8 or 16
 // consecutive elements of token g at the same k.  A step is 32 k of 16-bit
 // weights or 64 of 8-bit ones, which are converted in registers: every 8-bit
-// integer is a binary16 and a bfloat16 value.
+// integer is a binary16 and a bfloat16 value.  Shared memory, which weights and tokens both
+// enter and leave, is the busiest unit of these kernels next to memory.
 #pragma once
 
 #include "product.cuh"
@@ -54,7 +56,8 @@ __device__ __forceinline__ void mma_step(float (&d)[4], const uint32_t (&lo)[4],
     mma_16x8x16<BF16>(d, lo[2], hi[2], lo[3], hi[3], x[2], x[3]);
 }
 
-// Four 8-bit integers as two pairs of 16-bit values, exactly.
+// Four 8-bit integers as two pairs of 16-bit values, exactly, by the common way without
+// conversions: an integer below the bits of a power of two reads as their sum.
 //   binary16: a byte b + 128 below the bits of 1024 reads 1152 + b; minus 1152.
 //   bfloat16: below the bits of 128 (units of one) the low seven bits read 128 + (b & 127),
 //             the sign bit alone 128 or 256; their difference is b.

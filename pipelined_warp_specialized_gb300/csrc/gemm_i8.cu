@@ -171,6 +171,7 @@ struct Widen {
 template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
 widen_kernel(const __grid_constant__ Widen p, int64_t K, int64_t ld) {
+    // (in this order: batch_kernel's early copies rest on it)
     grid_dependency_wait();
     allow_dependent_launch();
     const int64_t chunks = (K + 15) / 16, total = (p.rows[0] + p.rows[1]) * chunks;
@@ -415,8 +416,8 @@ align_bytes_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, i
 // are joined exactly.
 //
 // b's bytes bound it; it takes about twice as long (cold caches, through 16384 x 4096: 32
-// tokens 22.5 us, 64 24.0, 128 30.3, where b alone is 10; widening b in memory first takes 58
-// to 62).  8 us are the tokens' widening, the prologue and the joining of sums.  Of the rest the
+// tokens 22.3 us, 64 23.7, 128 29.5, where b alone is 10; widening b in memory first takes 58
+// to 62).  8 us are the tokens' widening (a launch), the prologue and the joining of sums.  Of the rest the
 // issue of multiplies and barriers is the most: a thread takes some 50 clocks a multiply and 100 or
 // more for each wait or commit, 1300 a stage, so with one for both groups 32 tokens took 30.1 us
 // wherever b was widened to (tensor or shared memory), with an arrival for each K block 33.
@@ -625,7 +626,7 @@ batch_kernel(const __grid_constant__ CUtensorMap tokens, const __grid_constant__
     } else if (warp == kBatchWarps) {
         // ======================================================== copies of the tokens
         // The kernel before widens them; this one starts once that one's own wait is over, so b is
-        // there already, and only this warp waits.
+        // there already, in L2, where its copies go (ptx.cuh), and only this warp waits.
         grid_dependency_wait();
         allow_dependent_launch();
         if (lane == 0) {

@@ -42,7 +42,8 @@ constexpr int kWarps = 8;
 
 // ---------------------------------------------------------------- router
 
-// s + p exactly, as s and an error added to c.
+// s + p exactly, as s and an error added to c (Knuth's sum of two numbers and its error, The Art of Computer
+// Programming, volume 2, 4.2.2).
 __device__ __forceinline__ void two_sum(float& s, float& c, float p) {
     const float t = __fadd_rn(s, p), b = __fsub_rn(t, s);
     c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)));
@@ -394,9 +395,10 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     __shared__ int finished;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     // Down reads the routing while gate and up still run: they let it start after their own wait for
-    // the router, so its results are there (one token's layer 20.6 to 17.4 us, with the second unit's claim
+    // the router, so its results are there, in L2, where they are read (ptx.cuh; one token's layer 20.6 to 17.4 us, with the second unit's claim
     // under way while the ring fills).  h is read, and units are claimed, behind the wait alone.
     if (!DOWN) {
+        // (in this order: down's early read rests on it)
         grid_dependency_wait();
         allow_dependent_launch();
     }

@@ -47,8 +47,9 @@ int sm_count_or_default();
 
 // The launch attribute of programmatic dependent launch: the grid may be
 // scheduled while the previous grid in the stream finishes (its kernel calls
-// grid_dependency_wait() before any global memory access), so the launch
-// latency and the set-up overlap the previous grid's tail.
+// grid_dependency_wait() before any global memory access, but for the early reads
+// that ptx.cuh names), so the launch latency and the set-up overlap the previous
+// grid's tail.
 inline cudaLaunchAttribute pdl_attribute() {
     cudaLaunchAttribute a;
     a.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -182,6 +182,15 @@ __device__ __forceinline__ void cluster_sync() {
 // and its memory operations are visible (at once for a grid launched
 // without the attribute).  allow_dependent_launch() lets the next grid in
 // the stream be scheduled before this one finishes.
+//
+// Two kernels read ahead of their own wait what was complete before the kernel that
+// launches them: the 8-bit product's batch kernel its weights, the experts' down
+// kernel the routing.  That rests on the kernel in front, one of the library's own in the same
+// call, which lets its dependents be scheduled only behind its own wait:
+// when one of them runs, every grid ahead of the one in front has completed and
+// flushed its writes.  PTX promises their visibility to the grid that waits;
+// the early reads therefore go past L1, to L2, where completed writes are.  Whatever the kernel in
+// front writes is read behind the reader's own wait alone.
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
