@@ -393,6 +393,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     __shared__ __align__(16) int queue[Claims::QUEUE];
     __shared__ __align__(16) float part[kWarps][2][16][8];      // (read and written in pairs)
     __shared__ int finished;
+    __shared__ uint32_t tile_tops[8];                           // gate and up: of a unit's tile, each token's largest |h|
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     // Down reads the routing while gate and up still run: they let it start after their own wait for
     // the router, so its results are there, in L2, where they are read (ptx.cuh; one token's layer 20.6 to 17.4 us, with the second unit's claim
@@ -413,6 +414,7 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     const int steps = static_cast<int>((length + STEP - 1) / STEP), stride = split * STEP;
     const int mine = (steps - part_of + split - 1) / split;     // of a unit; may be none
     const Claims claims{queue, p.counters + (DOWN ? 1 : 0), Claims::too_short(steps / split, ExpertsRing::STAGES)};
+    if (!DOWN && threadIdx.x < 8) tile_tops[threadIdx.x] = 0u;
     if (threadIdx.x == 0) claims.start();
     __syncthreads();
 
@@ -495,16 +497,16 @@ moe_experts_kernel(const __grid_constant__ Params p) {
     if (DOWN) {
         grid_dependency_wait();
         allow_dependent_launch();
+        if (static_cast<int>(threadIdx.x) * 32 < choices) {
+            // what the units and their joins ask for of each choice, into L1
+            prefetch_l1(p.tops + threadIdx.x * 32);
+            prefetch_l1(p.weights + threadIdx.x * 32);
+        }
     }
     const int second = threadIdx.x == 0 ? claims.claim() : 0;
 #pragma unroll
     for (int i = 0; i < ExpertsRing::STAGES - 1; ++i) fill();
     if (threadIdx.x == 0) claims.second(second);
-    if (DOWN && static_cast<int>(threadIdx.x) * 32 < choices) {
-        // what the units and their joins ask for of each choice, into L1
-        prefetch_l1(p.tops + threadIdx.x * 32);
-        prefetch_l1(p.weights + threadIdx.x * 32);
-    }
     __syncthreads();            // (if units are claimed, the first one fills the ring)
 
     // Down: the unit before's row block and the number of its arrival (thread 0's)
@@ -654,9 +656,14 @@ moe_experts_kernel(const __grid_constant__ Params p) {
                 // this warp's rows of each token
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                if (lane < 8 && top != 0u) atomicMax(p.tops + list[8 * i + lane], top);
+                if (lane < 8 && top != 0u) atomicMax(tile_tops + lane, top);
             }
             __syncthreads();
+            if (!DOWN && threadIdx.x < 8 && 8 * i + n < count) {
+                // the unit's, once for each token (an atomic of every warp made 64 tokens over 8 experts 4 us longer)
+                if (const uint32_t all = tile_tops[n]) atomicMax(p.tops + list[8 * i + n], all);
+                tile_tops[n] = 0u;
+            }
         }
         if (DOWN) {
             // (the barrier ordered the block's stores before this thread's fence)
