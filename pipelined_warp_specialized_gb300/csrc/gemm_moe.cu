@@ -8,8 +8,8 @@
 // projections with the activation, down projections with the weighted sum (both
 // moe_experts_kernel).  With few tokens the layer is bound by the
 // bytes of the chosen experts' weights (few.cuh), which is what one token or a few over
-// many experts come near (a token's six of 64 experts of 2048 x 4096 take 72 us in
-// all, their 302 MB alone 45; 16 tokens over 56 of 1536 x 4096 370 us, 2.1 GB alone 318).
+// many experts come near (a token's six of 64 experts of 2048 x 4096 take 76 us in
+// all, their 302 MB alone 45; 16 tokens over 56 of 1536 x 4096 375 us, 2.1 GB alone 318).
 //
 // Rounding.  Sums are fp32.  The router's logits decide between experts, so
 // they are summed to twice fp32's precision: two experts whose logits differ by
@@ -20,7 +20,9 @@
 // are binary16 values, whatever the tokens' type) into two binary16 values of
 // h times a power of two that brings the token's largest |h| to 2^14 .. 2^15: 22 bits, and
 // 2^-39 of that largest one, whatever the magnitudes.  The power and p are taken into
-// account in fp32 when sums are joined.
+// account in fp32 when sums are joined.  Two 16-bit values of the tokens' type, written by gate and
+// multiplied as they are, took 2 to 4 % less (one token's six experts 73.5 us, 76 so; 32 tokens in 8
+// bits 189 and 196), but are infinite in binary16 from 65520 on, and 16 bits in bfloat16.
 #include <type_traits>
 
 #include "few.cuh"
@@ -821,8 +823,8 @@ int launch_experts(Params p, const DeviceInfo& info, cudaStream_t stream) {
     // the most entries that the routing can give
     const int64_t entries = (choices < p.E ? choices : p.E) + choices / (8 * NT);
     const int64_t rows = DOWN ? p.K : p.ldh, steps = cdiv(DOWN ? p.F : p.K, step_k(FORM));
-    // units of 16 steps a warp, as long as every block has four of them (8 and 32 steps: 207 and 189
-    // against 191 us for 32 tokens over 32 experts of 2048 x 4096 in 8 bits, 378 and 394 against 380
+    // units of 16 steps a warp, as long as every block has four of them (8 and 32 steps: 209 and 197
+    // against 196 us for 32 tokens over 32 experts of 2048 x 4096 in 8 bits, 394 and 410 against 392
     // for 16 tokens over 56 of 1536 x 4096 in 16)
     p.groups = 1;
     while (p.groups < kWarps && steps * p.groups < 16 * kWarps && entries * cdiv(rows, 2 * p.groups * (DOWN ? 32 : 16)) >= 4 * fits) p.groups *= 2;
