@@ -968,3 +968,41 @@ def test_i8_ragged_weights_on_both_sides_of_a_tile_count(M, N, K):
     i8_check(out, i8_want(a, b, sa, sb), BF16)
     for ops in ((off_by_one(a), b), (a, off_by_one(b))):
         assert same_bits(pws.gemm_i8_nt(*ops, sa, sb, dtype=BF16), out)
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["16bit", "8bit"])
+@pytest.mark.parametrize("M", [1, 7, 30, 70])
+def test_moe_sizes_of_the_call_before_do_not_linger(M, i8):
+    """Calls in turn on the same workspace, captured and not, whose activations are 2^40 apart: each as when it ran first."""
+    x, wr, ws, scales, _ = layer(M, 128, 192, 6, F16, i8)
+    ws[2], scales = (ws[2], scales[:2] + (scales[2] / 64,)) if i8 else ((ws[2].float() / 64).to(F16), scales)
+    xs = [(x.float() * 2.0 ** k).to(F16) for k in (0, 10, -10, 10, 0, -10)]
+    want = [pws.gemm_moe_nt(v, wr, *ws, 2, scales=scales)[0] for v in xs]
+    torch.cuda.synchronize()
+    lone = []
+    for v in xs:
+        # (another workspace, full of another call's remains)
+        junk = torch.full((1 << 20,), 0x7E7E7E7E, dtype=torch.int32, device="cuda")
+        del junk
+        lone.append(pws.gemm_moe_nt(v, wr, *ws, 2, scales=scales)[0])
+        torch.cuda.synchronize()
+    static = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = pws.gemm_moe_nt(static, wr, *ws, 2, scales=scales)[0]
+    for _ in range(10):
+        for v, w, a in zip(xs, want, lone):
+            static.copy_(v)
+            graph.replay()
+            assert torch.isfinite(w).all() and same_bits(got, w) and same_bits(a, w)
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["16bit", "8bit"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,F,E", [(64, 203, 130, 40), (64, 208, 128, 1024), (70, 64, 77, 33), (64, 2050, 96, 36)])
+def test_moe_as_many_choices_as_there_can_be(M, K, F, E, dtype, i8):
+    x, wr, ws, scales, _ = layer(M, K, F, E, dtype, i8)
+    y, experts, weights = pws.gemm_moe_nt(x, wr, *ws, 32, scales=scales, normalize=False)
+    want, order, p, bound = moe_want_by_expert(x, wr, ws, scales, 32, "silu", False, held_in_fp32(dtype, i8))
+    assert torch.equal(experts, order) and ((weights.double() - p).abs() <= 2.0 ** -20 * p + 1e-30).all()
+    assert ((y.double() - want).abs() <= bound + half_unit(want.abs() + bound, dtype)).all()
